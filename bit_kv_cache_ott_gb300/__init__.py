@@ -16,7 +16,7 @@ import torch
 
 from . import synth  # noqa: F401  (seeded workloads)
 
-__all__ = ["OTTCache", "OTTError", "load", "status_str", "lib_path", "hbm_copy"]
+__all__ = ["OTTCache", "OTTError", "load", "status_str", "lib_path", "hbm_copy", "rope"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libott.so")
@@ -37,9 +37,15 @@ class StateExport(C.Structure):
                 ("bidx", "kcode", "ks", "kz", "vcode", "vs", "vz", "tk", "tv", "pidx", "pnorm", "pk", "pv")]
 
 
+class RopePlan(C.Structure):
+    _fields_ = [("axes", C.c_int), ("sections", C.c_int * 4), ("base", C.c_double), ("interleaved", C.c_int),
+                ("restart", C.c_int)]
+
+
 SYMBOLS = ("ott_create", "ott_create_ragged", "ott_create_paged", "ott_release_seq", "ott_prefill_seq",
            "ott_free_blocks", "ott_create_cold", "ott_create_pct", "ott_export_cold", "ott_destroy", "ott_prefill", "ott_prefill_lens", "ott_append", "ott_step_host",
-           "ott_decode_attn", "ott_decode_attn_static", "ott_decode_attn_topk", "ott_get_counts", "ott_get_seq_counts", "ott_block_count",
+           "ott_decode_attn", "ott_decode_attn_static", "ott_decode_attn_topk",
+           "ott_chunk_attn", "ott_append_chunk", "ott_decode_attn_window", "ott_rope", "ott_get_counts", "ott_get_seq_counts", "ott_block_count",
            "ott_export_state", "ott_check_device", "ott_device_bytes", "ott_status_str", "ott_hbm_copy", "ott_ex2_probe")
 
 
@@ -77,6 +83,10 @@ def load(build_if_missing: bool = False):
     L.ott_decode_attn.argtypes = [P, P, P, P]
     L.ott_decode_attn_static.argtypes = [P, P, P, P]
     L.ott_decode_attn_topk.argtypes = [P, P, P, i32, P, P]
+    L.ott_chunk_attn.argtypes = [P, P, P, P, P, i32, C.POINTER(i32), i32, i32, P]
+    L.ott_append_chunk.argtypes = [P, P, P, i32, C.POINTER(i32), P]
+    L.ott_decode_attn_window.argtypes = [P, P, P, i32, i32, P]
+    L.ott_rope.argtypes = [P, P, i32, P, P, i32, P, i32, i32, i32, C.POINTER(RopePlan), P]
     L.ott_get_counts.argtypes = [P, C.POINTER(i64), C.POINTER(i32), C.POINTER(i32), C.POINTER(i32)]
     L.ott_get_seq_counts.argtypes = [P, i32, C.POINTER(i64), C.POINTER(i32), C.POINTER(i32), C.POINTER(i32)]
     L.ott_block_count.argtypes = [P, i32]
@@ -126,6 +136,58 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, sections, base: float = 10000.0,
+         interleaved: bool = False, restart: bool = False, out_q: torch.Tensor | None = None,
+         out_k: torch.Tensor | None = None, stream=None):
+    """Rotary positions with len(sections) axes (ott_rope): q fp16 [B][Hq][n][d], k fp16 [B][Hkv][n][d] (either may be
+    None), pos int32 [axes][B][n], all contiguous on one CUDA device. sections: the pairs of channels that turn with
+    each axis; pair i is channels (i, half + i), half = sum(sections), or (2i, 2i + 1) if ``interleaved``; it turns by
+    pos * base ** -e with e = i / half, or j / sections[a] for an axis's j-th pair if ``restart``. Outputs may be the
+    inputs (in place). Returns (rotated q, rotated k), None for one that was not given."""
+    xs = [t for t in (q, k) if t is not None]
+    if not xs:
+        raise ValueError("rope: q or k must be given")
+    if any(not isinstance(t, torch.Tensor) or t.dim() != 4 for t in xs):
+        raise ValueError("rope: expected [B][H][n][d] tensors")
+    B, n, d, dev = xs[0].shape[0], xs[0].shape[2], xs[0].shape[3], xs[0].device
+    sections = [int(x) for x in sections]
+    if not 1 <= len(sections) <= 4:
+        raise ValueError("rope: one to four axes")
+    if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype != torch.int32:
+        raise TypeError("pos: expected a CUDA int32 tensor")
+    if tuple(pos.shape) != (len(sections), B, n) or not pos.is_contiguous():
+        raise ValueError(f"pos: expected contiguous shape {(len(sections), B, n)}, got {tuple(pos.shape)}")
+    ptr, outs, heads = [], [], []
+    for name, x, o in (("q", q, out_q), ("k", k, out_k)):
+        if x is None:
+            if o is not None:
+                raise ValueError(f"out_{name} without {name}")
+            ptr += [None, None]
+            outs.append(None)
+            heads.append(0)
+            continue
+        shp = (B, x.shape[1], n, d)
+        p = _dev_ptr(x, shp, name)
+        o = torch.empty_like(x) if o is None else o
+        ptr += [p, _dev_ptr(o, shp, f"out_{name}")]
+        outs.append(o)
+        heads.append(x.shape[1])
+    _same_device(dev, pos, *xs, *[o for o in outs if o is not None])
+    if B == 0 or sum(heads) == 0 or n == 0:
+        return tuple(outs)
+    plan = RopePlan(len(sections), (C.c_int * 4)(*sections), float(base), int(bool(interleaved)), int(bool(restart)))
+    with torch.cuda.device(dev):
+        _check(load().ott_rope(ptr[0], ptr[1], heads[0], ptr[2], ptr[3], heads[1], pos.data_ptr(), B, n, d,
+                               C.byref(plan), _stream(stream)), "ott_rope")
+    return tuple(outs)
+
+
+def _same_device(dev, *tensors):
+    for t in tensors:
+        if t.device != dev:
+            raise ValueError(f"tensors on {t.device} and {dev}")
+
+
 class OTTCache:
     """One OTT cache (one attention layer): ``create/prefill/append/decode_attn/destroy``.
     ``ragged=True`` creates it with ``ott_create_ragged`` so that ``prefill_lens``
@@ -161,6 +223,7 @@ class OTTCache:
             _check(create(B, Hq, Hkv, d, G, R, P, max_tokens, C.byref(h)),
                    "ott_create_ragged" if ragged else "ott_create")
         self._h = h
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def close(self):
         if getattr(self, "_h", None) and self._h.value:
@@ -247,6 +310,55 @@ class OTTCache:
             sp = sel.data_ptr()
         _check(load().ott_decode_attn_topk(self._h, _dev_ptr(q, shp, "q"), _dev_ptr(out, shp, "out"), int(K), sp,
                                            _stream(stream)), "ott_decode_attn_topk")
+        return out
+
+    def _lens(self, lens):
+        if lens is None:
+            return None
+        if len(lens) != self.B:
+            raise ValueError("lens must hold one length per sequence")
+        return (C.c_int * self.B)(*[int(x) for x in lens])
+
+    def chunk_attn(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens=None, window: int = 0, sinks: int = 0,
+                   out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """Attention of n new tokens per sequence over the cache and, causally, one another (ott_chunk_attn): q fp16
+        [B][Hq][n][d], k, v fp16 [B][Hkv][n][d], not yet in the cache; it is not changed. ``lens`` (ragged caches): the
+        new tokens of each sequence, at most n; rows behind them are neither read nor written. ``window`` > 0: a query
+        sees the last ``window`` tokens up to itself and the sequence's first ``sinks``."""
+        n = q.shape[2] if isinstance(q, torch.Tensor) and q.dim() == 4 else -1
+        shp, kshp = (self.B, self.Hq, n, self.d), (self.B, self.Hkv, n, self.d)
+        ptr = [_dev_ptr(q, shp, "q"), _dev_ptr(k, kshp, "k"), _dev_ptr(v, kshp, "v")]
+        if out is None:
+            out = torch.empty_like(q)
+        ptr.append(_dev_ptr(out, shp, "out"))
+        _same_device(self.device, q, k, v, out)
+        with torch.cuda.device(self.device):
+            _check(load().ott_chunk_attn(self._h, *ptr, n, self._lens(lens), int(window), int(sinks), _stream(stream)),
+                   "ott_chunk_attn")
+        return out
+
+    def append_chunk(self, k: torch.Tensor, v: torch.Tensor, lens=None, stream=None):
+        """Append n tokens per sequence, k, v fp16 [B][Hkv][n][d] (ott_append_chunk): the same as n appends. ``lens``
+        (ragged caches): sequence b takes its first lens[b] tokens, 0 included."""
+        n = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
+        shp = (self.B, self.Hkv, n, self.d)
+        ptr = [_dev_ptr(k, shp, "k"), _dev_ptr(v, shp, "v")]
+        _same_device(self.device, k, v)
+        with torch.cuda.device(self.device):
+            _check(load().ott_append_chunk(self._h, *ptr, n, self._lens(lens), _stream(stream)), "ott_append_chunk")
+
+    def decode_attn_window(self, q: torch.Tensor, window: int, sinks: int = 0, out: torch.Tensor | None = None,
+                           stream=None) -> torch.Tensor:
+        """decode_attn over the last ``window`` tokens and the first ``sinks`` (ott_decode_attn_window; window 0: all)."""
+        shp = (self.B, self.Hq, self.d)
+        qp = _dev_ptr(q, shp, "q")
+        if out is None:
+            out = torch.empty_like(q)
+        op = _dev_ptr(out, shp, "out")
+        _same_device(self.device, q, out)
+        with torch.cuda.device(self.device):
+            _check(load().ott_decode_attn_window(self._h, qp, op, int(window), int(sinks), _stream(stream)),
+                   "ott_decode_attn_window")
         return out
 
     def counts(self):

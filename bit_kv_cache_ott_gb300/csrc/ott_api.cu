@@ -106,21 +106,24 @@ cudaMemPool_t scratch_pool(int dev) {
     return pools[dev];
 }
 
+// Stream-ordered device memory from the library's pool, or else the device's
+// default pool; null if neither has it.
+void *stream_alloc(int dev, size_t bytes, cudaStream_t s) {
+    void *p = nullptr;
+    const cudaMemPool_t pool = scratch_pool(dev);
+    if (pool && cudaMallocFromPoolAsync(&p, bytes, pool, s) == cudaSuccess) return p;
+    cudaGetLastError();
+    if (cudaMallocAsync(&p, bytes, s) == cudaSuccess) return p;
+    cudaGetLastError();
+    return nullptr;
+}
+
 bool try_prefill_parallel(const ott_cache *c, const __half *K, const __half *V, long long unit_stride, int src_u0,
                           int u0, int nu, int nf, int shared_units, cudaStream_t s, cudaError_t &err) {
     err = cudaSuccess;
     if (!prefill_parallel_ok(c, nf, shared_units)) return false;
-    void *scratch = nullptr;
-    const size_t bytes = prefill_scratch_bytes(c, nu, nf);
-    const cudaMemPool_t pool = scratch_pool(c->device);
-    if (!pool || cudaMallocFromPoolAsync(&scratch, bytes, pool, s) != cudaSuccess) {
-        cudaGetLastError();
-        scratch = nullptr;
-        if (cudaMallocAsync(&scratch, bytes, s) != cudaSuccess) {
-            cudaGetLastError();
-            return false;
-        }
-    }
+    void *scratch = stream_alloc(c->device, prefill_scratch_bytes(c, nu, nf), s);
+    if (!scratch) return false;
     err = launch_prefill_parallel(c, K, V, unit_stride, src_u0, u0, nu, nf, static_cast<uint64_t *>(scratch), s);
     const cudaError_t e2 = cudaFreeAsync(scratch, s);
     if (err == cudaSuccess) err = e2;
@@ -128,6 +131,22 @@ bool try_prefill_parallel(const ott_cache *c, const __half *K, const __half *V, 
 }
 
 }  // namespace
+
+namespace ott {
+
+Scratch::Scratch(const ott_cache *c, size_t floats, cudaStream_t s) : ptr(c->part), owned(false), stream(s) {
+    if (floats <= c->part_floats) return;
+    ptr = stream_alloc(c->device, floats * sizeof(float), s);
+    owned = ptr != nullptr;
+}
+
+cudaError_t Scratch::release() {
+    if (!owned) return cudaSuccess;
+    owned = false;
+    return cudaFreeAsync(ptr, stream);
+}
+
+}  // namespace ott
 
 extern "C" {
 
@@ -309,6 +328,7 @@ int create_cache(int B, int Hq, int Hkv, int d, int G, int R, int P, int max_tok
     c->pnorm = reinterpret_cast<float *>(base + o_pn);
     c->pidx = reinterpret_cast<int32_t *>(base + o_pi);
     c->part = reinterpret_cast<float *>(base + o_part);
+    c->part_floats = sz_part / 4;
     c->ctl = reinterpret_cast<int *>(base + o_ctl);
     c->qdev = reinterpret_cast<__half *>(base + o_q);
     c->ck = sz_cold ? reinterpret_cast<__half *>(base + o_ck) : nullptr;
@@ -325,6 +345,7 @@ int create_cache(int B, int Hq, int Hkv, int d, int G, int R, int P, int max_tok
     e = cudaMemset(mem, 0, c->mem_bytes);
     if (e == cudaSuccess) e = set_kernel_attributes(d, gs, smem_optin);
     if (e == cudaSuccess) e = set_topk_attributes(d, gs, smem_optin);
+    if (e == cudaSuccess) e = set_chunk_attributes(d);
     if (e == cudaSuccess && c->paged) {
         // every pool slot free
         std::vector<int32_t> slots((size_t)pool_blocks);
@@ -568,6 +589,142 @@ int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t 
     if (e == cudaSuccess && sel && Kc > 0)
         e = cudaMemcpyAsync(sel, c->sel, (size_t)c->U * Kc * 4, cudaMemcpyDeviceToDevice, s);
     return fail_cuda(c, e);
+}
+
+namespace {
+
+// The checks that the calls on chunks and windows share, before anything else
+// is looked at: the cache's device is current, and lens fits its kind.
+int chunk_state(const ott_cache *c, const int *lens) {
+    if (c->poisoned || (lens && !c->ragged_capable)) return OTT_ERR_STATE;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return OTT_ERR_CUDA;
+    return dev == c->device ? OTT_OK : OTT_ERR_STATE;
+}
+
+bool lens_ok(const ott_cache *c, int n, const int *lens) {
+    for (int b = 0; lens && b < c->B; ++b)
+        if (lens[b] < 0 || lens[b] > n) return false;
+    return true;
+}
+
+long long seq_tokens(const ott_cache *c, int b) { return c->ragged ? c->Tb[b] : c->T; }
+
+int chunk_call(ott_cache *c, ChunkCall &call, void *stream) {
+    long long t_max = 0;
+    for (int b = 0; b < c->B; ++b) t_max = std::max(t_max, seq_tokens(c, b));
+    if (t_max + call.n > INT_MAX) return OTT_ERR_INVALID;
+    if (call.window > t_max + call.n) call.window = 0;   // nothing is hidden
+    cudaError_t e;
+    const int rc = run_chunk(c, call, static_cast<cudaStream_t>(stream), e);
+    return rc == OTT_ERR_CUDA ? fail_cuda(c, e) : rc;
+}
+
+}  // namespace
+
+int ott_chunk_attn(ott_cache *c, const void *q, const void *k, const void *v, void *out, int n, const int *lens,
+                   int window, int sinks, void *stream) {
+    if (!c) return OTT_ERR_INVALID;
+    if (const int rc = chunk_state(c, lens)) return rc;
+    if (n < 0 || window < 0 || sinks < 0 || !lens_ok(c, n, lens)) return OTT_ERR_INVALID;
+    if (n == 0) return OTT_OK;
+    if (!q || !k || !v || !out || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || out == q ||
+        out == k || out == v)
+        return OTT_ERR_INVALID;
+    ChunkCall call = {static_cast<const __half *>(q), static_cast<const __half *>(k), static_cast<const __half *>(v),
+                      static_cast<__half *>(out), n, lens, window, sinks};
+    return chunk_call(c, call, stream);
+}
+
+int ott_decode_attn_window(ott_cache *c, const void *q, void *out, int window, int sinks, void *stream) {
+    if (!c) return OTT_ERR_INVALID;
+    if (const int rc = chunk_state(c, nullptr)) return rc;
+    if (c->T < 1 || some_sequence_empty(c)) return OTT_ERR_STATE;
+    if (window < 0 || sinks < 0 || !q || !out || !aligned16(q) || !aligned16(out) || q == out) return OTT_ERR_INVALID;
+    ChunkCall call = {static_cast<const __half *>(q), nullptr, nullptr, static_cast<__half *>(out), 1, nullptr,
+                      window, sinks};
+    return chunk_call(c, call, stream);
+}
+
+int ott_append_chunk(ott_cache *c, const void *k, const void *v, int n, const int *lens, void *stream) {
+    if (!c) return OTT_ERR_INVALID;
+    if (const int rc = chunk_state(c, lens)) return rc;
+    if (n < 0 || !lens_ok(c, n, lens)) return OTT_ERR_INVALID;
+    if (n == 0) return OTT_OK;
+    if (!k || !v || !aligned16(k) || !aligned16(v)) return OTT_ERR_INVALID;
+    // per sequence: tokens and flushes afterwards
+    long long unit_flushes = 0;
+    bool any = false;
+    for (int b = 0; b < c->B; ++b) {
+        const int m = lens ? lens[b] : n;
+        const long long T = seq_tokens(c, b) + m;
+        if (T > c->max_tokens) return OTT_ERR_CAPACITY;
+        unit_flushes += (long long)(flushes_after(c, T) - (c->ragged ? c->nfb[b] : c->nf)) * c->Hkv;
+        any |= m > 0;
+    }
+    if (blocks_needed(c, unit_flushes) > c->free_blocks) return OTT_ERR_CAPACITY;
+    if (!any) return OTT_OK;
+    if ((c->paged || lens) && !c->ragged) to_per_sequence(c);
+    c->free_blocks -= blocks_needed(c, unit_flushes);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const __half *kh = static_cast<const __half *>(k), *vh = static_cast<const __half *>(v);
+    // Rounds: fill every ring up to its next flush (or the chunk's end), then
+    // flush the sequences that are full; the ring holds G + R tokens, exactly
+    // what a flush waits for. The host's counts move with what is queued.
+    std::vector<int> done(c->B, 0);
+    for (bool more = true; more;) {
+        more = false;
+        for (int b0 = 0; b0 < c->B; b0 += RAGGED_MAX) {
+            ChunkRange r;
+            r.n = std::min(c->B - b0, RAGGED_MAX);
+            bool some = false;
+            for (int x = 0; x < r.n; ++x) {
+                const int b = b0 + x, m = lens ? lens[b] : n, nf = c->ragged ? c->nfb[b] : c->nf;
+                const long long T = seq_tokens(c, b), T0 = T - (c->ragged ? done[b] : done[0]);
+                const long long room = (long long)nf * c->G + c->G + c->R - T;
+                r.from[x] = c->ragged ? done[b] : done[0];
+                r.to[x] = (int)std::min<long long>(m, r.from[x] + room);
+                r.slot[x] = (int)(T0 % c->ring);
+                some |= r.to[x] > r.from[x];
+            }
+            if (!some) continue;
+            cudaError_t e = launch_append_range(c, kh, vh, n, b0, r, s);
+            if (e != cudaSuccess) return fail_cuda(c, e);
+            if (!c->ragged) continue;   // counts move once, below
+            FlushList fl;
+            fl.n = 0;
+            for (int x = 0; x < r.n; ++x) {
+                const int b = b0 + x;
+                c->Tb[b] += r.to[x] - r.from[x];
+                done[b] = r.to[x];
+                if (flush_due_seq(c, b)) {
+                    fl.lb[fl.n] = b;
+                    fl.lj[fl.n] = c->nfb[b];
+                    ++fl.n;
+                }
+                more |= done[b] < (lens ? lens[b] : n);
+            }
+            if (fl.n > 0) c->blocks_settled = 0;
+            e = launch_flush_list(c, c->rk, c->rv, (long long)c->ring * c->d, c->ring, fl, s);
+            if (e != cudaSuccess) return fail_cuda(c, e);
+            for (int i = 0; i < fl.n; ++i) c->nfb[fl.lb[i]] += 1;
+            refresh_T(c);
+        }
+        if (!c->ragged) {
+            const int step = (int)std::min<long long>(n - done[0], (long long)c->nf * c->G + c->G + c->R - c->T);
+            c->T += step;
+            done[0] += step;
+            if (flush_due(c)) {
+                c->blocks_settled = 0;
+                const cudaError_t e = launch_flush(c, c->rk, c->rv, (long long)c->ring * c->d, c->ring,
+                                                   (long long)c->nf * c->G, c->nf, s);
+                if (e != cudaSuccess) return fail_cuda(c, e);
+                c->nf += 1;
+            }
+            more = done[0] < n;
+        }
+    }
+    return OTT_OK;
 }
 
 int ott_release_seq(ott_cache *c, int b, void *stream) {

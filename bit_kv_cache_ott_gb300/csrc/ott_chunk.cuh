@@ -1,0 +1,153 @@
+// ott_chunk.cuh -- what the kernels of ott_chunk_attn and
+// ott_decode_attn_window share: the launch's arguments, the table of its
+// sequences, the visibility rule, small device helpers.
+#pragma once
+
+#include <math_constants.h>
+
+#include "ott_internal.cuh"
+
+namespace ott {
+
+// One sequence of a launch.
+struct ChunkSeq {
+    long long base;    // its first work item; entry [nseq] holds the total
+    int ubase;         // its first work unit
+    int S;             // slices of query rows per kv head (0: no queries)
+    int T;             // tokens in the cache
+    int pos0;          // position of its first query
+    int nq;            // query tokens
+    int nnew;          // new tokens behind the cache's: nq, or 0 for a decode step
+    int nf, jlo;       // blocks; blocks j >= jlo may hold tokens of the window
+    int nsink;         // slots of the list of blocks j < jlo that hold one of the first tokens
+    int ntail, npool, ring_start;
+    int Sf, Iu;        // fp16 work items, all work items of a unit
+};
+struct ChunkTable {
+    ChunkSeq e[RAGGED_MAX + 1];
+};
+
+struct ChunkArgs {
+    const uint8_t *blk;
+    long long blk_bytes;
+    const int32_t *bidx, *bcnt, *bt, *sel, *pidx, *cidx;
+    const int *cmeta;
+    const __half *rk, *rv, *pk, *pv, *ck, *cv;
+    const __half *q, *k, *v;   // [B][Hq][n][d], [B][Hkv][n][d]
+    __half *out;
+    float *part;
+    int *ctl;
+    int n, B0, nseq;           // rows of room per sequence; the launch's sequences B0 .. B0 + nseq - 1
+    int Hq, Hkv, g, NB, G, P, C, ring;
+    int jfull;                 // blocks j >= jfull hold G tokens (norm criterion)
+    int CPB;                   // chunks (CHUNK_TILES tiles) per block
+    int window, sinks;         // window 0: no limit
+    long long W;               // work items
+    int NWp, MAXU, RV;         // active warps, units a warp's range can touch, rows of a partial
+    float sl2;                 // log2(e) / sqrt(d)
+};
+
+// Valid tokens of block j of unit u.
+__device__ __forceinline__ int chunk_block_cnt(const ChunkArgs &a, int u, int j) {
+    if (a.bcnt) return __ldg(a.bcnt + (size_t)u * a.NB + j);
+    return j >= a.jfull ? a.G : block_count(a.P, a.G, j);
+}
+
+// Position of fp16 token f of a unit: residual ring (oldest first), pool,
+// cold pool (oldest first), new tokens.
+__device__ __forceinline__ int chunk_fp16_pos(const ChunkArgs &a, const ChunkSeq &s, int u, int f, int ncold, int chead) {
+    if (f < s.ntail) return s.T - s.ntail + f;
+    f -= s.ntail;
+    if (f < s.npool) return __ldg(a.pidx + (size_t)u * a.P + f);
+    f -= s.npool;
+    if (f < ncold) {
+        int x = chead + f;
+        if (x >= a.C) x -= a.C;
+        return __ldg(a.cidx + (size_t)u * a.C + x);
+    }
+    return s.T + f - ncold;
+}
+__device__ __forceinline__ const __half *chunk_fp16_row(const ChunkArgs &a, const ChunkSeq &s, int b, int hkv, int u,
+                                                        int f, int ncold, int chead, bool val, int D) {
+    if (f < s.ntail) {
+        int x = s.ring_start + f;
+        if (x >= a.ring) x -= a.ring;
+        return (val ? a.rv : a.rk) + ((size_t)u * a.ring + x) * D;
+    }
+    f -= s.ntail;
+    if (f < s.npool) return (val ? a.pv : a.pk) + ((size_t)u * a.P + f) * D;
+    f -= s.npool;
+    if (f < ncold) {
+        int x = chead + f;
+        if (x >= a.C) x -= a.C;
+        return (val ? a.cv : a.ck) + ((size_t)u * a.C + x) * D;
+    }
+    return (val ? a.v : a.k) + (((size_t)b * a.Hkv + hkv) * a.n + (f - ncold)) * D;
+}
+
+// The token at t is seen from position p, whose window starts at lo.
+__device__ __forceinline__ bool chunk_sees(int t, int p, int lo, int sinks) { return t <= p && (t >= lo || t < sinks); }
+
+__device__ __forceinline__ uint32_t ch_smem(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ float ch_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t ch_h2(__half2 h) { return *reinterpret_cast<uint32_t *>(&h); }
+__device__ __forceinline__ __half2 ch_as_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
+
+// Dequantization in fp16x2 registers. The two codes at position p of a word
+// (w10 = w >> 10 serves p >= 5) are ORed into the mantissa of 2^(10-2c),
+// c = p mod 5, whose unit in the last place they are counted in: an exact
+// fp16 2^(10-2c) + code. One subtraction gives code - 1 (keys) or code
+// (values), exactly.
+__device__ __forceinline__ uint32_t ch_raw(uint32_t w, uint32_t w10, int p) {
+    const int c = cls_of_pos(p);
+    const uint32_t magic = (uint32_t)((25 - 2 * c) << 10) * 0x10001u;
+    return ((p < 5 ? w : w10) & (0x00030003u << (2 * c))) | magic;
+}
+__device__ __forceinline__ uint32_t ch_const(int p, int less) {   // -(2^(10-2c) + less) in both halves
+    const __half h = __float2half_rn(-(float)((1 << (10 - 2 * cls_of_pos(p))) + less));
+    return (uint32_t)__half_as_ushort(h) * 0x10001u;
+}
+// s * (code - 1): exact (a scale, its negative, zero or twice it)
+__device__ __forceinline__ uint32_t ch_key(uint32_t w, uint32_t w10, int p, uint32_t s2) {
+    const __half2 c1 = __hadd2(ch_as_h2(ch_raw(w, w10, p)), ch_as_h2(ch_const(p, 1)));
+    return ch_h2(__hmul2(c1, ch_as_h2(s2)));
+}
+// z + s * code, one rounding
+__device__ __forceinline__ uint32_t ch_val(uint32_t w, uint32_t w10, int p, uint32_t s2, uint32_t z2) {
+    const __half2 c = __hadd2(ch_as_h2(ch_raw(w, w10, p)), ch_as_h2(ch_const(p, 0)));
+    return ch_h2(__hfma2(c, ch_as_h2(s2), ch_as_h2(z2)));
+}
+// fp16x2 hi + lo = s + z exactly up to lo's rounding (the two-sum of both halves)
+__device__ __forceinline__ void ch_offset(uint32_t s2, uint32_t z2, uint32_t &hi, uint32_t &lo) {
+    const __half2 s = ch_as_h2(s2), z = ch_as_h2(z2);
+    const __half2 h = __hadd2_rn(z, s), b = __hsub2_rn(h, z);
+    lo = ch_h2(__hadd2_rn(__hsub2_rn(z, __hsub2_rn(h, b)), __hsub2_rn(s, b)));
+    hi = ch_h2(h);
+}
+
+// Items split over warps as evenly as integers allow (the decode kernel's rule).
+__device__ __forceinline__ long long ch_range_start(long long W, int NWp, long long w) {
+    const unsigned long long num = (unsigned long long)w * (unsigned long long)W;
+    if (num <= 0xffffffffull) return (long long)((unsigned)num / (unsigned)NWp);
+    return (long long)(num / (unsigned long long)NWp);
+}
+__device__ __forceinline__ int ch_warp_of(long long W, int NWp, long long x) {
+    return (int)(((unsigned long long)(x + 1) * (unsigned long long)NWp + (unsigned long long)W - 1) /
+                 (unsigned long long)W) - 1;
+}
+// Entry that holds work item x (x < W): the last one whose base is <= x.
+__device__ __forceinline__ int ch_entry_of(const ChunkTable &st, int nseq, long long x) {
+    int lo = 0, hi = nseq;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (st.e[mid].base <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+}  // namespace ott

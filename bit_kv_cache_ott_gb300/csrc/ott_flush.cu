@@ -909,6 +909,21 @@ __global__ void k_copy_tail(const __half *K, const __half *V, __half *rk, __half
     }
 }
 
+// Tokens [from, to) of each sequence's chunk, k, v [B][Hkv][n][d] -> the ring.
+// One 16-byte vector of k and of v per thread and step; y = unit.
+__global__ void k_append_range(const uint4 *__restrict__ k, const uint4 *__restrict__ v, __half *rk, __half *rv, int n,
+                               int Hkv, int d, int ring, int b0, const __grid_constant__ ChunkRange r) {
+    const int x = blockIdx.y / Hkv, u = b0 * Hkv + blockIdx.y, vpr = d / 8;
+    const int from = r.from[x], cnt = (r.to[x] - from) * vpr;
+    for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < cnt; e += gridDim.x * blockDim.x) {
+        const int t = from + e / vpr;
+        const size_t src = ((size_t)u * n + t) * vpr + e % vpr;
+        const size_t dst = ((size_t)u * ring + (size_t)(((long long)r.slot[x] + t) % ring)) * vpr + e % vpr;
+        reinterpret_cast<uint4 *>(rk)[dst] = k[src];
+        reinterpret_cast<uint4 *>(rv)[dst] = v[src];
+    }
+}
+
 // Canonical export of the quantized blocks of units [u0, u0+nu):
 //   kcode/vcode [nu][nf][G][d/4] bytes, ks/kz [nu][nf][d], vs/vz [nu][nf][G][d/32]
 struct ExportArgs {
@@ -1239,6 +1254,33 @@ cudaError_t launch_append_ragged(const ott_cache *c, const __half *k, const __ha
     return cudaLaunchKernelEx(&cfg, k_append_ragged, reinterpret_cast<const uint4 *>(k),
                               reinterpret_cast<const uint4 *>(v), c->rk, c->rv, c->U, c->Hkv, c->d, c->ring, st,
                               reinterpret_cast<const uint4 *>(qsrc), reinterpret_cast<uint4 *>(c->qdev), nq);
+}
+
+cudaError_t launch_append_range(const ott_cache *c, const __half *k, const __half *v, int n, int b0,
+                                const ChunkRange &r, cudaStream_t s) {
+    int most = 0;
+    for (int x = 0; x < r.n; ++x) most = std::max(most, r.to[x] - r.from[x]);
+    const int th = 256;
+    const long long bx = ((long long)most * (c->d / 8) + th - 1) / th;
+    // grid.y: the units, in rows of at most 65,535
+    for (int y = 0; y < r.n * c->Hkv;) {
+        // whole sequences per launch
+        const int per = std::max(1, 65535 / c->Hkv), x0 = y / c->Hkv, m = std::min(per, r.n - x0);
+        ChunkRange q = r;
+        if (x0 > 0)
+            for (int x = 0; x < m; ++x) {
+                q.from[x] = r.from[x0 + x];
+                q.to[x] = r.to[x0 + x];
+                q.slot[x] = r.slot[x0 + x];
+            }
+        k_append_range<<<dim3((unsigned)std::min<long long>(bx, 1024), (unsigned)(m * c->Hkv)), th, 0, s>>>(
+            reinterpret_cast<const uint4 *>(k), reinterpret_cast<const uint4 *>(v), c->rk, c->rv, n, c->Hkv, c->d,
+            c->ring, b0 + x0, q);
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        y += m * c->Hkv;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_copy_tail_units(const ott_cache *c, const __half *K, const __half *V, int u0, int nu,

@@ -152,6 +152,7 @@ struct ott_cache {
     float *pnorm;           // [U][P]
     int32_t *pidx;          // [U][P]
     float *part;            // [warps][maxu][2][gs][d+2] split-K partials
+    size_t part_floats;     // its size
     int *ctl;               // [1] status flag set by a bounded wait that timed out
     __half *qdev;           // [B][Hq][d] the queries of a step fed from host memory
     // sequences of different lengths (ott_create_ragged + ott_prefill_lens)
@@ -243,6 +244,35 @@ int decode_smem_bytes(int d, int gs);
 cudaError_t set_kernel_attributes(int d, int gs, int smem_max);
 cudaError_t set_flush_attributes(int d, int smem);
 bool decode_supported(int d);
+// A chunk's or a windowed decode's attention (ott_chunk_attn,
+// ott_decode_attn_window). k null: one query per sequence at the last token.
+struct ChunkCall {
+    const __half *q, *k, *v;
+    __half *out;
+    int n;             // rows of room per sequence
+    const int *lens;   // null: n each
+    int window, sinks;
+};
+cudaError_t set_chunk_attributes(int d);
+int run_chunk(const ott_cache *c, const ChunkCall &call, cudaStream_t s, cudaError_t &err);
+// Append tokens [from[b], to[b]) of a chunk to the ring of every sequence
+// b0 .. b0 + nseq - 1 (chunk token x becomes token T_b + x).
+struct ChunkRange {
+    int n;
+    int from[RAGGED_MAX], to[RAGGED_MAX];
+    int slot[RAGGED_MAX];   // ring slot of token T_b
+};
+cudaError_t launch_append_range(const ott_cache *c, const __half *k, const __half *v, int n, int b0,
+                                const ChunkRange &r, cudaStream_t s);
+// `floats` floats for the duration of a call: the cache's split-K scratch
+// where they fit, else stream-ordered memory (ptr null: none to be had).
+struct Scratch {
+    Scratch(const ott_cache *c, size_t floats, cudaStream_t s);
+    cudaError_t release();
+    void *ptr;
+    bool owned;
+    cudaStream_t stream;
+};
 // query heads per decode pass for gq query heads per kv head
 inline int slice_heads(int gq) { return (gq == 1 || gq == 2 || gq == 4) ? gq : 4; }
 

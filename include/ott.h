@@ -308,6 +308,92 @@ int ott_decode_attn_static(ott_cache *c, const void *q, void *out, void *stream)
  */
 int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t *sel, void *stream);
 
+/*
+ * Several new tokens per sequence, over a cache that holds some already (a
+ * chunk of a prompt, a continued conversation, a draft to verify). The loop
+ * is: ott_rope on the chunk's queries and keys, ott_chunk_attn, and then
+ * ott_append_chunk for the tokens that stay.
+ *
+ * A chunk has room for n tokens of every sequence; lens (HOST int32[B], read
+ * during the call, or NULL for n each) gives sequence b its lens[b] of them,
+ * 0 <= lens[b] <= n, the first rows of its room. Rows behind them are
+ * neither read nor written. lens other than NULL needs a cache from
+ * ott_create_ragged or ott_create_paged (OTT_ERR_STATE). n = 0 does nothing.
+ * These three calls need the cache's device to be the current one
+ * (OTT_ERR_STATE).
+ *
+ * window and sinks limit what a query sees: the query at position p (the
+ * token's index within its sequence) sees the token at position t <= p if
+ * t > p - window (the last `window` tokens, itself among them) or t < sinks
+ * (the sequence's first tokens, which stay visible). window = 0: every
+ * token (sinks is then ignored). window < 0 or sinks < 0: OTT_ERR_INVALID.
+ * Blocks of which no token is seen are not read. Tokens that a policy has
+ * discarded are seen by nobody.
+ */
+
+/*
+ * Attention of a chunk's queries over the cache and the chunk itself. q, out:
+ * DEVICE fp16 [B][Hq][n][d]; k, v: DEVICE fp16 [B][Hkv][n][d], the chunk's
+ * own keys and values, which the cache does not hold yet. Query i of
+ * sequence b has position T_b + i: it sees the cache's T_b tokens
+ * (dequantized blocks, residual ring, pool, cold pool) and the chunk's tokens
+ * 0 .. i. out = softmax(q . K^T / sqrt(d)) V, as ott_decode_attn after i + 1
+ * appends would give it if none of them flushed. The cache is read only and
+ * may be empty, in part or whole (plain causal attention over the chunk).
+ * out may not alias q, k or v.
+ * Softmax statistics and sums are fp32; the weights and the dequantized
+ * values are rounded to fp16 for the tensor cores (each at most 2^-11
+ * relative). Keys and values are served up to a magnitude of 48,000.
+ * Partial results go to the cache's split-K scratch, or where they are
+ * larger to stream-ordered scratch from the library's pool (see ott_prefill;
+ * OTT_ERR_OOM if none can be had, before anything is queued).
+ */
+int ott_chunk_attn(ott_cache *c, const void *q, const void *k, const void *v, void *out, int n, const int *lens,
+                   int window, int sinks, void *stream);
+
+/*
+ * Append a chunk: sequence b receives its lens[b] tokens (n with lens NULL)
+ * in order, exactly as that many ott_append calls would (the flushes that
+ * they make due included, in every variant). k, v: DEVICE fp16
+ * [B][Hkv][n][d]. An empty sequence may be filled this way.
+ * OTT_ERR_CAPACITY if a sequence would outgrow max_tokens or a paged pool
+ * lacks the blocks, before anything is queued.
+ */
+int ott_append_chunk(ott_cache *c, const void *k, const void *v, int n, const int *lens, void *stream);
+
+/*
+ * ott_decode_attn with a window: one query per sequence, at the position of
+ * the last token appended (p = T_b - 1). q, out: DEVICE fp16 [B][Hq][d].
+ * Precision and scratch as ott_chunk_attn.
+ */
+int ott_decode_attn_window(ott_cache *c, const void *q, void *out, int window, int sinks, void *stream);
+
+/*
+ * Rotary positions with several axes (time, height, width of a video, rows
+ * and columns of an image; one axis for text). q, q_out: DEVICE fp16
+ * [B][Hq][n][d]; k, k_out: DEVICE fp16 [B][Hkv][n][d]; pos: DEVICE int32
+ * [axes][B][n], any values. Hq or Hkv may be 0 (its pointers are then
+ * ignored). An output may be its input (in place) but may not overlap it
+ * otherwise. d: a multiple of 16 up to 256. A call rotates all n rows.
+ * The plan: sections[a] >= 1 pairs of channels turn with axis a, axis by
+ * axis; half = their sum <= d / 2. Pair i is channels (i, half + i), or
+ * (2i, 2i + 1) if interleaved; channels from 2 * half on are copied. Pair i
+ * turns by pos * base^-e with e = i / half, or, if restart is set, e = j /
+ * sections[a] for the axis's j-th pair. base >= 1. Angles are reduced
+ * exactly, also those of far positions; products are fp32, rounded once.
+ * Works on the current device.
+ */
+typedef struct {
+    int axes;
+    int sections[4];
+    double base;
+    int interleaved;
+    int restart;
+} ott_rope_plan;
+
+int ott_rope(const void *q, void *q_out, int Hq, const void *k, void *k_out, int Hkv, const int32_t *pos,
+             int B, int n, int d, const ott_rope_plan *plan, void *stream);
+
 /* Counts (same for every sequence and kv head): tokens seen, blocks (flushes),
  * residual tokens, pool tokens. Host-side, no device access. After
  * ott_prefill_lens the counts differ per sequence; this then reports
