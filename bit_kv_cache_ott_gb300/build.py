@@ -16,8 +16,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libott.so")
-SOURCES = ["ott_api.cu", "ott_flush.cu", "ott_decode.cu", "ott_topk.cu", "ott_chunk.cu", "ott_rope.cu",
-           "ott_peak.cu"]
+SOURCES = ["ott_api.cu", "ott_flush.cu", "ott_decode.cu", "ott_topk.cu", "ott_chunk.cu", "ott_chunk_tiles.cu",
+           "ott_rope.cu", "ott_peak.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
                      f"-I{os.path.join(ROOT, 'include')}"]

@@ -35,6 +35,7 @@ namespace {
 
 constexpr int FI = 8;                       // fp16 tokens per work item
 constexpr int CT = CHUNK_TILES * TILE;      // block slots per work item
+constexpr int ROWS_MAX = 16;                // query rows per kv head up to which this kernel serves a call
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -670,21 +671,6 @@ __global__ void __launch_bounds__(SINK_THREADS)
     for (int x = found + threadIdx.x; x < nsink; x += SINK_THREADS) out[x] = -1;
 }
 
-template <typename... KArgs, typename... Args>
-cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 template <int D, int NC>
 cudaError_t launch_rows(const ChunkArgs &a, const ChunkTable &st, int sms, cudaStream_t s) {
     using C = RowsCfg<D, NC>;
@@ -704,7 +690,8 @@ cudaError_t rows_attribute() {
 struct Plan {
     ChunkArgs a;
     ChunkTable st;
-    int NC;
+    int NC;       // groups of 8 rows, 0: tiles (ott_chunk_tiles.cu)
+    int nC;       // tiles: CTAs
     bool sinks, any;
     size_t part_floats;
 };
@@ -753,8 +740,10 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
     const bool decode = call.k == nullptr;
     int nq_max = 0;
     for (int x = 0; x < a.nseq; ++x) nq_max = std::max(nq_max, call.lens ? call.lens[B0 + x] : call.n);
-    p.NC = (long long)nq_max * c->gq <= 8 ? 1 : 2;
-    const int RB = 8 * p.NC;
+    const long long rows = (long long)nq_max * c->gq;
+    p.NC = rows <= 8 ? 1 : (rows <= ROWS_MAX ? 2 : 0);
+    const bool tiles = p.NC == 0;
+    const int RB = tiles ? 256 : 8 * p.NC;
     a.RV = (int)std::min<long long>(RB, (long long)nq_max * c->gq);
     long long base = 0, units = 0;
     int min_iu = INT_MAX;
@@ -774,8 +763,11 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
         s.ntail = (int)(s.T - tail);
         s.ring_start = (int)(tail % c->ring);
         s.npool = pool_after(c->P, c->G, s.nf, c->pct);
-        if (a.window > 0 && s.pos0 - a.window + 1 > 0) {
-            s.jlo = std::min(s.nf, (s.pos0 - a.window + 1) / c->G);
+        // the windows of all its queries start here or later; of tiles, each
+        // has a range of its own, and the list covers the last one's
+        const int lo = s.pos0 + (tiles ? std::max(0, s.nq - 1) : 0) - a.window + 1;
+        if (a.window > 0 && lo > 0) {
+            s.jlo = std::min(s.nf, lo / c->G);
             s.nsink = std::min(a.sinks, s.jlo);
         }
         s.Sf = (int)(((long long)s.ntail + s.npool + a.C + s.nnew + FI - 1) / FI);
@@ -783,12 +775,18 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
         s.S = (int)(((long long)s.nq * c->gq + RB - 1) / RB);
         if (s.S == 0) continue;
         p.sinks |= s.nsink > 0;
+        if (tiles) continue;
         s.Iu = (int)iu;
         min_iu = (int)std::min<long long>(min_iu, iu);
         if (iu > INT_MAX || iu * c->Hkv * s.S > INT_MAX) return false;
         base += iu * c->Hkv * s.S;
         units += (long long)c->Hkv * s.S;
         if (units > INT_MAX) return false;
+    }
+    if (tiles) {
+        if (!plan_tiles(c, a, p.st, p.nC, p.part_floats)) return false;
+        p.any = a.W > 0;
+        return true;
     }
     p.st.e[a.nseq] = ChunkSeq{};
     p.st.e[a.nseq].base = base;
@@ -812,6 +810,7 @@ cudaError_t launch_plan(const ott_cache *c, const Plan &p, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     if (p.sinks)
         e = launch_pdl(k_window_sinks, dim3((unsigned)(a.nseq * a.Hkv)), SINK_THREADS, 0, s, a, p.st, c->sel);
+    if (e == cudaSuccess && p.NC == 0) return launch_tiles(c, a, p.st, p.nC, s);
     if (e == cudaSuccess)
         e = p.NC == 1 ? launch_rows<D, 1>(a, p.st, c->sm_count, s) : launch_rows<D, 2>(a, p.st, c->sm_count, s);
     if (e != cudaSuccess) return e;
@@ -827,7 +826,8 @@ cudaError_t launch_plan(const ott_cache *c, const Plan &p, cudaStream_t s) {
 cudaError_t set_chunk_attributes(int d) {
     const cudaError_t e = d == 128 ? rows_attribute<128, 1>() : rows_attribute<64, 1>();
     if (e != cudaSuccess) return e;
-    return d == 128 ? rows_attribute<128, 2>() : rows_attribute<64, 2>();
+    const cudaError_t e2 = d == 128 ? rows_attribute<128, 2>() : rows_attribute<64, 2>();
+    return e2 == cudaSuccess ? set_tiles_attributes(d) : e2;
 }
 
 int run_chunk(const ott_cache *c, const ChunkCall &call, cudaStream_t s, cudaError_t &err) {

@@ -150,4 +150,24 @@ __device__ __forceinline__ int ch_entry_of(const ChunkTable &st, int nseq, long 
     return lo;
 }
 
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t smem, cudaStream_t s, const Args &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// ott_chunk_tiles.cu
+cudaError_t set_tiles_attributes(int d);
+bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, size_t &part_floats);
+cudaError_t launch_tiles(const ott_cache *c, const ChunkArgs &a, const ChunkTable &st, int nC, cudaStream_t s);
+
 }  // namespace ott

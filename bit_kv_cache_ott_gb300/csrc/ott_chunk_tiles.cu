@@ -1,0 +1,907 @@
+// ott_chunk_tiles.cu -- attention of many query rows per kv head over the OTT
+// stores (ott_chunk_attn with long chunks), on the tcgen05 tensor cores.
+//
+// Mathematics: as in ott_chunk.cu (exact key operand s * (code - 1), the
+// rows' q . (z + s) apart; weights and values rounded to fp16). The sum
+// q . (z + s) comes out of the same product: next to 112 tokens the key tile
+// of a step holds, for each of its 7 groups of 16 tokens, the two fp16
+// numbers hi + lo = z + s of the group's block as rows 112 + 2w and 113 + 2w.
+// One 128 x 128 product then gives the raw scores and the offsets; the
+// softmax adds a group's offset to its 16 columns inside the multiply-add
+// that it makes anyway. A group may come from any block or be 16 fp16 tokens
+// (offset rows zero), so blocks of any size, lists of blocks, rings and pools
+// pack into full steps.
+//
+// A CTA (512 threads, one per SM) serves up to 256 rows of one (sequence, kv
+// head), as two tiles of 128 rows (row v = token * g + head) that share every
+// dequantized step:
+//   warps 0-3, 4-7  softmax of tile 0 and 1: a thread per row. S from TMEM,
+//                   running maximum (the output is rescaled only when it has
+//                   grown by 2^8), weights back into S's columns as fp16.
+//   warps 8-14      producers: warp w dequantizes group w of each step from
+//                   the packed words into the swizzled key tile (K-major,
+//                   128-byte rows) and value tile (V transposed, K-major,
+//                   32-byte rows per group). The words' order is that of mma
+//                   fragments, (8 rows) x (16 bytes) per warp store, which
+//                   the swizzle spreads over all banks.
+//   warp 15         issues the products. Order on the tensor pipe:
+//                   S0(j), O1(j-1), S1(j), O0(j): while one tile's weights are
+//                   computed, the other tile's products run.
+// TMEM: S0, S1 (fp32 128 columns, the weights overwrite the first 56), O0, O1.
+// Work is cut into steps; every CTA gets an equal run of the steps of all
+// tiles, so long caches with few rows are split and there is no tail. A tile
+// cut between CTAs leaves partials, merged by k_tiles_combine.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "ott_chunk.cuh"
+
+namespace ott {
+namespace {
+
+constexpr int GRPS = 7;              // groups of 16 tokens per step
+constexpr int STEP_TOK = 16 * GRPS;
+constexpr int ROWS = 128;            // rows of a tile
+constexpr int THREADS = 512;
+constexpr int PROD0 = 8, MMA_WARP = 15;
+constexpr int REG_SM = 160, REG_PR = 96;   // registers per thread of the softmax warps and the others
+constexpr int META = 4;              // steps of group metadata in flight
+constexpr float GROW = 8.0f;         // log2: the output is rescaled when the maximum has grown by this
+constexpr int MIN_STEPS = 4;         // steps per CTA at least (a run's fixed cost is about two)
+
+template <int D>
+struct TCfg {
+    static constexpr int ATOMS = D / 64;                   // 128-byte columns of a K-major tile
+    static constexpr int QB = ROWS * D * 2, KB = ROWS * D * 2, VG = D * 32, VB = GRPS * VG;
+    static constexpr int OFF_Q = 0, OFF_K = 2 * QB, OFF_V = OFF_K + 2 * KB;
+    static constexpr int OFF_POS = OFF_V + 2 * VB;          // int pos[META][STEP_TOK]
+    static constexpr int OFF_FLAG = OFF_POS + META * STEP_TOK * 4;   // int flag[META][8]
+    static constexpr int OFF_BAR = OFF_FLAG + META * 32;    // barriers, tmem address, abort flag
+    static constexpr int SMEM = OFF_BAR + 256 + 1024;       // + alignment to 1024
+    __host__ __device__ static constexpr uint32_t S(int t) { return 128u * t; }
+    __host__ __device__ static constexpr uint32_t O(int t) { return 256u + (uint32_t)D * t; }
+};
+
+enum { B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_SFULL = 8, B_PFULL = 10, B_OFULL = 12, B_COUNT = 13 };
+
+struct TileArgs {
+    ChunkArgs a;
+    int CPT;          // groups of 16 slots per block
+    int nC;           // CTAs
+    long long W;      // steps of all tiles
+    float *part;      // [nC][2][D + 2][256]
+};
+
+// A tile pair of a (sequence, kv head): its rows, and the groups that they see.
+struct Tile {
+    int e, hkv, p;            // entry, kv head, pair
+    int rows;                 // valid rows
+    int jlo;                  // blocks [jlo, nf) and the listed ones before
+    int nlo;                  // first group of new tokens that is seen
+    int gq, gf, gn;           // groups: quantized, fp16 (ring, pool, cold pool), new
+    int steps;
+};
+
+__host__ __device__ inline void tile_extent(const ChunkArgs &a, int cpt, const ChunkSeq &s, int p, Tile &t) {
+    const int v0 = 256 * p, vend = s.nq * a.g;
+    t.p = p;
+    t.rows = vend - v0 < 256 ? vend - v0 : 256;
+    const int first = v0 / a.g, last = (v0 + t.rows - 1) / a.g;   // tokens of the first and last row
+    t.jlo = 0;
+    t.nlo = 0;
+    if (a.window > 0) {
+        const int lo = s.pos0 + first - a.window + 1;   // the first row's window
+        t.jlo = lo <= 0 ? 0 : (lo / a.G < s.nf ? lo / a.G : s.nf);
+        // new tokens before the window (none of them a first token of the sequence)
+        if (s.T >= a.sinks && lo > s.T) t.nlo = (lo - s.T) / 16;
+    }
+    t.gq = (s.nf - t.jlo + (t.jlo > 0 ? s.nsink : 0)) * cpt;
+    t.gf = (s.ntail + s.npool + a.C + 15) / 16;
+    t.gn = s.nnew > 0 ? last / 16 + 1 - t.nlo : 0;
+    t.steps = (t.gq + t.gf + t.gn + GRPS - 1) / GRPS;
+}
+
+// The tile that holds step x, and the step's number in it. Warp-collective.
+__device__ __forceinline__ Tile tile_at(const TileArgs &ta, const ChunkTable &st, long long x, int &step) {
+    const ChunkArgs &a = ta.a;
+    Tile t;
+    t.e = ch_entry_of(st, a.nseq, x);
+    const ChunkSeq &s = st.e[t.e];
+    const unsigned rel = (unsigned)(x - s.base);
+    t.hkv = (int)(rel / (unsigned)s.Iu);             // Iu: steps of one kv head's tiles
+    int left = (int)(rel % (unsigned)s.Iu);
+    const int lane = threadIdx.x & 31;
+    for (int p0 = 0;; p0 += 32) {                    // ends: s.S tiles hold Iu steps
+        int n = 0;
+        if (p0 + lane < s.S) {
+            Tile u;
+            tile_extent(a, ta.CPT, s, p0 + lane, u);
+            n = u.steps;
+        }
+        int inc = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, inc > left && inc - n <= left);
+        if (hit || p0 + 32 >= s.S) {
+            const int l = hit ? __ffs(hit) - 1 : 0;
+            step = left - __shfl_sync(0xffffffffu, inc - n, l);
+            tile_extent(a, ta.CPT, s, min(p0 + l, s.S - 1), t);
+            return t;
+        }
+        left -= __shfl_sync(0xffffffffu, inc, 31);
+    }
+}
+
+// ---------------------------------------------------------------- PTX
+__device__ __forceinline__ void bar_init(uint64_t *b, int n) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(ch_smem(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t *b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(ch_smem(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t *b, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(ch_smem(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ unsigned long long now_ns() {
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+    return t;
+}
+// Bounded wait: gives up after a second, or once another role has.
+__device__ __forceinline__ bool bar_wait_slow(uint64_t *b, uint32_t parity, volatile int *gave_up) {
+    const unsigned long long end = now_ns() + 1000000000ull;
+    for (;;) {
+        for (int k = 0; k < 64; ++k)
+            if (bar_try(b, parity)) return true;
+        if (*gave_up) return false;
+        if (now_ns() > end) {
+            *gave_up = 1;
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *gave_up) {
+    if (bar_try(b, parity)) return true;
+    return bar_wait_slow(b, parity, gave_up);
+}
+// All 512 threads, each role from its own place in the code.
+__device__ __forceinline__ void cta_sync() { asm volatile("barrier.sync 0;" ::: "memory"); }
+// The same by whole warps: all lanes go on together or give up together.
+__device__ __forceinline__ bool bar_wait_warp(uint64_t *b, uint32_t parity, volatile int *gave_up) {
+    return __all_sync(0xffffffffu, bar_wait(b, parity, gave_up));
+}
+__device__ __forceinline__ void tc_commit(uint64_t *b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(ch_smem(b)) : "memory");
+}
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// The registers of the loads before it are valid from here on: `tie` keeps
+// the compiler from moving their uses above the wait.
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tie16(float *f) {
+    asm volatile("" : "+f"(f[0]), "+f"(f[1]), "+f"(f[2]), "+f"(f[3]), "+f"(f[4]), "+f"(f[5]), "+f"(f[6]), "+f"(f[7]),
+                      "+f"(f[8]), "+f"(f[9]), "+f"(f[10]), "+f"(f[11]), "+f"(f[12]), "+f"(f[13]), "+f"(f[14]), "+f"(f[15]));
+}
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tm_ld16(uint32_t at, float *f) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at));
+#pragma unroll
+    for (int x = 0; x < 16; ++x) f[x] = __uint_as_float(r[x]);
+}
+__device__ __forceinline__ void tm_st16(uint32_t at, const float *f) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+        "f"(f[0]), "f"(f[1]), "f"(f[2]), "f"(f[3]), "f"(f[4]), "f"(f[5]), "f"(f[6]), "f"(f[7]), "f"(f[8]), "f"(f[9]),
+        "f"(f[10]), "f"(f[11]), "f"(f[12]), "f"(f[13]), "f"(f[14]), "f"(f[15])
+        : "memory");
+}
+__device__ __forceinline__ void tm_st8(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// Shared-memory matrix descriptor: K-major, swizzled rows of 128 (kind 2) or
+// 32 (kind 6) bytes, 8-row groups `group` bytes apart.
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t group, uint32_t kind) {
+    return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | ((uint64_t)(group >> 4) << 32) | (1ull << 46) |
+           ((uint64_t)kind << 61);
+}
+// fp16 x fp16 -> fp32, M = 128, both operands K-major
+__host__ __device__ constexpr uint32_t instr_desc(int n) {
+    return (1u << 4) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(ROWS / 16) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, bool acc) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(at), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// ---------------------------------------------------------------- producers
+// What a producer warp makes next.
+struct Group {
+    const uint8_t *src;    // quantized: the block
+    int kind;              // 0 nothing, 1 quantized, 2 fp16
+    int sub;               // quantized: group of the block; fp16: first token f
+    int cnt;               // valid tokens
+    int j;                 // block
+};
+
+template <int D>
+__device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s, const Tile &t, int cpt, int u, int ncold,
+                                          int x) {
+    Group g;
+    g.src = nullptr;
+    g.kind = 0;
+    g.sub = g.cnt = g.j = 0;
+    if (x < t.gq) {
+        const int jp = x / cpt, ns = t.jlo > 0 ? s.nsink : 0;
+        int j = t.jlo + jp - ns;
+        if (jp < ns) {
+            j = __ldg(a.sel + (size_t)u * a.NB + jp);
+            if (j >= t.jlo) j = -1;   // in the window's own range
+        }
+        if (j >= 0) {
+            g.sub = x % cpt;
+            g.j = j;
+            g.cnt = min(16, chunk_block_cnt(a, u, j) - 16 * g.sub);
+            if (g.cnt > 0) {
+                g.kind = 1;
+                const size_t own = (size_t)u * a.NB + j;
+                g.src = a.blk + (a.bt ? (size_t)__ldg(a.bt + own) : own) * a.blk_bytes;
+            }
+        }
+    } else if (x < t.gq + t.gf + t.gn) {
+        // ring, pool and cold pool in whole groups, then the new tokens from group nlo on
+        const int nhot = s.ntail + s.npool + ncold;
+        x -= t.gq;
+        g.kind = 2;
+        if (x < t.gf) {
+            g.sub = 16 * x;
+            g.cnt = nhot - g.sub;
+        } else {
+            g.sub = nhot + 16 * (x - t.gf + t.nlo);
+            g.cnt = nhot + s.nnew - g.sub;
+        }
+        g.cnt = min(16, g.cnt);
+        if (g.cnt <= 0) g.kind = 0;
+    }
+    return g;
+}
+
+template <int D>
+__device__ void produce(const TileArgs &ta, const ChunkSeq &s, const Tile &t, uint8_t *sm, uint64_t *bar,
+                        volatile int *gave_up, int j0, int j1, uint32_t it) {
+    using C = TCfg<D>;
+    constexpr int NKT = D / 16, NW = D / 32;
+    const ChunkArgs &a = ta.a;
+    const int w = (threadIdx.x >> 5) - PROD0, lane = threadIdx.x & 31, r = lane >> 2, i = lane & 3;
+    const int b = a.B0 + t.e, u = b * a.Hkv + t.hkv;
+    const int ncold = a.C > 0 ? __ldg(a.cmeta + 2 * u) : 0, chead = a.C > 0 ? __ldg(a.cmeta + 2 * u + 1) : 0;
+    // the rows' positions and window starts that decide whether a group needs a mask
+    const int first = 256 * t.p / a.g, last = (256 * t.p + t.rows - 1) / a.g;
+    const int pmin = s.pos0 + first, lomax = a.window > 0 ? s.pos0 + last - a.window + 1 : 0;
+    uint32_t kr[4 + 4 * NKT], vr[32 > 4 + 2 * NKT ? 32 : 4 + 2 * NKT];
+
+    auto load_k = [&](const Group &g) {
+        if (g.kind == 1) {
+            const uint8_t *tb = g.src + ksz_bytes(D) + (size_t)g.sub * tile_bytes(D);
+            if constexpr (NW == 4) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(tb) + lane);
+                kr[0] = x.x; kr[1] = x.y; kr[2] = x.z; kr[3] = x.w;
+            } else {
+                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(tb) + lane);
+                kr[0] = x.x; kr[1] = x.y;
+            }
+#pragma unroll
+            for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(g.src + 4 * (16 * kt + 2 * i + 8 * o)));
+                    kr[4 + 4 * kt + 2 * o] = x.x;
+                    kr[4 + 4 * kt + 2 * o + 1] = x.y;
+                }
+        } else if (g.kind == 2) {
+            constexpr int CPR = D / 8, RPI = 32 / CPR;   // 16-byte chunks per row, rows per load
+#pragma unroll
+            for (int x = 0; x < 16 / RPI; ++x) {
+                const int row = RPI * x + lane / CPR;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row < g.cnt)
+                    v = __ldg(reinterpret_cast<const uint4 *>(
+                                  chunk_fp16_row(a, s, b, t.hkv, u, g.sub + row, ncold, chead, false, D)) + lane % CPR);
+                kr[4 * x] = v.x; kr[4 * x + 1] = v.y; kr[4 * x + 2] = v.z; kr[4 * x + 3] = v.w;
+            }
+        }
+    };
+    auto load_v = [&](const Group &g) {
+        if (g.kind == 1) {
+            const uint8_t *tb = g.src + ksz_bytes(D) + (size_t)g.sub * tile_bytes(D);
+            if constexpr (NW == 4) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(tb + tile_v_off(D)) + lane);
+                vr[0] = x.x; vr[1] = x.y; vr[2] = x.z; vr[3] = x.w;
+            } else {
+                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(tb + tile_v_off(D)) + lane);
+                vr[0] = x.x; vr[1] = x.y;
+            }
+#pragma unroll
+            for (int gm = 0; gm < NKT / 2; ++gm) {
+                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(tb + tile_sz_off(D)) + gm * 4 + i);
+                vr[4 + 4 * gm] = x.x; vr[5 + 4 * gm] = x.y; vr[6 + 4 * gm] = x.z; vr[7 + 4 * gm] = x.w;
+            }
+        } else if (g.kind == 2) {
+#pragma unroll
+            for (int th = 0; th < 2; ++th) {
+                const int row = r + 8 * th;
+                const __half *p = row < g.cnt ? chunk_fp16_row(a, s, b, t.hkv, u, g.sub + row, ncold, chead, true, D) : nullptr;
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    vr[th * (D / 8) + c] = p ? __ldg(reinterpret_cast<const uint32_t *>(p + 8 * c + 2 * i)) : 0u;
+            }
+        }
+    };
+
+    Group g = group_at<D>(a, s, t, ta.CPT, u, ncold, GRPS * j0 + w);
+    load_k(g);
+    load_v(g);
+    Group gn = group_at<D>(a, s, t, ta.CPT, u, ncold, j0 + 1 < j1 ? GRPS * (j0 + 1) + w : INT_MAX);
+    for (int j = j0; j < j1; ++j, ++it) {
+        const int slot = it & 1;
+        const uint32_t par = ((it >> 1) & 1u) ^ 1u;
+        uint8_t *kb = sm + C::OFF_K + slot * C::KB, *vb = sm + C::OFF_V + slot * C::VB + w * C::VG;
+        if (!bar_wait_warp(&bar[B_KEMPTY + slot], par, gave_up)) return;
+        // key rows 16w .. 16w+15, offset rows 112 + 2w and 113 + 2w
+        uint8_t *row = kb + (16 * w + r) * 128 + 4 * i;
+        if (g.kind == 1) {
+            uint32_t k10[NW];
+#pragma unroll
+            for (int x = 0; x < NW; ++x) k10[x] = kr[x] >> 10;
+            uint32_t hi[2] = {0, 0}, lw[2] = {0, 0};
+#pragma unroll
+            for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+                for (int o = 0; o < 2; ++o) {
+                    const uint32_t x0 = kr[4 + 4 * kt + 2 * o], x1 = kr[4 + 4 * kt + 2 * o + 1];
+                    const uint32_t s2 = __byte_perm(x0, x1, 0x5410);
+                    if ((r % NKT) == kt) {   // lane (r, i) makes the offsets of k-tile r
+                        hi[o] = s2;
+                        lw[o] = __byte_perm(x0, x1, 0x7632);
+                    }
+#pragma unroll
+                    for (int th = 0; th < 2; ++th) {
+                        const int q = o * NKT + kt, wi = 2 * (q >> 3) + th;
+                        *reinterpret_cast<uint32_t *>(row + (kt / 4) * (ROWS * 128) + th * 1024 +
+                                                      (((2 * (kt & 3) + o) ^ r) << 4)) = ch_key(kr[wi], k10[wi], q & 7, s2);
+                    }
+                }
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                uint32_t h2, l2;
+                ch_offset(hi[o], lw[o], h2, l2);
+                hi[o] = h2;
+                lw[o] = l2;
+            }
+            if (r < NKT) {
+                const int kt = r;
+#pragma unroll
+                for (int o = 0; o < 2; ++o)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int er = STEP_TOK + 2 * w + x;
+                        *reinterpret_cast<uint32_t *>(kb + (kt / 4) * (ROWS * 128) + er * 128 +
+                                                      (((2 * (kt & 3) + o) ^ (er & 7)) << 4) + 4 * i) = x ? lw[o] : hi[o];
+                    }
+            }
+        } else {
+            constexpr int CPR = D / 8, RPI = 32 / CPR;
+#pragma unroll
+            for (int x = 0; x < 16 / RPI; ++x) {
+                const int rw = 16 * w + RPI * x + lane / CPR, ch = lane % CPR;
+                const uint4 v = g.kind == 2 ? make_uint4(kr[4 * x], kr[4 * x + 1], kr[4 * x + 2], kr[4 * x + 3])
+                                            : make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4 *>(kb + (ch / 8) * (ROWS * 128) + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4)) = v;
+            }
+            if (lane < 2 * CPR) {
+                const int er = STEP_TOK + 2 * w + lane / CPR, ch = lane % CPR;
+                *reinterpret_cast<uint4 *>(kb + (ch / 8) * (ROWS * 128) + er * 128 + (((ch & 7) ^ (er & 7)) << 4)) =
+                    make_uint4(0, 0, 0, 0);
+            }
+        }
+        // whether some row does not see some token of the group, and the positions that decide it
+        const int ms = it % META;
+        int pos = INT_MAX;
+        if (lane < 16 && lane < g.cnt && g.kind) {
+            if (g.kind == 2)
+                pos = chunk_fp16_pos(a, s, u, g.sub + lane, ncold, chead);
+            else
+                pos = a.window > 0 ? __ldg(a.bidx + ((size_t)u * a.NB + g.j) * a.G + 16 * g.sub + lane) : 0;
+        }
+        const bool hidden = lane < 16 && !(pos <= pmin && (pos >= lomax || pos < a.sinks));
+        if (lane < 16) reinterpret_cast<volatile int *>(sm + C::OFF_POS)[ms * STEP_TOK + 16 * w + lane] = pos;
+        const unsigned any = __ballot_sync(0xffffffffu, hidden);
+        if (lane == 0) reinterpret_cast<volatile int *>(sm + C::OFF_FLAG)[ms * 8 + w] = any != 0;
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar[B_KFULL + slot]);
+        load_k(gn);   // in flight under the value tile
+
+        if (!bar_wait_warp(&bar[B_VEMPTY + slot], par, gave_up)) return;
+        uint8_t *v0 = vb + r * 32 + 4 * i + ((r >> 2) << 4), *v1 = vb + r * 32 + 4 * i + (((r >> 2) ^ 1) << 4);
+        if (g.kind == 1) {
+            uint32_t v10[NW];
+#pragma unroll
+            for (int x = 0; x < NW; ++x) v10[x] = vr[x] >> 10;
+#pragma unroll
+            for (int gm = 0; gm < NKT / 2; ++gm) {
+                const uint32_t *z = vr + 4 + 4 * gm;
+                const uint32_t s2[2] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[2], z[3], 0x5410)};
+                const uint32_t z2[2] = {__byte_perm(z[0], z[1], 0x7632), __byte_perm(z[2], z[3], 0x7632)};
+#pragma unroll
+                for (int mm = 0; mm < 2; ++mm)
+#pragma unroll
+                    for (int tp = 0; tp < 2; ++tp)
+#pragma unroll
+                        for (int half = 0; half < 2; ++half) {
+                            const int mt = 2 * gm + mm, q = half * NKT + mt, wi = 2 * (q >> 3) + tp;
+                            *reinterpret_cast<uint32_t *>((tp ? v1 : v0) + (16 * mt + 8 * half) * 32) =
+                                ch_val(vr[wi], v10[wi], q & 7, s2[tp], z2[tp]);
+                        }
+            }
+        } else {
+#pragma unroll
+            for (int th = 0; th < 2; ++th)
+#pragma unroll
+                for (int c = 0; c < D / 8; ++c)
+                    *reinterpret_cast<uint32_t *>((th ? v1 : v0) + 8 * c * 32) =
+                        transpose8x8(g.kind == 2 ? vr[th * (D / 8) + c] : 0u);
+        }
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar[B_VFULL + slot]);
+        load_v(gn);
+        g = gn;
+        gn = group_at<D>(a, s, t, ta.CPT, u, ncold, j + 2 < j1 ? GRPS * (j + 2) + w : INT_MAX);
+    }
+}
+
+// ---------------------------------------------------------------- products
+template <int D>
+__device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint32_t tmem, int nt, int steps, uint32_t it,
+                         uint32_t (&ct)[2]) {
+    using C = TCfg<D>;
+    const uint32_t base = ch_smem(sm);
+    auto scores = [&](int t, int slot) {
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            const uint32_t off = (k / 4) * (ROWS * 128) + (k & 3) * 32;
+            mma_ss(tmem + C::S(t), smem_desc(base + C::OFF_Q + t * C::QB + off, 1024, 2),
+                   smem_desc(base + C::OFF_K + slot * C::KB + off, 1024, 2), instr_desc(128), k > 0);
+        }
+    };
+    auto values = [&](int t, int slot, bool acc) {
+#pragma unroll
+        for (int k = 0; k < GRPS; ++k)
+            mma_ts(tmem + C::O(t), tmem + C::S(t) + 8 * k, smem_desc(base + C::OFF_V + slot * C::VB + k * C::VG, 256, 6),
+                   instr_desc(D), acc || k > 0);
+    };
+    for (int j = 0; j < steps; ++j, ++it) {
+        const int slot = it & 1, prev = slot ^ 1;
+        const uint32_t par = (it >> 1) & 1u;
+        if (!bar_wait(&bar[B_KFULL + slot], par, gave_up)) break;
+        tc_after();
+        scores(0, slot);
+        tc_commit(&bar[B_SFULL]);
+        if (nt == 2) {
+            if (j > 0) {
+                if (!bar_wait(&bar[B_PFULL + 1], (ct[1] - 1) & 1u, gave_up)) break;
+                tc_after();
+                values(1, prev, j > 1);
+                tc_commit(&bar[B_VEMPTY + prev]);
+            }
+            scores(1, slot);
+            tc_commit(&bar[B_SFULL + 1]);
+            ++ct[1];
+        }
+        tc_commit(&bar[B_KEMPTY + slot]);
+        if (!bar_wait(&bar[B_PFULL], ct[0] & 1u, gave_up)) break;
+        ++ct[0];
+        if (!bar_wait(&bar[B_VFULL + slot], par, gave_up)) break;
+        tc_after();
+        values(0, slot, j > 0);
+        if (nt == 1) tc_commit(&bar[B_VEMPTY + slot]);
+    }
+    if (nt == 2 && !*gave_up && bar_wait(&bar[B_PFULL + 1], (ct[1] - 1) & 1u, gave_up)) {
+        tc_after();
+        values(1, (it - 1) & 1, steps > 1);
+        tc_commit(&bar[B_VEMPTY + ((it - 1) & 1)]);
+    }
+    tc_commit(&bar[B_OFULL]);
+}
+
+// ---------------------------------------------------------------- softmax
+template <int D>
+__device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, uint8_t *sm, uint64_t *bar,
+                        volatile int *gave_up, uint32_t tmem, int tile, int steps, uint32_t it, uint32_t cnt, float &m_ref,
+                        float &l) {
+    using C = TCfg<D>;
+    const ChunkArgs &a = ta.a;
+    const int wq = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const uint32_t lanes = (uint32_t)(32 * wq) << 16;
+    const uint32_t ts = tmem + C::S(tile) + lanes, to = tmem + C::O(tile) + lanes;
+    const int row = ROWS * tile + 32 * wq + lane;
+    const int pos = s.pos0 + (256 * t.p + min(row, t.rows - 1)) / a.g, lo = a.window > 0 ? pos - a.window + 1 : 0;
+    m_ref = -CUDART_INF_F;
+    l = 0.0f;
+    for (int j = 0; j < steps; ++j, ++it, ++cnt) {
+        if (!bar_wait_warp(&bar[B_SFULL + tile], cnt & 1u, gave_up)) return false;
+        tc_after();
+        float e[16], x[STEP_TOK];
+        tm_ld16(ts + STEP_TOK, e);
+#pragma unroll
+        for (int k = 0; k < GRPS; ++k) tm_ld16(ts + 16 * k, x + 16 * k);
+        wait_ld();
+        tie16(e);
+#pragma unroll
+        for (int k = 0; k < GRPS; ++k) tie16(x + 16 * k);
+        const int ms = it % META;
+        const volatile int *flag = reinterpret_cast<volatile int *>(sm + C::OFF_FLAG) + ms * 8;
+        float mx = -CUDART_INF_F, off[GRPS];
+#pragma unroll
+        for (int k = 0; k < GRPS; ++k) {
+            off[k] = (e[2 * k] + e[2 * k + 1]) * a.sl2;
+            if (flag[k]) {
+                const volatile int *tp = reinterpret_cast<volatile int *>(sm + C::OFF_POS) + ms * STEP_TOK + 16 * k;
+#pragma unroll
+                for (int c = 0; c < 16; ++c)
+                    if (!chunk_sees(tp[c], pos, lo, a.sinks)) x[16 * k + c] = -CUDART_INF_F;
+            }
+            float g = x[16 * k];
+#pragma unroll
+            for (int c = 1; c < 16; ++c) g = fmaxf(g, x[16 * k + c]);
+            mx = fmaxf(mx, fmaf(g, a.sl2, off[k]));
+        }
+        const bool grow = mx > m_ref + GROW && m_ref != -CUDART_INF_F;
+        if (__any_sync(0xffffffffu, grow)) {
+            // the previous step's products are complete (the scores were issued behind them)
+            const float al = grow ? ch_ex2(m_ref - mx) : 1.0f;
+            l *= al;
+            if (grow) m_ref = mx;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tm_ld16(to + c, o);
+                wait_ld();
+                tie16(o);
+#pragma unroll
+                for (int y = 0; y < 16; ++y) o[y] *= al;
+                tm_st16(to + c, o);
+            }
+        }
+        if (m_ref == -CUDART_INF_F) m_ref = mx;   // the first token that the row sees: its output is zero so far
+        const float mm = m_ref == -CUDART_INF_F ? 0.0f : m_ref;
+        float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < GRPS; ++k) {
+            const float2 ad = make_float2(off[k] - mm, off[k] - mm), sc = make_float2(a.sl2, a.sl2);
+            uint32_t p8[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const float2 v = __ffma2_rn(make_float2(x[16 * k + 2 * c], x[16 * k + 2 * c + 1]), sc, ad);
+                const float2 p = make_float2(ch_ex2(v.x), ch_ex2(v.y));
+                sum = __fadd2_rn(sum, p);
+                p8[c] = ch_h2(__floats2half2_rn(p.x, p.y));
+            }
+            tm_st8(ts + 8 * k, p8);
+        }
+        l += sum.x + sum.y;
+        wait_st();
+        tc_before();
+        bar_arrive(&bar[B_PFULL + tile]);
+    }
+    return true;
+}
+
+// The output of a tile's row, or its part of it. Warps of the softmax.
+template <int D>
+__device__ void finish(const TileArgs &ta, const Tile &t, uint32_t tmem, int tile, bool whole, int slot, float m, float l) {
+    using C = TCfg<D>;
+    const ChunkArgs &a = ta.a;
+    const int wq = (threadIdx.x >> 5) & 3, row = ROWS * tile + 32 * wq + (threadIdx.x & 31), v = 256 * t.p + row;
+    const uint32_t to = tmem + C::O(tile) + ((uint32_t)(32 * wq) << 16);
+    if (whole) {
+        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+        __half *o = a.out + (((size_t)(a.B0 + t.e) * a.Hq + t.hkv * a.g + v % a.g) * a.n + v / a.g) * D;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+            float f[16];
+            tm_ld16(to + c, f);
+            wait_ld();
+            tie16(f);
+            uint32_t h[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) h[y] = ch_h2(__floats2half2_rn(f[2 * y] * inv, f[2 * y + 1] * inv));
+            if (row < t.rows) {
+                *reinterpret_cast<uint4 *>(o + c) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4 *>(o + c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
+            }
+        }
+    } else {   // maximum, sum, output: a column of rows each
+        float *pb = ta.part + ((size_t)blockIdx.x * 2 + slot) * (D + 2) * 256 + row;
+        pb[0] = m;
+        pb[256] = l;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+            float f[16];
+            tm_ld16(to + c, f);
+            wait_ld();
+            tie16(f);
+#pragma unroll
+            for (int y = 0; y < 16; ++y) pb[(size_t)(2 + c + y) * 256] = f[y];
+        }
+    }
+    tc_before();
+}
+
+enum { SOFTMAX, MULTIPLY, PRODUCE };
+
+// A CTA's run of steps, tile by tile, in one of its roles. The roles have
+// loops of their own so that each keeps to its own register budget; the two
+// barriers of a tile are met by all of them.
+template <int D, int ROLE>
+__device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm, uint64_t *bar, volatile int *gave_up,
+                          uint32_t tmem) {
+    using C = TCfg<D>;
+    const ChunkArgs &a = ta.a;
+    long long x = ch_range_start(ta.W, ta.nC, blockIdx.x);
+    const long long x1 = ch_range_start(ta.W, ta.nC, blockIdx.x + 1);
+    uint32_t it = 0, ct[2] = {0, 0};   // steps done by the CTA, and by each tile
+    for (uint32_t run = 0; x < x1; ++run) {
+        int j0;
+        const Tile t = tile_at(ta, st, x, j0);
+        const ChunkSeq &s = st.e[t.e];
+        const int j1 = (int)min((long long)t.steps, j0 + (x1 - x)), n = j1 - j0;
+        const int nt = t.rows > ROWS ? 2 : 1;
+        // queries into the swizzled tiles, rows past the last zero
+        for (int e = threadIdx.x; e < nt * ROWS * (D / 8); e += THREADS) {
+            const int row = e / (D / 8), ch = e % (D / 8), rw = row % ROWS;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < t.rows) {
+                const int vv = 256 * t.p + row;
+                v = __ldg(reinterpret_cast<const uint4 *>(
+                              a.q + (((size_t)(a.B0 + t.e) * a.Hq + t.hkv * a.g + vv % a.g) * a.n + vv / a.g) * D) + ch);
+            }
+            *reinterpret_cast<uint4 *>(sm + C::OFF_Q + row / ROWS * C::QB + (ch / 8) * (ROWS * 128) + rw * 128 +
+                                       (((ch & 7) ^ (rw & 7)) << 4)) = v;
+        }
+        proxy_fence();
+        cta_sync();
+        if constexpr (ROLE == SOFTMAX) {
+            const int tile = threadIdx.x / ROWS;
+            float m, l;
+            if (tile < nt && softmax<D>(ta, s, t, sm, bar, gave_up, tmem, tile, n, it, ct[tile], m, l) &&
+                bar_wait_warp(&bar[B_OFULL], run & 1u, gave_up)) {
+                tc_after();
+                finish<D>(ta, t, tmem, tile, n == t.steps, run > 0, m, l);
+            }
+        } else if constexpr (ROLE == MULTIPLY) {
+            if ((threadIdx.x & 31) == 0) {
+                uint32_t c2[2] = {ct[0], ct[1]};
+                multiply<D>(sm, bar, gave_up, tmem, nt, n, it, c2);
+            }
+            __syncwarp();
+        } else {
+            produce<D>(ta, s, t, sm, bar, gave_up, j0, j1, it);
+        }
+        it += (uint32_t)n;
+        ct[0] += (uint32_t)n;
+        if (nt == 2) ct[1] += (uint32_t)n;
+        x += n;
+        cta_sync();
+        if (*gave_up) break;
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS, 1)
+    k_chunk_tiles(const __grid_constant__ TileArgs ta, const __grid_constant__ ChunkTable st) {
+    using C = TCfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (ch_smem(smem_raw) & 1023u)) & 1023u);
+    uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(sm + C::OFF_BAR + 128);
+    volatile int *gave_up = reinterpret_cast<volatile int *>(sm + C::OFF_BAR + 132);
+    const ChunkArgs &a = ta.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int k = 0; k < 2; ++k) {
+            bar_init(&bar[B_KFULL + k], GRPS);
+            bar_init(&bar[B_VFULL + k], GRPS);
+            bar_init(&bar[B_KEMPTY + k], 1);
+            bar_init(&bar[B_VEMPTY + k], 1);
+            bar_init(&bar[B_SFULL + k], 1);
+            bar_init(&bar[B_PFULL + k], ROWS);
+        }
+        bar_init(&bar[B_OFULL], 1);
+        *gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // key rows that no group fills
+    for (int x = threadIdx.x; x < 2 * C::ATOMS * 2 * 32; x += THREADS) {
+        const int slot = x / (C::ATOMS * 64), at = x / 64 % C::ATOMS, rw = 126 + x / 32 % 2;
+        *reinterpret_cast<uint32_t *>(sm + C::OFF_K + slot * C::KB + at * (ROWS * 128) + rw * 128 + (x % 32) * 4) = 0;
+    }
+    if (warp == MMA_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(ch_smem(tm)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = *tm;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // 8 x 32 x (REG_SM + REG_PR) = the 512 x 128 registers of the launch
+    if (warp < PROD0) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SM));
+        role_loop<D, SOFTMAX>(ta, st, sm, bar, gave_up, tmem);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_PR));
+        if (warp == MMA_WARP)
+            role_loop<D, MULTIPLY>(ta, st, sm, bar, gave_up, tmem);
+        else
+            role_loop<D, PRODUCE>(ta, st, sm, bar, gave_up, tmem);
+    }
+    if (*gave_up && threadIdx.x == 0) atomicExch(&a.ctl[1], 1);
+    if (warp == MMA_WARP) {
+        // after a wait that gave up, products may still be in flight: one more bounded wait for them
+        if (*gave_up && lane == 0) {
+            bar_init(&bar[B_COUNT], 1);
+            tc_commit(&bar[B_COUNT]);
+            const unsigned long long end = now_ns() + 1000000000ull;
+            while (!bar_try(&bar[B_COUNT], 0) && now_ns() < end) {
+            }
+        }
+        __syncwarp();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    }
+}
+
+// Merge the parts of the tiles that CTAs share: 32 rows per CTA, lane = row,
+// D / 8 channels per warp.
+template <int D>
+__global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ TileArgs ta, const __grid_constant__ ChunkTable st) {
+    const ChunkArgs &a = ta.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // the tile: x = (pair of the largest sequence, 32 rows), y = kv head, z = entry
+    const ChunkSeq &s = st.e[blockIdx.z];
+    const int p = blockIdx.x / 8, row = 32 * (blockIdx.x % 8) + lane;
+    if (p >= s.S) return;
+    Tile t;
+    long long ts = s.base + (long long)blockIdx.y * s.Iu;
+    {
+        long long before = 0;
+        for (int q = lane; q < p; q += 32) {
+            tile_extent(a, ta.CPT, s, q, t);
+            before += t.steps;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+        ts += before;
+    }
+    tile_extent(a, ta.CPT, s, p, t);
+    if (32 * (blockIdx.x % 8) >= t.rows) return;
+    const int c0 = ch_warp_of(ta.W, ta.nC, ts), c1 = ch_warp_of(ta.W, ta.nC, ts + t.steps - 1);
+    if (c0 == c1) return;   // written whole
+    const int slot0 = ch_range_start(ta.W, ta.nC, c0) < ts ? 1 : 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int CH = D / 8;
+    float M = -CUDART_INF_F, L = 0.0f, acc[CH];
+#pragma unroll
+    for (int y = 0; y < CH; ++y) acc[y] = 0.0f;
+    for (int c = c0; c <= c1; ++c) {
+        const float *pb = ta.part + ((size_t)c * 2 + (c == c0 ? slot0 : 0)) * (D + 2) * 256 + row;
+        const float m = pb[0], l = pb[256];
+        float f[CH];
+#pragma unroll
+        for (int y = 0; y < CH; ++y) f[y] = pb[(size_t)(2 + CH * warp + y) * 256];
+        const float mn = fmaxf(M, m);
+        if (mn == -CUDART_INF_F) continue;
+        const float so = ch_ex2(M - mn), sn = ch_ex2(m - mn);
+        L = L * so + l * sn;
+#pragma unroll
+        for (int y = 0; y < CH; ++y) acc[y] = acc[y] * so + f[y] * sn;
+        M = mn;
+    }
+    if (row >= t.rows) return;
+    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
+    const int vv = 256 * p + row;
+    __half *o = a.out + (((size_t)(a.B0 + blockIdx.z) * a.Hq + blockIdx.y * a.g + vv % a.g) * a.n + vv / a.g) * D + CH * warp;
+#pragma unroll
+    for (int y = 0; y < CH; y += 8)
+        *reinterpret_cast<uint4 *>(o + y) = make_uint4(
+            ch_h2(__floats2half2_rn(acc[y] * inv, acc[y + 1] * inv)), ch_h2(__floats2half2_rn(acc[y + 2] * inv, acc[y + 3] * inv)),
+            ch_h2(__floats2half2_rn(acc[y + 4] * inv, acc[y + 5] * inv)), ch_h2(__floats2half2_rn(acc[y + 6] * inv, acc[y + 7] * inv)));
+}
+
+template <int D>
+cudaError_t launch_t(const TileArgs &ta, const ChunkTable &st, int pairs, cudaStream_t s) {
+    cudaError_t e = launch_pdl(k_chunk_tiles<D>, dim3((unsigned)ta.nC), THREADS, (size_t)TCfg<D>::SMEM, s, ta, st);
+    if (e != cudaSuccess || ta.nC == 1) return e;
+    return launch_pdl(k_tiles_combine<D>, dim3(8u * pairs, (unsigned)ta.a.Hkv, (unsigned)ta.a.nseq), 256, 0, s, ta, st);
+}
+
+}  // namespace
+
+cudaError_t set_tiles_attributes(int d) {
+    return d == 128 ? cudaFuncSetAttribute(k_chunk_tiles<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<128>::SMEM)
+                    : cudaFuncSetAttribute(k_chunk_tiles<64>, cudaFuncAttributeMaxDynamicSharedMemorySize, TCfg<64>::SMEM);
+}
+
+// The launch's table in tiles: S pairs of tiles per kv head, Iu their steps.
+// false: the sizes do not fit the kernel's 32-bit counters.
+bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, size_t &part_floats) {
+    const int cpt = ntiles_of(c->G);
+    long long base = 0;
+    for (int x = 0; x < a.nseq; ++x) {
+        ChunkSeq &s = st.e[x];
+        s.base = base;
+        s.S = (int)(((long long)s.nq * a.g + 255) / 256);
+        long long steps = 0;
+        if (((long long)s.nf + s.nsink) * cpt + ((long long)s.ntail + s.npool + a.C + s.nq) / 16 + 4 > INT_MAX) return false;
+        for (int p = 0; p < s.S; ++p) {
+            Tile t;
+            tile_extent(a, cpt, s, p, t);
+            steps += t.steps;
+            if (steps * a.Hkv > INT_MAX) return false;
+        }
+        s.Iu = (int)steps;
+        base += steps * a.Hkv;
+    }
+    st.e[a.nseq] = ChunkSeq{};
+    st.e[a.nseq].base = a.W = base;
+    nC = (int)std::max<long long>(1, std::min<long long>(c->sm_count, base / MIN_STEPS));
+    part_floats = nC > 1 ? (size_t)nC * 2 * (c->d + 2) * 256 : 1;
+    return true;
+}
+
+cudaError_t launch_tiles(const ott_cache *c, const ChunkArgs &a, const ChunkTable &st, int nC, cudaStream_t s) {
+    TileArgs ta;
+    ta.a = a;
+    ta.CPT = ntiles_of(c->G);
+    ta.nC = nC;
+    ta.W = a.W;
+    ta.part = a.part;
+    int pairs = 0;
+    for (int x = 0; x < a.nseq; ++x) pairs = std::max(pairs, st.e[x].S);
+    return c->d == 128 ? launch_t<128>(ta, st, pairs, s) : launch_t<64>(ta, st, pairs, s);
+}
+
+}  // namespace ott
