@@ -317,20 +317,10 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
         uint8_t *stage = stg + sg * C::STAGE;
         const bool fp = cc.off < s.Sf;
         if (mt_.x > 0) {
-            // token indices for the window rule, fetched under the wait
-            int tok[CHUNK_TILES][2];
             const bool wnd = a.window > 0;
             const int k = fp ? 0 : (cc.off - s.Sf) % a.CPB;
-            if (!fp && wnd) {
-                const int32_t *bi = a.bidx + ((size_t)u * a.NB + mt_.y) * a.G + CT * k;
-#pragma unroll
-                for (int tau = 0; tau < CHUNK_TILES; ++tau)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int x = 16 * tau + r + 8 * h;
-                        tok[tau][h] = x < mt_.x ? __ldg(bi + x) : INT_MAX;
-                    }
-            }
+            const int32_t *bi = a.bidx + ((size_t)u * a.NB + mt_.y) * a.G + CT * k;   // the chunk's token indices
+            if (!fp && wnd && lane < 8) asm volatile("prefetch.global.L1 [%0];" ::"l"(bi + min(8 * lane, mt_.x - 1)));
             if (!mbar_wait(&bars[sg], (phase >> sg) & 1u)) {
                 if (lane == 0) atomicExch(&a.ctl[1], 1);
                 // let the other copies in flight land before giving up the buffers
@@ -410,18 +400,20 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) off2[nc][x] = (d[nc][x] + d[nc][2 + x]) * a.sl2;
                 }
+                // one tile of 16 slots at a time: a loop body that the
+                // instruction cache holds (four tiles unrolled measured twice the time)
                 const int nt = (mt_.x + TILE - 1) / TILE;
-                float sc[CHUNK_TILES][NC][4], mx[NC][2];
-#pragma unroll
-                for (int nc = 0; nc < NC; ++nc) mx[nc][0] = mx[nc][1] = -CUDART_INF_F;
-#pragma unroll
-                for (int tau = 0; tau < CHUNK_TILES; ++tau) {
+#pragma unroll 1
+                for (int tau = 0; tau < nt; ++tau) {
+                    const uint8_t *tb = stage + KSZ + tau * TB;
+                    float sc[NC][4], sd[NC][4], mx[NC][2];   // two chains of products, even and odd k-tiles
 #pragma unroll
                     for (int nc = 0; nc < NC; ++nc)
-                        sc[tau][nc][0] = sc[tau][nc][1] = sc[tau][nc][2] = sc[tau][nc][3] = 0.0f;
-                    if (tau < nt) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) sc[nc][x] = sd[nc][x] = 0.0f;
+                    {
                         uint32_t w[NW], w10[NW];
-                        lds_words<NW>(stage + KSZ + tau * TB + tile_k_off(D) + lane * NW * 4, w);
+                        lds_words<NW>(tb + tile_k_off(D) + lane * NW * 4, w);
 #pragma unroll
                         for (int x = 0; x < NW; ++x) w10[x] = w[x] >> 10;
 #pragma unroll
@@ -436,88 +428,74 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                                 }
 #pragma unroll
                             for (int nc = 0; nc < NC; ++nc)
-                                mma16816(sc[tau][nc], f4[0], f4[1], f4[2], f4[3], Bq[nc][kt][0], Bq[nc][kt][1]);
+                                mma16816(kt & 1 ? sd[nc] : sc[nc], f4[0], f4[1], f4[2], f4[3], Bq[nc][kt][0], Bq[nc][kt][1]);
                         }
+#pragma unroll
+                        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+                            for (int x = 0; x < 4; ++x) sc[nc][x] += sd[nc][x];
                     }
-                    if (mt_.x < 16 * tau + 16) {   // the block's last tile
+                    if (wnd || mt_.x < 16 * tau + 16) {   // a window, or the block's last tile
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            if (16 * tau + r + 8 * h >= mt_.x) {
-#pragma unroll
-                                for (int nc = 0; nc < NC; ++nc)
-                                    sc[tau][nc][2 * h] = sc[tau][nc][2 * h + 1] = -CUDART_INF_F;
-                            }
-                    }
-                    if (wnd) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
+                        for (int h = 0; h < 2; ++h) {
+                            const int x = 16 * tau + r + 8 * h;
+                            const int t = x >= mt_.x ? INT_MAX : (wnd ? __ldg(bi + x) : 0);
 #pragma unroll
                             for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-                                for (int x = 0; x < 2; ++x)
-                                    if (!chunk_sees(tok[tau][h], pos[nc][x], lo[nc][x], a.sinks))
-                                        sc[tau][nc][2 * h + x] = -CUDART_INF_F;
+                                for (int y = 0; y < 2; ++y)
+                                    if (!chunk_sees(t, pos[nc][y], lo[nc][y], a.sinks)) sc[nc][2 * h + y] = -CUDART_INF_F;
+                        }
                     }
 #pragma unroll
                     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
+                        for (int x = 0; x < 2; ++x) mx[nc][x] = fmaf(fmaxf(sc[nc][x], sc[nc][2 + x]), a.sl2, off2[nc][x]);
+                    rescale(mx);
+                    uint32_t bp[NC][2];   // weights, B operand: tokens 2i, 2i + 1 (+ 8) of column r
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc) {
+                        float add[2];
+#pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            mx[nc][x] = fmaxf(mx[nc][x], fmaxf(sc[tau][nc][x], sc[tau][nc][2 + x]));
-                }
+                            add[x] = off2[nc][x] - (m_run[nc][x] == -CUDART_INF_F ? 0.0f : m_run[nc][x]);
 #pragma unroll
-                for (int nc = 0; nc < NC; ++nc)
+                        for (int h = 0; h < 2; ++h) {
+                            float p[2];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) mx[nc][x] = fmaf(mx[nc][x], a.sl2, off2[nc][x]);
-                rescale(mx);
-                float add[NC][2];
-#pragma unroll
-                for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        add[nc][x] = off2[nc][x] - (m_run[nc][x] == -CUDART_INF_F ? 0.0f : m_run[nc][x]);
-#pragma unroll
-                for (int tau = 0; tau < CHUNK_TILES; ++tau)
-                    if (tau < nt) {
-                        uint32_t bp[NC][2];   // weights, B operand: tokens 2i, 2i + 1 (+ 8) of column r
-#pragma unroll
-                        for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float p[2];
-#pragma unroll
-                                for (int x = 0; x < 2; ++x) {
-                                    p[x] = ch_ex2(fmaf(sc[tau][nc][2 * h + x], a.sl2, add[nc][x]));
-                                    l_run[nc][x] += p[x];
-                                }
-                                bp[nc][h] = transpose8x8(ch_h2(__floats2half2_rn(p[0], p[1])));
+                            for (int x = 0; x < 2; ++x) {
+                                p[x] = ch_ex2(fmaf(sc[nc][2 * h + x], a.sl2, add[x]));
+                                l_run[nc][x] += p[x];
                             }
-                        const uint8_t *tb = stage + KSZ + tau * TB;
-                        uint32_t w[NW], w10[NW];
-                        lds_words<NW>(tb + tile_v_off(D) + lane * NW * 4, w);
-#pragma unroll
-                        for (int x = 0; x < NW; ++x) w10[x] = w[x] >> 10;
-#pragma unroll
-                        for (int gm = 0; gm < NKT / 2; ++gm) {   // a value group: 32 channels, two m-tiles
-                            const uint4 sz = *reinterpret_cast<const uint4 *>(tb + tile_sz_off(D) + (gm * 4 + i) * 16);
-                            const uint32_t s2[2] = {__byte_perm(sz.x, sz.y, 0x5410), __byte_perm(sz.z, sz.w, 0x5410)};
-                            const uint32_t z2[2] = {__byte_perm(sz.x, sz.y, 0x7632), __byte_perm(sz.z, sz.w, 0x7632)};
-#pragma unroll
-                            for (int mm = 0; mm < 2; ++mm) {
-                                const int mt = 2 * gm + mm;
-                                uint32_t f4[4];   // (channels r + 8 half, tokens 2i + 8 tp): f4[half + 2 tp]
-#pragma unroll
-                                for (int tp = 0; tp < 2; ++tp)
-#pragma unroll
-                                    for (int half = 0; half < 2; ++half) {
-                                        const int q = half * NKT + mt, wi = 2 * (q >> 3) + tp;
-                                        f4[half + 2 * tp] = ch_val(w[wi], w10[wi], q & 7, s2[tp], z2[tp]);
-                                    }
-#pragma unroll
-                                for (int nc = 0; nc < NC; ++nc)
-                                    mma16816(acc[nc][mt], f4[0], f4[1], f4[2], f4[3], bp[nc][0], bp[nc][1]);
-                            }
+                            bp[nc][h] = transpose8x8(ch_h2(__floats2half2_rn(p[0], p[1])));
                         }
                     }
+                    uint32_t w[NW], w10[NW];
+                    lds_words<NW>(tb + tile_v_off(D) + lane * NW * 4, w);
+#pragma unroll
+                    for (int x = 0; x < NW; ++x) w10[x] = w[x] >> 10;
+#pragma unroll
+                    for (int gm = 0; gm < NKT / 2; ++gm) {   // a value group: 32 channels, two m-tiles
+                        const uint4 sz = *reinterpret_cast<const uint4 *>(tb + tile_sz_off(D) + (gm * 4 + i) * 16);
+                        const uint32_t s2[2] = {__byte_perm(sz.x, sz.y, 0x5410), __byte_perm(sz.z, sz.w, 0x5410)};
+                        const uint32_t z2[2] = {__byte_perm(sz.x, sz.y, 0x7632), __byte_perm(sz.z, sz.w, 0x7632)};
+#pragma unroll
+                        for (int mm = 0; mm < 2; ++mm) {
+                            const int mt = 2 * gm + mm;
+                            uint32_t f4[4];   // (channels r + 8 half, tokens 2i + 8 tp): f4[half + 2 tp]
+#pragma unroll
+                            for (int tp = 0; tp < 2; ++tp)
+#pragma unroll
+                                for (int half = 0; half < 2; ++half) {
+                                    const int q = half * NKT + mt, wi = 2 * (q >> 3) + tp;
+                                    f4[half + 2 * tp] = ch_val(w[wi], w10[wi], q & 7, s2[tp], z2[tp]);
+                                }
+#pragma unroll
+                            for (int nc = 0; nc < NC; ++nc)
+                                mma16816(acc[nc][mt], f4[0], f4[1], f4[2], f4[3], bp[nc][0], bp[nc][1]);
+                        }
+                    }
+                }
             }
         }
         // refill the stage, move on

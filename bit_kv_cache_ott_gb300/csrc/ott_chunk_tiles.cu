@@ -56,8 +56,8 @@ struct TCfg {
     static constexpr int QB = ROWS * D * 2, KB = ROWS * D * 2, VG = D * 32, VB = GRPS * VG;
     static constexpr int OFF_Q = 0, OFF_K = 2 * QB, OFF_V = OFF_K + 2 * KB;
     static constexpr int OFF_POS = OFF_V + 2 * VB;          // int pos[META][STEP_TOK]
-    static constexpr int OFF_FLAG = OFF_POS + META * STEP_TOK * 4;   // int flag[META][8]
-    static constexpr int OFF_BAR = OFF_FLAG + META * 32;    // barriers, tmem address, abort flag
+    static constexpr int OFF_FLAG = OFF_POS + META * STEP_TOK * 4;   // a byte of flag[META][8] per group
+    static constexpr int OFF_BAR = OFF_FLAG + META * 8;    // barriers, tmem address, abort flag
     static constexpr int SMEM = OFF_BAR + 256 + 1024;       // + alignment to 1024
     __host__ __device__ static constexpr uint32_t S(int t) { return 128u * t; }
     __host__ __device__ static constexpr uint32_t O(int t) { return 256u + (uint32_t)D * t; }
@@ -218,25 +218,29 @@ __device__ __forceinline__ void tm_st8(uint32_t at, const uint32_t (&r)[8]) {
                  : "memory");
 }
 // Shared-memory matrix descriptor: K-major, swizzled rows of 128 (kind 2) or
-// 32 (kind 6) bytes, 8-row groups `group` bytes apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t group, uint32_t kind) {
-    return (uint64_t)((addr >> 4) & 0x3fff) | (1ull << 16) | ((uint64_t)(group >> 4) << 32) | (1ull << 46) |
-           ((uint64_t)kind << 61);
+// 32 (kind 6) bytes, 8-row groups `group` bytes apart. The low word holds the
+// address in 16-byte units (and a field that swizzled layouts ignore), so
+// that a step along the operand is an addition to it.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr >> 4) & 0x3fff) | (1u << 16); }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t group, uint32_t kind) {
+    return (group >> 4) | (1u << 14) | (kind << 29);
 }
 // fp16 x fp16 -> fp32, M = 128, both operands K-major
 __host__ __device__ constexpr uint32_t instr_desc(int n) {
     return (1u << 4) | ((uint32_t)(n / 8) << 17) | ((uint32_t)(ROWS / 16) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(ad), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+        "{\n .reg .pred p;\n .reg .b64 x, y;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n setp.ne.u32 p, %5, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint64_t bd, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint32_t b, uint32_t hi, uint32_t idesc, bool acc) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(at), "l"(bd), "r"(idesc), "r"((uint32_t)acc)
+        "{\n .reg .pred p;\n .reg .b64 y;\n mov.b64 y, {%2, %3};\n setp.ne.u32 p, %5, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}" ::"r"(d),
+        "r"(at), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -255,24 +259,23 @@ struct Group {
     int j;                 // block
 };
 
-template <int D>
-__device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s, const Tile &t, int cpt, int u, int ncold,
-                                          int x) {
+// Group x of a tile; jp, sub = x / cpt, x % cpt.
+__device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s, const Tile &t, int u, int ncold, int x,
+                                          int jp, int sub) {
     Group g;
     g.src = nullptr;
-    g.kind = 0;
-    g.sub = g.cnt = g.j = 0;
+    g.kind = g.sub = g.cnt = g.j = 0;
     if (x < t.gq) {
-        const int jp = x / cpt, ns = t.jlo > 0 ? s.nsink : 0;
+        const int ns = t.jlo > 0 ? s.nsink : 0;
         int j = t.jlo + jp - ns;
         if (jp < ns) {
             j = __ldg(a.sel + (size_t)u * a.NB + jp);
             if (j >= t.jlo) j = -1;   // in the window's own range
         }
         if (j >= 0) {
-            g.sub = x % cpt;
+            g.sub = sub;
             g.j = j;
-            g.cnt = min(16, chunk_block_cnt(a, u, j) - 16 * g.sub);
+            g.cnt = min(16, chunk_block_cnt(a, u, j) - 16 * sub);
             if (g.cnt > 0) {
                 g.kind = 1;
                 const size_t own = (size_t)u * a.NB + j;
@@ -283,7 +286,6 @@ __device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s,
         // ring, pool and cold pool in whole groups, then the new tokens from group nlo on
         const int nhot = s.ntail + s.npool + ncold;
         x -= t.gq;
-        g.kind = 2;
         if (x < t.gf) {
             g.sub = 16 * x;
             g.cnt = nhot - g.sub;
@@ -292,7 +294,7 @@ __device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s,
             g.cnt = nhot + s.nnew - g.sub;
         }
         g.cnt = min(16, g.cnt);
-        if (g.cnt <= 0) g.kind = 0;
+        g.kind = g.cnt > 0 ? 2 : 0;
     }
     return g;
 }
@@ -369,14 +371,22 @@ __device__ void produce(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
         }
     };
 
-    Group g = group_at<D>(a, s, t, ta.CPT, u, ncold, GRPS * j0 + w);
-    load_k(g);
-    load_v(g);
-    Group gn = group_at<D>(a, s, t, ta.CPT, u, ncold, j0 + 1 < j1 ? GRPS * (j0 + 1) + w : INT_MAX);
-    for (int j = j0; j < j1; ++j, ++it) {
+    // Round j makes step j's group while step j + 1's words are on their way;
+    // round j0 - 1 only starts the first loads (one copy of the code each).
+    Group g, gn;
+    int xn = GRPS * j0 + w, jp = xn / ta.CPT, sub = xn % ta.CPT;
+    g.kind = g.cnt = g.sub = g.j = 0;
+    g.src = nullptr;
+#pragma unroll 1
+    for (int j = j0 - 1; j < j1; ++j) {
+        gn = group_at(a, s, t, u, ncold, j + 1 < j1 ? xn : INT_MAX, jp, sub);
+        xn += GRPS;
+        for (sub += GRPS; sub >= ta.CPT; sub -= ta.CPT) ++jp;
         const int slot = it & 1;
         const uint32_t par = ((it >> 1) & 1u) ^ 1u;
         uint8_t *kb = sm + C::OFF_K + slot * C::KB, *vb = sm + C::OFF_V + slot * C::VB + w * C::VG;
+        const bool made = j >= j0;
+        if (made) {
         if (!bar_wait_warp(&bar[B_KEMPTY + slot], par, gave_up)) return;
         // key rows 16w .. 16w+15, offset rows 112 + 2w and 113 + 2w
         uint8_t *row = kb + (16 * w + r) * 128 + 4 * i;
@@ -437,22 +447,26 @@ __device__ void produce(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
         }
         // whether some row does not see some token of the group, and the positions that decide it
         const int ms = it % META;
-        int pos = INT_MAX;
-        if (lane < 16 && lane < g.cnt && g.kind) {
-            if (g.kind == 2)
-                pos = chunk_fp16_pos(a, s, u, g.sub + lane, ncold, chead);
-            else
-                pos = a.window > 0 ? __ldg(a.bidx + ((size_t)u * a.NB + g.j) * a.G + 16 * g.sub + lane) : 0;
+        bool hidden = false;
+        if (g.kind != 1 || g.cnt < 16 || a.window > 0) {
+            int pos = INT_MAX;
+            if (lane < 16 && lane < g.cnt && g.kind) {
+                if (g.kind == 2)
+                    pos = chunk_fp16_pos(a, s, u, g.sub + lane, ncold, chead);
+                else
+                    pos = a.window > 0 ? __ldg(a.bidx + ((size_t)u * a.NB + g.j) * a.G + 16 * g.sub + lane) : 0;
+            }
+            hidden = __any_sync(0xffffffffu, lane < 16 && !(pos <= pmin && (pos >= lomax || pos < a.sinks)));
+            if (lane < 16) reinterpret_cast<volatile int *>(sm + C::OFF_POS)[ms * STEP_TOK + 16 * w + lane] = pos;
         }
-        const bool hidden = lane < 16 && !(pos <= pmin && (pos >= lomax || pos < a.sinks));
-        if (lane < 16) reinterpret_cast<volatile int *>(sm + C::OFF_POS)[ms * STEP_TOK + 16 * w + lane] = pos;
-        const unsigned any = __ballot_sync(0xffffffffu, hidden);
-        if (lane == 0) reinterpret_cast<volatile int *>(sm + C::OFF_FLAG)[ms * 8 + w] = any != 0;
+        if (lane == 0) *reinterpret_cast<volatile uint8_t *>(sm + C::OFF_FLAG + ms * 8 + w) = hidden;
         proxy_fence();
         __syncwarp();
         if (lane == 0) bar_arrive(&bar[B_KFULL + slot]);
+        }
         load_k(gn);   // in flight under the value tile
 
+        if (made) {
         if (!bar_wait_warp(&bar[B_VEMPTY + slot], par, gave_up)) return;
         uint8_t *v0 = vb + r * 32 + 4 * i + ((r >> 2) << 4), *v1 = vb + r * 32 + 4 * i + (((r >> 2) ^ 1) << 4);
         if (g.kind == 1) {
@@ -486,9 +500,10 @@ __device__ void produce(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
         proxy_fence();
         __syncwarp();
         if (lane == 0) bar_arrive(&bar[B_VFULL + slot]);
+        ++it;
+        }
         load_v(gn);
         g = gn;
-        gn = group_at<D>(a, s, t, ta.CPT, u, ncold, j + 2 < j1 ? GRPS * (j + 2) + w : INT_MAX);
     }
 }
 
@@ -497,20 +512,23 @@ template <int D>
 __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint32_t tmem, int nt, int steps, uint32_t it,
                          uint32_t (&ct)[2]) {
     using C = TCfg<D>;
-    const uint32_t base = ch_smem(sm);
+    const uint32_t base = ch_smem(sm), dq = desc_lo(base + C::OFF_Q), dk = desc_lo(base + C::OFF_K),
+                   dv = desc_lo(base + C::OFF_V);
     auto scores = [&](int t, int slot) {
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
-            const uint32_t off = (k / 4) * (ROWS * 128) + (k & 3) * 32;
-            mma_ss(tmem + C::S(t), smem_desc(base + C::OFF_Q + t * C::QB + off, 1024, 2),
-                   smem_desc(base + C::OFF_K + slot * C::KB + off, 1024, 2), instr_desc(128), k > 0);
+            constexpr uint32_t HI = desc_hi(1024, 2);
+            const uint32_t off = ((k / 4) * (ROWS * 128) + (k & 3) * 32) / 16;
+            mma_ss(tmem + C::S(t), dq + t * (C::QB / 16) + off, dk + slot * (C::KB / 16) + off, HI, instr_desc(128), k > 0);
         }
     };
     auto values = [&](int t, int slot, bool acc) {
 #pragma unroll
-        for (int k = 0; k < GRPS; ++k)
-            mma_ts(tmem + C::O(t), tmem + C::S(t) + 8 * k, smem_desc(base + C::OFF_V + slot * C::VB + k * C::VG, 256, 6),
-                   instr_desc(D), acc || k > 0);
+        for (int k = 0; k < GRPS; ++k) {
+            constexpr uint32_t HI = desc_hi(256, 6);
+            mma_ts(tmem + C::O(t), tmem + C::S(t) + 8 * k, dv + slot * (C::VB / 16) + k * (C::VG / 16), HI, instr_desc(D),
+                   acc || k > 0);
+        }
     };
     for (int j = 0; j < steps; ++j, ++it) {
         const int slot = it & 1, prev = slot ^ 1;
@@ -563,6 +581,25 @@ __device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
     for (int j = 0; j < steps; ++j, ++it, ++cnt) {
         if (!bar_wait_warp(&bar[B_SFULL + tile], cnt & 1u, gave_up)) return false;
         tc_after();
+        // groups with a token that some row does not see: -inf into its scores
+        const int ms = it % META;
+        unsigned long long flags = *reinterpret_cast<const volatile unsigned long long *>(sm + C::OFF_FLAG + ms * 8);
+        if (flags) {
+            const volatile int *tp = reinterpret_cast<volatile int *>(sm + C::OFF_POS) + ms * STEP_TOK;
+#pragma unroll 1
+            for (int k = 0; k < GRPS; ++k, flags >>= 8)
+                if (flags & 0xff) {
+                    float f[16];
+                    tm_ld16(ts + 16 * k, f);
+                    wait_ld();
+                    tie16(f);
+#pragma unroll
+                    for (int c = 0; c < 16; ++c)
+                        if (!chunk_sees(tp[16 * k + c], pos, lo, a.sinks)) f[c] = -CUDART_INF_F;
+                    tm_st16(ts + 16 * k, f);
+                }
+            wait_st();
+        }
         float e[16], x[STEP_TOK];
         tm_ld16(ts + STEP_TOK, e);
 #pragma unroll
@@ -571,22 +608,17 @@ __device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
         tie16(e);
 #pragma unroll
         for (int k = 0; k < GRPS; ++k) tie16(x + 16 * k);
-        const int ms = it % META;
-        const volatile int *flag = reinterpret_cast<volatile int *>(sm + C::OFF_FLAG) + ms * 8;
         float mx = -CUDART_INF_F, off[GRPS];
 #pragma unroll
         for (int k = 0; k < GRPS; ++k) {
             off[k] = (e[2 * k] + e[2 * k + 1]) * a.sl2;
-            if (flag[k]) {
-                const volatile int *tp = reinterpret_cast<volatile int *>(sm + C::OFF_POS) + ms * STEP_TOK + 16 * k;
+            float g[3] = {x[16 * k], x[16 * k + 1], x[16 * k + 2]};   // short chains of three-way maxima
 #pragma unroll
-                for (int c = 0; c < 16; ++c)
-                    if (!chunk_sees(tp[c], pos, lo, a.sinks)) x[16 * k + c] = -CUDART_INF_F;
-            }
-            float g = x[16 * k];
+            for (int c = 3; c < 15; c += 6)
 #pragma unroll
-            for (int c = 1; c < 16; ++c) g = fmaxf(g, x[16 * k + c]);
-            mx = fmaxf(mx, fmaf(g, a.sl2, off[k]));
+                for (int y = 0; y < 3; ++y) g[y] = fmaxf(fmaxf(g[y], x[16 * k + c + 2 * y]), x[16 * k + c + 2 * y + 1]);
+            g[0] = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], x[16 * k + 15]));
+            mx = fmaxf(mx, fmaf(g[0], a.sl2, off[k]));
         }
         const bool grow = mx > m_ref + GROW && m_ref != -CUDART_INF_F;
         if (__any_sync(0xffffffffu, grow)) {
@@ -751,6 +783,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         bar_init(&bar[B_OFULL], 1);
         *gave_up = 0;
+        for (int k = 0; k < META; ++k) *reinterpret_cast<unsigned long long *>(sm + C::OFF_FLAG + 8 * k) = 0;   // byte 7 stays
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // key rows that no group fills
