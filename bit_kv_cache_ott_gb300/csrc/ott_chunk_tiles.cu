@@ -19,9 +19,8 @@
 //                   running maximum (the output is rescaled only when it has
 //                   grown by 2^8), weights back into S's columns as fp16.
 //   warps 8-14      producers: warp w dequantizes group w of each step from
-//                   the packed words into the swizzled key tile (K-major,
-//                   128-byte rows) and value tile (V transposed, K-major,
-//                   32-byte rows per group). The words' order is that of mma
+//                   the packed words into the swizzled key tile and value
+//                   tile (V transposed; both K-major). The words' order is that of mma
 //                   fragments, (8 rows) x (16 bytes) per warp store, which
 //                   the swizzle spreads over all banks.
 //   warp 15         issues the products. Order on the tensor pipe:
@@ -45,7 +44,7 @@ constexpr int STEP_TOK = 16 * GRPS;
 constexpr int ROWS = 128;            // rows of a tile
 constexpr int THREADS = 512;
 constexpr int PROD0 = 8, MMA_WARP = 15;
-constexpr int REG_SM = 160, REG_PR = 96;   // registers per thread of the softmax warps and the others
+constexpr int REG_SM = 152, REG_PR = 104;   // registers per thread of the softmax warps and the others
 constexpr int META = 4;              // steps of group metadata in flight
 constexpr float GROW = 8.0f;         // log2: the output is rescaled when the maximum has grown by this
 constexpr int MIN_STEPS = 4;         // steps per CTA at least (a run's fixed cost is about two)
@@ -53,11 +52,12 @@ constexpr int MIN_STEPS = 4;         // steps per CTA at least (a run's fixed co
 template <int D>
 struct TCfg {
     static constexpr int ATOMS = D / 64;                   // 128-byte columns of a K-major tile
-    static constexpr int QB = ROWS * D * 2, KB = ROWS * D * 2, VG = D * 32, VB = GRPS * VG;
+    static constexpr int QB = ROWS * D * 2, KB = ROWS * D * 2, VB = 2 * D * 128;
     static constexpr int OFF_Q = 0, OFF_K = 2 * QB, OFF_V = OFF_K + 2 * KB;
     static constexpr int OFF_POS = OFF_V + 2 * VB;          // int pos[META][STEP_TOK]
     static constexpr int OFF_FLAG = OFF_POS + META * STEP_TOK * 4;   // a byte of flag[META][8] per group
-    static constexpr int OFF_BAR = OFF_FLAG + META * 8;    // barriers, tmem address, abort flag
+    static constexpr int OFF_HDR = OFF_FLAG + META * 8;         // a block's key scales and zeros per producer
+    static constexpr int OFF_BAR = OFF_HDR + GRPS * 4 * D;    // barriers, tmem address, abort flag
     static constexpr int SMEM = OFF_BAR + 256 + 1024;       // + alignment to 1024
     __host__ __device__ static constexpr uint32_t S(int t) { return 128u * t; }
     __host__ __device__ static constexpr uint32_t O(int t) { return 256u + (uint32_t)D * t; }
@@ -80,7 +80,7 @@ struct Tile {
     int jlo;                  // blocks [jlo, nf) and the listed ones before
     int nlo;                  // first group of new tokens that is seen
     int gq, gf, gn;           // groups: quantized, fp16 (ring, pool, cold pool), new
-    int steps;
+    int sq, steps;            // steps of quantized groups, then of the others; all steps
 };
 
 __host__ __device__ inline void tile_extent(const ChunkArgs &a, int cpt, const ChunkSeq &s, int p, Tile &t) {
@@ -99,7 +99,8 @@ __host__ __device__ inline void tile_extent(const ChunkArgs &a, int cpt, const C
     t.gq = (s.nf - t.jlo + (t.jlo > 0 ? s.nsink : 0)) * cpt;
     t.gf = (s.ntail + s.npool + a.C + 15) / 16;
     t.gn = s.nnew > 0 ? last / 16 + 1 - t.nlo : 0;
-    t.steps = (t.gq + t.gf + t.gn + GRPS - 1) / GRPS;
+    t.sq = (t.gq + GRPS - 1) / GRPS;
+    t.steps = t.sq + (t.gf + t.gn + GRPS - 1) / GRPS;
 }
 
 // The tile that holds step x, and the step's number in it. Warp-collective.
@@ -174,6 +175,12 @@ __device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile 
     if (bar_try(b, parity)) return true;
     return bar_wait_slow(b, parity, gave_up);
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+    return one != 0;
+}
 // All 512 threads, each role from its own place in the code.
 __device__ __forceinline__ void cta_sync() { asm volatile("barrier.sync 0;" ::: "memory"); }
 // The same by whole warps: all lanes go on together or give up together.
@@ -217,8 +224,10 @@ __device__ __forceinline__ void tm_st8(uint32_t at, const uint32_t (&r)[8]) {
                  "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
-// Shared-memory matrix descriptor: K-major, swizzled rows of 128 (kind 2) or
-// 32 (kind 6) bytes, 8-row groups `group` bytes apart. The low word holds the
+// Shared-memory matrix descriptor: K-major, swizzled rows of 128 bytes (kind
+// 2), 8-row groups `group` bytes apart. (Value tiles in 32-byte rows, one
+// group of tokens each, measured 127 cycles per product of 16 tokens instead
+// of 64: those are read 32 bytes at a time.) The low word holds the
 // address in 16-byte units (and a field that swizzled layouts ignore), so
 // that a step along the operand is an addition to it.
 __device__ __forceinline__ uint32_t desc_lo(uint32_t addr) { return ((addr >> 4) & 0x3fff) | (1u << 16); }
@@ -250,267 +259,356 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 
 // ---------------------------------------------------------------- producers
-// What a producer warp makes next.
-struct Group {
-    const uint8_t *src;    // quantized: the block
-    int kind;              // 0 nothing, 1 quantized, 2 fp16
-    int sub;               // quantized: group of the block; fp16: first token f
-    int cnt;               // valid tokens
-    int j;                 // block
-};
+// Orders within the tiles. Scores do not depend on the order of the channels
+// as long as queries and keys share it, outputs not on that of a group's
+// tokens, and the order of the output's channels is undone where it is read.
+// So they are chosen for wide stores that meet no bank twice:
+//   channels of a key row: the 8 fp16x2 that a lane unpacks from a word are
+//     adjacent, 4 per 16-byte chunk (chan_at);
+//   tokens of a group: 2i, 2i + 1, 2i + 8, 2i + 9 are adjacent (slot_of), in
+//     the key rows (hence in the scores and weights) and in the value rows;
+//   value rows (channels): the low three bits of the channel rotated (vrow),
+//     so that 16 lanes of an 8-byte store meet all 8 chunks.
+// Byte offset, before the swizzle, of channels c, c + 1 (c = 16 kt + 2 i + 8 o)
+// in a key row, as (128-byte column, 16-byte chunk, word of it).
+template <int D>
+__device__ __forceinline__ uint32_t chan_at(int kt, int o, int i, int row) {
+    const int q = o * (D / 16) + kt, p = q & 7;
+    return (uint32_t)((q >> 3) * (ROWS * 128) + row * 128 + (((2 * i + (p >> 2)) ^ (row & 7)) << 4) + (p & 3) * 4);
+}
+__device__ __forceinline__ int slot_of(int t) { return 4 * ((t & 7) >> 1) + 2 * (t >> 3) + (t & 1); }
+__host__ __device__ constexpr int vrow(int r) { return ((r << 1) & 6) | (r >> 2); }
 
-// Group x of a tile; jp, sub = x / cpt, x % cpt.
-__device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s, const Tile &t, int u, int ncold, int x,
-                                          int jp, int sub) {
+// One 16-byte piece of an fp16 row (8 channels from 8 * ch on) into a tile of key rows.
+template <int D>
+__device__ __forceinline__ void put_row_piece(uint8_t *tile, int row, int ch, uint4 v) {
+    const int kt = ch >> 1, o = ch & 1;
+    *reinterpret_cast<uint32_t *>(tile + chan_at<D>(kt, o, 0, row)) = v.x;
+    *reinterpret_cast<uint32_t *>(tile + chan_at<D>(kt, o, 1, row)) = v.y;
+    *reinterpret_cast<uint32_t *>(tile + chan_at<D>(kt, o, 2, row)) = v.z;
+    *reinterpret_cast<uint32_t *>(tile + chan_at<D>(kt, o, 3, row)) = v.w;
+}
+
+// Group x of the tile's quantized ones.
+struct Group {
+    const uint8_t *src;    // the block
+    int j;                 // its number, -1: none
+    int sub;               // group of the block
+    int left;              // valid tokens of the block from the group's first on (<= 0: none)
+};
+__device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s, const Tile &t, int cpt, int u, int x) {
     Group g;
+    if (x >= t.gq) {
+        g.src = nullptr;
+        g.j = -1;
+        g.sub = g.left = 0;
+        return g;
+    }
+    const int ns = t.jlo > 0 ? s.nsink : 0, jp = x / cpt;
+    g.sub = x % cpt;
+    g.left = 0;
     g.src = nullptr;
-    g.kind = g.sub = g.cnt = g.j = 0;
-    if (x < t.gq) {
-        const int ns = t.jlo > 0 ? s.nsink : 0;
-        int j = t.jlo + jp - ns;
-        if (jp < ns) {
-            j = __ldg(a.sel + (size_t)u * a.NB + jp);
-            if (j >= t.jlo) j = -1;   // in the window's own range
-        }
-        if (j >= 0) {
-            g.sub = sub;
-            g.j = j;
-            g.cnt = min(16, chunk_block_cnt(a, u, j) - 16 * sub);
-            if (g.cnt > 0) {
-                g.kind = 1;
-                const size_t own = (size_t)u * a.NB + j;
-                g.src = a.blk + (a.bt ? (size_t)__ldg(a.bt + own) : own) * a.blk_bytes;
-            }
-        }
-    } else if (x < t.gq + t.gf + t.gn) {
-        // ring, pool and cold pool in whole groups, then the new tokens from group nlo on
-        const int nhot = s.ntail + s.npool + ncold;
-        x -= t.gq;
-        if (x < t.gf) {
-            g.sub = 16 * x;
-            g.cnt = nhot - g.sub;
-        } else {
-            g.sub = nhot + 16 * (x - t.gf + t.nlo);
-            g.cnt = nhot + s.nnew - g.sub;
-        }
-        g.cnt = min(16, g.cnt);
-        g.kind = g.cnt > 0 ? 2 : 0;
+    g.j = t.jlo + jp - ns;
+    if (jp < ns) {
+        g.j = __ldg(a.sel + (size_t)u * a.NB + jp);
+        if (g.j >= t.jlo) g.j = -1;   // in the window's own range
+    }
+    if (g.j >= 0) {
+        g.left = chunk_block_cnt(a, u, g.j) - 16 * g.sub;
+        const size_t own = (size_t)u * a.NB + g.j;
+        g.src = a.blk + (a.bt ? (size_t)__ldg(a.bt + own) : own) * a.blk_bytes;
     }
     return g;
 }
 
+// A tile's quantized groups are made first, then the fp16 ones, each kind
+// dealt to the 7 warps in runs: a warp walks through its blocks and meets a
+// block's key scales once, and all warps are busy with the same kind (a step
+// takes as long as its slowest group). In each of the two loops, round k
+// makes a group while the next one's words are on their way; round -1 only
+// starts the first loads (one copy of the code).
 template <int D>
-__device__ void produce(const TileArgs &ta, const ChunkSeq &s, const Tile &t, uint8_t *sm, uint64_t *bar,
-                        volatile int *gave_up, int j0, int j1, uint32_t it) {
+struct Producer {
     using C = TCfg<D>;
-    constexpr int NKT = D / 16, NW = D / 32;
-    const ChunkArgs &a = ta.a;
-    const int w = (threadIdx.x >> 5) - PROD0, lane = threadIdx.x & 31, r = lane >> 2, i = lane & 3;
-    const int b = a.B0 + t.e, u = b * a.Hkv + t.hkv;
-    const int ncold = a.C > 0 ? __ldg(a.cmeta + 2 * u) : 0, chead = a.C > 0 ? __ldg(a.cmeta + 2 * u + 1) : 0;
-    // the rows' positions and window starts that decide whether a group needs a mask
-    const int first = 256 * t.p / a.g, last = (256 * t.p + t.rows - 1) / a.g;
-    const int pmin = s.pos0 + first, lomax = a.window > 0 ? s.pos0 + last - a.window + 1 : 0;
-    uint32_t kr[4 + 4 * NKT], vr[32 > 4 + 2 * NKT ? 32 : 4 + 2 * NKT];
+    static constexpr int NKT = D / 16, NW = D / 32;
+    static constexpr int CPR = D / 8, RPI = 32 / CPR;   // 16-byte pieces of an fp16 row, rows per load of a warp
+    const TileArgs &ta;
+    const ChunkArgs &a;
+    const ChunkSeq &s;
+    const Tile &t;
+    uint8_t *const sm;
+    uint64_t *const bar;
+    volatile int *const gave_up;
+    const int w, lane, r, i, b, u;
+    int pmin, lomax;       // smallest position, largest window start of the rows
+    uint32_t it;
 
-    auto load_k = [&](const Group &g) {
-        if (g.kind == 1) {
-            const uint8_t *tb = g.src + ksz_bytes(D) + (size_t)g.sub * tile_bytes(D);
-            if constexpr (NW == 4) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(tb) + lane);
-                kr[0] = x.x; kr[1] = x.y; kr[2] = x.z; kr[3] = x.w;
-            } else {
-                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(tb) + lane);
-                kr[0] = x.x; kr[1] = x.y;
-            }
-#pragma unroll
-            for (int kt = 0; kt < NKT; ++kt)
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(g.src + 4 * (16 * kt + 2 * i + 8 * o)));
-                    kr[4 + 4 * kt + 2 * o] = x.x;
-                    kr[4 + 4 * kt + 2 * o + 1] = x.y;
-                }
-        } else if (g.kind == 2) {
-            constexpr int CPR = D / 8, RPI = 32 / CPR;   // 16-byte chunks per row, rows per load
-#pragma unroll
-            for (int x = 0; x < 16 / RPI; ++x) {
-                const int row = RPI * x + lane / CPR;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (row < g.cnt)
-                    v = __ldg(reinterpret_cast<const uint4 *>(
-                                  chunk_fp16_row(a, s, b, t.hkv, u, g.sub + row, ncold, chead, false, D)) + lane % CPR);
-                kr[4 * x] = v.x; kr[4 * x + 1] = v.y; kr[4 * x + 2] = v.z; kr[4 * x + 3] = v.w;
-            }
+    __device__ Producer(const TileArgs &ta_, const ChunkSeq &s_, const Tile &t_, uint8_t *sm_, uint64_t *bar_,
+                        volatile int *gave_up_, uint32_t it_)
+        : ta(ta_), a(ta_.a), s(s_), t(t_), sm(sm_), bar(bar_), gave_up(gave_up_), w((threadIdx.x >> 5) - PROD0),
+          lane(threadIdx.x & 31), r(lane >> 2), i(lane & 3), b(a.B0 + t.e), u(b * a.Hkv + t.hkv), it(it_) {
+        pmin = s.pos0 + 256 * t.p / a.g;
+        lomax = a.window > 0 ? s.pos0 + (256 * t.p + t.rows - 1) / a.g - a.window + 1 : 0;
+    }
+    __device__ bool wait(int which) {
+        return bar_wait_warp(&bar[which + (it & 1)], ((it >> 1) & 1u) ^ 1u, gave_up);
+    }
+    // The tile's part is written: pos (of lane < 16's token, INT_MAX: none)
+    // decides whether some row does not see it, where `ask`.
+    __device__ void key_done(bool ask, int pos) {
+        bool hidden = false;
+        if (ask) {
+            hidden = __any_sync(0xffffffffu, lane < 16 && !(pos <= pmin && (pos >= lomax || pos < a.sinks)));
+            if (lane < 16)
+                reinterpret_cast<volatile int *>(sm + C::OFF_POS)[(it % META) * STEP_TOK + 16 * w + slot_of(lane)] = pos;
         }
-    };
-    auto load_v = [&](const Group &g) {
-        if (g.kind == 1) {
-            const uint8_t *tb = g.src + ksz_bytes(D) + (size_t)g.sub * tile_bytes(D);
-            if constexpr (NW == 4) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(tb + tile_v_off(D)) + lane);
-                vr[0] = x.x; vr[1] = x.y; vr[2] = x.z; vr[3] = x.w;
-            } else {
-                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(tb + tile_v_off(D)) + lane);
-                vr[0] = x.x; vr[1] = x.y;
+        if (lane == 0) *reinterpret_cast<volatile uint8_t *>(sm + C::OFF_FLAG + (it % META) * 8 + w) = hidden;
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar[B_KFULL + (it & 1)]);
+    }
+    __device__ void value_done() {
+        proxy_fence();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar[B_VFULL + (it & 1)]);
+        ++it;
+    }
+    __device__ uint8_t *key_tile() const { return sm + C::OFF_K + (it & 1) * C::KB; }
+    // this lane's place in the value tile's row vrow(r)
+    __device__ uint8_t *value_at() const {
+        return sm + C::OFF_V + (it & 1) * C::VB + (w / 4) * (D * 128) + vrow(r) * 128 +
+               (((2 * (w & 3) + (i >> 1)) ^ vrow(r)) << 4) + 8 * (i & 1);
+    }
+
+    // Quantized groups x, x + 1 .. x + n - 1 (none from gq on).
+    __device__ bool quantized(int x, int n) {
+        const int cpt = ta.CPT;
+        uint32_t kr[NW], vr[NW], zr[2 * NKT], ks2[NKT][2];
+        uint8_t *const stage = sm + C::OFF_HDR + w * ksz_bytes(D);   // the block's key scales and zeros
+        const int row0 = slot_of(r), row1 = slot_of(r + 8);
+        const uint32_t k0 = (16 * w + row0) * 128 + ((2 * i ^ (row0 & 7)) << 4), k1 = (16 * w + row1) * 128 + ((2 * i ^ (row1 & 7)) << 4);
+        Group g, gn, gb;             // made, next, first of the next block
+        uint4 hb = make_uint4(0, 0, 0, 0);
+        int xb = -1;                 // gb's number
+        g.left = g.sub = 0;
+        g.j = -1;
+        g.src = nullptr;
+        gn = gb = g;
+        int fresh = 0;               // steps for which the block's offset rows still have to be written
+#pragma unroll 1
+        for (int k = -1; k < n; ++k) {
+            bool enter = false;
+            if (g.left > 16 && g.sub + 1 < cpt) {
+                gn.sub += 1;
+                gn.left -= 16;
+            } else if (k + 1 < n) {
+                const int xn = x + k + 1;
+                if (xn == xb) {
+                    gn = gb;
+                } else {   // the run's first group, or one behind a short block's tokens
+                    gn = group_at(a, s, t, cpt, u, xn);
+                    if (gn.left > 0 && lane < D / 4) hb = __ldg(reinterpret_cast<const uint4 *>(gn.src) + lane);
+                }
+                enter = gn.left > 0;
             }
+            if (k >= 0) {
+                if (!wait(B_KEMPTY)) return false;
+                uint8_t *kb = key_tile();
+                if (g.left > 0) {
+                    uint32_t k10[NW];
 #pragma unroll
-            for (int gm = 0; gm < NKT / 2; ++gm) {
-                const uint4 x = __ldg(reinterpret_cast<const uint4 *>(tb + tile_sz_off(D)) + gm * 4 + i);
-                vr[4 + 4 * gm] = x.x; vr[5 + 4 * gm] = x.y; vr[6 + 4 * gm] = x.z; vr[7 + 4 * gm] = x.w;
+                    for (int y = 0; y < NW; ++y) k10[y] = kr[y] >> 10;
+#pragma unroll
+                    for (int th = 0; th < 2; ++th)
+#pragma unroll
+                        for (int q0 = 0; q0 < 2 * NKT; q0 += 4) {   // 4 fp16x2 of a word: a chunk
+                            const int wi = 2 * (q0 >> 3) + th;
+                            uint32_t f[4];
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                f[y] = ch_key(kr[wi], k10[wi], (q0 + y) & 7, ks2[(q0 + y) % NKT][(q0 + y) / NKT]);
+                            // chunk 2i + 1 is chunk 2i with its lowest bit turned, whatever the swizzle
+                            *reinterpret_cast<uint4 *>(kb + (((th ? k1 : k0) + (q0 >> 3) * (ROWS * 128)) ^ ((q0 & 4) << 2))) =
+                                make_uint4(f[0], f[1], f[2], f[3]);
+                        }
+                    if (fresh > 0) {
+                        // offset rows 112 + 2w, 113 + 2w; lane (r, i) makes the channels of k-tile r
+                        --fresh;
+                        if (r < NKT) {
+#pragma unroll
+                            for (int o = 0; o < 2; ++o) {
+                                const uint2 z = *reinterpret_cast<const uint2 *>(stage + 4 * (16 * r + 2 * i + 8 * o));
+                                uint32_t hi, lw;
+                                ch_offset(__byte_perm(z.x, z.y, 0x5410), __byte_perm(z.x, z.y, 0x7632), hi, lw);
+                                *reinterpret_cast<uint32_t *>(kb + chan_at<D>(r, o, i, STEP_TOK + 2 * w)) = hi;
+                                *reinterpret_cast<uint32_t *>(kb + chan_at<D>(r, o, i, STEP_TOK + 2 * w + 1)) = lw;
+                            }
+                        }
+                    }
+                } else {
+                    zero_keys(kb);
+                    fresh = 2;
+                }
+                const bool ask = g.left < 16 || a.window > 0;
+                int pos = INT_MAX;
+                if (ask && lane < 16 && lane < g.left)
+                    pos = a.window > 0 ? __ldg(a.bidx + ((size_t)u * a.NB + g.j) * a.G + 16 * g.sub + lane) : 0;
+                key_done(ask, pos);
             }
-        } else if (g.kind == 2) {
+            if (enter) {   // the block's scales, through shared memory; then the next block's are fetched
+                __syncwarp();
+                if (lane < D / 4) *reinterpret_cast<uint4 *>(stage + 16 * lane) = hb;
+                __syncwarp();
+#pragma unroll
+                for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+                    for (int o = 0; o < 2; ++o) {
+                        const uint2 z = *reinterpret_cast<const uint2 *>(stage + 4 * (16 * kt + 2 * i + 8 * o));
+                        ks2[kt][o] = __byte_perm(z.x, z.y, 0x5410);
+                    }
+                fresh = 2;   // both slots
+                xb = x + k + 1 - gn.sub + cpt;
+                if (xb < x + n) {
+                    gb = group_at(a, s, t, cpt, u, xb);
+                    if (gb.left > 0 && lane < D / 4) hb = __ldg(reinterpret_cast<const uint4 *>(gb.src) + lane);
+                }
+            }
+            const bool load = k + 1 < n && gn.left > 0;
+            const uint8_t *tb = gn.src + ksz_bytes(D) + (size_t)gn.sub * tile_bytes(D);
+            if (load) words(tb, kr);   // in flight under the value tile
+            if (k >= 0) {
+                if (!wait(B_VEMPTY)) return false;
+                uint8_t *vb = value_at();
+                if (g.left > 0) {
+                    uint32_t v10[NW];
+#pragma unroll
+                    for (int y = 0; y < NW; ++y) v10[y] = vr[y] >> 10;
+#pragma unroll
+                    for (int gm = 0; gm < NKT / 2; ++gm) {
+                        const uint32_t *z = zr + 4 * gm;
+                        const uint32_t s2[2] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[2], z[3], 0x5410)};
+                        const uint32_t z2[2] = {__byte_perm(z[0], z[1], 0x7632), __byte_perm(z[2], z[3], 0x7632)};
+#pragma unroll
+                        for (int mm = 0; mm < 2; ++mm)
+#pragma unroll
+                            for (int half = 0; half < 2; ++half) {
+                                const int mt = 2 * gm + mm, q = half * NKT + mt, wi = 2 * (q >> 3);
+                                *reinterpret_cast<uint2 *>(vb + (16 * mt + 8 * half) * 128) =
+                                    make_uint2(ch_val(vr[wi], v10[wi], q & 7, s2[0], z2[0]),
+                                               ch_val(vr[wi + 1], v10[wi + 1], q & 7, s2[1], z2[1]));
+                            }
+                    }
+                } else {
+                    zero_values(vb);
+                }
+                value_done();
+            }
+            if (load) {
+                words(tb + tile_v_off(D), vr);
+#pragma unroll
+                for (int gm = 0; gm < NKT / 2; ++gm) {
+                    const uint4 z = __ldg(reinterpret_cast<const uint4 *>(tb + tile_sz_off(D)) + gm * 4 + i);
+                    zr[4 * gm] = z.x; zr[4 * gm + 1] = z.y; zr[4 * gm + 2] = z.z; zr[4 * gm + 3] = z.w;
+                }
+            }
+            g = gn;
+        }
+        return true;
+    }
+
+    // n groups from the x-th of the fp16 ones on: ring, pool and cold pool in
+    // whole groups, then the new tokens from group nlo on; past them, nothing.
+    // Loads wait here: registers for a group ahead would be taken from the
+    // other loop, which has most of the work.
+    __device__ bool plain(int x, int n) {
+        const int ncold = a.C > 0 ? __ldg(a.cmeta + 2 * u) : 0, chead = a.C > 0 ? __ldg(a.cmeta + 2 * u + 1) : 0;
+        const int nhot = s.ntail + s.npool + ncold;
+#pragma unroll 1
+        for (int y = x; y < x + n; ++y) {
+            int f = 0, left = 0;   // first token, tokens left
+            if (y < t.gf) {
+                f = 16 * y;
+                left = nhot - f;
+            } else if (y < t.gf + t.gn) {
+                f = nhot + 16 * (y - t.gf + t.nlo);
+                left = nhot + s.nnew - f;
+            }
+            uint4 kr[16 / RPI];
+#pragma unroll
+            for (int e = 0; e < 16 / RPI; ++e) kr[e] = make_uint4(0, 0, 0, 0);
+            if (left > 0) {
+#pragma unroll
+                for (int e = 0; e < 16 / RPI; ++e) {
+                    const int row = RPI * e + lane / CPR;
+                    const uint4 *p = reinterpret_cast<const uint4 *>(
+                        chunk_fp16_row(a, s, b, t.hkv, u, f + min(row, left - 1), ncold, chead, false, D)) + lane % CPR;
+                    if (row < left) kr[e] = __ldg(p);
+                }
+            }
+            if (!wait(B_KEMPTY)) return false;
+            uint8_t *kb = key_tile();
+#pragma unroll
+            for (int e = 0; e < 16 / RPI; ++e)
+                put_row_piece<D>(kb, 16 * w + slot_of(RPI * e + lane / CPR), lane % CPR, kr[e]);
+            if (lane < 2 * CPR)
+                *reinterpret_cast<uint4 *>(kb + (lane % CPR / 8) * (ROWS * 128) + (STEP_TOK + 2 * w + lane / CPR) * 128 +
+                                           (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+            key_done(true, lane < 16 && lane < left ? chunk_fp16_pos(a, s, u, f + lane, ncold, chead) : INT_MAX);
+
+            uint32_t vr[2][D / 8];
 #pragma unroll
             for (int th = 0; th < 2; ++th) {
                 const int row = r + 8 * th;
-                const __half *p = row < g.cnt ? chunk_fp16_row(a, s, b, t.hkv, u, g.sub + row, ncold, chead, true, D) : nullptr;
+                const __half *p = left > 0 ? chunk_fp16_row(a, s, b, t.hkv, u, f + min(row, left - 1), ncold, chead, true, D) : nullptr;
 #pragma unroll
                 for (int c = 0; c < D / 8; ++c)
-                    vr[th * (D / 8) + c] = p ? __ldg(reinterpret_cast<const uint32_t *>(p + 8 * c + 2 * i)) : 0u;
+                    vr[th][c] = row < left ? __ldg(reinterpret_cast<const uint32_t *>(p + 8 * c + 2 * i)) : 0u;
             }
+            if (!wait(B_VEMPTY)) return false;
+            uint8_t *vb = value_at();
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+                *reinterpret_cast<uint2 *>(vb + 8 * c * 128) = make_uint2(transpose8x8(vr[0][c]), transpose8x8(vr[1][c]));
+            value_done();
         }
-    };
-
-    // Round j makes step j's group while step j + 1's words are on their way;
-    // round j0 - 1 only starts the first loads (one copy of the code each).
-    Group g, gn;
-    int xn = GRPS * j0 + w, jp = xn / ta.CPT, sub = xn % ta.CPT;
-    g.kind = g.cnt = g.sub = g.j = 0;
-    g.src = nullptr;
-#pragma unroll 1
-    for (int j = j0 - 1; j < j1; ++j) {
-        gn = group_at(a, s, t, u, ncold, j + 1 < j1 ? xn : INT_MAX, jp, sub);
-        xn += GRPS;
-        for (sub += GRPS; sub >= ta.CPT; sub -= ta.CPT) ++jp;
-        const int slot = it & 1;
-        const uint32_t par = ((it >> 1) & 1u) ^ 1u;
-        uint8_t *kb = sm + C::OFF_K + slot * C::KB, *vb = sm + C::OFF_V + slot * C::VB + w * C::VG;
-        const bool made = j >= j0;
-        if (made) {
-        if (!bar_wait_warp(&bar[B_KEMPTY + slot], par, gave_up)) return;
-        // key rows 16w .. 16w+15, offset rows 112 + 2w and 113 + 2w
-        uint8_t *row = kb + (16 * w + r) * 128 + 4 * i;
-        if (g.kind == 1) {
-            uint32_t k10[NW];
-#pragma unroll
-            for (int x = 0; x < NW; ++x) k10[x] = kr[x] >> 10;
-            uint32_t hi[2] = {0, 0}, lw[2] = {0, 0};
-#pragma unroll
-            for (int kt = 0; kt < NKT; ++kt)
-#pragma unroll
-                for (int o = 0; o < 2; ++o) {
-                    const uint32_t x0 = kr[4 + 4 * kt + 2 * o], x1 = kr[4 + 4 * kt + 2 * o + 1];
-                    const uint32_t s2 = __byte_perm(x0, x1, 0x5410);
-                    if ((r % NKT) == kt) {   // lane (r, i) makes the offsets of k-tile r
-                        hi[o] = s2;
-                        lw[o] = __byte_perm(x0, x1, 0x7632);
-                    }
-#pragma unroll
-                    for (int th = 0; th < 2; ++th) {
-                        const int q = o * NKT + kt, wi = 2 * (q >> 3) + th;
-                        *reinterpret_cast<uint32_t *>(row + (kt / 4) * (ROWS * 128) + th * 1024 +
-                                                      (((2 * (kt & 3) + o) ^ r) << 4)) = ch_key(kr[wi], k10[wi], q & 7, s2);
-                    }
-                }
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                uint32_t h2, l2;
-                ch_offset(hi[o], lw[o], h2, l2);
-                hi[o] = h2;
-                lw[o] = l2;
-            }
-            if (r < NKT) {
-                const int kt = r;
-#pragma unroll
-                for (int o = 0; o < 2; ++o)
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int er = STEP_TOK + 2 * w + x;
-                        *reinterpret_cast<uint32_t *>(kb + (kt / 4) * (ROWS * 128) + er * 128 +
-                                                      (((2 * (kt & 3) + o) ^ (er & 7)) << 4) + 4 * i) = x ? lw[o] : hi[o];
-                    }
-            }
-        } else {
-            constexpr int CPR = D / 8, RPI = 32 / CPR;
-#pragma unroll
-            for (int x = 0; x < 16 / RPI; ++x) {
-                const int rw = 16 * w + RPI * x + lane / CPR, ch = lane % CPR;
-                const uint4 v = g.kind == 2 ? make_uint4(kr[4 * x], kr[4 * x + 1], kr[4 * x + 2], kr[4 * x + 3])
-                                            : make_uint4(0, 0, 0, 0);
-                *reinterpret_cast<uint4 *>(kb + (ch / 8) * (ROWS * 128) + rw * 128 + (((ch & 7) ^ (rw & 7)) << 4)) = v;
-            }
-            if (lane < 2 * CPR) {
-                const int er = STEP_TOK + 2 * w + lane / CPR, ch = lane % CPR;
-                *reinterpret_cast<uint4 *>(kb + (ch / 8) * (ROWS * 128) + er * 128 + (((ch & 7) ^ (er & 7)) << 4)) =
-                    make_uint4(0, 0, 0, 0);
-            }
-        }
-        // whether some row does not see some token of the group, and the positions that decide it
-        const int ms = it % META;
-        bool hidden = false;
-        if (g.kind != 1 || g.cnt < 16 || a.window > 0) {
-            int pos = INT_MAX;
-            if (lane < 16 && lane < g.cnt && g.kind) {
-                if (g.kind == 2)
-                    pos = chunk_fp16_pos(a, s, u, g.sub + lane, ncold, chead);
-                else
-                    pos = a.window > 0 ? __ldg(a.bidx + ((size_t)u * a.NB + g.j) * a.G + 16 * g.sub + lane) : 0;
-            }
-            hidden = __any_sync(0xffffffffu, lane < 16 && !(pos <= pmin && (pos >= lomax || pos < a.sinks)));
-            if (lane < 16) reinterpret_cast<volatile int *>(sm + C::OFF_POS)[ms * STEP_TOK + 16 * w + lane] = pos;
-        }
-        if (lane == 0) *reinterpret_cast<volatile uint8_t *>(sm + C::OFF_FLAG + ms * 8 + w) = hidden;
-        proxy_fence();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bar[B_KFULL + slot]);
-        }
-        load_k(gn);   // in flight under the value tile
-
-        if (made) {
-        if (!bar_wait_warp(&bar[B_VEMPTY + slot], par, gave_up)) return;
-        uint8_t *v0 = vb + r * 32 + 4 * i + ((r >> 2) << 4), *v1 = vb + r * 32 + 4 * i + (((r >> 2) ^ 1) << 4);
-        if (g.kind == 1) {
-            uint32_t v10[NW];
-#pragma unroll
-            for (int x = 0; x < NW; ++x) v10[x] = vr[x] >> 10;
-#pragma unroll
-            for (int gm = 0; gm < NKT / 2; ++gm) {
-                const uint32_t *z = vr + 4 + 4 * gm;
-                const uint32_t s2[2] = {__byte_perm(z[0], z[1], 0x5410), __byte_perm(z[2], z[3], 0x5410)};
-                const uint32_t z2[2] = {__byte_perm(z[0], z[1], 0x7632), __byte_perm(z[2], z[3], 0x7632)};
-#pragma unroll
-                for (int mm = 0; mm < 2; ++mm)
-#pragma unroll
-                    for (int tp = 0; tp < 2; ++tp)
-#pragma unroll
-                        for (int half = 0; half < 2; ++half) {
-                            const int mt = 2 * gm + mm, q = half * NKT + mt, wi = 2 * (q >> 3) + tp;
-                            *reinterpret_cast<uint32_t *>((tp ? v1 : v0) + (16 * mt + 8 * half) * 32) =
-                                ch_val(vr[wi], v10[wi], q & 7, s2[tp], z2[tp]);
-                        }
-            }
-        } else {
-#pragma unroll
-            for (int th = 0; th < 2; ++th)
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    *reinterpret_cast<uint32_t *>((th ? v1 : v0) + 8 * c * 32) =
-                        transpose8x8(g.kind == 2 ? vr[th * (D / 8) + c] : 0u);
-        }
-        proxy_fence();
-        __syncwarp();
-        if (lane == 0) bar_arrive(&bar[B_VFULL + slot]);
-        ++it;
-        }
-        load_v(gn);
-        g = gn;
+        return true;
     }
+
+    __device__ static void words(const uint8_t *p, uint32_t (&d)[NW]) {
+        const int lane = threadIdx.x & 31;
+        if constexpr (NW == 4) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p) + lane);
+            d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
+        } else {
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p) + lane);
+            d[0] = x.x; d[1] = x.y;
+        }
+    }
+    __device__ void zero_keys(uint8_t *kb) const {
+#pragma unroll 1
+        for (int e = lane; e < 18 * CPR; e += 32) {
+            const int row = e / CPR < 16 ? 16 * w + e / CPR : STEP_TOK + 2 * w + e / CPR - 16, ch = e % CPR;
+            *reinterpret_cast<uint4 *>(kb + (ch / 8) * (ROWS * 128) + row * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+    }
+    __device__ static void zero_values(uint8_t *vb) {
+#pragma unroll 1
+        for (int c = 0; c < D / 8; ++c) *reinterpret_cast<uint2 *>(vb + 8 * c * 128) = make_uint2(0u, 0u);
+    }
+};
+
+template <int D>
+__device__ void produce(const TileArgs &ta, const ChunkSeq &s, const Tile &t, uint8_t *sm, uint64_t *bar,
+                        volatile int *gave_up, int j0, int j1, uint32_t it) {
+    Producer<D> p(ta, s, t, sm, bar, gave_up, it);
+    if (j0 < t.sq && !p.quantized(p.w * t.sq + j0, min(j1, t.sq) - j0)) return;
+    if (j1 > t.sq) p.plain(p.w * (t.steps - t.sq) + max(j0 - t.sq, 0), j1 - max(j0, t.sq));
 }
 
 // ---------------------------------------------------------------- products
 template <int D>
 __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint32_t tmem, int nt, int steps, uint32_t it,
-                         uint32_t (&ct)[2]) {
+                         uint32_t c0, uint32_t c1) {
     using C = TCfg<D>;
     const uint32_t base = ch_smem(sm), dq = desc_lo(base + C::OFF_Q), dk = desc_lo(base + C::OFF_K),
                    dv = desc_lo(base + C::OFF_V);
@@ -525,43 +623,61 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
     auto values = [&](int t, int slot, bool acc) {
 #pragma unroll
         for (int k = 0; k < GRPS; ++k) {
-            constexpr uint32_t HI = desc_hi(256, 6);
-            mma_ts(tmem + C::O(t), tmem + C::S(t) + 8 * k, dv + slot * (C::VB / 16) + k * (C::VG / 16), HI, instr_desc(D),
+            constexpr uint32_t HI = desc_hi(1024, 2);
+            mma_ts(tmem + C::O(t), tmem + C::S(t) + 8 * k, dv + slot * (C::VB / 16) + ((k / 4) * (D * 128) + (k & 3) * 32) / 16, HI, instr_desc(D),
                    acc || k > 0);
         }
     };
+    // the whole warp keeps the loop, so that the operands stay in uniform
+    // registers; one lane issues
     for (int j = 0; j < steps; ++j, ++it) {
         const int slot = it & 1, prev = slot ^ 1;
         const uint32_t par = (it >> 1) & 1u;
-        if (!bar_wait(&bar[B_KFULL + slot], par, gave_up)) break;
+        if (!bar_wait_warp(&bar[B_KFULL + slot], par, gave_up)) break;
         tc_after();
-        scores(0, slot);
-        tc_commit(&bar[B_SFULL]);
+        if (elect_one()) {
+            scores(0, slot);
+            tc_commit(&bar[B_SFULL]);
+        }
+        __syncwarp();
         if (nt == 2) {
             if (j > 0) {
-                if (!bar_wait(&bar[B_PFULL + 1], (ct[1] - 1) & 1u, gave_up)) break;
+                if (!bar_wait_warp(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up)) break;
                 tc_after();
-                values(1, prev, j > 1);
-                tc_commit(&bar[B_VEMPTY + prev]);
             }
-            scores(1, slot);
-            tc_commit(&bar[B_SFULL + 1]);
-            ++ct[1];
+            if (elect_one()) {
+                if (j > 0) {
+                    values(1, prev, j > 1);
+                    tc_commit(&bar[B_VEMPTY + prev]);
+                }
+                scores(1, slot);
+                tc_commit(&bar[B_SFULL + 1]);
+            }
+            ++c1;
         }
-        tc_commit(&bar[B_KEMPTY + slot]);
-        if (!bar_wait(&bar[B_PFULL], ct[0] & 1u, gave_up)) break;
-        ++ct[0];
-        if (!bar_wait(&bar[B_VFULL + slot], par, gave_up)) break;
+        if (elect_one()) tc_commit(&bar[B_KEMPTY + slot]);
+        __syncwarp();
+        if (!bar_wait_warp(&bar[B_PFULL], c0 & 1u, gave_up)) break;
+        ++c0;
+        if (!bar_wait_warp(&bar[B_VFULL + slot], par, gave_up)) break;
         tc_after();
-        values(0, slot, j > 0);
-        if (nt == 1) tc_commit(&bar[B_VEMPTY + slot]);
+        if (elect_one()) {
+            values(0, slot, j > 0);
+            if (nt == 1) tc_commit(&bar[B_VEMPTY + slot]);
+        }
+        __syncwarp();
     }
-    if (nt == 2 && !*gave_up && bar_wait(&bar[B_PFULL + 1], (ct[1] - 1) & 1u, gave_up)) {
-        tc_after();
-        values(1, (it - 1) & 1, steps > 1);
-        tc_commit(&bar[B_VEMPTY + ((it - 1) & 1)]);
+    const int last = (it - 1) & 1;
+    const bool more = nt == 2 && !__any_sync(0xffffffffu, *gave_up) && bar_wait_warp(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up);
+    tc_after();
+    if (elect_one()) {
+        if (more) {
+            values(1, last, steps > 1);
+            tc_commit(&bar[B_VEMPTY + last]);
+        }
+        tc_commit(&bar[B_OFULL]);
     }
-    tc_commit(&bar[B_OFULL]);
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------- softmax
@@ -656,7 +772,8 @@ __device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
         l += sum.x + sum.y;
         wait_st();
         tc_before();
-        bar_arrive(&bar[B_PFULL + tile]);
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar[B_PFULL + tile]);
     }
     return true;
 }
@@ -679,7 +796,10 @@ __device__ void finish(const TileArgs &ta, const Tile &t, uint32_t tmem, int til
             tie16(f);
             uint32_t h[8];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) h[y] = ch_h2(__floats2half2_rn(f[2 * y] * inv, f[2 * y + 1] * inv));
+            for (int y = 0; y < 8; ++y) {   // channels 2y, 2y + 1 of the 16, from their columns
+                const int c0 = (2 * y & 8) + vrow(2 * y & 7), c1 = (2 * y & 8) + vrow((2 * y & 7) + 1);
+                h[y] = ch_h2(__floats2half2_rn(f[c0] * inv, f[c1] * inv));
+            }
             if (row < t.rows) {
                 *reinterpret_cast<uint4 *>(o + c) = make_uint4(h[0], h[1], h[2], h[3]);
                 *reinterpret_cast<uint4 *>(o + c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
@@ -696,7 +816,7 @@ __device__ void finish(const TileArgs &ta, const Tile &t, uint32_t tmem, int til
             wait_ld();
             tie16(f);
 #pragma unroll
-            for (int y = 0; y < 16; ++y) pb[(size_t)(2 + c + y) * 256] = f[y];
+            for (int y = 0; y < 16; ++y) pb[(size_t)(2 + c + y) * 256] = f[(y & 8) + vrow(y & 7)];
         }
     }
     tc_before();
@@ -730,8 +850,7 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
                 v = __ldg(reinterpret_cast<const uint4 *>(
                               a.q + (((size_t)(a.B0 + t.e) * a.Hq + t.hkv * a.g + vv % a.g) * a.n + vv / a.g) * D) + ch);
             }
-            *reinterpret_cast<uint4 *>(sm + C::OFF_Q + row / ROWS * C::QB + (ch / 8) * (ROWS * 128) + rw * 128 +
-                                       (((ch & 7) ^ (rw & 7)) << 4)) = v;
+            put_row_piece<D>(sm + C::OFF_Q + row / ROWS * C::QB, rw, ch, v);
         }
         proxy_fence();
         cta_sync();
@@ -744,11 +863,7 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
                 finish<D>(ta, t, tmem, tile, n == t.steps, run > 0, m, l);
             }
         } else if constexpr (ROLE == MULTIPLY) {
-            if ((threadIdx.x & 31) == 0) {
-                uint32_t c2[2] = {ct[0], ct[1]};
-                multiply<D>(sm, bar, gave_up, tmem, nt, n, it, c2);
-            }
-            __syncwarp();
+            multiply<D>(sm, bar, gave_up, tmem, nt, n, it, ct[0], ct[1]);
         } else {
             produce<D>(ta, s, t, sm, bar, gave_up, j0, j1, it);
         }
@@ -779,7 +894,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             bar_init(&bar[B_KEMPTY + k], 1);
             bar_init(&bar[B_VEMPTY + k], 1);
             bar_init(&bar[B_SFULL + k], 1);
-            bar_init(&bar[B_PFULL + k], ROWS);
+            bar_init(&bar[B_PFULL + k], ROWS / 32);
         }
         bar_init(&bar[B_OFULL], 1);
         *gave_up = 0;
@@ -798,7 +913,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_before();
     __syncthreads();
     tc_after();
-    const uint32_t tmem = *tm;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tm, 0);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // 8 x 32 x (REG_SM + REG_PR) = the 512 x 128 registers of the launch
