@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 
     uint32_t phase = 0;
     int sg = 0;
+    const Magic mg;
     while (cc.x < x1) {
         const ChunkSeq &s = st.e[cc.e];
         const int2 mt_ = meta[sg];
@@ -424,7 +425,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 #pragma unroll
                                 for (int th = 0; th < 2; ++th) {
                                     const int q = o * NKT + kt, wi = 2 * (q >> 3) + th;
-                                    f4[th + 2 * o] = ch_key(w[wi], w10[wi], q & 7, ks2[kt][o]);
+                                    f4[th + 2 * o] = ch_key(mg, w[wi], w10[wi], q & 7, ks2[kt][o]);
                                 }
 #pragma unroll
                             for (int nc = 0; nc < NC; ++nc)
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 #pragma unroll
                                 for (int half = 0; half < 2; ++half) {
                                     const int q = half * NKT + mt, wi = 2 * (q >> 3) + tp;
-                                    f4[half + 2 * tp] = ch_val(w[wi], w10[wi], q & 7, s2[tp], z2[tp]);
+                                    f4[half + 2 * tp] = ch_val(mg, w[wi], w10[wi], q & 7, s2[tp], z2[tp]);
                                 }
 #pragma unroll
                             for (int nc = 0; nc < NC; ++nc)

@@ -102,23 +102,34 @@ __device__ __forceinline__ __half2 ch_as_h2(uint32_t w) { return *reinterpret_ca
 // c = p mod 5, whose unit in the last place they are counted in: an exact
 // fp16 2^(10-2c) + code. One subtraction gives code - 1 (keys) or code
 // (values), exactly.
-__device__ __forceinline__ uint32_t ch_raw(uint32_t w, uint32_t w10, int p) {
+// Magic holds the five 2^(10-2c) in registers, so that extraction is one
+// three-input operation (it takes one immediate, the mask).
+struct Magic {
+    uint32_t m[5];
+    __device__ __forceinline__ Magic() {
+#pragma unroll
+        for (int c = 0; c < 5; ++c) {
+            m[c] = (uint32_t)((25 - 2 * c) << 10) * 0x10001u;
+            asm volatile("" : "+r"(m[c]));   // a register's value from here on
+        }
+    }
+};
+__device__ __forceinline__ uint32_t ch_raw(const Magic &mg, uint32_t w, uint32_t w10, int p) {
     const int c = cls_of_pos(p);
-    const uint32_t magic = (uint32_t)((25 - 2 * c) << 10) * 0x10001u;
-    return ((p < 5 ? w : w10) & (0x00030003u << (2 * c))) | magic;
+    return ((p < 5 ? w : w10) & (0x00030003u << (2 * c))) | mg.m[c];
 }
 __device__ __forceinline__ uint32_t ch_const(int p, int less) {   // -(2^(10-2c) + less) in both halves
     const __half h = __float2half_rn(-(float)((1 << (10 - 2 * cls_of_pos(p))) + less));
     return (uint32_t)__half_as_ushort(h) * 0x10001u;
 }
 // s * (code - 1): exact (a scale, its negative, zero or twice it)
-__device__ __forceinline__ uint32_t ch_key(uint32_t w, uint32_t w10, int p, uint32_t s2) {
-    const __half2 c1 = __hadd2(ch_as_h2(ch_raw(w, w10, p)), ch_as_h2(ch_const(p, 1)));
+__device__ __forceinline__ uint32_t ch_key(const Magic &mg, uint32_t w, uint32_t w10, int p, uint32_t s2) {
+    const __half2 c1 = __hadd2(ch_as_h2(ch_raw(mg, w, w10, p)), ch_as_h2(ch_const(p, 1)));
     return ch_h2(__hmul2(c1, ch_as_h2(s2)));
 }
 // z + s * code, one rounding
-__device__ __forceinline__ uint32_t ch_val(uint32_t w, uint32_t w10, int p, uint32_t s2, uint32_t z2) {
-    const __half2 c = __hadd2(ch_as_h2(ch_raw(w, w10, p)), ch_as_h2(ch_const(p, 0)));
+__device__ __forceinline__ uint32_t ch_val(const Magic &mg, uint32_t w, uint32_t w10, int p, uint32_t s2, uint32_t z2) {
+    const __half2 c = __hadd2(ch_as_h2(ch_raw(mg, w, w10, p)), ch_as_h2(ch_const(p, 0)));
     return ch_h2(__hfma2(c, ch_as_h2(s2), ch_as_h2(z2)));
 }
 // fp16x2 hi + lo = s + z exactly up to lo's rounding (the two-sum of both halves)

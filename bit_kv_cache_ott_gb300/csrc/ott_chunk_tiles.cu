@@ -44,7 +44,6 @@ constexpr int STEP_TOK = 16 * GRPS;
 constexpr int ROWS = 128;            // rows of a tile
 constexpr int THREADS = 512;
 constexpr int PROD0 = 8, MMA_WARP = 15;
-constexpr int REG_SM = 152, REG_PR = 104;   // registers per thread of the softmax warps and the others
 constexpr int META = 4;              // steps of group metadata in flight
 constexpr float GROW = 8.0f;         // log2: the output is rescaled when the maximum has grown by this
 constexpr int MIN_STEPS = 4;         // steps per CTA at least (a run's fixed cost is about two)
@@ -394,6 +393,7 @@ struct Producer {
         g.j = -1;
         g.src = nullptr;
         gn = gb = g;
+        const Magic mg;
         int fresh = 0;               // steps for which the block's offset rows still have to be written
 #pragma unroll 1
         for (int k = -1; k < n; ++k) {
@@ -418,6 +418,7 @@ struct Producer {
                     uint32_t k10[NW];
 #pragma unroll
                     for (int y = 0; y < NW; ++y) k10[y] = kr[y] >> 10;
+                    uint8_t *const p[4] = {kb + k0, kb + (k0 ^ 16), kb + k1, kb + (k1 ^ 16)};
 #pragma unroll
                     for (int th = 0; th < 2; ++th)
 #pragma unroll
@@ -426,9 +427,9 @@ struct Producer {
                             uint32_t f[4];
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
-                                f[y] = ch_key(kr[wi], k10[wi], (q0 + y) & 7, ks2[(q0 + y) % NKT][(q0 + y) / NKT]);
+                                f[y] = ch_key(mg, kr[wi], k10[wi], (q0 + y) & 7, ks2[(q0 + y) % NKT][(q0 + y) / NKT]);
                             // chunk 2i + 1 is chunk 2i with its lowest bit turned, whatever the swizzle
-                            *reinterpret_cast<uint4 *>(kb + (((th ? k1 : k0) + (q0 >> 3) * (ROWS * 128)) ^ ((q0 & 4) << 2))) =
+                            *reinterpret_cast<uint4 *>(p[2 * th + ((q0 >> 2) & 1)] + (q0 >> 3) * (ROWS * 128)) =
                                 make_uint4(f[0], f[1], f[2], f[3]);
                         }
                     if (fresh > 0) {
@@ -494,8 +495,8 @@ struct Producer {
                             for (int half = 0; half < 2; ++half) {
                                 const int mt = 2 * gm + mm, q = half * NKT + mt, wi = 2 * (q >> 3);
                                 *reinterpret_cast<uint2 *>(vb + (16 * mt + 8 * half) * 128) =
-                                    make_uint2(ch_val(vr[wi], v10[wi], q & 7, s2[0], z2[0]),
-                                               ch_val(vr[wi + 1], v10[wi + 1], q & 7, s2[1], z2[1]));
+                                    make_uint2(ch_val(mg, vr[wi], v10[wi], q & 7, s2[0], z2[0]),
+                                               ch_val(mg, vr[wi + 1], v10[wi + 1], q & 7, s2[1], z2[1]));
                             }
                     }
                 } else {
@@ -681,6 +682,14 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
 }
 
 // ---------------------------------------------------------------- softmax
+__device__ __forceinline__ float max16(const float *x) {   // short chains of three-way maxima
+    float g[3] = {x[0], x[1], x[2]};
+#pragma unroll
+    for (int c = 3; c < 15; c += 6)
+#pragma unroll
+        for (int y = 0; y < 3; ++y) g[y] = fmaxf(fmaxf(g[y], x[c + 2 * y]), x[c + 2 * y + 1]);
+    return fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], x[15]));
+}
 template <int D>
 __device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, uint8_t *sm, uint64_t *bar,
                         volatile int *gave_up, uint32_t tmem, int tile, int steps, uint32_t it, uint32_t cnt, float &m_ref,
@@ -716,26 +725,29 @@ __device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
                 }
             wait_st();
         }
-        float e[16], x[STEP_TOK];
+        // The maximum: groups 4..6 first, then 0..3, which stay in registers
+        // (64 of them; 4..6 are read again below, behind the weights of 0..3,
+        // whose columns they do not share).
+        float e[16], x[64];
         tm_ld16(ts + STEP_TOK, e);
 #pragma unroll
-        for (int k = 0; k < GRPS; ++k) tm_ld16(ts + 16 * k, x + 16 * k);
+        for (int k = 4; k < GRPS; ++k) tm_ld16(ts + 16 * k, x + 16 * (k - 4));
         wait_ld();
         tie16(e);
 #pragma unroll
-        for (int k = 0; k < GRPS; ++k) tie16(x + 16 * k);
+        for (int k = 0; k < 3; ++k) tie16(x + 16 * k);
         float mx = -CUDART_INF_F, off[GRPS];
 #pragma unroll
-        for (int k = 0; k < GRPS; ++k) {
-            off[k] = (e[2 * k] + e[2 * k + 1]) * a.sl2;
-            float g[3] = {x[16 * k], x[16 * k + 1], x[16 * k + 2]};   // short chains of three-way maxima
+        for (int k = 0; k < GRPS; ++k) off[k] = (e[2 * k] + e[2 * k + 1]) * a.sl2;
 #pragma unroll
-            for (int c = 3; c < 15; c += 6)
+        for (int k = 4; k < GRPS; ++k) mx = fmaxf(mx, fmaf(max16(x + 16 * (k - 4)), a.sl2, off[k]));
 #pragma unroll
-                for (int y = 0; y < 3; ++y) g[y] = fmaxf(fmaxf(g[y], x[16 * k + c + 2 * y]), x[16 * k + c + 2 * y + 1]);
-            g[0] = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], x[16 * k + 15]));
-            mx = fmaxf(mx, fmaf(g[0], a.sl2, off[k]));
-        }
+        for (int k = 0; k < 4; ++k) tm_ld16(ts + 16 * k, x + 16 * k);
+        wait_ld();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tie16(x + 16 * k);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fmaf(max16(x + 16 * k), a.sl2, off[k]));
         const bool grow = mx > m_ref + GROW && m_ref != -CUDART_INF_F;
         if (__any_sync(0xffffffffu, grow)) {
             // the previous step's products are complete (the scores were issued behind them)
@@ -756,19 +768,32 @@ __device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
         if (m_ref == -CUDART_INF_F) m_ref = mx;   // the first token that the row sees: its output is zero so far
         const float mm = m_ref == -CUDART_INF_F ? 0.0f : m_ref;
         float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < GRPS; ++k) {
+        auto weights = [&](int k, const float *y) {
             const float2 ad = make_float2(off[k] - mm, off[k] - mm), sc = make_float2(a.sl2, a.sl2);
             uint32_t p8[8];
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-                const float2 v = __ffma2_rn(make_float2(x[16 * k + 2 * c], x[16 * k + 2 * c + 1]), sc, ad);
+                const float2 v = __ffma2_rn(make_float2(y[2 * c], y[2 * c + 1]), sc, ad);
                 const float2 p = make_float2(ch_ex2(v.x), ch_ex2(v.y));
                 sum = __fadd2_rn(sum, p);
                 p8[c] = ch_h2(__floats2half2_rn(p.x, p.y));
             }
             tm_st8(ts + 8 * k, p8);
-        }
+        };
+        weights(0, x);
+        weights(1, x + 16);
+        weights(2, x + 32);
+        tm_ld16(ts + 64, x);
+        tm_ld16(ts + 80, x + 16);
+        tm_ld16(ts + 96, x + 32);
+        weights(3, x + 48);
+        wait_ld();
+        tie16(x);
+        tie16(x + 16);
+        tie16(x + 32);
+        weights(4, x);
+        weights(5, x + 16);
+        weights(6, x + 32);
         l += sum.x + sum.y;
         wait_st();
         tc_before();
@@ -916,12 +941,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tm, 0);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // 8 x 32 x (REG_SM + REG_PR) = the 512 x 128 registers of the launch
     if (warp < PROD0) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REG_SM));
         role_loop<D, SOFTMAX>(ta, st, sm, bar, gave_up, tmem);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REG_PR));
         if (warp == MMA_WARP)
             role_loop<D, MULTIPLY>(ta, st, sm, bar, gave_up, tmem);
         else
