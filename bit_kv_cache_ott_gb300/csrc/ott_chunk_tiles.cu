@@ -157,22 +157,20 @@ __device__ __forceinline__ unsigned long long now_ns() {
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
     return t;
 }
-// Bounded wait: gives up after a second, or once another role has.
-__device__ __forceinline__ bool bar_wait_slow(uint64_t *b, uint32_t parity, volatile int *gave_up) {
-    const unsigned long long end = now_ns() + 1000000000ull;
-    for (;;) {
-        for (int k = 0; k < 64; ++k)
-            if (bar_try(b, parity)) return true;
-        if (*gave_up) return false;
-        if (now_ns() > end) {
-            *gave_up = 1;
-            return false;
+// Bounded wait: gives up after a second, or once another role has. A role
+// whose wait gave up goes on (every later wait then ends at once, every
+// address stays what it would have been), so that warps stay together and
+// all roles reach the end; the status word tells the host.
+__device__ __forceinline__ void bar_wait(uint64_t *b, uint32_t parity, volatile int *gave_up) {   // whole warps
+    if (!bar_try(b, parity)) {
+        const unsigned long long end = now_ns() + 1000000000ull;
+        for (int k = 0; !bar_try(b, parity); ++k) {
+            if (k & 63) continue;
+            if (*gave_up) break;
+            if (now_ns() > end) *gave_up = 1;
         }
     }
-}
-__device__ __forceinline__ bool bar_wait(uint64_t *b, uint32_t parity, volatile int *gave_up) {
-    if (bar_try(b, parity)) return true;
-    return bar_wait_slow(b, parity, gave_up);
+    __syncwarp();
 }
 // One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -182,10 +180,6 @@ __device__ __forceinline__ bool elect_one() {
 }
 // All 512 threads, each role from its own place in the code.
 __device__ __forceinline__ void cta_sync() { asm volatile("barrier.sync 0;" ::: "memory"); }
-// The same by whole warps: all lanes go on together or give up together.
-__device__ __forceinline__ bool bar_wait_warp(uint64_t *b, uint32_t parity, volatile int *gave_up) {
-    return __all_sync(0xffffffffu, bar_wait(b, parity, gave_up));
-}
 __device__ __forceinline__ void tc_commit(uint64_t *b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(ch_smem(b)) : "memory");
 }
@@ -349,9 +343,7 @@ struct Producer {
         pmin = s.pos0 + 256 * t.p / a.g;
         lomax = a.window > 0 ? s.pos0 + (256 * t.p + t.rows - 1) / a.g - a.window + 1 : 0;
     }
-    __device__ bool wait(int which) {
-        return bar_wait_warp(&bar[which + (it & 1)], ((it >> 1) & 1u) ^ 1u, gave_up);
-    }
+    __device__ void wait(int which) { bar_wait(&bar[which + (it & 1)], ((it >> 1) & 1u) ^ 1u, gave_up); }
     // The tile's part is written: pos (of lane < 16's token, INT_MAX: none)
     // decides whether some row does not see it, where `ask`.
     __device__ void key_done(bool ask, int pos) {
@@ -380,7 +372,7 @@ struct Producer {
     }
 
     // Quantized groups x, x + 1 .. x + n - 1 (none from gq on).
-    __device__ bool quantized(int x, int n) {
+    __device__ void quantized(int x, int n) {
         const int cpt = ta.CPT;
         uint32_t kr[NW], vr[NW], zr[2 * NKT], ks2[NKT][2];
         uint8_t *const stage = sm + C::OFF_HDR + w * ksz_bytes(D);   // the block's key scales and zeros
@@ -412,7 +404,7 @@ struct Producer {
                 enter = gn.left > 0;
             }
             if (k >= 0) {
-                if (!wait(B_KEMPTY)) return false;
+                wait(B_KEMPTY);
                 uint8_t *kb = key_tile();
                 if (g.left > 0) {
                     uint32_t k10[NW];
@@ -478,7 +470,7 @@ struct Producer {
             const uint8_t *tb = gn.src + ksz_bytes(D) + (size_t)gn.sub * tile_bytes(D);
             if (load) words(tb, kr);   // in flight under the value tile
             if (k >= 0) {
-                if (!wait(B_VEMPTY)) return false;
+                wait(B_VEMPTY);
                 uint8_t *vb = value_at();
                 if (g.left > 0) {
                     uint32_t v10[NW];
@@ -514,14 +506,13 @@ struct Producer {
             }
             g = gn;
         }
-        return true;
     }
 
     // n groups from the x-th of the fp16 ones on: ring, pool and cold pool in
     // whole groups, then the new tokens from group nlo on; past them, nothing.
     // Loads wait here: registers for a group ahead would be taken from the
     // other loop, which has most of the work.
-    __device__ bool plain(int x, int n) {
+    __device__ void plain(int x, int n) {
         const int ncold = a.C > 0 ? __ldg(a.cmeta + 2 * u) : 0, chead = a.C > 0 ? __ldg(a.cmeta + 2 * u + 1) : 0;
         const int nhot = s.ntail + s.npool + ncold;
 #pragma unroll 1
@@ -546,7 +537,7 @@ struct Producer {
                     if (row < left) kr[e] = __ldg(p);
                 }
             }
-            if (!wait(B_KEMPTY)) return false;
+            wait(B_KEMPTY);
             uint8_t *kb = key_tile();
 #pragma unroll
             for (int e = 0; e < 16 / RPI; ++e)
@@ -565,14 +556,13 @@ struct Producer {
                 for (int c = 0; c < D / 8; ++c)
                     vr[th][c] = row < left ? __ldg(reinterpret_cast<const uint32_t *>(p + 8 * c + 2 * i)) : 0u;
             }
-            if (!wait(B_VEMPTY)) return false;
+            wait(B_VEMPTY);
             uint8_t *vb = value_at();
 #pragma unroll
             for (int c = 0; c < D / 8; ++c)
                 *reinterpret_cast<uint2 *>(vb + 8 * c * 128) = make_uint2(transpose8x8(vr[0][c]), transpose8x8(vr[1][c]));
             value_done();
         }
-        return true;
     }
 
     __device__ static void words(const uint8_t *p, uint32_t (&d)[NW]) {
@@ -602,7 +592,7 @@ template <int D>
 __device__ void produce(const TileArgs &ta, const ChunkSeq &s, const Tile &t, uint8_t *sm, uint64_t *bar,
                         volatile int *gave_up, int j0, int j1, uint32_t it) {
     Producer<D> p(ta, s, t, sm, bar, gave_up, it);
-    if (j0 < t.sq && !p.quantized(p.w * t.sq + j0, min(j1, t.sq) - j0)) return;
+    if (j0 < t.sq) p.quantized(p.w * t.sq + j0, min(j1, t.sq) - j0);
     if (j1 > t.sq) p.plain(p.w * (t.steps - t.sq) + max(j0 - t.sq, 0), j1 - max(j0, t.sq));
 }
 
@@ -634,7 +624,7 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
     for (int j = 0; j < steps; ++j, ++it) {
         const int slot = it & 1, prev = slot ^ 1;
         const uint32_t par = (it >> 1) & 1u;
-        if (!bar_wait_warp(&bar[B_KFULL + slot], par, gave_up)) break;
+        bar_wait(&bar[B_KFULL + slot], par, gave_up);
         tc_after();
         if (elect_one()) {
             scores(0, slot);
@@ -642,10 +632,8 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
         }
         __syncwarp();
         if (nt == 2) {
-            if (j > 0) {
-                if (!bar_wait_warp(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up)) break;
-                tc_after();
-            }
+            if (j > 0) bar_wait(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up);
+            tc_after();
             if (elect_one()) {
                 if (j > 0) {
                     values(1, prev, j > 1);
@@ -653,14 +641,16 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
                 }
                 scores(1, slot);
                 tc_commit(&bar[B_SFULL + 1]);
+                tc_commit(&bar[B_KEMPTY + slot]);
             }
             ++c1;
+        } else {
+            if (elect_one()) tc_commit(&bar[B_KEMPTY + slot]);
         }
-        if (elect_one()) tc_commit(&bar[B_KEMPTY + slot]);
         __syncwarp();
-        if (!bar_wait_warp(&bar[B_PFULL], c0 & 1u, gave_up)) break;
+        bar_wait(&bar[B_VFULL + slot], par, gave_up);
+        bar_wait(&bar[B_PFULL], c0 & 1u, gave_up);
         ++c0;
-        if (!bar_wait_warp(&bar[B_VFULL + slot], par, gave_up)) break;
         tc_after();
         if (elect_one()) {
             values(0, slot, j > 0);
@@ -669,10 +659,10 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
         __syncwarp();
     }
     const int last = (it - 1) & 1;
-    const bool more = nt == 2 && !__any_sync(0xffffffffu, *gave_up) && bar_wait_warp(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up);
+    if (nt == 2) bar_wait(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up);
     tc_after();
     if (elect_one()) {
-        if (more) {
+        if (nt == 2) {
             values(1, last, steps > 1);
             tc_commit(&bar[B_VEMPTY + last]);
         }
@@ -691,7 +681,7 @@ __device__ __forceinline__ float max16(const float *x) {   // short chains of th
     return fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], x[15]));
 }
 template <int D>
-__device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, uint8_t *sm, uint64_t *bar,
+__device__ void softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, uint8_t *sm, uint64_t *bar,
                         volatile int *gave_up, uint32_t tmem, int tile, int steps, uint32_t it, uint32_t cnt, float &m_ref,
                         float &l) {
     using C = TCfg<D>;
@@ -704,7 +694,7 @@ __device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
     m_ref = -CUDART_INF_F;
     l = 0.0f;
     for (int j = 0; j < steps; ++j, ++it, ++cnt) {
-        if (!bar_wait_warp(&bar[B_SFULL + tile], cnt & 1u, gave_up)) return false;
+        bar_wait(&bar[B_SFULL + tile], cnt & 1u, gave_up);
         tc_after();
         // groups with a token that some row does not see: -inf into its scores
         const int ms = it % META;
@@ -800,7 +790,6 @@ __device__ bool softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
         __syncwarp();
         if (lane == 0) bar_arrive(&bar[B_PFULL + tile]);
     }
-    return true;
 }
 
 // The output of a tile's row, or its part of it. Warps of the softmax.
@@ -882,8 +871,9 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
         if constexpr (ROLE == SOFTMAX) {
             const int tile = threadIdx.x / ROWS;
             float m, l;
-            if (tile < nt && softmax<D>(ta, s, t, sm, bar, gave_up, tmem, tile, n, it, ct[tile], m, l) &&
-                bar_wait_warp(&bar[B_OFULL], run & 1u, gave_up)) {
+            if (tile < nt) {
+                softmax<D>(ta, s, t, sm, bar, gave_up, tmem, tile, n, it, ct[tile], m, l);
+                bar_wait(&bar[B_OFULL], run & 1u, gave_up);
                 tc_after();
                 finish<D>(ta, t, tmem, tile, n == t.steps, run > 0, m, l);
             }
@@ -897,7 +887,6 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
         if (nt == 2) ct[1] += (uint32_t)n;
         x += n;
         cta_sync();
-        if (*gave_up) break;
     }
 }
 
