@@ -33,6 +33,7 @@
 namespace ott {
 namespace {
 
+constexpr float GROW = 8.0f;                // log2: see rescale
 constexpr int FI = 8;                       // fp16 tokens per work item
 constexpr int CT = CHUNK_TILES * TILE;      // block slots per work item
 constexpr int ROWS_MAX = 16;                // query rows per kv head up to which this kernel serves a call
@@ -111,20 +112,38 @@ struct RowsCfg {
     static_assert(2 * FI * RS * 2 <= STAGE && STAGE % 128 == 0, "fp16 items fit a stage");
 };
 
+// A work item: its unit (entry, kv head, slice of rows), its number in the
+// unit, and for one of a block the block's place and the chunk; all kept up
+// by additions (a division per item costs as much as a tile of tokens).
 struct Cursor {
     long long x;
-    int e, h, off;   // entry, (kv head, slice) of the entry, item of the unit
+    int e, hkv, sl, off, jp, k;
+    int Sf, Iu;   // of the entry
+    __device__ __forceinline__ void unit(const ChunkTable &st) {
+        off = jp = k = 0;
+        Sf = st.e[e].Sf;
+        Iu = st.e[e].Iu;
+    }
+    // true: the next item is another unit's
+    __device__ __forceinline__ bool next(const ChunkArgs &a, const ChunkTable &st) {
+        ++x;
+        if (off++ >= Sf && ++k == a.CPB) {
+            k = 0;
+            ++jp;
+        }
+        if (off < Iu) return false;
+        if (++sl == st.e[e].S) {
+            sl = 0;
+            if (++hkv == a.Hkv) {
+                hkv = 0;
+                do ++e;
+                while (e < a.nseq && st.e[e].S == 0);
+            }
+        }
+        unit(st);
+        return true;
+    }
 };
-
-__device__ __forceinline__ void cursor_next(Cursor &c, const ChunkArgs &a, const ChunkTable &st) {
-    ++c.x;
-    if (++c.off < st.e[c.e].Iu) return;
-    c.off = 0;
-    if (++c.h < a.Hkv * st.e[c.e].S) return;
-    c.h = 0;
-    do ++c.e;
-    while (c.e < a.nseq && st.e[c.e].S == 0);
-}
 
 template <int D, int NC>
 __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
@@ -151,8 +170,15 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     {
         const ChunkSeq &s = st.e[ic.e];
         const unsigned rel = (unsigned)(x0 - s.base);   // a sequence's items fit 32 bits (checked on the host)
-        ic.h = (int)(rel / (unsigned)s.Iu);
-        ic.off = (int)(rel % (unsigned)s.Iu);
+        const int h = (int)(rel / (unsigned)s.Iu), off = (int)(rel % (unsigned)s.Iu);
+        ic.hkv = h / s.S;
+        ic.sl = h % s.S;
+        ic.unit(st);
+        ic.off = off;
+        if (off > s.Sf) {
+            ic.jp = (off - s.Sf) / a.CPB;
+            ic.k = (off - s.Sf) % a.CPB;
+        }
     }
     Cursor cc = ic;
 
@@ -162,10 +188,10 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     };
     auto issue = [&](const Cursor &c, int sg) {
         const ChunkSeq &s = st.e[c.e];
-        const int hkv = c.h / s.S, b = a.B0 + c.e, u = b * a.Hkv + hkv;
+        const int hkv = c.hkv, b = a.B0 + c.e, u = b * a.Hkv + hkv;
         uint8_t *dst = stg + sg * C::STAGE;
         int2 m = make_int2(0, 0);
-        if (c.off < s.Sf) {
+        if (c.off < c.Sf) {
             int ncold, chead;
             cold_of(u, ncold, chead);
             const int f0 = c.off * FI, cnt = min(FI, s.ntail + s.npool + ncold + s.nnew - f0);
@@ -182,7 +208,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 }
             }
         } else {
-            const int qi = c.off - s.Sf, jp = qi / a.CPB, k = qi % a.CPB;
+            const int jp = c.jp, k = c.k;
             const int j = jp < s.nsink ? __ldg(a.sel + (size_t)u * a.NB + jp) : s.jlo + jp - s.nsink;
             const int rem = j < 0 ? 0 : min(CT, chunk_block_cnt(a, u, j) - CT * k);
             if (rem > 0) {
@@ -211,11 +237,11 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 
     auto begin_unit = [&](const Cursor &c) {
         const ChunkSeq &s = st.e[c.e];
-        hkv = c.h / s.S;
+        hkv = c.hkv;
         b = a.B0 + c.e;
         u = b * a.Hkv + hkv;
         cold_of(u, ncold, chead);
-        const int v0 = (c.h % s.S) * C::RB, vend = s.nq * a.g;
+        const int v0 = c.sl * C::RB, vend = s.nq * a.g;
         cnt_rows = min(C::RB, vend - v0);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
@@ -264,30 +290,29 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
             }
         ++uo;
     };
-    // New running maxima for the raw maxima mx (log2 units); the old sums and
-    // outputs are rescaled where one has grown.
+    // Scores whose largest (log2 units) are mx in this lane: the reference
+    // that weights are taken against moves up, and the sums and outputs are
+    // rescaled, only when one has grown by 2^GROW (weights stay below 2^GROW,
+    // far inside fp16; the common case is one vote and no exchange).
     auto rescale = [&](float (&mx)[NC][2]) {
         bool grew = false;
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                float v = mx[nc][x];
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                mx[nc][x] = fmaxf(m_run[nc][x], v);
-                grew |= mx[nc][x] > m_run[nc][x];
-            }
+            for (int x = 0; x < 2; ++x) grew |= mx[nc][x] > m_run[nc][x] + GROW;
         if (!__any_sync(0xffffffffu, grew)) return;
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc) {
             float al[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-                al[x] = mx[nc][x] > m_run[nc][x] ? ch_ex2(m_run[nc][x] - mx[nc][x]) : 1.0f;
+                float v = fmaxf(mx[nc][x], m_run[nc][x]);
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                al[x] = v > m_run[nc][x] ? ch_ex2(m_run[nc][x] - v) : 1.0f;
                 l_run[nc][x] *= al[x];
-                m_run[nc][x] = mx[nc][x];
+                m_run[nc][x] = v;
             }
 #pragma unroll
             for (int mt = 0; mt < NKT; ++mt) {
@@ -303,7 +328,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     int st_issue = 0;
     for (int k = 0; k < NST && ic.x < x1; ++k) {
         issue(ic, st_issue);
-        cursor_next(ic, a, st);
+        ic.next(a, st);
         st_issue = st_issue + 1 == NST ? 0 : st_issue + 1;
     }
     begin_unit(cc);
@@ -316,10 +341,10 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
         const ChunkSeq &s = st.e[cc.e];
         const int2 mt_ = meta[sg];
         uint8_t *stage = stg + sg * C::STAGE;
-        const bool fp = cc.off < s.Sf;
+        const bool fp = cc.off < cc.Sf;
         if (mt_.x > 0) {
             const bool wnd = a.window > 0;
-            const int k = fp ? 0 : (cc.off - s.Sf) % a.CPB;
+            const int k = cc.k;
             const int32_t *bi = a.bidx + ((size_t)u * a.NB + mt_.y) * a.G + CT * k;   // the chunk's token indices
             if (!fp && wnd && lane < 8) asm volatile("prefetch.global.L1 [%0];" ::"l"(bi + min(8 * lane, mt_.x - 1)));
             if (!mbar_wait(&bars[sg], (phase >> sg) & 1u)) {
@@ -504,17 +529,14 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         if (ic.x < x1) {
             issue(ic, sg);
-            cursor_next(ic, a, st);
+            ic.next(a, st);
             __syncwarp();
         }
-        const int e0 = cc.e, h0 = cc.h;
-        cursor_next(cc, a, st);
+        const bool other = cc.next(a, st);
         sg = sg + 1 == NST ? 0 : sg + 1;
-        if (cc.x >= x1) {
+        if (other || cc.x >= x1) {
             end_unit();
-        } else if (cc.e != e0 || cc.h != h0) {
-            end_unit();
-            begin_unit(cc);
+            if (cc.x < x1) begin_unit(cc);
         }
     }
 }

@@ -116,7 +116,9 @@ struct Magic {
 };
 __device__ __forceinline__ uint32_t ch_raw(const Magic &mg, uint32_t w, uint32_t w10, int p) {
     const int c = cls_of_pos(p);
-    return ((p < 5 ? w : w10) & (0x00030003u << (2 * c))) | mg.m[c];
+    uint32_t d;   // (w & mask) | magic, as one operation
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(p < 5 ? w : w10), "r"(0x00030003u << (2 * c)), "r"(mg.m[c]));
+    return d;
 }
 __device__ __forceinline__ uint32_t ch_const(int p, int less) {   // -(2^(10-2c) + less) in both halves
     const __half h = __float2half_rn(-(float)((1 << (10 - 2 * cls_of_pos(p))) + less));
