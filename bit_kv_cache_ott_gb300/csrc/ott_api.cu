@@ -345,7 +345,7 @@ int create_cache(int B, int Hq, int Hkv, int d, int G, int R, int P, int max_tok
     e = cudaMemset(mem, 0, c->mem_bytes);
     if (e == cudaSuccess) e = set_kernel_attributes(d, gs, smem_optin);
     if (e == cudaSuccess) e = set_topk_attributes(d, gs, smem_optin);
-    if (e == cudaSuccess) e = set_chunk_attributes(d);
+    if (e == cudaSuccess) e = set_chunk_attributes(d, smem_optin);
     if (e == cudaSuccess && c->paged) {
         // every pool slot free
         std::vector<int32_t> slots((size_t)pool_blocks);

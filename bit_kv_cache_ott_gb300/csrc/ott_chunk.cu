@@ -36,6 +36,7 @@ namespace {
 constexpr float GROW = 8.0f;                // log2: see rescale
 constexpr int FI = 8;                       // fp16 tokens per work item
 constexpr int CT = CHUNK_TILES * TILE;      // block slots per work item
+constexpr int DEC_ROWS_MAX = 4;             // query rows per kv head up to which the decode kernel serves a call
 constexpr int ROWS_MAX = 16;                // query rows per kv head up to which this kernel serves a call
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -691,7 +692,9 @@ cudaError_t rows_attribute() {
 struct Plan {
     ChunkArgs a;
     ChunkTable st;
-    int NC;       // groups of 8 rows, 0: tiles (ott_chunk_tiles.cu)
+    int NC;       // this file's kernel: groups of 8 rows; 0: another's
+    int gs;       // the decode kernel in rows mode: rows per slice; 0: tiles (ott_chunk_tiles.cu)
+    int ipb;      // work items per block
     int nC;       // tiles: CTAs
     bool sinks, any;
     size_t part_floats;
@@ -742,10 +745,21 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
     int nq_max = 0;
     for (int x = 0; x < a.nseq; ++x) nq_max = std::max(nq_max, call.lens ? call.lens[B0 + x] : call.n);
     const long long rows = (long long)nq_max * c->gq;
-    p.NC = rows <= 8 ? 1 : (rows <= ROWS_MAX ? 2 : 0);
-    const bool tiles = p.NC == 0;
-    const int RB = tiles ? 256 : 8 * p.NC;
-    a.RV = (int)std::min<long long>(RB, (long long)nq_max * c->gq);
+    p.gs = rows <= DEC_ROWS_MAX ? slice_heads((int)rows) : 0;
+    p.NC = p.gs ? 0 : (rows <= 8 ? 1 : (rows <= ROWS_MAX ? 2 : 0));
+    const bool tiles = p.gs == 0 && p.NC == 0;
+    const int RB = tiles ? 256 : (p.gs ? p.gs : 8 * p.NC);
+    a.RV = p.gs ? p.gs : (int)std::min<long long>(RB, (long long)nq_max * c->gq);
+    // decode kernel: whole blocks as items where there are fewer of them than
+    // warps (each item's fixed cost is then paid once per block)
+    long long blocks = 0;
+    for (int x = 0; p.gs && x < a.nseq; ++x) {
+        const int b = B0 + x, nq = call.lens ? call.lens[b] : call.n;
+        const long long T = c->ragged ? c->Tb[b] : c->T, seen = call.window > 0 ? std::min<long long>(T, call.window + nq) : T;
+        blocks += (seen / c->G + 1) * c->Hkv * ((nq * (long long)c->gq + RB - 1) / RB);
+    }
+    p.ipb = p.gs && blocks < (long long)c->sm_count * DEC_WARPS ? 1 : a.CPB;
+    const int fi = p.gs ? FP16_CHUNK : FI;
     long long base = 0, units = 0;
     int min_iu = INT_MAX;
     p.sinks = false;
@@ -771,8 +785,8 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
             s.jlo = std::min(s.nf, lo / c->G);
             s.nsink = std::min(a.sinks, s.jlo);
         }
-        s.Sf = (int)(((long long)s.ntail + s.npool + a.C + s.nnew + FI - 1) / FI);
-        const long long iu = s.Sf + (long long)(s.nf - s.jlo + s.nsink) * a.CPB;
+        s.Sf = (int)(((long long)s.ntail + s.npool + a.C + s.nnew + fi - 1) / fi);
+        const long long iu = s.Sf + (long long)(s.nf - s.jlo + s.nsink) * p.ipb;
         s.S = (int)(((long long)s.nq * c->gq + RB - 1) / RB);
         if (s.S == 0) continue;
         p.sinks |= s.nsink > 0;
@@ -798,10 +812,10 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
         p.part_floats = 0;
         return true;
     }
-    a.NWp = (int)std::min<long long>(a.W, (long long)c->sm_count * (p.NC == 1 ? 16 : 8));
+    a.NWp = (int)std::min<long long>(a.W, (long long)c->sm_count * (p.gs ? DEC_WARPS : p.NC == 1 ? 16 : 8));
     const long long L = (a.W + a.NWp - 1) / a.NWp;   // items of a warp's range, at most
     a.MAXU = (int)std::min<long long>(L, (L - 1) / min_iu + 2);
-    p.part_floats = (size_t)a.NWp * a.MAXU * a.RV * (c->d + 2);
+    p.part_floats = (size_t)a.NWp * a.MAXU * a.RV * (c->d + 2) * (p.gs ? 2 : 1);
     return true;
 }
 
@@ -811,6 +825,7 @@ cudaError_t launch_plan(const ott_cache *c, const Plan &p, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     if (p.sinks)
         e = launch_pdl(k_window_sinks, dim3((unsigned)(a.nseq * a.Hkv)), SINK_THREADS, 0, s, a, p.st, c->sel);
+    if (e == cudaSuccess && p.gs > 0) return launch_decode_rows(c, a, p.st, p.gs, p.ipb, s);
     if (e == cudaSuccess && p.NC == 0) return launch_tiles(c, a, p.st, p.nC, s);
     if (e == cudaSuccess)
         e = p.NC == 1 ? launch_rows<D, 1>(a, p.st, c->sm_count, s) : launch_rows<D, 2>(a, p.st, c->sm_count, s);
@@ -824,8 +839,10 @@ cudaError_t launch_plan(const ott_cache *c, const Plan &p, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t set_chunk_attributes(int d) {
-    const cudaError_t e = d == 128 ? rows_attribute<128, 1>() : rows_attribute<64, 1>();
+cudaError_t set_chunk_attributes(int d, int smem_max) {
+    cudaError_t e = set_decode_rows_attributes(d, smem_max);
+    if (e != cudaSuccess) return e;
+    e = d == 128 ? rows_attribute<128, 1>() : rows_attribute<64, 1>();
     if (e != cudaSuccess) return e;
     const cudaError_t e2 = d == 128 ? rows_attribute<128, 2>() : rows_attribute<64, 2>();
     return e2 == cudaSuccess ? set_tiles_attributes(d) : e2;

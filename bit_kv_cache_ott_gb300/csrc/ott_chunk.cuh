@@ -178,6 +178,9 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, int threads, size_t sm
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// ott_decode.cu: the decode kernel in rows mode, gs rows per slice
+cudaError_t launch_decode_rows(const ott_cache *c, const ChunkArgs &a, const ChunkTable &st, int gs, int ipb, cudaStream_t s);
+cudaError_t set_decode_rows_attributes(int d, int smem_max);
 // ott_chunk_tiles.cu
 cudaError_t set_tiles_attributes(int d);
 bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, size_t &part_floats);

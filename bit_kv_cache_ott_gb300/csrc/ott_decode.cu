@@ -31,9 +31,10 @@
 //     channels for P.V, fp32 accumulation, online softmax across chunks.
 #include <math_constants.h>
 
+#include <algorithm>
 #include <type_traits>
 
-#include "ott_internal.cuh"
+#include "ott_chunk.cuh"
 
 namespace ott {
 namespace {
@@ -162,7 +163,35 @@ struct DecodeArgs {
     // paged pool (ragged caches from ott_create_paged): block j of unit u is
     // pool slot bt[u*NB + j]; null otherwise
     const int32_t *bt;
+    // Rows mode (a chunk's few queries, a windowed query): a kv head's g
+    // "heads" are its g = n * gq query rows, row v = token * gq + head; new
+    // tokens follow the fp16 stores; a row sees the tokens that its position
+    // and window allow
+    const __half *knew, *vnew;   // [B][Hkv][n][d]
+    const int32_t *bidx, *pidx, *cidx;
+    int n, gq, B0, window, sinks;
 };
+
+// Rows mode: a unit as one of its lanes sees it. Lanes hold one score column
+// each, so one row's position and window start.
+struct RowsUnit {
+    const ChunkSeq *s;
+    int b, hkv, v0;   // sequence, kv head, first row of the slice
+    int pos, lo;      // of this lane's row
+};
+__device__ __forceinline__ RowsUnit rows_unit(const DecodeArgs &a, const ChunkTable &st, long long x, int GQ) {
+    RowsUnit r;
+    const int e = ch_entry_of(st, a.B, x);
+    r.s = &st.e[e];
+    const unsigned h = (unsigned)(x - r.s->base) / (unsigned)r.s->Iu;
+    r.b = a.B0 + e;
+    r.hkv = (int)(h / (unsigned)r.s->S);
+    r.v0 = (int)(h % (unsigned)r.s->S) * GQ;
+    const int v = min(r.v0 + (int)(threadIdx.x & 3u) % GQ, r.s->nq * a.gq - 1);
+    r.pos = r.s->pos0 + v / a.gq;
+    r.lo = a.window > 0 ? r.pos - a.window + 1 : 0;
+    return r;
+}
 
 template <int D, int GQ>
 struct Cfg {
@@ -182,8 +211,9 @@ struct Cfg {
 
 // Valid tokens of block j of unit u: fixed by (P, G, j) when displaced pool
 // tokens are written back, written by the flush under the cold-pool policy.
-template <bool CO>
+template <bool CO, bool MS = false>
 __device__ __forceinline__ int block_cnt(const DecodeArgs &a, int u, int j) {
+    if (MS && a.bcnt) return __ldg(a.bcnt + (size_t)u * a.NB + j);
     if constexpr (CO) return __ldg(a.bcnt + (size_t)u * a.NB + j);
     return j >= a.jfull ? a.G : block_count(a.P, a.G, j);
 }
@@ -217,8 +247,8 @@ __device__ __forceinline__ size_t part_slot(const DecodeArgs &a, int w, int unit
 // Per-sequence counts: scalars in DecodeArgs when every sequence has the
 // same length, a table (kernel parameter) when the batch is ragged.
 struct NoTable {};
-template <bool RG>
-using TableT = typename std::conditional<RG, SeqTable, NoTable>::type;
+template <bool RG, bool MS = false>
+using TableT = typename std::conditional<MS, ChunkTable, typename std::conditional<RG, SeqTable, NoTable>::type>::type;
 
 struct UnitInfo {
     long long ub;       // the unit's first work item
@@ -226,10 +256,20 @@ struct UnitInfo {
 };
 
 // The unit holding work item x (x < W), with its counts.
-template <bool RG>
-__device__ __forceinline__ UnitInfo unit_at(const DecodeArgs &a, const TableT<RG> &st, long long x) {
+template <bool RG, bool MS = false>
+__device__ __forceinline__ UnitInfo unit_at(const DecodeArgs &a, const TableT<RG, MS> &st, long long x) {
     UnitInfo r;
-    if constexpr (RG) {
+    if constexpr (MS) {
+        const ChunkSeq &e = st.e[ch_entry_of(st, a.B, x)];
+        const int h = (int)((unsigned)(x - e.base) / (unsigned)e.Iu);
+        r.u = e.ubase + h;
+        r.ub = e.base + (long long)h * e.Iu;
+        r.ntail = e.ntail;
+        r.npool = e.npool;
+        r.ring_start = e.ring_start;
+        r.Sf = e.Sf;
+        r.Iu = e.Iu;
+    } else if constexpr (RG) {
         int lo = 0, hi = a.B;   // e[lo].base <= x < e[hi].base
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -270,9 +310,15 @@ __device__ __forceinline__ void lds_words(const uint8_t *p, uint32_t (&w)[NW]) {
 
 // The GQ query heads of work unit u (a kv-head slice); heads of a padded
 // last slice repeat the kv head's last query head (their results are unused).
-template <int D, int GQ>
-__device__ void load_queries(const DecodeArgs &a, int u, float *qsm, int lane) {
-    if (a.S == 1 && a.g == GQ) {
+template <int D, int GQ, bool MS = false>
+__device__ void load_queries(const DecodeArgs &a, int u, float *qsm, int lane, const RowsUnit &ru) {
+    if constexpr (MS) {
+        for (int e = lane; e < GQ * D / 2; e += 32) {
+            const int v = min(ru.v0 + e / (D / 2), ru.s->nq * a.gq - 1);
+            reinterpret_cast<__half2 *>(qsm)[e] = reinterpret_cast<const __half2 *>(
+                a.q + (((size_t)ru.b * a.Hq + ru.hkv * a.gq + v % a.gq) * a.n + v / a.gq) * D)[e % (D / 2)];
+        }
+    } else if (a.S == 1 && a.g == GQ) {
         const int b = u / a.Hkv, hkv = u % a.Hkv;
         const __half2 *qp = reinterpret_cast<const __half2 *>(a.q + ((size_t)b * a.Hq + hkv * GQ) * D);
         for (int e = lane; e < GQ * D / 2; e += 32) reinterpret_cast<__half2 *>(qsm)[e] = qp[e];
@@ -300,10 +346,10 @@ __device__ void load_queries(const DecodeArgs &a, int u, float *qsm, int lane) {
 // tiles are all full (the common case: every block after the pool fills holds
 // G tokens) runs a body without any masking; the ragged last chunk of a short
 // block takes the masked body.
-template <int D, int GQ, bool CO, bool TK, bool RG>
+template <int D, int GQ, bool CO, bool TK, bool RG, bool MS>
 __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, int q0, int q1, uint8_t *stg0,
                               uint8_t *stg1, uint64_t *bars, uint32_t &phase, float *qsm, __half *qhl,
-                              int lane) {
+                              int lane, const RowsUnit &ru) {
     using C = Cfg<D, GQ>;
     constexpr int NKT = C::NKT, NW = C::NW, NG = C::NG, GPV = C::GPV, NV = C::NV;
     constexpr int KSZ = ksz_bytes(D), TB = tile_bytes(D);
@@ -311,7 +357,16 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
     const int r = lane >> 2, i = lane & 3;
 
     // tokens of the block at position j of the segment (0: no block there)
+    // rows mode: the listed blocks of the first tokens, then those of the window
+    auto block_of = [&](int j) -> int {
+        if (j >= ru.s->nsink) return ru.s->jlo + j - ru.s->nsink;
+        return __ldg(a.sel + (size_t)u * a.NB + j);
+    };
     auto cnt_at = [&](int j) -> int {
+        if constexpr (MS) {
+            const int bj = block_of(j);
+            return bj < 0 ? 0 : block_cnt<CO, true>(a, u, bj);
+        }
         if constexpr (TK) {
             const int bj = __ldg(a.sel + (size_t)u * a.Ksel + j);
             return bj < 0 ? 0 : block_cnt<CO>(a, u, bj);
@@ -352,9 +407,10 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
             const int vt = (c.cnt + TILE - 1) / TILE;
             const int t0 = c.k * CHUNK_TILES, nt = min(CHUNK_TILES, vt - t0);
             int bj = c.j;
+            if constexpr (MS) bj = block_of(c.j);
             if constexpr (TK) bj = __ldg(a.sel + (size_t)u * a.Ksel + c.j);
             size_t bslot = (size_t)u * a.NB + bj;
-            if constexpr (RG) {
+            if constexpr (RG || MS) {
                 if (a.bt) bslot = (size_t)__ldg(a.bt + bslot);
             }
             const uint8_t *bsrc = a.blk + bslot * a.blk_bytes;
@@ -381,7 +437,7 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
         advance(ic);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    load_queries<D, GQ>(a, uq, qsm, lane);
+    load_queries<D, GQ, MS>(a, uq, qsm, lane, ru);
 
     // Cooperative per-block constants: lane L handles channel pairs
     // (2L + 64m, 2L + 64m + 1); the channels' class scales stay in registers
@@ -442,6 +498,18 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
     int st = 0;
     while (!past(cc)) {
         uint8_t *stage = st ? stg1 : stg0;
+        // a window hides tokens by their indices: fetched under the wait
+        int tok[CHUNK_TILES][2];
+        if (MS && a.window > 0) {
+            const int32_t *bi = a.bidx + ((size_t)u * a.NB + block_of(cc.j)) * a.G + CT * cc.k;
+#pragma unroll
+            for (int tau = 0; tau < CHUNK_TILES; ++tau)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int x = 16 * tau + r + 8 * h;
+                    tok[tau][h] = x < cc.cnt - CT * cc.k ? __ldg(bi + x) : 0;
+                }
+        }
         if (!mbar_wait(&bars[st], (phase >> st) & 1u)) {
             if (lane == 0) atomicExch(&a.ctl[1], 1);
             // let the other copy in flight land before giving up the buffers
@@ -549,6 +617,11 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
                         const int slotk = 16 * (t0 + tau) + r;
                         if (slotk >= cj) sc[tau][0] = -CUDART_INF_F;
                         if (slotk + 8 >= cj) sc[tau][1] = -CUDART_INF_F;
+                    }
+                    if (MS && a.window > 0) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (!chunk_sees(tok[tau][h], ru.pos, ru.lo, a.sinks)) sc[tau][h] = -CUDART_INF_F;
                     }
                 }
             }
@@ -756,21 +829,22 @@ __device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1,
 // Under the cold-pool policy the fp16 tokens continue with the cold pool
 // (token f >= ntail + npool: its (f - ntail - npool)-th oldest entry); its
 // size is read on the device, and the host sizes the items for C entries.
-template <int D, int GQ, bool CO>
+template <int D, int GQ, bool CO, bool MS>
 __device__ bool fp16_segment(const DecodeArgs &a, const UnitInfo &ui, size_t slot, int u, int uq, int c0, int c1,
-                             uint8_t *stg0, uint8_t *stg1, uint64_t *bars, uint32_t &phase, float *qsm, int lane) {
+                             uint8_t *stg0, uint8_t *stg1, uint64_t *bars, uint32_t &phase, float *qsm, int lane,
+                             const RowsUnit &ru) {
     constexpr int NKT = D / 16;
     constexpr int RS = D + 8;                 // padded row stride (halves)
     constexpr int SUB = 8;                    // tokens per sub-tile
     const int r = lane >> 2, i = lane & 3;
     int ncold = 0, chead = 0;
-    if constexpr (CO) {
+    if constexpr (CO || MS) {
         if (a.C > 0) {
             ncold = __ldg(a.cmeta + 2 * u);
             chead = __ldg(a.cmeta + 2 * u + 1);
         }
     }
-    const int nhot = ui.ntail + ui.npool, nfp = nhot + ncold;
+    const int nhot = ui.ntail + ui.npool, nfp = nhot + ncold + (MS ? ru.s->nnew : 0);
     const int fb = c0 * FP16_CHUNK, fe = max(fb, min(c1 * FP16_CHUNK, nfp));
     const int nsub = (fe - fb + SUB - 1) / SUB;
 
@@ -781,7 +855,11 @@ __device__ bool fp16_segment(const DecodeArgs &a, const UnitInfo &ui, size_t slo
             if (s >= a.ring) s -= a.ring;
             return base + ((size_t)u * a.ring + s) * D;
         }
-        if constexpr (CO) {
+        if constexpr (MS) {
+            if (f >= nhot + ncold)
+                return (val ? a.vnew : a.knew) + (((size_t)ru.b * a.Hkv + ru.hkv) * a.n + (f - nhot - ncold)) * D;
+        }
+        if constexpr (CO || MS) {
             if (f >= nhot) {
                 int s = chead + (f - nhot);   // f - nhot < ncold <= C
                 if (s >= a.C) s -= a.C;
@@ -811,7 +889,7 @@ __device__ bool fp16_segment(const DecodeArgs &a, const UnitInfo &ui, size_t slo
         issue(k, st_issue);
         st_issue ^= 1;
     }
-    load_queries<D, GQ>(a, uq, qsm, lane);
+    load_queries<D, GQ, MS>(a, uq, qsm, lane, ru);
     // score B operand: column r = (head r/2, piece r&1); q is exact in fp16
     const int hB = r >> 1;
     uint32_t Bq[NKT][2];
@@ -852,6 +930,19 @@ __device__ bool fp16_segment(const DecodeArgs &a, const UnitInfo &ui, size_t slo
             mma16816(d, b0, 0u, b2, 0u, Bq[kt + 1][0], Bq[kt + 1][1]);
         }
         float lg = (r < nvalid && i < GQ) ? d[0] * a.sl2 : -CUDART_INF_F;
+        if constexpr (MS) {
+            const int f = fb + k * SUB + r;
+            if (r < nvalid && (a.window > 0 || f >= nhot + ncold)) {
+                int t = ru.s->T + f - nhot - ncold;   // a new token
+                if (f < ui.ntail)
+                    t = ru.s->T - ui.ntail + f;
+                else if (f < nhot)
+                    t = __ldg(a.pidx + (size_t)u * a.P + (f - ui.ntail));
+                else if (f < nhot + ncold)
+                    t = __ldg(a.cidx + (size_t)u * a.C + (chead + f - nhot) % a.C);
+                if (!chunk_sees(t, ru.pos, ru.lo, a.sinks)) lg = -CUDART_INF_F;
+            }
+        }
         float mloc = lg;
         mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 4));
         mloc = fmaxf(mloc, __shfl_xor_sync(0xffffffffu, mloc, 8));
@@ -904,8 +995,8 @@ __device__ bool fp16_segment(const DecodeArgs &a, const UnitInfo &ui, size_t slo
     return true;
 }
 
-template <int D, int GQ, bool RG, bool CO, bool TK>
-__global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_decode(DecodeArgs a, const __grid_constant__ TableT<RG> st) {
+template <int D, int GQ, bool RG, bool CO, bool TK, bool MS = false>
+__global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_decode(DecodeArgs a, const __grid_constant__ TableT<RG, MS> st) {
     using C = Cfg<D, GQ>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -931,31 +1022,42 @@ __global__ void __launch_bounds__(DEC_WARPS * 32, 1) k_decode(DecodeArgs a, cons
     if (gw >= a.NWp) return;
     // Top-K: launched as a programmatic dependent of the block selection;
     // the selected blocks are that grid's results
-    if constexpr (TK) asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (rows mode: launched behind whatever wrote the blocks and the list)
+    if constexpr (TK || MS) asm volatile("griddepcontrol.wait;" ::: "memory");
     long long x = range_start(a.W, a.NWp, gw);
     const long long x1 = range_start(a.W, a.NWp, gw + 1);
-    const int u_first = unit_at<RG>(a, st, x).u;
+    const int u_first = unit_at<RG, MS>(a, st, x).u;
     while (x < x1) {
-        const UnitInfo ui = unit_at<RG>(a, st, x);
+        const UnitInfo ui = unit_at<RG, MS>(a, st, x);
         const int u = ui.u;                           // work unit (kv-head slice)
-        const int ud = a.S == 1 ? u : u / a.S;        // its kv unit: the cache data
+        RowsUnit ru = {};
+        if constexpr (MS) ru = rows_unit(a, st, x, GQ);
+        const int ud = MS ? ru.b * a.Hkv + ru.hkv : a.S == 1 ? u : u / a.S;   // its kv unit: the cache data
         const long long ubase = ui.ub;
         const int off = (int)(x - ubase);
         if (off < ui.Sf) {
             const int end = (int)min(x1 - ubase, (long long)ui.Sf);
-            if (!fp16_segment<D, GQ, CO>(a, ui, part_slot(a, gw, u - u_first, 0), ud, u, off, end, stg0, stg1, bars,
-                                     phase, qsm, lane))
+            if (!fp16_segment<D, GQ, CO, MS>(a, ui, part_slot(a, gw, u - u_first, 0), ud, u, off, end, stg0, stg1,
+                                             bars, phase, qsm, lane, ru))
                 return;
             x = ubase + end;
         } else {
             const int end = (int)min(x1 - ubase, (long long)ui.Iu);
-            if (!quant_segment<D, GQ, CO, TK, RG>(a, part_slot(a, gw, u - u_first, 1), ud, u, off - ui.Sf, end - ui.Sf,
-                                      stg0, stg1, bars, phase, qsm, qhl, lane))
+            if (!quant_segment<D, GQ, CO, TK, RG, MS>(a, part_slot(a, gw, u - u_first, 1), ud, u, off - ui.Sf,
+                                                      end - ui.Sf, stg0, stg1, bars, phase, qsm, qhl, lane, ru))
                 return;
             x = ubase + end;
         }
     }
 }
+
+// Slices per kv head and first unit of a sequence, in rows mode.
+__device__ __forceinline__ int st_slices(const ChunkTable &st, int b) { return st.e[b].S; }
+__device__ __forceinline__ int st_units(const ChunkTable &st, int b) { return st.e[b].ubase; }
+template <typename T>
+__device__ __forceinline__ int st_slices(const T &, int) { return 0; }
+template <typename T>
+__device__ __forceinline__ int st_units(const T &, int) { return 0; }
 
 // Merge the partials of each (sequence, query head). A CTA of `cw` warps
 // serves one (b, hq): the candidate segments of its unit -- (warp, item type)
@@ -972,24 +1074,33 @@ constexpr int COMB_GRP = 8;     // candidate segments a warp loads at a time
 // CS > 1: the channels of a head are split over CS CTAs (each merges every
 // partial's max and sum, and its own D/CS channels), so that a batch with
 // few query heads still spreads its partials' loads over many SMs.
-template <int D, int GQ, bool RG, int CS>
-__global__ void __launch_bounds__(COMB_MAXW * 32) k_combine(DecodeArgs a, const __grid_constant__ TableT<RG> st) {
+template <int D, int GQ, bool RG, int CS, bool MS = false>
+__global__ void __launch_bounds__(COMB_MAXW * 32) k_combine(DecodeArgs a, const __grid_constant__ TableT<RG, MS> st) {
     constexpr int DC = D / CS, CPL = DC / 32, GRP = COMB_GRP;
     static_assert(CPL >= 1, "at least one channel per lane");
     __shared__ float red[COMB_MAXW][DC + 2];
     const int cw = blockDim.x >> 5, wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int bh = blockIdx.x / CS, cs = blockIdx.x % CS;
     // work unit of query head hq: kv head hq / g, slice (hq mod g) / GQ
-    const int b = bh / a.Hq, hq = bh % a.Hq, hkv = hq / a.g, hs = hq % a.g, h = hs % GQ;
-    const int uv = hkv * a.S + hs / GQ, u = b * a.Hkv * a.S + uv;
+    int b = bh / a.Hq, hq = bh % a.Hq, hkv = hq / a.g, hs = hq % a.g;
+    if constexpr (MS) {   // bh = (sequence of the launch, query head, token); hs = its row
+        b = bh / (a.Hq * a.n);
+        hq = bh / a.n % a.Hq;
+        hkv = hq / a.gq;
+        if (bh % a.n >= st.e[b].nq) return;
+        hs = bh % a.n * a.gq + hq % a.gq;
+    }
+    const int h = hs % GQ;
+    const int Sh = MS ? st_slices(st, b) : a.S;   // slices per kv head
+    const int uv = hkv * Sh + hs / GQ, u = MS ? st_units(st, b) + uv : b * a.Hkv * a.S + uv;
     const int ch0 = cs * DC + lane * CPL;   // this lane's first channel
     // The unit's items are [ub, ub + Sf) fp16 then [ub + Sf, ue) quantized; the
     // decode warps holding them are contiguous ranges [f0, f1] and [q0, q1].
     // Only the first of them can have started in an earlier unit.
     long long ub;
     int Iu, Sf;
-    if constexpr (RG) {
-        const SeqEntry &e = st.e[b];
+    if constexpr (RG || MS) {
+        const auto &e = st.e[b];
         ub = e.base + (long long)uv * e.Iu;
         Iu = e.Iu;
         Sf = e.Sf;
@@ -1003,7 +1114,7 @@ __global__ void __launch_bounds__(COMB_MAXW * 32) k_combine(DecodeArgs a, const 
     const int f1 = Sf > 0 ? warp_of(a.W, a.NWp, um - 1) : wa - 1;
     const int q0 = um < ue ? warp_of(a.W, a.NWp, um) : 0, q1 = um < ue ? warp_of(a.W, a.NWp, ue - 1) : -1;
     const int n0 = f1 - wa + 1, ncand = n0 + (q1 - q0 + 1);
-    const int uo_a = u - unit_at<RG>(a, st, range_start(a.W, a.NWp, wa)).u;   // unit offset within warp wa's slots
+    const int uo_a = u - unit_at<RG, MS>(a, st, range_start(a.W, a.NWp, wa)).u;   // unit offset within warp wa's slots
     // everything above depends on the arguments only; the partials are the
     // decode grid's results
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1075,6 +1186,10 @@ __global__ void __launch_bounds__(COMB_MAXW * 32) k_combine(DecodeArgs a, const 
         }
     }
     __half *o = a.out + ((size_t)b * a.Hq + hq) * D + ch0;
+    if constexpr (MS) {
+        o = a.out + ((size_t)a.B0 * a.Hq * a.n + bh) * D + ch0;
+        if (L == 0.0f) L = 1.0f;   // a policy has discarded every token of the window: zeros
+    }
     // one vector store per lane (out may be host memory)
     if constexpr (CPL == 1) {
         *o = __float2half_rn(acc[0] / L);
@@ -1280,7 +1395,90 @@ cudaError_t launch_decode_topk_t(const ott_cache *c, const __half *q, __half *ou
                         : launch_decode_t<D, GQ, false, false, true>(c, q, out, c->part, s, Kc);
 }
 
+// Rows mode (ott_chunk_attn with few rows, ott_decode_attn_window): the table
+// is laid out in slices of GQ rows.
+template <int D, int GQ>
+cudaError_t launch_rows_t(const ott_cache *c, const ChunkArgs &r, const ChunkTable &st, int ipb, cudaStream_t s) {
+    DecodeArgs a = {};
+    a.blk = r.blk;
+    a.blk_bytes = r.blk_bytes;
+    a.NB = r.NB;
+    a.rk = r.rk;
+    a.rv = r.rv;
+    a.ring = r.ring;
+    a.pk = r.pk;
+    a.pv = r.pv;
+    a.P = r.P;
+    a.q = r.q;
+    a.out = r.out;
+    a.part = r.part;
+    a.ctl = r.ctl;
+    a.Hq = r.Hq;
+    a.Hkv = r.Hkv;
+    a.G = r.G;
+    a.g = a.gq = r.g;
+    a.S = 1;
+    a.jfull = r.jfull;
+    a.CPB = r.CPB;
+    a.IPB = ipb;
+    a.W = r.W;
+    a.NWp = r.NWp;
+    a.MAXU = r.MAXU;
+    a.NSM = c->sm_count;
+    a.sl2 = r.sl2;
+    a.B = r.nseq;
+    a.bcnt = r.bcnt;
+    a.ck = r.ck;
+    a.cv = r.cv;
+    a.cmeta = r.cmeta;
+    a.C = r.C;
+    a.sel = r.sel;
+    a.bt = r.bt;
+    a.knew = r.k;
+    a.vnew = r.v;
+    a.bidx = r.bidx;
+    a.pidx = r.pidx;
+    a.cidx = r.cidx;
+    a.n = r.n;
+    a.B0 = r.B0;
+    a.window = r.window;
+    a.sinks = r.sinks;
+    const int wpc = (a.NWp + c->sm_count - 1) / c->sm_count;
+    cudaError_t e = launch_pdl(k_decode<D, GQ, false, false, false, true>, dim3((unsigned)c->sm_count), wpc * 32,
+                               (size_t)Cfg<D, GQ>::WARP_SMEM * wpc, s, a, st);
+    if (e != cudaSuccess) return e;
+    // about two rounds of partials per combine warp; few heads: channels split (as launch_combine)
+    const long long heads = (long long)a.B * a.Hq * a.n, units = st.e[a.B].ubase;
+    const long long per_unit_warps = (a.NWp + units - 1) / units + 1;
+    const int cw = (int)std::max<long long>(1, std::min<long long>((2 * per_unit_warps + 2 * COMB_GRP - 1) / (2 * COMB_GRP), COMB_MAXW));
+    const int cs = heads * 4 <= 2LL * a.NSM && D == 128 ? 4 : heads * 2 <= 2LL * a.NSM ? 2 : 1;
+    const dim3 grid((unsigned)(heads * cs));
+    if (cs == 4) return launch_pdl(k_combine<D, GQ, false, (D / 32 >= 4 ? 4 : 1), true>, grid, 32 * cw, 0, s, a, st);
+    if (cs == 2) return launch_pdl(k_combine<D, GQ, false, 2, true>, grid, 32 * cw, 0, s, a, st);
+    return launch_pdl(k_combine<D, GQ, false, 1, true>, grid, 32 * cw, 0, s, a, st);
+}
+
 }  // namespace
+
+cudaError_t launch_decode_rows(const ott_cache *c, const ChunkArgs &a, const ChunkTable &st, int gs, int ipb, cudaStream_t s) {
+#define OTT_ROWS(D_, G_) \
+    if (c->d == D_ && gs == G_) return launch_rows_t<D_, G_>(c, a, st, ipb, s);
+    OTT_ROWS(128, 1) OTT_ROWS(128, 2) OTT_ROWS(128, 4) OTT_ROWS(64, 1) OTT_ROWS(64, 2) OTT_ROWS(64, 4)
+#undef OTT_ROWS
+    return cudaErrorInvalidValue;
+}
+
+// Any query-row group: rows mode slices by the call's rows, not by the
+// cache's heads, so its kernels' attributes are set for every group size.
+cudaError_t set_decode_rows_attributes(int d, int smem_max) {
+    cudaError_t e = cudaSuccess;
+#define OTT_RATTR(D_, G_)                                                                                      \
+    if (e == cudaSuccess && d == D_)                                                                           \
+        e = cudaFuncSetAttribute(k_decode<D_, G_, false, false, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max);
+    OTT_RATTR(128, 1) OTT_RATTR(128, 2) OTT_RATTR(128, 4) OTT_RATTR(64, 1) OTT_RATTR(64, 2) OTT_RATTR(64, 4)
+#undef OTT_RATTR
+    return e;
+}
 
 bool decode_supported(int d) { return d == 64 || d == 128; }
 

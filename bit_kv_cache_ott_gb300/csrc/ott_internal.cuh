@@ -253,7 +253,7 @@ struct ChunkCall {
     const int *lens;   // null: n each
     int window, sinks;
 };
-cudaError_t set_chunk_attributes(int d);
+cudaError_t set_chunk_attributes(int d, int smem_max);
 int run_chunk(const ott_cache *c, const ChunkCall &call, cudaStream_t s, cudaError_t &err);
 // Append tokens [from[b], to[b]) of a chunk to the ring of every sequence
 // b0 .. b0 + nseq - 1 (chunk token x becomes token T_b + x).
