@@ -10,6 +10,7 @@ kernels. There is no CPU fallback: if the library is missing or cannot load,
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import torch
@@ -149,43 +150,70 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, sect
         raise ValueError("rope: q or k must be given")
     if any(not isinstance(t, torch.Tensor) or t.dim() != 4 for t in xs):
         raise ValueError("rope: expected [B][H][n][d] tensors")
-    B, n, d, dev = xs[0].shape[0], xs[0].shape[2], xs[0].shape[3], xs[0].device
-    sections = [int(x) for x in sections]
+    B, _, n, d = xs[0].shape
+    sections = tuple(int(x) for x in sections)
     if not 1 <= len(sections) <= 4:
         raise ValueError("rope: one to four axes")
     if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype != torch.int32:
         raise TypeError("pos: expected a CUDA int32 tensor")
     if tuple(pos.shape) != (len(sections), B, n) or not pos.is_contiguous():
         raise ValueError(f"pos: expected contiguous shape {(len(sections), B, n)}, got {tuple(pos.shape)}")
+    idx = xs[0].get_device()
     ptr, outs, heads = [], [], []
     for name, x, o in (("q", q, out_q), ("k", k, out_k)):
         if x is None:
             if o is not None:
                 raise ValueError(f"out_{name} without {name}")
-            ptr += [None, None]
+            ptr += (None, None)
             outs.append(None)
             heads.append(0)
             continue
-        shp = (B, x.shape[1], n, d)
-        p = _dev_ptr(x, shp, name)
-        o = torch.empty_like(x) if o is None else o
-        ptr += [p, _dev_ptr(o, shp, f"out_{name}")]
+        H = x.shape[1]
+        p = _dev_ptr(x, (B, H, n, d), name)
+        if o is None:
+            o = torch.empty_like(x)
+            ptr += (p, o.data_ptr())
+        else:
+            ptr += (p, _dev_ptr(o, (B, H, n, d), f"out_{name}"))
         outs.append(o)
-        heads.append(x.shape[1])
-    _same_device(dev, pos, *xs, *[o for o in outs if o is not None])
+        heads.append(H)
+    _same_device(idx, pos, *xs, *[o for o in outs if o is not None])
     if B == 0 or sum(heads) == 0 or n == 0:
         return tuple(outs)
-    plan = RopePlan(len(sections), (C.c_int * 4)(*sections), float(base), int(bool(interleaved)), int(bool(restart)))
-    with torch.cuda.device(dev):
-        _check(load().ott_rope(ptr[0], ptr[1], heads[0], ptr[2], ptr[3], heads[1], pos.data_ptr(), B, n, d,
-                               C.byref(plan), _stream(stream)), "ott_rope")
+    plan = _rope_plan(sections, float(base), bool(interleaved), bool(restart))
+    _on_device(idx, load().ott_rope, "ott_rope", ptr[0], ptr[1], heads[0], ptr[2], ptr[3], heads[1], pos.data_ptr(), B,
+               n, d, plan, _stream_of(stream, idx))
     return tuple(outs)
 
 
-def _same_device(dev, *tensors):
+@functools.lru_cache(maxsize=64)
+def _rope_plan(sections, base, interleaved, restart):
+    return C.byref(RopePlan(len(sections), (C.c_int * 4)(*sections), base, int(interleaved), int(restart)))
+
+
+def _same_device(idx, *tensors):
     for t in tensors:
-        if t.device != dev:
-            raise ValueError(f"tensors on {t.device} and {dev}")
+        if t.get_device() != idx:
+            raise ValueError(f"tensors on {t.device} and cuda:{idx}")
+
+
+def _stream_of(stream, idx: int) -> int:
+    """The raw stream to queue on: the given one, else device idx's current one."""
+    return (torch.cuda.current_stream(idx) if stream is None else stream).cuda_stream
+
+
+def _on_device(idx: int, fn, what: str, *args):
+    """fn(*args) with device idx current (a context manager per call costs more than most of these kernels)."""
+    prev = torch.cuda.current_device()
+    if prev == idx:
+        rc = fn(*args)
+    else:
+        torch.cuda.set_device(idx)
+        try:
+            rc = fn(*args)
+        finally:
+            torch.cuda.set_device(prev)
+    _check(rc, what)
 
 
 class OTTCache:
@@ -223,7 +251,7 @@ class OTTCache:
             _check(create(B, Hq, Hkv, d, G, R, P, max_tokens, C.byref(h)),
                    "ott_create_ragged" if ragged else "ott_create")
         self._h = h
-        self.device = torch.device("cuda", torch.cuda.current_device())
+        self._dev = torch.cuda.current_device()
 
     def close(self):
         if getattr(self, "_h", None) and self._h.value:
@@ -331,10 +359,9 @@ class OTTCache:
         if out is None:
             out = torch.empty_like(q)
         ptr.append(_dev_ptr(out, shp, "out"))
-        _same_device(self.device, q, k, v, out)
-        with torch.cuda.device(self.device):
-            _check(load().ott_chunk_attn(self._h, *ptr, n, self._lens(lens), int(window), int(sinks), _stream(stream)),
-                   "ott_chunk_attn")
+        _same_device(self._dev, q, k, v, out)
+        _on_device(self._dev, load().ott_chunk_attn, "ott_chunk_attn", self._h, *ptr, n, self._lens(lens), int(window),
+                   int(sinks), _stream_of(stream, self._dev))
         return out
 
     def append_chunk(self, k: torch.Tensor, v: torch.Tensor, lens=None, stream=None):
@@ -343,9 +370,9 @@ class OTTCache:
         n = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
         shp = (self.B, self.Hkv, n, self.d)
         ptr = [_dev_ptr(k, shp, "k"), _dev_ptr(v, shp, "v")]
-        _same_device(self.device, k, v)
-        with torch.cuda.device(self.device):
-            _check(load().ott_append_chunk(self._h, *ptr, n, self._lens(lens), _stream(stream)), "ott_append_chunk")
+        _same_device(self._dev, k, v)
+        _on_device(self._dev, load().ott_append_chunk, "ott_append_chunk", self._h, *ptr, n, self._lens(lens),
+                   _stream_of(stream, self._dev))
 
     def decode_attn_window(self, q: torch.Tensor, window: int, sinks: int = 0, out: torch.Tensor | None = None,
                            stream=None) -> torch.Tensor:
@@ -355,10 +382,9 @@ class OTTCache:
         if out is None:
             out = torch.empty_like(q)
         op = _dev_ptr(out, shp, "out")
-        _same_device(self.device, q, out)
-        with torch.cuda.device(self.device):
-            _check(load().ott_decode_attn_window(self._h, qp, op, int(window), int(sinks), _stream(stream)),
-                   "ott_decode_attn_window")
+        _same_device(self._dev, q, out)
+        _on_device(self._dev, load().ott_decode_attn_window, "ott_decode_attn_window", self._h, qp, op, int(window),
+                   int(sinks), _stream_of(stream, self._dev))
         return out
 
     def counts(self):

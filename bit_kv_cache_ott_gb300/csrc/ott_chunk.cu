@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
 // `sinks` tokens, ascending, into sel[u][0 .. nsink), -1 behind them. A
 // block's indices ascend, so its first one decides; a token lies in one
 // block at most, so there are at most `sinks` such blocks.
-constexpr int SINK_THREADS = 128;
+constexpr int SINK_THREADS = 256, SINK_PER = 4;   // blocks per thread and round, their loads in flight together
 __global__ void __launch_bounds__(SINK_THREADS)
     k_window_sinks(const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkTable st, int32_t *sel) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -649,25 +649,35 @@ __global__ void __launch_bounds__(SINK_THREADS)
     const int jlo = st.e[e].jlo, nsink = st.e[e].nsink;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (nsink == 0) return;
-    __shared__ int wcnt[SINK_THREADS / 32];
+    constexpr int NWARP = SINK_THREADS / 32;
+    __shared__ int wcnt[SINK_PER][NWARP];
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
     int32_t *out = sel + (size_t)u * a.NB;
     int found = 0;
-    for (int j0 = 0; j0 < jlo; j0 += SINK_THREADS) {
-        const int j = j0 + threadIdx.x;
-        const bool has = j < jlo && chunk_block_cnt(a, u, j) > 0 &&
-                         __ldg(a.bidx + ((size_t)u * a.NB + j) * a.G) < a.sinks;
-        const unsigned bal = __ballot_sync(0xffffffffu, has);
-        if (lane == 0) wcnt[wid] = __popc(bal);
-        __syncthreads();
-        int before = found, total = 0;
-        for (int x = 0; x < SINK_THREADS / 32; ++x) {
-            before += x < wid ? wcnt[x] : 0;
-            total += wcnt[x];
+    for (int j0 = 0; j0 < jlo; j0 += SINK_THREADS * SINK_PER) {
+        int first[SINK_PER];
+#pragma unroll
+        for (int y = 0; y < SINK_PER; ++y) {
+            const int j = j0 + y * SINK_THREADS + threadIdx.x;
+            first[y] = j < jlo && chunk_block_cnt(a, u, j) > 0 ? __ldg(a.bidx + ((size_t)u * a.NB + j) * a.G) : INT_MAX;
         }
-        const int at = before + __popc(bal & ((1u << lane) - 1u));
-        if (has && at < nsink) out[at] = j;
-        found += total;
+        unsigned bal[SINK_PER];
+#pragma unroll
+        for (int y = 0; y < SINK_PER; ++y) {
+            bal[y] = __ballot_sync(0xffffffffu, first[y] < a.sinks);
+            if (lane == 0) wcnt[y][wid] = __popc(bal[y]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < SINK_PER; ++y) {
+            int before = found;
+            for (int x = 0; x < NWARP; ++x) {
+                before += x < wid ? wcnt[y][x] : 0;
+                found += wcnt[y][x];
+            }
+            const int at = before + __popc(bal[y] & ((1u << lane) - 1u));
+            if (first[y] < a.sinks && at < nsink) out[at] = j0 + y * SINK_THREADS + threadIdx.x;
+        }
         __syncthreads();
     }
     for (int x = found + threadIdx.x; x < nsink; x += SINK_THREADS) out[x] = -1;
@@ -726,7 +736,7 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
     a.ctl = c->ctl;
     a.n = call.n;
     a.B0 = B0;
-    a.nseq = std::min(c->B - B0, RAGGED_MAX);
+    a.nseq = std::min(c->B - B0, CHUNK_SEQS);
     a.Hq = c->Hq;
     a.Hkv = c->Hkv;
     a.g = c->gq;
@@ -853,14 +863,14 @@ int run_chunk(const ott_cache *c, const ChunkCall &call, cudaStream_t s, cudaErr
     if ((long long)c->Hq * call.n > INT_MAX) return OTT_ERR_INVALID;
     Plan p;
     size_t need = 0;
-    for (int B0 = 0; B0 < c->B; B0 += RAGGED_MAX) {
+    for (int B0 = 0; B0 < c->B; B0 += CHUNK_SEQS) {
         if (!make_plan(c, call, B0, p)) return OTT_ERR_INVALID;
         need = std::max(need, p.part_floats);
     }
     if (need == 0) return OTT_OK;
     Scratch scr(c, need, s);
     if (!scr.ptr) return OTT_ERR_OOM;
-    for (int B0 = 0; B0 < c->B && err == cudaSuccess; B0 += RAGGED_MAX) {
+    for (int B0 = 0; B0 < c->B && err == cudaSuccess; B0 += CHUNK_SEQS) {
         make_plan(c, call, B0, p);
         if (!p.any) continue;
         p.a.part = static_cast<float *>(scr.ptr);

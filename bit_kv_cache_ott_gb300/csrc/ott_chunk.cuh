@@ -23,8 +23,11 @@ struct ChunkSeq {
     int ntail, npool, ring_start;
     int Sf, Iu;        // fp16 work items, all work items of a unit
 };
+// A kernel parameter: 64 sequences (4 KB) per launch; a table of 256 made
+// every launch of a small batch about a microsecond longer.
+constexpr int CHUNK_SEQS = 64;
 struct ChunkTable {
-    ChunkSeq e[RAGGED_MAX + 1];
+    ChunkSeq e[CHUNK_SEQS + 1];
 };
 
 struct ChunkArgs {

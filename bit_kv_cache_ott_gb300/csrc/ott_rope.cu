@@ -19,6 +19,7 @@
 // Measured on one GB300 (see the launch rule below for both sides).
 #include <climits>
 #include <cmath>
+#include <cstring>
 
 #include "ott_internal.cuh"
 
@@ -198,13 +199,30 @@ extern "C" int ott_rope(const void *q, void *q_out, int Hq, const void *k, void 
     a.half = half;
     a.interleaved = plan->interleaved != 0;
     a.tokens = (long long)B * n;
-    int i = 0;
-    for (int x = 0; x < plan->axes; ++x)
-        for (int j = 0; j < plan->sections[x]; ++j, ++i) {
-            const double e = plan->restart ? (double)j / plan->sections[x] : (double)i / half;
-            a.F[i] = (uint64_t)std::ldexp(std::pow(plan->base, -e) / 6.283185307179586476925, 64);
-            a.axis[i] = (uint8_t)x;
-        }
+    // a plan's frequencies: up to 128 powers, found once per thread and plan
+    struct Ladder {
+        ott_rope_plan plan;
+        bool set = false;
+        uint64_t F[ROPE_MAX_PAIRS];
+        uint8_t axis[ROPE_MAX_PAIRS];
+    };
+    static thread_local Ladder lad;
+    bool same = lad.set && lad.plan.axes == plan->axes && lad.plan.base == plan->base &&
+                (lad.plan.restart != 0) == (plan->restart != 0);
+    for (int x = 0; same && x < plan->axes; ++x) same = lad.plan.sections[x] == plan->sections[x];
+    if (!same) {
+        int i = 0;
+        for (int x = 0; x < plan->axes; ++x)
+            for (int j = 0; j < plan->sections[x]; ++j, ++i) {
+                const double e = plan->restart ? (double)j / plan->sections[x] : (double)i / half;
+                lad.F[i] = (uint64_t)std::ldexp(std::pow(plan->base, -e) / 6.283185307179586476925, 64);
+                lad.axis[i] = (uint8_t)x;
+            }
+        lad.plan = *plan;
+        lad.set = true;
+    }
+    std::memcpy(a.F, lad.F, sizeof(uint64_t) * half);
+    std::memcpy(a.axis, lad.axis, half);
     const bool vec = half % 8 == 0;
     a.rot_groups = vec ? half / 8 : half;
     a.groups = vec ? d / 16 : d / 2;
