@@ -646,6 +646,53 @@ int ott_decode_attn_window(ott_cache *c, const void *q, void *out, int window, i
     return chunk_call(c, call, stream);
 }
 
+namespace {
+
+// Every flush that n more tokens make due on a uniform batch, in one pass.
+// False: no scratch to be had (or a CUDA error, which poisons the handle).
+bool chunk_pass(ott_cache *c, const __half *k, const __half *v, int n, int take, int u0, int nu, cudaStream_t s) {
+    const int m = flushes_after(c, c->T + take) - c->nf;
+    void *scratch = stream_alloc(c->device, chunk_flush_bytes(c, nu, c->nf, m), s);
+    if (!scratch) return false;
+    c->blocks_settled = 0;
+    cudaError_t e = launch_chunk_flushes(c, k, v, n, u0, nu, c->T, c->nf, m, static_cast<uint64_t *>(scratch), s);
+    const cudaError_t e2 = cudaFreeAsync(scratch, s);
+    if (e == cudaSuccess) e = e2;
+    return fail_cuda(c, e) == OTT_OK;
+}
+
+// After the flushes of a chunk: the tokens that no flush has taken, into the
+// rings (behind the flushes, which may still read the slots they go to), and
+// the counts.
+int chunk_tail(ott_cache *c, const __half *k, const __half *v, int n, const int *lens, cudaStream_t s) {
+    for (int b0 = 0; b0 < c->B; b0 += RAGGED_MAX) {
+        ChunkRange r;
+        r.n = std::min(c->B - b0, RAGGED_MAX);
+        for (int x = 0; x < r.n; ++x) {
+            const int b = b0 + x, m = lens ? lens[b] : n;
+            const long long T = seq_tokens(c, b), first = (long long)flushes_after(c, T + m) * c->G;
+            r.from[x] = (int)std::min<long long>(m, std::max(0LL, first - T));
+            r.to[x] = m;
+            r.slot[x] = (int)(T % c->ring);
+        }
+        const cudaError_t e = launch_append_range(c, k, v, n, b0, r, s);
+        if (e != cudaSuccess) return fail_cuda(c, e);
+    }
+    if (c->ragged) {
+        for (int b = 0; b < c->B; ++b) {
+            c->Tb[b] += lens ? lens[b] : n;
+            c->nfb[b] = flushes_after(c, c->Tb[b]);
+        }
+        refresh_T(c);
+    } else {
+        c->T += n;
+        c->nf = flushes_after(c, c->T);
+    }
+    return OTT_OK;
+}
+
+}  // namespace
+
 int ott_append_chunk(ott_cache *c, const void *k, const void *v, int n, const int *lens, void *stream) {
     if (!c) return OTT_ERR_INVALID;
     if (const int rc = chunk_state(c, lens)) return rc;
@@ -668,6 +715,53 @@ int ott_append_chunk(ott_cache *c, const void *k, const void *v, int n, const in
     c->free_blocks -= blocks_needed(c, unit_flushes);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const __half *kh = static_cast<const __half *>(k), *vh = static_cast<const __half *>(v);
+    // Two flushes or more: all of them in one pass where that is faster than
+    // a round of launches each. A pass covers the whole uniform batch, or one
+    // sequence (five launches, about 25 us); a round covers every sequence (a
+    // copy and a flush, about 17 us while its units fit the SMs). A prompt of
+    // 8192 tokens in chunks of 1024, 8 units: 1.08 ms of appends in rounds,
+    // 0.33 ms in passes.
+    {
+        int most = 0, active = 0;
+        bool ok = true;
+        for (int b = 0; b < (c->ragged ? c->B : 1); ++b) {
+            const int nf = c->ragged ? c->nfb[b] : c->nf;
+            const int m = flushes_after(c, seq_tokens(c, b) + (lens ? lens[b] : n)) - nf;
+            most = std::max(most, m);
+            active += m > 0;
+            ok = ok && chunk_flushes_ok(c, nf);
+        }
+        if (ok && most >= 2 && (!c->ragged || (2 * most >= 3 * active && c->U < c->sm_count))) {
+            bool done = true;
+            if (!c->ragged) {
+                done = chunk_pass(c, kh, vh, n, n, 0, c->U, s);
+            } else {
+                // all scratch before the first pass: a pass that cannot be had leaves the rounds to do everything
+                size_t bytes = 0;
+                for (int b = 0; b < c->B; ++b) {
+                    const int m = flushes_after(c, c->Tb[b] + (lens ? lens[b] : n)) - c->nfb[b];
+                    if (m > 0) bytes = std::max(bytes, chunk_flush_bytes(c, c->Hkv, c->nfb[b], m));
+                }
+                void *scratch = stream_alloc(c->device, bytes, s);
+                done = scratch != nullptr;
+                cudaError_t e = cudaSuccess;
+                for (int b = 0; done && e == cudaSuccess && b < c->B; ++b) {
+                    const int m = flushes_after(c, c->Tb[b] + (lens ? lens[b] : n)) - c->nfb[b];
+                    if (m > 0)
+                        e = launch_chunk_flushes(c, kh, vh, n, b * c->Hkv, c->Hkv, c->Tb[b], c->nfb[b], m,
+                                                 static_cast<uint64_t *>(scratch), s);
+                }
+                if (done) {
+                    const cudaError_t e2 = cudaFreeAsync(scratch, s);
+                    if (e == cudaSuccess) e = e2;
+                    c->blocks_settled = 0;
+                    if (e != cudaSuccess) return fail_cuda(c, e);
+                }
+            }
+            if (c->poisoned) return OTT_ERR_CUDA;
+            if (done) return chunk_tail(c, kh, vh, n, lens, s);
+        }
+    }
     // Rounds: fill every ring up to its next flush (or the chunk's end), then
     // flush the sequences that are full; the ring holds G + R tokens, exactly
     // what a flush waits for. The host's counts move with what is queued.

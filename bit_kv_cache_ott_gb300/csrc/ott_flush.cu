@@ -134,6 +134,35 @@ __device__ __forceinline__ uint32_t half2_bits(__half a, __half b) {
     return (uint32_t)__half_as_ushort(a) | ((uint32_t)__half_as_ushort(b) << 16);
 }
 
+// The flushes of a chunk appended to units that hold T tokens: groups j0,
+// j0 + 1 .. at once, as a prompt's. Tokens before T lie in the ring, the
+// others in the chunk (the source, its first row token T); the pool that the
+// units had (off = 1; none at off = 0) is the first list of the pool history
+// and its rows are copied aside, since the last group writes the new pool.
+struct ChunkFlushes {
+    int lists;                    // lists per unit: off + groups; 0: a prompt
+    int off, j0, ring;
+    long long T, t_first;         // t_first: first token of group j0
+    const __half *rk, *rv;        // [U][ring][d]
+    const uint64_t *gtop;         // [nu][lists][P] each list's keys
+    const __half *pk, *pv;        // [nu][P][d] the old pool's rows
+};
+// Where token t of unit u (the uu-th of the pass) lies; `key` is its (norm, index).
+template <int D>
+__device__ __forceinline__ const __half *chunk_flush_row(const ChunkFlushes &c, const __half *src, bool val, int u, int uu,
+                                                         int P, int np, uint64_t key, long long t) {
+    if (t >= c.T) return src + (size_t)(t - c.T) * D;
+    if (t >= c.t_first) return (val ? c.rv : c.rk) + ((size_t)u * c.ring + (size_t)(t % c.ring)) * D;
+    const uint64_t *list = c.gtop + (size_t)uu * c.lists * P;   // the old pool: rows in the order of its keys
+    int lo = 0, hi = np - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (list[mid] < key) lo = mid + 1;
+        else hi = mid;
+    }
+    return (val ? c.pv : c.pk) + ((size_t)uu * P + lo) * D;
+}
+
 struct FlushArgs {
     uint8_t *blk;
     int32_t *bidx;
@@ -155,8 +184,9 @@ struct FlushArgs {
     // launch (CTA i: unit pf_u0 + i / pf_nf, group i % pf_nf); the pool
     // before group j is read from the pool history (keys of the pool after
     // flush j - 1, ascending) and its rows from the prefill source
-    const uint64_t *phist;       // [nu][pf_nf][P], or null
+    const uint64_t *phist;       // [nu][lists][P], or null
     int pf_nf, pf_u0;
+    ChunkFlushes cf;             // a chunk's flushes (lists > 0), else a prompt's
     int src_u0;                  // the source holds units src_u0, src_u0 + 1, ...
     long long src_unit_stride;   // elements between units in the source
     long long src_mod;           // slot = token mod src_mod
@@ -185,9 +215,15 @@ __global__ void __launch_bounds__(FLUSH_THREADS, 2) k_flush(FlushArgs a, const _
     const uint64_t *ph = nullptr;      // parallel prefill: the pool before this group
     if (a.phist) {
         u = a.pf_u0 + blockIdx.x / a.pf_nf;
-        jj = blockIdx.x % a.pf_nf;
+        const int x = blockIdx.x % a.pf_nf;
+        if (a.cf.lists > 0) {
+            jj = a.cf.j0 + x;
+            if (x + a.cf.off > 0) ph = a.phist + ((size_t)(u - a.pf_u0) * a.cf.lists + x + a.cf.off - 1) * a.P;
+        } else {
+            jj = x;
+            if (jj > 0) ph = a.phist + ((size_t)(u - a.pf_u0) * a.pf_nf + (jj - 1)) * a.P;
+        }
         t0 = (long long)jj * a.G;
-        if (jj > 0) ph = a.phist + ((size_t)(u - a.pf_u0) * a.pf_nf + (jj - 1)) * a.P;
     } else if (fl.n > 0) {
         const int e = blockIdx.x / a.Hkv;
         u = fl.lb[e] * a.Hkv + blockIdx.x % a.Hkv;
@@ -231,7 +267,13 @@ __global__ void __launch_bounds__(FLUSH_THREADS, 2) k_flush(FlushArgs a, const _
         for (int e = tid; e < nc * VPR; e += nth) {
             const int row = e / VPR, v8 = e % VPR;
             const __half *sk, *sv;
-            if (row < np0 && !ph) {
+            if (a.cf.lists > 0) {
+                const uint64_t key0 = row < np0 ? ph[row] : 0;
+                const long long t = row < np0 ? (long long)(uint32_t)key0 : t0 + (row - np0);
+                const int np = min(P, a.cf.j0 * G);
+                sk = chunk_flush_row<D>(a.cf, srcK, false, u, u - a.pf_u0, P, np, key0, t);
+                sv = chunk_flush_row<D>(a.cf, srcV, true, u, u - a.pf_u0, P, np, key0, t);
+            } else if (row < np0 && !ph) {
                 const size_t off = ((size_t)u * P + row) * D;
                 sk = a.pk + off;
                 sv = a.pv + off;
@@ -391,7 +433,7 @@ __global__ void __launch_bounds__(FLUSH_THREADS, 2) k_flush(FlushArgs a, const _
     }
     // 5. the new pool (old pool rows are already staged in shared memory);
     // a parallel prefill keeps only the last group's
-    const bool write_pool = !a.phist || jj == a.pf_nf - 1;
+    const bool write_pool = !a.phist || (int)(blockIdx.x % a.pf_nf) == a.pf_nf - 1;
     {
         uint4 *pk_u = reinterpret_cast<uint4 *>(a.pk + (size_t)u * P * D);
         uint4 *pv_u = reinterpret_cast<uint4 *>(a.pv + (size_t)u * P * D);
@@ -585,7 +627,7 @@ inline size_t pf_group_smem_bytes(int d, int G) { return (size_t)G * (d + 8) * 2
 template <int D>
 __global__ void __launch_bounds__(PF_THREADS) k_pf_group(const __half *__restrict__ srcK, long long src_unit_stride,
                                                          int src_u0, int u0, int nf, int G, int P,
-                                                         uint64_t *__restrict__ gtop) {
+                                                         uint64_t *__restrict__ gtop, const ChunkFlushes cf) {
     // the group's keys, staged by coalesced asynchronous copies into rows
     // padded to D + 8 halves (each thread then reads its own row without
     // bank conflicts), and the group's (norm, index) keys
@@ -594,11 +636,13 @@ __global__ void __launch_bounds__(PF_THREADS) k_pf_group(const __half *__restric
     __half *rows = reinterpret_cast<__half *>(pf_sm);
     uint64_t *gkey = reinterpret_cast<uint64_t *>(pf_sm + (size_t)G * RS * 2);   // [G]
     const int uu = blockIdx.x / nf, j = blockIdx.x % nf, u = u0 + uu;
-    const long long t0 = (long long)j * G;
-    const __half *base = srcK + (size_t)(u - src_u0) * src_unit_stride + (size_t)t0 * D;
+    const long long t0 = cf.t_first + (long long)j * G;
+    const __half *unit = srcK + (size_t)(u - src_u0) * src_unit_stride;   // its row 0 is token T (a prompt: 0)
     for (int e = threadIdx.x; e < G * VPR; e += blockDim.x) {
         const int r = e / VPR, v8 = e % VPR;
-        cp_async16(rows + (size_t)r * RS + 8 * v8, base + (size_t)r * D + 8 * v8);
+        const long long t = t0 + r;
+        const __half *p = t >= cf.T ? unit + (size_t)(t - cf.T) * D : cf.rk + ((size_t)u * cf.ring + (size_t)(t % cf.ring)) * D;
+        cp_async16(rows + (size_t)r * RS + 8 * v8, p + 8 * v8);
     }
     cp_async_wait_all();
     __syncthreads();
@@ -619,7 +663,7 @@ __global__ void __launch_bounds__(PF_THREADS) k_pf_group(const __half *__restric
     }
     __syncthreads();
     const int nb = min(P, G);
-    uint64_t *dst = gtop + ((size_t)uu * nf + j) * P;
+    uint64_t *dst = gtop + ((size_t)uu * (cf.lists > 0 ? cf.lists : nf) + cf.off + j) * P;
     for (int t = threadIdx.x; t < G; t += blockDim.x) {
         const uint64_t k = gkey[t];
         int r = 0;
@@ -628,6 +672,22 @@ __global__ void __launch_bounds__(PF_THREADS) k_pf_group(const __half *__restric
     }
 }
 
+
+// The old pool of every unit of a chunk's flushes: its keys into list 0, its
+// rows aside. One CTA per unit.
+__global__ void __launch_bounds__(PF_THREADS) k_cf_pool(const float *__restrict__ pnorm, const int32_t *__restrict__ pidx,
+                                                        const uint4 *__restrict__ pk, const uint4 *__restrict__ pv, int u0,
+                                                        int P, int np, int vpr, uint64_t *__restrict__ gtop, int lists,
+                                                        uint4 *__restrict__ dk, uint4 *__restrict__ dv) {
+    const int uu = blockIdx.x, u = u0 + uu;
+    for (int k = threadIdx.x; k < np; k += blockDim.x)
+        gtop[(size_t)uu * lists * P + k] =
+            ((uint64_t)__float_as_uint(pnorm[(size_t)u * P + k]) << 32) | (uint32_t)pidx[(size_t)u * P + k];
+    for (int e = threadIdx.x; e < np * vpr; e += blockDim.x) {
+        dk[(size_t)uu * P * vpr + e] = pk[(size_t)u * P * vpr + e];
+        dv[(size_t)uu * P * vpr + e] = pv[(size_t)u * P * vpr + e];
+    }
+}
 
 // Outputs [k0, k1) (0-based, k1 <= na + nb) of the merge of the ascending
 // lists A (na keys) and B (nb keys), all keys distinct, through emit(k, key):
@@ -1090,6 +1150,7 @@ FlushArgs flush_args(const ott_cache *c, const __half *srcK, const __half *srcV,
     a.phist = nullptr;
     a.pf_nf = 0;
     a.pf_u0 = 0;
+    a.cf = ChunkFlushes{};
     a.src_unit_stride = src_unit_stride;
     a.src_mod = src_mod;
     a.t0 = t0;
@@ -1148,6 +1209,10 @@ static int scan_chunks(const ott_cache *c, int nu, int nf) {
     return C < 1 ? 1 : (int)C;
 }
 
+// nl lists per unit in the pool history (the groups', after the old pool's
+// for a chunk).
+static cudaError_t run_pf_scan(const ott_cache *c, const uint64_t *gtop, uint64_t *phist, int nu, int nl, cudaStream_t s);
+
 cudaError_t launch_prefill_parallel(const ott_cache *c, const __half *srcK, const __half *srcV,
                                     long long src_unit_stride, int src_u0, int u0, int nu, int nf,
                                     uint64_t *scratch, cudaStream_t s) {
@@ -1160,35 +1225,14 @@ cudaError_t launch_prefill_parallel(const ott_cache *c, const __half *srcK, cons
     if (P > 0) {   // with no pool every block is its own group: pass 3 alone
     if (c->d == 128)
         k_pf_group<128><<<(int)groups, PF_THREADS, pf_group_smem_bytes(128, G), s>>>(
-            srcK, src_unit_stride, src_u0, u0, nf, G, P, gtop);
+            srcK, src_unit_stride, src_u0, u0, nf, G, P, gtop, ChunkFlushes{});
     else
         k_pf_group<64><<<(int)groups, PF_THREADS, pf_group_smem_bytes(64, G), s>>>(
-            srcK, src_unit_stride, src_u0, u0, nf, G, P, gtop);
+            srcK, src_unit_stride, src_u0, u0, nf, G, P, gtop, ChunkFlushes{});
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    // C chunks per unit, one CTA each; a warp per 4 groups of a chunk (fewer,
-    // smaller CTAs cover the SMs in one wave), at most SCAN_WARPS, within
-    // the shared memory
-    int optin = 0;
-    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, c->device);
+    e = run_pf_scan(c, gtop, phist, nu, nf, s);
     if (e != cudaSuccess) return e;
-    const int C = scan_chunks(c, nu, nf), cg = (nf + C - 1) / C;
-    uint64_t *gtot = C > 1 ? phist + (size_t)nu * nf * P : nullptr;
-    int sw = (cg + 4 - 1) / 4;
-    sw = sw < 1 ? 1 : (sw > SCAN_WARPS ? SCAN_WARPS : sw);
-    while (sw > 1 && scan_smem_bytes(sw, P) > (size_t)optin) --sw;
-    k_pf_scan<<<nu * C, 32 * sw, scan_smem_bytes(sw, P), s>>>(gtop, phist, nf, G, P, cg, C, gtot);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    if (C > 1) {
-        int cw = cg < SCAN_WARPS ? cg : SCAN_WARPS;
-        const size_t room = (size_t)optin - sizeof(int) * 2 * CARRY_MAX_CHUNKS;   // after the static counts
-        while (cw > 1 && carry_smem_bytes(C, cw, P) > room) --cw;
-        if (carry_smem_bytes(C, cw, P) > room) return cudaErrorInvalidValue;
-        k_pf_carry<<<nu * (C - 1), 32 * cw, carry_smem_bytes(C, cw, P), s>>>(phist, gtot, nf, G, P, cg, C);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-    }
     }
     FlushArgs a = flush_args(c, srcK, srcV, src_unit_stride, LLONG_MAX, 0, 0);
     a.src_u0 = src_u0;
@@ -1198,6 +1242,96 @@ cudaError_t launch_prefill_parallel(const ott_cache *c, const __half *srcK, cons
     FlushList none;
     none.n = 0;
     return run_flush(c, a, none, (int)groups, s);
+}
+
+static cudaError_t run_pf_scan(const ott_cache *c, const uint64_t *gtop, uint64_t *phist, int nu, int nl, cudaStream_t s) {
+    const int G = c->G, P = c->P;
+    cudaError_t e = cudaSuccess;
+    // C chunks per unit, one CTA each; a warp per 4 groups of a chunk (fewer,
+    // smaller CTAs cover the SMs in one wave), at most SCAN_WARPS, within
+    // the shared memory
+    int optin = 0;
+    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, c->device);
+    if (e != cudaSuccess) return e;
+    const int C = scan_chunks(c, nu, nl), cg = (nl + C - 1) / C;
+    uint64_t *gtot = C > 1 ? phist + (size_t)nu * nl * P : nullptr;
+    int sw = (cg + 4 - 1) / 4;
+    sw = sw < 1 ? 1 : (sw > SCAN_WARPS ? SCAN_WARPS : sw);
+    while (sw > 1 && scan_smem_bytes(sw, P) > (size_t)optin) --sw;
+    k_pf_scan<<<nu * C, 32 * sw, scan_smem_bytes(sw, P), s>>>(gtop, phist, nl, G, P, cg, C, gtot);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    if (C > 1) {
+        int cw = cg < SCAN_WARPS ? cg : SCAN_WARPS;
+        const size_t room = (size_t)optin - sizeof(int) * 2 * CARRY_MAX_CHUNKS;   // after the static counts
+        while (cw > 1 && carry_smem_bytes(C, cw, P) > room) --cw;
+        if (carry_smem_bytes(C, cw, P) > room) return cudaErrorInvalidValue;
+        k_pf_carry<<<nu * (C - 1), 32 * cw, carry_smem_bytes(C, cw, P), s>>>(phist, gtot, nl, G, P, cg, C);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
+}
+
+// A chunk's flushes in one pass: the norm criterion, and a pool that the
+// first group's list can stand beside (each list holds min(P, G) keys, and
+// the old pool is full from the first flush on if P <= G).
+bool chunk_flushes_ok(const ott_cache *c, int nf_old) {
+    return c->cold < 0 && c->pct < 0 && (nf_old == 0 || c->P <= c->G);
+}
+
+size_t chunk_flush_bytes(const ott_cache *c, int nu, int nf_old, int groups) {
+    const int off = nf_old > 0 && c->P > 0;
+    return prefill_scratch_bytes(c, nu, groups + off) + (off ? (size_t)2 * nu * c->P * c->d * 2 : 0) + 32;
+}
+
+// Flushes [j0, j0 + groups) of units [u0, u0 + nu) with T tokens, the chunk's
+// rows at k, v [unit][n][d] (unit 0 first).
+cudaError_t launch_chunk_flushes(const ott_cache *c, const __half *k, const __half *v, int n, int u0, int nu, long long T,
+                                 int j0, int groups, uint64_t *scratch, cudaStream_t s) {
+    const int G = c->G, P = c->P, off = j0 > 0 && P > 0, nl = groups + off;
+    uint64_t *gtop = scratch, *phist = scratch + (size_t)nu * nl * P;
+    const long long ctas = (long long)nu * groups;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    // the old pool's rows: behind the lists and the scan's totals
+    uint4 *rows = reinterpret_cast<uint4 *>((reinterpret_cast<uintptr_t>(scratch) + prefill_scratch_bytes(c, nu, nl) + 15) & ~(uintptr_t)15);
+    ChunkFlushes cf = {};
+    cf.lists = nl;
+    cf.off = off;
+    cf.j0 = j0;
+    cf.ring = c->ring;
+    cf.T = T;
+    cf.t_first = (long long)j0 * G;
+    cf.rk = c->rk;
+    cf.rv = c->rv;
+    cf.gtop = gtop;
+    cf.pk = reinterpret_cast<const __half *>(rows);
+    cf.pv = cf.pk + (size_t)nu * P * c->d;
+    cudaError_t e = cudaSuccess;
+    if (P > 0) {
+        const int vpr = c->d / 8;
+        if (off)
+            k_cf_pool<<<nu, PF_THREADS, 0, s>>>(c->pnorm, c->pidx, reinterpret_cast<const uint4 *>(c->pk),
+                                                reinterpret_cast<const uint4 *>(c->pv), u0, P, pool_after(P, G, j0), vpr, gtop,
+                                                nl, rows, rows + (size_t)nu * P * vpr);
+        if (c->d == 128)
+            k_pf_group<128><<<(int)ctas, PF_THREADS, pf_group_smem_bytes(128, G), s>>>(k, (long long)n * 128, 0, u0, groups, G,
+                                                                                       P, gtop, cf);
+        else
+            k_pf_group<64><<<(int)ctas, PF_THREADS, pf_group_smem_bytes(64, G), s>>>(k, (long long)n * 64, 0, u0, groups, G, P,
+                                                                                     gtop, cf);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = run_pf_scan(c, gtop, phist, nu, nl, s);
+        if (e != cudaSuccess) return e;
+    }
+    FlushArgs a = flush_args(c, k, v, (long long)n * c->d, LLONG_MAX, 0, 0);
+    a.phist = phist;
+    a.pf_nf = groups;
+    a.pf_u0 = u0;
+    a.cf = cf;
+    FlushList none;
+    none.n = 0;
+    return run_flush(c, a, none, (int)ctas, s);
 }
 
 size_t prefill_scratch_bytes(const ott_cache *c, int nu, int nf) {

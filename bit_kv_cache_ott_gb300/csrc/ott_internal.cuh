@@ -232,6 +232,11 @@ size_t prefill_scratch_bytes(const ott_cache *c, int nu, int nf);
 cudaError_t launch_prefill_parallel(const ott_cache *c, const __half *srcK, const __half *srcV,
                                     long long src_unit_stride, int src_u0, int u0, int nu, int nf,
                                     uint64_t *scratch, cudaStream_t s);
+// The same for a chunk appended to units that hold T tokens.
+bool chunk_flushes_ok(const ott_cache *c, int nf_old);
+size_t chunk_flush_bytes(const ott_cache *c, int nu, int nf_old, int groups);
+cudaError_t launch_chunk_flushes(const ott_cache *c, const __half *k, const __half *v, int n, int u0, int nu, long long T,
+                                 int j0, int groups, uint64_t *scratch, cudaStream_t s);
 cudaError_t launch_decode(const ott_cache *c, const __half *q, __half *out, cudaStream_t s);
 cudaError_t launch_decode_topk(const ott_cache *c, const __half *q, __half *out, int Kc, cudaStream_t s);
 cudaError_t launch_topk_select(const ott_cache *c, const __half *q, int K, int Kc, cudaStream_t s);

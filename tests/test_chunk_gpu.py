@@ -134,6 +134,12 @@ def test_more_sequences_than_one_launch_takes(ott):
     ("uniform", 2, 2, 1, 64, 16, 0, 9, 47, 1),          # the last token that a flush waits for
     ("uniform", 2, 2, 1, 64, 16, 0, 9, 47, 2),
     ("ragged", 4, 2, 2, 64, 16, 3, 5, [0, 1, 37, 200], [70, 0, 1, 33]),
+    ("uniform", 1, 2, 2, 64, 16, 4, 40, 100, 150),      # a pool larger than a group
+    ("uniform", 1, 2, 2, 64, 16, 4, 0, 100, 150),       # no pool
+    ("uniform", 3, 2, 2, 128, 32, 8, 32, 300, 700),     # the pool as large as a group, many flushes
+    ("uniform", 1, 1, 1, 64, 16, 4, 16, 20, 2000),      # a scan over many lists
+    ("ragged", 1, 2, 1, 128, 32, 8, 12, [95], [300]),
+    ("paged", 2, 2, 2, 64, 16, 3, 8, [0, 333], [260, 80]),
     ("paged", 3, 2, 1, 128, 32, 4, 6, [10, 300, 35], [100, 3, 0]),
     ("paged", 2, 2, 1, 128, 32, 4, 6, 40, 60),
     ("cold", 2, 2, 1, 64, 16, 4, 8, 100, 77),
