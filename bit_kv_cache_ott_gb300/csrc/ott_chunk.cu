@@ -439,10 +439,10 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 #pragma unroll
                         for (int x = 0; x < 4; ++x) sc[nc][x] = sd[nc][x] = 0.0f;
                     {
-                        uint32_t w[NW], w10[NW];
+                        uint32_t w[NW], w8[NW];
                         lds_words<NW>(tb + tile_k_off(D) + lane * NW * 4, w);
 #pragma unroll
-                        for (int x = 0; x < NW; ++x) w10[x] = w[x] >> 10;
+                        for (int x = 0; x < NW; ++x) w8[x] = w[x] >> 8;
 #pragma unroll
                         for (int kt = 0; kt < NKT; ++kt) {
                             uint32_t f4[4];   // (token r + 8 th, channels 16 kt + 8 o): f4[th + 2 o]
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 #pragma unroll
                                 for (int th = 0; th < 2; ++th) {
                                     const int q = o * NKT + kt, wi = 2 * (q >> 3) + th;
-                                    f4[th + 2 * o] = ch_key(mg, w[wi], w10[wi], q & 7, ks2[kt][o]);
+                                    f4[th + 2 * o] = ch_key(mg, w[wi], w8[wi], q & 7, ks2[kt][o]);
                                 }
 #pragma unroll
                             for (int nc = 0; nc < NC; ++nc)
@@ -497,10 +497,10 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                             bp[nc][h] = transpose8x8(ch_h2(__floats2half2_rn(p[0], p[1])));
                         }
                     }
-                    uint32_t w[NW], w10[NW];
+                    uint32_t w[NW], w8[NW];
                     lds_words<NW>(tb + tile_v_off(D) + lane * NW * 4, w);
 #pragma unroll
-                    for (int x = 0; x < NW; ++x) w10[x] = w[x] >> 10;
+                    for (int x = 0; x < NW; ++x) w8[x] = w[x] >> 8;
 #pragma unroll
                     for (int gm = 0; gm < NKT / 2; ++gm) {   // a value group: 32 channels, two m-tiles
                         const uint4 sz = *reinterpret_cast<const uint4 *>(tb + tile_sz_off(D) + (gm * 4 + i) * 16);
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 #pragma unroll
                                 for (int half = 0; half < 2; ++half) {
                                     const int q = half * NKT + mt, wi = 2 * (q >> 3) + tp;
-                                    f4[half + 2 * tp] = ch_val(mg, w[wi], w10[wi], q & 7, s2[tp], z2[tp]);
+                                    f4[half + 2 * tp] = ch_val(mg, w[wi], w8[wi], q & 7, s2[tp], z2[tp]);
                                 }
 #pragma unroll
                             for (int nc = 0; nc < NC; ++nc)

@@ -101,40 +101,39 @@ __device__ __forceinline__ uint32_t ch_h2(__half2 h) { return *reinterpret_cast<
 __device__ __forceinline__ __half2 ch_as_h2(uint32_t w) { return *reinterpret_cast<__half2 *>(&w); }
 
 // Dequantization in fp16x2 registers. The two codes at position p of a word
-// (w10 = w >> 10 serves p >= 5) are ORed into the mantissa of 2^(10-2c),
-// c = p mod 5, whose unit in the last place they are counted in: an exact
-// fp16 2^(10-2c) + code. One subtraction gives code - 1 (keys) or code
-// (values), exactly.
-// Magic holds the five 2^(10-2c) in registers, so that extraction is one
-// three-input operation (it takes one immediate, the mask).
+// (w8 = w >> 8 serves p >= 4) are ORed into the mantissa of 2^(10-2c), c = p
+// mod 4, whose unit in the last place they are counted in: an exact fp16
+// 2^(10-2c) + code. One subtraction gives code - 1 (keys) or code (values),
+// exactly. Magic holds the four 2^(10-2c) in registers, so that extraction is
+// one three-input operation (it takes one immediate, the mask).
 struct Magic {
-    uint32_t m[5];
+    uint32_t m[4];
     __device__ __forceinline__ Magic() {
 #pragma unroll
-        for (int c = 0; c < 5; ++c) {
+        for (int c = 0; c < 4; ++c) {
             m[c] = (uint32_t)((25 - 2 * c) << 10) * 0x10001u;
             asm volatile("" : "+r"(m[c]));   // a register's value from here on
         }
     }
 };
-__device__ __forceinline__ uint32_t ch_raw(const Magic &mg, uint32_t w, uint32_t w10, int p) {
-    const int c = cls_of_pos(p);
+__device__ __forceinline__ uint32_t ch_raw(const Magic &mg, uint32_t w, uint32_t w8, int p) {
+    const int c = p & 3;
     uint32_t d;   // (w & mask) | magic, as one operation
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(p < 5 ? w : w10), "r"(0x00030003u << (2 * c)), "r"(mg.m[c]));
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(p < 4 ? w : w8), "r"(0x00030003u << (2 * c)), "r"(mg.m[c]));
     return d;
 }
 __device__ __forceinline__ uint32_t ch_const(int p, int less) {   // -(2^(10-2c) + less) in both halves
-    const __half h = __float2half_rn(-(float)((1 << (10 - 2 * cls_of_pos(p))) + less));
+    const __half h = __float2half_rn(-(float)((1 << (10 - 2 * (p & 3))) + less));
     return (uint32_t)__half_as_ushort(h) * 0x10001u;
 }
 // s * (code - 1): exact (a scale, its negative, zero or twice it)
-__device__ __forceinline__ uint32_t ch_key(const Magic &mg, uint32_t w, uint32_t w10, int p, uint32_t s2) {
-    const __half2 c1 = __hadd2(ch_as_h2(ch_raw(mg, w, w10, p)), ch_as_h2(ch_const(p, 1)));
+__device__ __forceinline__ uint32_t ch_key(const Magic &mg, uint32_t w, uint32_t w8, int p, uint32_t s2) {
+    const __half2 c1 = __hadd2(ch_as_h2(ch_raw(mg, w, w8, p)), ch_as_h2(ch_const(p, 1)));
     return ch_h2(__hmul2(c1, ch_as_h2(s2)));
 }
 // z + s * code, one rounding
-__device__ __forceinline__ uint32_t ch_val(const Magic &mg, uint32_t w, uint32_t w10, int p, uint32_t s2, uint32_t z2) {
-    const __half2 c = __hadd2(ch_as_h2(ch_raw(mg, w, w10, p)), ch_as_h2(ch_const(p, 0)));
+__device__ __forceinline__ uint32_t ch_val(const Magic &mg, uint32_t w, uint32_t w8, int p, uint32_t s2, uint32_t z2) {
+    const __half2 c = __hadd2(ch_as_h2(ch_raw(mg, w, w8, p)), ch_as_h2(ch_const(p, 0)));
     return ch_h2(__hfma2(c, ch_as_h2(s2), ch_as_h2(z2)));
 }
 // fp16x2 hi + lo = s + z exactly up to lo's rounding (the two-sum of both halves)

@@ -56,9 +56,11 @@ struct TCfg {
     static constexpr int OFF_Q = 0, OFF_K = 2 * QB, OFF_V = OFF_K + 2 * KB;
     static constexpr int OFF_POS = OFF_V + 2 * VB;          // int pos[META][STEP_TOK]
     static constexpr int OFF_FLAG = OFF_POS + META * STEP_TOK * 4;   // a byte of flag[META][8] per group
-    static constexpr int OFF_HDR = OFF_FLAG + META * 8;         // a block's key scales and zeros per producer
-    static constexpr int OFF_BAR = OFF_HDR + GRPS * 4 * D;    // barriers, tmem address, abort flag
+    // per producer: 16 fp16 rows, or the key scales and zeros of a block
+    static constexpr int OFF_STG = (OFF_FLAG + META * 8 + 1023) / 1024 * 1024;
+    static constexpr int OFF_BAR = OFF_STG + GRPS * 32 * D;    // barriers, tmem address, abort flag
     static constexpr int SMEM = OFF_BAR + 256 + 1024;       // + alignment to 1024
+    static_assert(SMEM <= 227 * 1024, "shared memory");
     __host__ __device__ static constexpr uint32_t S(int t) { return 128u * t; }
     __host__ __device__ static constexpr uint32_t O(int t) { return 256u + (uint32_t)D * t; }
 };
@@ -376,11 +378,13 @@ struct Producer {
     __device__ void quantized(int x, int n) {
         const int cpt = ta.CPT;
         uint32_t kr[NW], vr[NW], zr[2 * NKT], ks2[NKT][2];
-        uint8_t *const stage = sm + C::OFF_HDR + w * ksz_bytes(D);   // the block's key scales and zeros
+        uint8_t *const stage = sm + C::OFF_STG + w * (32 * D);   // the block's key scales and zeros
+        // (the next block's wait in registers: a copy into shared memory in
+        // flight holds up every fence of the proxies behind it)
         const int row0 = slot_of(r), row1 = slot_of(r + 8);
         const uint32_t k0 = (16 * w + row0) * 128 + ((2 * i ^ (row0 & 7)) << 4), k1 = (16 * w + row1) * 128 + ((2 * i ^ (row1 & 7)) << 4);
         Group g, gn, gb;             // made, next, first of the next block
-        uint4 hb = make_uint4(0, 0, 0, 0);
+        uint4 hb = make_uint4(0, 0, 0, 0);   // gb's
         int xb = -1;                 // gb's number
         g.left = g.sub = 0;
         g.j = -1;
@@ -408,9 +412,9 @@ struct Producer {
                 wait(B_KEMPTY);
                 uint8_t *kb = key_tile();
                 if (g.left > 0) {
-                    uint32_t k10[NW];
+                    uint32_t k8[NW];
 #pragma unroll
-                    for (int y = 0; y < NW; ++y) k10[y] = kr[y] >> 10;
+                    for (int y = 0; y < NW; ++y) k8[y] = kr[y] >> 8;
                     uint8_t *const p[4] = {kb + k0, kb + (k0 ^ 16), kb + k1, kb + (k1 ^ 16)};
 #pragma unroll
                     for (int th = 0; th < 2; ++th)
@@ -420,7 +424,7 @@ struct Producer {
                             uint32_t f[4];
 #pragma unroll
                             for (int y = 0; y < 4; ++y)
-                                f[y] = ch_key(mg, kr[wi], k10[wi], (q0 + y) & 7, ks2[(q0 + y) % NKT][(q0 + y) / NKT]);
+                                f[y] = ch_key(mg, kr[wi], k8[wi], (q0 + y) & 7, ks2[(q0 + y) % NKT][(q0 + y) / NKT]);
                             // chunk 2i + 1 is chunk 2i with its lowest bit turned, whatever the swizzle
                             *reinterpret_cast<uint4 *>(p[2 * th + ((q0 >> 2) & 1)] + (q0 >> 3) * (ROWS * 128)) =
                                 make_uint4(f[0], f[1], f[2], f[3]);
@@ -474,9 +478,9 @@ struct Producer {
                 wait(B_VEMPTY);
                 uint8_t *vb = value_at();
                 if (g.left > 0) {
-                    uint32_t v10[NW];
+                    uint32_t v8[NW];
 #pragma unroll
-                    for (int y = 0; y < NW; ++y) v10[y] = vr[y] >> 10;
+                    for (int y = 0; y < NW; ++y) v8[y] = vr[y] >> 8;
 #pragma unroll
                     for (int gm = 0; gm < NKT / 2; ++gm) {
                         const uint32_t *z = zr + 4 * gm;
@@ -488,8 +492,8 @@ struct Producer {
                             for (int half = 0; half < 2; ++half) {
                                 const int mt = 2 * gm + mm, q = half * NKT + mt, wi = 2 * (q >> 3);
                                 *reinterpret_cast<uint2 *>(vb + (16 * mt + 8 * half) * 128) =
-                                    make_uint2(ch_val(mg, vr[wi], v10[wi], q & 7, s2[0], z2[0]),
-                                               ch_val(mg, vr[wi + 1], v10[wi + 1], q & 7, s2[1], z2[1]));
+                                    make_uint2(ch_val(mg, vr[wi], v8[wi], q & 7, s2[0], z2[0]),
+                                               ch_val(mg, vr[wi + 1], v8[wi + 1], q & 7, s2[1], z2[1]));
                             }
                     }
                 } else {
@@ -511,11 +515,14 @@ struct Producer {
 
     // n groups from the x-th of the fp16 ones on: ring, pool and cold pool in
     // whole groups, then the new tokens from group nlo on; past them, nothing.
-    // Loads wait here: registers for a group ahead would be taken from the
-    // other loop, which has most of the work.
+    // A lane finds one row, the keys' or the values' (lane mod 16), and passes
+    // its address round; keys come through registers, values through shared
+    // memory, both under one wait. (Loads a group ahead would take registers
+    // that the other loop, which has most of the work, would spill.)
     __device__ void plain(int x, int n) {
         const int ncold = a.C > 0 ? __ldg(a.cmeta + 2 * u) : 0, chead = a.C > 0 ? __ldg(a.cmeta + 2 * u + 1) : 0;
         const int nhot = s.ntail + s.npool + ncold;
+        uint8_t *const stage = sm + C::OFF_STG + w * (32 * D);   // 16 rows, 16-byte chunks turned by the row
 #pragma unroll 1
         for (int y = x; y < x + n; ++y) {
             int f = 0, left = 0;   // first token, tokens left
@@ -526,18 +533,28 @@ struct Producer {
                 f = nhot + 16 * (y - t.gf + t.nlo);
                 left = nhot + s.nnew - f;
             }
+            unsigned long long at = 0;
+            if ((lane & 15) < left)
+                at = reinterpret_cast<unsigned long long>(
+                    chunk_fp16_row(a, s, b, t.hkv, u, f + (lane & 15), ncold, chead, lane >= 16, D));
             uint4 kr[16 / RPI];
 #pragma unroll
-            for (int e = 0; e < 16 / RPI; ++e) kr[e] = make_uint4(0, 0, 0, 0);
-            if (left > 0) {
-#pragma unroll
-                for (int e = 0; e < 16 / RPI; ++e) {
-                    const int row = RPI * e + lane / CPR;
-                    const uint4 *p = reinterpret_cast<const uint4 *>(
-                        chunk_fp16_row(a, s, b, t.hkv, u, f + min(row, left - 1), ncold, chead, false, D)) + lane % CPR;
-                    if (row < left) kr[e] = __ldg(p);
-                }
+            for (int e = 0; e < 16 / RPI; ++e) {
+                const unsigned long long p = __shfl_sync(0xffffffffu, at, RPI * e + lane / CPR);
+                kr[e] = make_uint4(0, 0, 0, 0);
+                if (p) kr[e] = __ldg(reinterpret_cast<const uint4 *>(p) + lane % CPR);
             }
+#pragma unroll
+            for (int e = 0; e < 16 / RPI; ++e) {
+                const int row = RPI * e + lane / CPR, ch = lane % CPR;
+                const unsigned long long p = __shfl_sync(0xffffffffu, at, 16 + row);
+                // no row: zeros (nothing is read)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ch_smem(stage + row * (2 * D) + ((ch ^ (row & 7)) << 4))),
+                             "l"(p ? reinterpret_cast<const uint8_t *>(p) + 16 * ch : reinterpret_cast<const uint8_t *>(a.q)),
+                             "r"(p ? 16 : 0)
+                             : "memory");
+            }
+            const int pos = lane < 16 && lane < left ? chunk_fp16_pos(a, s, u, f + lane, ncold, chead) : INT_MAX;
             wait(B_KEMPTY);
             uint8_t *kb = key_tile();
 #pragma unroll
@@ -546,22 +563,21 @@ struct Producer {
             if (lane < 2 * CPR)
                 *reinterpret_cast<uint4 *>(kb + (lane % CPR / 8) * (ROWS * 128) + (STEP_TOK + 2 * w + lane / CPR) * 128 +
                                            (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-            key_done(true, lane < 16 && lane < left ? chunk_fp16_pos(a, s, u, f + lane, ncold, chead) : INT_MAX);
-
-            uint32_t vr[2][D / 8];
-#pragma unroll
-            for (int th = 0; th < 2; ++th) {
-                const int row = r + 8 * th;
-                const __half *p = left > 0 ? chunk_fp16_row(a, s, b, t.hkv, u, f + min(row, left - 1), ncold, chead, true, D) : nullptr;
-#pragma unroll
-                for (int c = 0; c < D / 8; ++c)
-                    vr[th][c] = row < left ? __ldg(reinterpret_cast<const uint32_t *>(p + 8 * c + 2 * i)) : 0u;
-            }
-            wait(B_VEMPTY);
+            key_done(true, pos);
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            wait(B_VEMPTY);   // (its __syncwarp covers the copies)
             uint8_t *vb = value_at();
+            const int row = lane & 15, cb = lane >> 4;   // ldmatrix: the row and block that this lane names
 #pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-                *reinterpret_cast<uint2 *>(vb + 8 * c * 128) = make_uint2(transpose8x8(vr[0][c]), transpose8x8(vr[1][c]));
+            for (int c = 0; c < D / 8; c += 2) {
+                uint32_t m[4];   // tokens 0..7 and 8..15 of channels 8c .., then of 8c + 8 ..
+                asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(m[0]), "=r"(m[1]), "=r"(m[2]), "=r"(m[3])
+                             : "r"(ch_smem(stage + row * (2 * D) + (((c + cb) ^ (row & 7)) << 4)))
+                             : "memory");
+                *reinterpret_cast<uint2 *>(vb + 8 * c * 128) = make_uint2(m[0], m[1]);
+                *reinterpret_cast<uint2 *>(vb + 8 * (c + 1) * 128) = make_uint2(m[2], m[3]);
+            }
             value_done();
         }
     }
