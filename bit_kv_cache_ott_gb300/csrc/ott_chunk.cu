@@ -706,6 +706,7 @@ struct Plan {
     int gs;       // the decode kernel in rows mode: rows per slice; 0: tiles (ott_chunk_tiles.cu)
     int ipb;      // work items per block
     int nC;       // tiles: CTAs
+    bool whole;   // ... each with a tile of its own
     bool sinks, any;
     size_t part_floats;
 };
@@ -809,7 +810,7 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
         if (units > INT_MAX) return false;
     }
     if (tiles) {
-        if (!plan_tiles(c, a, p.st, p.nC, p.part_floats)) return false;
+        if (!plan_tiles(c, a, p.st, p.nC, p.whole, p.part_floats)) return false;
         p.any = a.W > 0;
         return true;
     }
@@ -836,7 +837,7 @@ cudaError_t launch_plan(const ott_cache *c, const Plan &p, cudaStream_t s) {
     if (p.sinks)
         e = launch_pdl(k_window_sinks, dim3((unsigned)(a.nseq * a.Hkv)), SINK_THREADS, 0, s, a, p.st, c->sel);
     if (e == cudaSuccess && p.gs > 0) return launch_decode_rows(c, a, p.st, p.gs, p.ipb, s);
-    if (e == cudaSuccess && p.NC == 0) return launch_tiles(c, a, p.st, p.nC, s);
+    if (e == cudaSuccess && p.NC == 0) return launch_tiles(c, a, p.st, p.nC, p.whole, s);
     if (e == cudaSuccess)
         e = p.NC == 1 ? launch_rows<D, 1>(a, p.st, c->sm_count, s) : launch_rows<D, 2>(a, p.st, c->sm_count, s);
     if (e != cudaSuccess) return e;

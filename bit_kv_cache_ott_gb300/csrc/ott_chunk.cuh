@@ -185,7 +185,7 @@ cudaError_t launch_decode_rows(const ott_cache *c, const ChunkArgs &a, const Chu
 cudaError_t set_decode_rows_attributes(int d, int smem_max);
 // ott_chunk_tiles.cu
 cudaError_t set_tiles_attributes(int d);
-bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, size_t &part_floats);
-cudaError_t launch_tiles(const ott_cache *c, const ChunkArgs &a, const ChunkTable &st, int nC, cudaStream_t s);
+bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, bool &whole, size_t &part_floats);
+cudaError_t launch_tiles(const ott_cache *c, const ChunkArgs &a, const ChunkTable &st, int nC, bool whole, cudaStream_t s);
 
 }  // namespace ott

@@ -47,7 +47,8 @@ constexpr int PROD0 = 8, MMA_WARP = 15;
 constexpr int META = 4;              // steps of group metadata in flight
 constexpr float GROW = 8.0f;         // log2: the output is rescaled when the maximum has grown by this
 constexpr int MAX_STEPS = 768, MAX_WAVES = 8;   // steps per CTA before there are more CTAs than SMs (see plan_tiles)
-constexpr int MIN_STEPS = 4;         // steps per CTA at least (a run's fixed cost is about two)
+constexpr int MIN_STEPS = 2;         // steps per CTA at least
+constexpr int FIXED = 3;             // a tile's fixed cost (find it, queries, fill the pipeline, output) in steps of 2 us
 
 template <int D>
 struct TCfg {
@@ -71,8 +72,9 @@ struct TileArgs {
     ChunkArgs a;
     int CPT;          // groups of 16 slots per block
     int nC;           // CTAs
-    long long W;      // steps of all tiles
+    long long W;      // places of all tiles: FIXED and its steps each
     float *part;      // [nC][2][D + 2][256]
+    int whole;        // CTA i takes tile i whole, else an equal run of steps
 };
 
 // A tile pair of a (sequence, kv head): its rows, and the groups that they see.
@@ -105,22 +107,24 @@ __host__ __device__ inline void tile_extent(const ChunkArgs &a, int cpt, const C
     t.steps = t.sq + (t.gf + t.gn + GRPS - 1) / GRPS;
 }
 
-// The tile that holds step x, and the step's number in it. Warp-collective.
+// The tile that holds place x, and the place's number in it: a tile has FIXED
+// places, so that CTAs with many short tiles get fewer steps, and then its
+// steps. Warp-collective.
 __device__ __forceinline__ Tile tile_at(const TileArgs &ta, const ChunkTable &st, long long x, int &step) {
     const ChunkArgs &a = ta.a;
     Tile t;
     t.e = ch_entry_of(st, a.nseq, x);
     const ChunkSeq &s = st.e[t.e];
     const unsigned rel = (unsigned)(x - s.base);
-    t.hkv = (int)(rel / (unsigned)s.Iu);             // Iu: steps of one kv head's tiles
+    t.hkv = (int)(rel / (unsigned)s.Iu);             // Iu: places of one kv head's tiles
     int left = (int)(rel % (unsigned)s.Iu);
     const int lane = threadIdx.x & 31;
-    for (int p0 = 0;; p0 += 32) {                    // ends: s.S tiles hold Iu steps
+    for (int p0 = 0;; p0 += 32) {                    // ends: s.S tiles hold Iu places
         int n = 0;
         if (p0 + lane < s.S) {
             Tile u;
             tile_extent(a, ta.CPT, s, p0 + lane, u);
-            n = u.steps;
+            n = u.steps + FIXED;
         }
         int inc = n;
 #pragma unroll
@@ -137,6 +141,23 @@ __device__ __forceinline__ Tile tile_at(const TileArgs &ta, const ChunkTable &st
         }
         left -= __shfl_sync(0xffffffffu, inc, 31);
     }
+}
+
+// Tile number i of the launch where every CTA takes one: an entry's last rows
+// (of all its heads) first, since they see the most.
+__device__ __forceinline__ Tile tile_number(const TileArgs &ta, const ChunkTable &st, int i) {
+    Tile t;
+    int lo = 0, hi = ta.a.nseq;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (st.e[mid].ubase <= i) lo = mid;
+        else hi = mid;
+    }
+    const ChunkSeq &s = st.e[lo];
+    t.e = lo;
+    t.hkv = (i - s.ubase) % ta.a.Hkv;
+    tile_extent(ta.a, ta.CPT, s, s.S - 1 - (i - s.ubase) / ta.a.Hkv, t);
+    return t;
 }
 
 // ---------------------------------------------------------------- PTX
@@ -181,8 +202,9 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
     return one != 0;
 }
-// All 512 threads, each role from its own place in the code.
-__device__ __forceinline__ void cta_sync() { asm volatile("barrier.sync 0;" ::: "memory"); }
+// The softmax warps and the product warp, each from its own place in the
+// code: the tile's queries are in place, the last tile's output is read.
+__device__ __forceinline__ void tile_sync() { asm volatile("barrier.sync 1, %0;" ::"n"(32 * (PROD0 + 1)) : "memory"); }
 __device__ __forceinline__ void tc_commit(uint64_t *b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(ch_smem(b)) : "memory");
 }
@@ -856,45 +878,62 @@ __device__ void finish(const TileArgs &ta, const Tile &t, uint32_t tmem, int til
 enum { SOFTMAX, MULTIPLY, PRODUCE };
 
 // A CTA's run of steps, tile by tile, in one of its roles. The roles have
-// loops of their own so that each keeps to its own register budget; the two
-// barriers of a tile are met by all of them.
+// loops of their own, so that each keeps to its own registers. The producers
+// run on into the next tile while the last one's output is read and the next
+// one's queries are fetched.
 template <int D, int ROLE>
 __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm, uint64_t *bar, volatile int *gave_up,
                           uint32_t tmem) {
     using C = TCfg<D>;
     const ChunkArgs &a = ta.a;
-    long long x = ch_range_start(ta.W, ta.nC, blockIdx.x);
-    const long long x1 = ch_range_start(ta.W, ta.nC, blockIdx.x + 1);
+    long long x = ta.whole ? 0 : ch_range_start(ta.W, ta.nC, blockIdx.x);
+    const long long x1 = ta.whole ? 1 : ch_range_start(ta.W, ta.nC, blockIdx.x + 1);
     uint32_t it = 0, ct[2] = {0, 0};   // steps done by the CTA, and by each tile
-    for (uint32_t run = 0; x < x1; ++run) {
-        int j0;
-        const Tile t = tile_at(ta, st, x, j0);
+    for (uint32_t run = 0; x < x1;) {
+        int at = 0;
+        const Tile t = ta.whole ? tile_number(ta, st, blockIdx.x) : tile_at(ta, st, x, at);
         const ChunkSeq &s = st.e[t.e];
-        const int j1 = (int)min((long long)t.steps, j0 + (x1 - x)), n = j1 - j0;
+        const int end = ta.whole ? t.steps + FIXED : (int)min((long long)t.steps + FIXED, at + (x1 - x));
+        const int j0 = max(0, at - FIXED), j1 = max(0, end - FIXED), n = j1 - j0;
+        x += ta.whole ? 1 : end - at;
+        if (n == 0) continue;   // the run ends before the tile's steps
         const int nt = t.rows > ROWS ? 2 : 1;
-        // queries into the swizzled tiles, rows past the last zero
-        for (int e = threadIdx.x; e < nt * ROWS * (D / 8); e += THREADS) {
-            const int row = e / (D / 8), ch = e % (D / 8), rw = row % ROWS;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < t.rows) {
-                const int vv = 256 * t.p + row;
-                v = __ldg(reinterpret_cast<const uint4 *>(
-                              a.q + (((size_t)(a.B0 + t.e) * a.Hq + t.hkv * a.g + vv % a.g) * a.n + vv / a.g) * D) + ch);
-            }
-            put_row_piece<D>(sm + C::OFF_Q + row / ROWS * C::QB, rw, ch, v);
-        }
-        proxy_fence();
-        cta_sync();
         if constexpr (ROLE == SOFTMAX) {
+            // queries into the swizzled tiles, rows past the last zero; a
+            // warp takes rows 8 or 16 apart, its loads in flight together
+            constexpr int CPR = D / 8, RPW = 32 / CPR, STEP = PROD0 * RPW, BATCH = 8;
+            const int ch = threadIdx.x % CPR, r0 = threadIdx.x / CPR;
+            const __half *const q0 = a.q + (size_t)(a.B0 + t.e) * a.Hq * a.n * D + (size_t)t.hkv * a.g * a.n * D + 8 * ch;
+#pragma unroll 1
+            for (int rr = r0; rr < nt * ROWS; rr += STEP * BATCH) {
+                uint4 v[BATCH];
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) {
+                    const int row = rr + STEP * y, vv = 256 * t.p + row, tk = vv / a.g;
+                    v[y] = make_uint4(0, 0, 0, 0);
+                    if (row < t.rows) v[y] = __ldg(reinterpret_cast<const uint4 *>(q0 + ((size_t)(vv - tk * a.g) * a.n + tk) * D));
+                }
+#pragma unroll
+                for (int y = 0; y < BATCH; ++y) {
+                    const int row = rr + STEP * y;
+                    put_row_piece<D>(sm + C::OFF_Q + row / ROWS * C::QB, row % ROWS, ch, v[y]);
+                }
+            }
+            proxy_fence();
+            tile_sync();
             const int tile = threadIdx.x / ROWS;
-            float m, l;
             if (tile < nt) {
+                float m, l;
                 softmax<D>(ta, s, t, sm, bar, gave_up, tmem, tile, n, it, ct[tile], m, l);
                 bar_wait(&bar[B_OFULL], run & 1u, gave_up);
                 tc_after();
                 finish<D>(ta, t, tmem, tile, n == t.steps, run > 0, m, l);
+            } else {
+                bar_wait(&bar[B_OFULL], run & 1u, gave_up);   // its products may still read the queries
             }
         } else if constexpr (ROLE == MULTIPLY) {
+            tile_sync();
+            tc_after();
             multiply<D>(sm, bar, gave_up, tmem, nt, n, it, ct[0], ct[1]);
         } else {
             produce<D>(ta, s, t, sm, bar, gave_up, j0, j1, it);
@@ -902,8 +941,7 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
         it += (uint32_t)n;
         ct[0] += (uint32_t)n;
         if (nt == 2) ct[1] += (uint32_t)n;
-        x += n;
-        cta_sync();
+        ++run;
     }
 }
 
@@ -955,6 +993,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         else
             role_loop<D, PRODUCE>(ta, st, sm, bar, gave_up, tmem);
     }
+    __syncthreads();
     if (*gave_up && threadIdx.x == 0) atomicExch(&a.ctl[1], 1);
     if (warp == MMA_WARP) {
         // after a wait that gave up, products may still be in flight: one more bounded wait for them
@@ -986,7 +1025,7 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
         long long before = 0;
         for (int q = lane; q < p; q += 32) {
             tile_extent(a, ta.CPT, s, q, t);
-            before += t.steps;
+            before += t.steps + FIXED;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -994,7 +1033,7 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
     }
     tile_extent(a, ta.CPT, s, p, t);
     if (32 * (blockIdx.x % 8) >= t.rows) return;
-    const int c0 = ch_warp_of(ta.W, ta.nC, ts), c1 = ch_warp_of(ta.W, ta.nC, ts + t.steps - 1);
+    const int c0 = ch_warp_of(ta.W, ta.nC, ts + FIXED), c1 = ch_warp_of(ta.W, ta.nC, ts + FIXED + t.steps - 1);
     if (c0 == c1) return;   // written whole
     const int slot0 = ch_range_start(ta.W, ta.nC, c0) < ts ? 1 : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -1002,18 +1041,33 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
     float M = -CUDART_INF_F, L = 0.0f, acc[CH];
 #pragma unroll
     for (int y = 0; y < CH; ++y) acc[y] = 0.0f;
-    for (int c = c0; c <= c1; ++c) {
-        const float *pb = ta.part + ((size_t)c * 2 + (c == c0 ? slot0 : 0)) * (D + 2) * 256 + row;
-        const float m = pb[0], l = pb[256];
-        float f[CH];
+    constexpr int AHEAD = 4;   // parts whose loads are in flight together
+    for (int c = c0; c <= c1; c += AHEAD) {
+        float m[AHEAD], l[AHEAD], f[AHEAD][CH];
 #pragma unroll
-        for (int y = 0; y < CH; ++y) f[y] = pb[(size_t)(2 + CH * warp + y) * 256];
-        const float mn = fmaxf(M, m);
+        for (int z = 0; z < AHEAD; ++z) {
+            const int cc = min(c + z, c1);
+            const float *pb = ta.part + ((size_t)cc * 2 + (cc == c0 ? slot0 : 0)) * (D + 2) * 256 + row;
+            m[z] = c + z <= c1 ? pb[0] : -CUDART_INF_F;
+            l[z] = pb[256];
+#pragma unroll
+            for (int y = 0; y < CH; ++y) f[z][y] = pb[(size_t)(2 + CH * warp + y) * 256];
+        }
+        float mn = M;
+#pragma unroll
+        for (int z = 0; z < AHEAD; ++z) mn = fmaxf(mn, m[z]);
         if (mn == -CUDART_INF_F) continue;
-        const float so = ch_ex2(M - mn), sn = ch_ex2(m - mn);
-        L = L * so + l * sn;
+        const float so = ch_ex2(M - mn);
+        L *= so;
 #pragma unroll
-        for (int y = 0; y < CH; ++y) acc[y] = acc[y] * so + f[y] * sn;
+        for (int y = 0; y < CH; ++y) acc[y] *= so;
+#pragma unroll
+        for (int z = 0; z < AHEAD; ++z) {
+            const float sn = ch_ex2(m[z] - mn);
+            L = fmaf(l[z], sn, L);
+#pragma unroll
+            for (int y = 0; y < CH; ++y) acc[y] = fmaf(f[z][y], sn, acc[y]);
+        }
         M = mn;
     }
     if (row >= t.rows) return;
@@ -1030,7 +1084,7 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
 template <int D>
 cudaError_t launch_t(const TileArgs &ta, const ChunkTable &st, int pairs, cudaStream_t s) {
     cudaError_t e = launch_pdl(k_chunk_tiles<D>, dim3((unsigned)ta.nC), THREADS, (size_t)TCfg<D>::SMEM, s, ta, st);
-    if (e != cudaSuccess || ta.nC == 1) return e;
+    if (e != cudaSuccess || ta.nC == 1 || ta.whole) return e;
     return launch_pdl(k_tiles_combine<D>, dim3(8u * pairs, (unsigned)ta.a.Hkv, (unsigned)ta.a.nseq), 256, 0, s, ta, st);
 }
 
@@ -1043,43 +1097,65 @@ cudaError_t set_tiles_attributes(int d) {
 
 // The launch's table in tiles: S pairs of tiles per kv head, Iu their steps.
 // false: the sizes do not fit the kernel's 32-bit counters.
-bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, size_t &part_floats) {
+bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, bool &whole, size_t &part_floats) {
     const int cpt = ntiles_of(c->G);
-    long long base = 0;
+    long long base = 0, tiles = 0;
+    int longest = 0;
     for (int x = 0; x < a.nseq; ++x) {
         ChunkSeq &s = st.e[x];
         s.base = base;
+        s.ubase = (int)tiles;
         s.S = (int)(((long long)s.nq * a.g + 255) / 256);
         long long steps = 0;
         if (((long long)s.nf + s.nsink) * cpt + ((long long)s.ntail + s.npool + a.C + s.nq) / 16 + 4 > INT_MAX) return false;
         for (int p = 0; p < s.S; ++p) {
             Tile t;
             tile_extent(a, cpt, s, p, t);
-            steps += t.steps;
+            steps += t.steps + FIXED;
+            longest = std::max(longest, t.steps);
             if (steps * a.Hkv > INT_MAX) return false;
         }
         s.Iu = (int)steps;
         base += steps * a.Hkv;
+        tiles += (long long)s.S * a.Hkv;
+        if (tiles > INT_MAX) return false;
     }
     st.e[a.nseq] = ChunkSeq{};
     st.e[a.nseq].base = a.W = base;
+    st.e[a.nseq].ubase = (int)tiles;
     // The tensor cores truncate as they accumulate: a sum over 1,200 steps
     // shrank by 7e-5 of itself (a third of an fp16 rounding). Runs of at most
     // MAX_STEPS, merged in fp32, keep that below 4e-5 and cost 2-3% on a
     // 131K-token chunk (3.14 ms without).
-    const long long waves = std::min<long long>(MAX_WAVES, (base + (long long)c->sm_count * MAX_STEPS - 1) / ((long long)c->sm_count * MAX_STEPS));
-    nC = (int)std::max<long long>(1, std::min<long long>(c->sm_count * std::max(1LL, waves), base / MIN_STEPS));
-    part_floats = nC > 1 ? (size_t)nC * 2 * (c->d + 2) * 256 : 1;
+    const double sms = c->sm_count, W = (double)base, nT = (double)tiles;
+    const long long waves = std::max<long long>(1, std::min<long long>(MAX_WAVES, (base + (long long)c->sm_count * MAX_STEPS - 1) / ((long long)c->sm_count * MAX_STEPS)));
+    // Equal runs of places, or a tile per CTA: by their estimated times. A
+    // merge costs 2.5 steps and 0.1 per part of a tile. 333 new tokens of five
+    // short sequences (100 tiles): 41 us in runs, 17 with a tile per CTA.
+    const double one = tiles <= c->sm_count ? FIXED + longest : W / sms + longest / 2.0;
+    double best = 1e30;
+    for (int div = 1; div <= 4; div *= 2) {
+        const long long n = std::max<long long>(1, std::min<long long>((long long)c->sm_count * waves, (base - FIXED * tiles) / MIN_STEPS) / div);
+        const double run = W / n, cost = std::ceil(n / sms) * (FIXED + run) + (n > 1 ? 2.5 + 0.1 * (W / nT) / run : 0);
+        if (cost < best) {
+            best = cost;
+            nC = (int)n;
+        }
+    }
+    whole = longest <= MAX_STEPS && one <= best;
+    if (whole) nC = (int)tiles;
+    part_floats = !whole && nC > 1 ? (size_t)nC * 2 * (c->d + 2) * 256 : 1;
     return true;
 }
 
-cudaError_t launch_tiles(const ott_cache *c, const ChunkArgs &a, const ChunkTable &st, int nC, cudaStream_t s) {
+cudaError_t launch_tiles(const ott_cache *c, const ChunkArgs &a, const ChunkTable &st, int nC, bool whole, cudaStream_t s) {
     TileArgs ta;
     ta.a = a;
     ta.CPT = ntiles_of(c->G);
     ta.nC = nC;
     ta.W = a.W;
     ta.part = a.part;
+    ta.whole = whole;
     int pairs = 0;
     for (int x = 0; x < a.nseq; ++x) pairs = std::max(pairs, st.e[x].S);
     return c->d == 128 ? launch_t<128>(ta, st, pairs, s) : launch_t<64>(ta, st, pairs, s);
