@@ -766,7 +766,7 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
     long long blocks = 0;
     for (int x = 0; p.gs && x < a.nseq; ++x) {
         const int b = B0 + x, nq = call.lens ? call.lens[b] : call.n;
-        const long long T = c->ragged ? c->Tb[b] : c->T, seen = call.window > 0 ? std::min<long long>(T, call.window + nq) : T;
+        const long long T = c->ragged ? c->Tb[b] : c->T, seen = call.window > 0 ? std::min<long long>(T, (long long)call.window + nq) : T;
         blocks += (seen / c->G + 1) * c->Hkv * ((nq * (long long)c->gq + RB - 1) / RB);
     }
     p.ipb = p.gs && blocks < (long long)c->sm_count * DEC_WARPS ? 1 : a.CPB;

@@ -2,15 +2,15 @@
 // stores (ott_chunk_attn with long chunks), on the tcgen05 tensor cores.
 //
 // Mathematics: as in ott_chunk.cu (exact key operand s * (code - 1), the
-// rows' q . (z + s) apart; weights and values rounded to fp16). The sum
-// q . (z + s) comes out of the same product: next to 112 tokens the key tile
-// of a step holds, for each of its 7 groups of 16 tokens, the two fp16
-// numbers hi + lo = z + s of the group's block as rows 112 + 2w and 113 + 2w.
-// One 128 x 128 product then gives the raw scores and the offsets; the
-// softmax adds a group's offset to its 16 columns inside the multiply-add
-// that it makes anyway. A group may come from any block or be 16 fp16 tokens
-// (offset rows zero), so blocks of any size, lists of blocks, rings and pools
-// pack into full steps.
+// rows' q . (z + s) apart; weights and values rounded to fp16). The offset
+// q . z + q . s comes out of the same product: next to 112 tokens the key
+// tile of a step holds, for each of its 7 groups of 16 tokens, the zeros and
+// the scales of the group's block as rows 112 + 2w and 113 + 2w. One 128 x
+// 128 product then gives the raw scores and the offsets; the softmax adds a
+// group's offset to its 16 columns inside the multiply-add that it makes
+// anyway. A group may come from any block or be 16 fp16 tokens (those two
+// rows zero), so blocks of any size, lists of blocks, rings and pools pack
+// into full steps.
 //
 // A CTA (512 threads, one per SM) serves up to 256 rows of one (sequence, kv
 // head), as two tiles of 128 rows (row v = token * g + head) that share every
@@ -27,9 +27,20 @@
 //                   S0(j), O1(j-1), S1(j), O0(j): while one tile's weights are
 //                   computed, the other tile's products run.
 // TMEM: S0, S1 (fp32 128 columns, the weights overwrite the first 56), O0, O1.
-// Work is cut into steps; every CTA gets an equal run of the steps of all
-// tiles, so long caches with few rows are split and there is no tail. A tile
-// cut between CTAs leaves partials, merged by k_tiles_combine.
+// Work is cut into steps. Either every CTA gets an equal run of the steps of
+// all tiles, so that long caches with few rows are split and there is no
+// tail (a tile cut between CTAs leaves partials, merged by k_tiles_combine),
+// or a tile of its own, whichever is estimated to end first (plan_tiles).
+//
+// What bounds it: a step is 1,920 cycles of products (the key tile's 16 extra
+// rows among them); the products alone, with nothing made and no softmax,
+// take 704 us for 2,048 tokens over 32K (8 kv heads, 4 heads each), all of it
+// 835 us: the producers' and the softmax's instructions share the schedulers
+// with one another. Dequantizing to fp16 in a pass of its own instead would
+// write six times the cache's bytes and read them for every pair of tiles; three tiles of rows or a second
+// softmax set do not fit TMEM; a sixth of the tokens less per step buys exact
+// values (their zeros and scales as further rows) but sums that cancel, and
+// lost accuracy over 131K tokens to the truncating accumulators.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -48,7 +59,7 @@ constexpr int META = 4;              // steps of group metadata in flight
 constexpr float GROW = 8.0f;         // log2: the output is rescaled when the maximum has grown by this
 constexpr int MAX_STEPS = 768, MAX_WAVES = 8;   // steps per CTA before there are more CTAs than SMs (see plan_tiles)
 constexpr int MIN_STEPS = 2;         // steps per CTA at least
-constexpr int FIXED = 3;             // a tile's fixed cost (find it, queries, fill the pipeline, output) in steps of 2 us
+constexpr int FIXED = 4;             // a tile's fixed cost (find it, queries, fill the pipeline, output) in steps of 2 us
 
 template <int D>
 struct TCfg {
@@ -181,13 +192,13 @@ __device__ __forceinline__ unsigned long long now_ns() {
     asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
     return t;
 }
-// Bounded wait: gives up after a second, or once another role has. A role
+// Bounded wait: gives up after four seconds, or once another role has. A role
 // whose wait gave up goes on (every later wait then ends at once, every
 // address stays what it would have been), so that warps stay together and
 // all roles reach the end; the status word tells the host.
 __device__ __forceinline__ void bar_wait(uint64_t *b, uint32_t parity, volatile int *gave_up) {   // whole warps
     if (!bar_try(b, parity)) {
-        const unsigned long long end = now_ns() + 1000000000ull;
+        const unsigned long long end = now_ns() + 4000000000ull;
         for (int k = 0; !bar_try(b, parity); ++k) {
             if (k & 63) continue;
             if (*gave_up) break;
@@ -452,16 +463,14 @@ struct Producer {
                                 make_uint4(f[0], f[1], f[2], f[3]);
                         }
                     if (fresh > 0) {
-                        // offset rows 112 + 2w, 113 + 2w; lane (r, i) makes the channels of k-tile r
+                        // rows 112 + 2w, 113 + 2w: z and s; lane (r, i) copies the channels of k-tile r
                         --fresh;
                         if (r < NKT) {
 #pragma unroll
                             for (int o = 0; o < 2; ++o) {
                                 const uint2 z = *reinterpret_cast<const uint2 *>(stage + 4 * (16 * r + 2 * i + 8 * o));
-                                uint32_t hi, lw;
-                                ch_offset(__byte_perm(z.x, z.y, 0x5410), __byte_perm(z.x, z.y, 0x7632), hi, lw);
-                                *reinterpret_cast<uint32_t *>(kb + chan_at<D>(r, o, i, STEP_TOK + 2 * w)) = hi;
-                                *reinterpret_cast<uint32_t *>(kb + chan_at<D>(r, o, i, STEP_TOK + 2 * w + 1)) = lw;
+                                *reinterpret_cast<uint32_t *>(kb + chan_at<D>(r, o, i, STEP_TOK + 2 * w)) = __byte_perm(z.x, z.y, 0x7632);
+                                *reinterpret_cast<uint32_t *>(kb + chan_at<D>(r, o, i, STEP_TOK + 2 * w + 1)) = __byte_perm(z.x, z.y, 0x5410);
                             }
                         }
                     }
@@ -886,16 +895,18 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
                           uint32_t tmem) {
     using C = TCfg<D>;
     const ChunkArgs &a = ta.a;
-    long long x = ta.whole ? 0 : ch_range_start(ta.W, ta.nC, blockIdx.x);
-    const long long x1 = ta.whole ? 1 : ch_range_start(ta.W, ta.nC, blockIdx.x + 1);
+    // (places from the run's start on: fewer registers than the places)
+    int done = 0;
+    const long long x0 = ta.whole ? 0 : ch_range_start(ta.W, ta.nC, blockIdx.x);
+    const int todo = ta.whole ? 1 : (int)(ch_range_start(ta.W, ta.nC, blockIdx.x + 1) - x0);
     uint32_t it = 0, ct[2] = {0, 0};   // steps done by the CTA, and by each tile
-    for (uint32_t run = 0; x < x1;) {
+    for (uint32_t run = 0; done < todo;) {
         int at = 0;
-        const Tile t = ta.whole ? tile_number(ta, st, blockIdx.x) : tile_at(ta, st, x, at);
+        const Tile t = ta.whole ? tile_number(ta, st, blockIdx.x) : tile_at(ta, st, x0 + done, at);
         const ChunkSeq &s = st.e[t.e];
-        const int end = ta.whole ? t.steps + FIXED : (int)min((long long)t.steps + FIXED, at + (x1 - x));
+        const int end = ta.whole ? t.steps + FIXED : min(t.steps + FIXED, at + (todo - done));
         const int j0 = max(0, at - FIXED), j1 = max(0, end - FIXED), n = j1 - j0;
-        x += ta.whole ? 1 : end - at;
+        done += ta.whole ? 1 : end - at;
         if (n == 0) continue;   // the run ends before the tile's steps
         const int nt = t.rows > ROWS ? 2 : 1;
         if constexpr (ROLE == SOFTMAX) {
@@ -1098,6 +1109,7 @@ cudaError_t set_tiles_attributes(int d) {
 // The launch's table in tiles: S pairs of tiles per kv head, Iu their steps.
 // false: the sizes do not fit the kernel's 32-bit counters.
 bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, bool &whole, size_t &part_floats) {
+    if (a.Hkv > 65535) return false;   // a grid dimension of the merge
     const int cpt = ntiles_of(c->G);
     long long base = 0, tiles = 0;
     int longest = 0;
@@ -1130,13 +1142,13 @@ bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, bool 
     const double sms = c->sm_count, W = (double)base, nT = (double)tiles;
     const long long waves = std::max<long long>(1, std::min<long long>(MAX_WAVES, (base + (long long)c->sm_count * MAX_STEPS - 1) / ((long long)c->sm_count * MAX_STEPS)));
     // Equal runs of places, or a tile per CTA: by their estimated times. A
-    // merge costs 2.5 steps and 0.1 per part of a tile. 333 new tokens of five
+    // merge costs 4 steps and 0.1 per part of a tile. 333 new tokens of five
     // short sequences (100 tiles): 41 us in runs, 17 with a tile per CTA.
     const double one = tiles <= c->sm_count ? FIXED + longest : W / sms + longest / 2.0;
     double best = 1e30;
     for (int div = 1; div <= 4; div *= 2) {
         const long long n = std::max<long long>(1, std::min<long long>((long long)c->sm_count * waves, (base - FIXED * tiles) / MIN_STEPS) / div);
-        const double run = W / n, cost = std::ceil(n / sms) * (FIXED + run) + (n > 1 ? 2.5 + 0.1 * (W / nT) / run : 0);
+        const double run = W / n, cost = std::ceil(n / sms) * (FIXED + run) + (n > 1 ? 4 + 0.1 * (W / nT) / run : 0);
         if (cost < best) {
             best = cost;
             nC = (int)n;

@@ -970,15 +970,16 @@ __global__ void k_copy_tail(const __half *K, const __half *V, __half *rk, __half
 }
 
 // Tokens [from, to) of each sequence's chunk, k, v [B][Hkv][n][d] -> the ring.
-// One 16-byte vector of k and of v per thread and step; y = unit.
+// One 16-byte vector of k and of v per thread and step; `per` CTAs per unit.
 __global__ void k_append_range(const uint4 *__restrict__ k, const uint4 *__restrict__ v, __half *rk, __half *rv, int n,
-                               int Hkv, int d, int ring, int b0, const __grid_constant__ ChunkRange r) {
-    const int x = blockIdx.y / Hkv, u = b0 * Hkv + blockIdx.y, vpr = d / 8;
-    const int from = r.from[x], cnt = (r.to[x] - from) * vpr;
-    for (int e = blockIdx.x * blockDim.x + threadIdx.x; e < cnt; e += gridDim.x * blockDim.x) {
+                               int Hkv, int d, int ring, int b0, int per, const __grid_constant__ ChunkRange r) {
+    const int ul = blockIdx.x / per, x = ul / Hkv, vpr = d / 8;
+    const size_t u = (size_t)b0 * Hkv + ul;
+    const int from = r.from[x], cnt = (r.to[x] - from) * vpr;   // at most G + R tokens
+    for (int e = blockIdx.x % per * blockDim.x + threadIdx.x; e < cnt; e += per * blockDim.x) {
         const int t = from + e / vpr;
-        const size_t src = ((size_t)u * n + t) * vpr + e % vpr;
-        const size_t dst = ((size_t)u * ring + (size_t)(((long long)r.slot[x] + t) % ring)) * vpr + e % vpr;
+        const size_t src = (u * n + t) * vpr + e % vpr;
+        const size_t dst = (u * ring + (size_t)(((long long)r.slot[x] + t) % ring)) * vpr + e % vpr;
         reinterpret_cast<uint4 *>(rk)[dst] = k[src];
         reinterpret_cast<uint4 *>(rv)[dst] = v[src];
     }
@@ -1394,27 +1395,12 @@ cudaError_t launch_append_range(const ott_cache *c, const __half *k, const __hal
                                 const ChunkRange &r, cudaStream_t s) {
     int most = 0;
     for (int x = 0; x < r.n; ++x) most = std::max(most, r.to[x] - r.from[x]);
-    const int th = 256;
-    const long long bx = ((long long)most * (c->d / 8) + th - 1) / th;
-    // grid.y: the units, in rows of at most 65,535
-    for (int y = 0; y < r.n * c->Hkv;) {
-        // whole sequences per launch
-        const int per = std::max(1, 65535 / c->Hkv), x0 = y / c->Hkv, m = std::min(per, r.n - x0);
-        ChunkRange q = r;
-        if (x0 > 0)
-            for (int x = 0; x < m; ++x) {
-                q.from[x] = r.from[x0 + x];
-                q.to[x] = r.to[x0 + x];
-                q.slot[x] = r.slot[x0 + x];
-            }
-        k_append_range<<<dim3((unsigned)std::min<long long>(bx, 1024), (unsigned)(m * c->Hkv)), th, 0, s>>>(
-            reinterpret_cast<const uint4 *>(k), reinterpret_cast<const uint4 *>(v), c->rk, c->rv, n, c->Hkv, c->d,
-            c->ring, b0 + x0, q);
-        const cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-        y += m * c->Hkv;
-    }
-    return cudaSuccess;
+    const int th = 256, per = std::max(1, std::min(64, (most * (c->d / 8) + th - 1) / th));
+    const long long ctas = (long long)r.n * c->Hkv * per;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    k_append_range<<<(unsigned)ctas, th, 0, s>>>(reinterpret_cast<const uint4 *>(k), reinterpret_cast<const uint4 *>(v), c->rk,
+                                                 c->rv, n, c->Hkv, c->d, c->ring, b0, per, r);
+    return cudaGetLastError();
 }
 
 cudaError_t launch_copy_tail_units(const ott_cache *c, const __half *K, const __half *V, int u0, int nu,

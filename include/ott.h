@@ -341,9 +341,12 @@ int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t 
  * appends would give it if none of them flushed. The cache is read only and
  * may be empty, in part or whole (plain causal attention over the chunk).
  * out may not alias q, k or v.
- * Softmax statistics and sums are fp32; the weights and the dequantized
- * values are rounded to fp16 for the tensor cores (each at most 2^-11
- * relative). Keys and values are served up to a magnitude of 48,000.
+ * Softmax statistics and sums are fp32; with more than four query rows per
+ * kv head (n * Hq / Hkv) the weights and the dequantized values are rounded
+ * to fp16 for the tensor cores (each at most 2^-11 relative). Keys and
+ * values, the chunk's too, are finite and at most 48,000 in magnitude: a
+ * value that is not finite spoils rows that do not see it as well. A call
+ * gives the same bits every time.
  * Partial results go to the cache's split-K scratch, or where they are
  * larger to stream-ordered scratch from the library's pool (see ott_prefill;
  * OTT_ERR_OOM if none can be had, before anything is queued).
@@ -364,7 +367,8 @@ int ott_append_chunk(ott_cache *c, const void *k, const void *v, int n, const in
 /*
  * ott_decode_attn with a window: one query per sequence, at the position of
  * the last token appended (p = T_b - 1). q, out: DEVICE fp16 [B][Hq][d].
- * Precision and scratch as ott_chunk_attn.
+ * A query whose every token in sight a policy has discarded gets zeros.
+ * Precision and scratch as ott_chunk_attn; OTT_ERR_STATE as ott_decode_attn.
  */
 int ott_decode_attn_window(ott_cache *c, const void *q, void *out, int window, int sinks, void *stream);
 
