@@ -211,7 +211,8 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
         } else {
             const int jp = c.jp, k = c.k;
             const int j = jp < s.nsink ? __ldg(a.sel + (size_t)u * a.NB + jp) : s.jlo + jp - s.nsink;
-            const int rem = j < 0 ? 0 : min(CT, chunk_block_cnt(a, u, j) - CT * k);
+            // of a listed block, the first tokens: they come first
+            const int rem = j < 0 ? 0 : min(CT, (jp < s.nsink ? min(a.sinks, chunk_block_cnt(a, u, j)) : chunk_block_cnt(a, u, j)) - CT * k);
             if (rem > 0) {
                 m = make_int2(rem, j);
                 if (lane == 0) {

@@ -94,7 +94,8 @@ struct Tile {
     int rows;                 // valid rows
     int jlo;                  // blocks [jlo, nf) and the listed ones before
     int nlo;                  // first group of new tokens that is seen
-    int gq, gf, gn;           // groups: quantized, fp16 (ring, pool, cold pool), new
+    int cps, gs;              // groups per listed block, of all listed blocks
+    int gq, gf, gn;           // groups: quantized (the listed blocks' first), fp16 (ring, pool, cold pool), new
     int sq, steps;            // steps of quantized groups, then of the others; all steps
 };
 
@@ -111,7 +112,10 @@ __host__ __device__ inline void tile_extent(const ChunkArgs &a, int cpt, const C
         // new tokens before the window (none of them a first token of the sequence)
         if (s.T >= a.sinks && lo > s.T) t.nlo = (lo - s.T) / 16;
     }
-    t.gq = (s.nf - t.jlo + (t.jlo > 0 ? s.nsink : 0)) * cpt;
+    // of a listed block, only the groups that can hold first tokens (they come first)
+    t.cps = a.sinks / 16 < cpt ? (a.sinks + 15) / 16 : cpt;
+    t.gs = t.jlo > 0 ? s.nsink * t.cps : 0;
+    t.gq = t.gs + (s.nf - t.jlo) * cpt;
     t.gf = (s.ntail + s.npool + a.C + 15) / 16;
     t.gn = s.nnew > 0 ? last / 16 + 1 - t.nlo : 0;
     t.sq = (t.gq + GRPS - 1) / GRPS;
@@ -324,6 +328,7 @@ struct Group {
     int j;                 // its number, -1: none
     int sub;               // group of the block
     int left;              // valid tokens of the block from the group's first on (<= 0: none)
+    int per;               // groups of the block
 };
 __device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s, const Tile &t, int cpt, int u, int x) {
     Group g;
@@ -331,19 +336,23 @@ __device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s,
         g.src = nullptr;
         g.j = -1;
         g.sub = g.left = 0;
+        g.per = cpt;
         return g;
     }
-    const int ns = t.jlo > 0 ? s.nsink : 0, jp = x / cpt;
-    g.sub = x % cpt;
+    const bool listed = x < t.gs;
+    const int per = listed ? t.cps : cpt, y = listed ? x : x - t.gs, jp = y / per;
+    g.sub = y % per;
+    g.per = per;
     g.left = 0;
     g.src = nullptr;
-    g.j = t.jlo + jp - ns;
-    if (jp < ns) {
+    g.j = t.jlo + jp;
+    if (listed) {
         g.j = __ldg(a.sel + (size_t)u * a.NB + jp);
         if (g.j >= t.jlo) g.j = -1;   // in the window's own range
     }
     if (g.j >= 0) {
-        g.left = chunk_block_cnt(a, u, g.j) - 16 * g.sub;
+        const int cnt = chunk_block_cnt(a, u, g.j);
+        g.left = (listed ? min(cnt, a.sinks) : cnt) - 16 * g.sub;
         const size_t own = (size_t)u * a.NB + g.j;
         g.src = a.blk + (a.bt ? (size_t)__ldg(a.bt + own) : own) * a.blk_bytes;
     }
@@ -419,7 +428,7 @@ struct Producer {
         Group g, gn, gb;             // made, next, first of the next block
         uint4 hb = make_uint4(0, 0, 0, 0);   // gb's
         int xb = -1;                 // gb's number
-        g.left = g.sub = 0;
+        g.left = g.sub = g.per = 0;
         g.j = -1;
         g.src = nullptr;
         gn = gb = g;
@@ -428,7 +437,7 @@ struct Producer {
 #pragma unroll 1
         for (int k = -1; k < n; ++k) {
             bool enter = false;
-            if (g.left > 16 && g.sub + 1 < cpt) {
+            if (g.left > 16 && g.sub + 1 < g.per) {
                 gn.sub += 1;
                 gn.left -= 16;
             } else if (k + 1 < n) {
@@ -496,7 +505,7 @@ struct Producer {
                         ks2[kt][o] = __byte_perm(z.x, z.y, 0x5410);
                     }
                 fresh = 2;   // both slots
-                xb = x + k + 1 - gn.sub + cpt;
+                xb = x + k + 1 - gn.sub + gn.per;
                 if (xb < x + n) {
                     gb = group_at(a, s, t, cpt, u, xb);
                     if (gb.left > 0 && lane < D / 4) hb = __ldg(reinterpret_cast<const uint4 *>(gb.src) + lane);

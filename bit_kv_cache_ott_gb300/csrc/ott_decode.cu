@@ -365,7 +365,9 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
     auto cnt_at = [&](int j) -> int {
         if constexpr (MS) {
             const int bj = block_of(j);
-            return bj < 0 ? 0 : block_cnt<CO, true>(a, u, bj);
+            if (bj < 0) return 0;
+            const int n = block_cnt<CO, true>(a, u, bj);
+            return j < ru.s->nsink ? min(n, a.sinks) : n;   // a listed block: its first tokens come first
         }
         if constexpr (TK) {
             const int bj = __ldg(a.sel + (size_t)u * a.Ksel + j);
@@ -383,7 +385,11 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
     // move to the next chunk that holds tokens (or past the segment)
     auto settle = [&](Cursor &c) {
         while (!past(c) && CT * c.k >= c.cnt) {
-            ++c.j;
+            // the list ends with its first empty slot
+            if (MS && c.j < ru.s->nsink && c.cnt == 0)
+                c.j = ru.s->nsink;
+            else
+                ++c.j;
             c.k = 0;
             c.cnt = c.j <= jl ? cnt_at(c.j) : 0;
         }
