@@ -285,11 +285,6 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t at, uint32_t b, uint
         "r"(at), "r"(b), "r"(hi), "r"(idesc), "r"((uint32_t)acc)
         : "memory");
 }
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-    uint32_t y;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
 
 // ---------------------------------------------------------------- producers
 // Orders within the tiles. Scores do not depend on the order of the channels
