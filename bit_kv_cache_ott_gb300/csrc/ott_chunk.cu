@@ -23,6 +23,11 @@
 // copies run ahead of the products through a ring of stages that does not
 // stop at the borders of units. A warp leaves one partial (max, sum,
 // unnormalised output) per unit that it touches; k_chunk_combine merges them.
+//
+// What bounds it: the instructions that unpack codes into operands, of which
+// 8 or 16 columns of products do not make enough use; the copies run ahead
+// and HBM waits. Batch 32 x 4K, 32 heads of d = 128 (405 MB of cache): 184 us
+// with 4 rows (NC = 1) and 188 with 8, 2.2 TB/s; 258 with 16 rows (NC = 2).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -36,8 +41,13 @@ namespace {
 constexpr float GROW = 8.0f;                // log2: see rescale
 constexpr int FI = 8;                       // fp16 tokens per work item
 constexpr int CT = CHUNK_TILES * TILE;      // block slots per work item
-constexpr int DEC_ROWS_MAX = 4;             // query rows per kv head up to which the decode kernel serves a call
-constexpr int ROWS_MAX = 16;                // query rows per kv head up to which this kernel serves a call
+// Query rows per kv head up to which the decode kernel (its rows mode) and
+// then this file's kernel serve a call; the tcgen05 tiles take the rest. Batch
+// 32 x 4K, 32 heads: 4 rows 131 us in rows mode, 184 here (rows mode has one
+// slice of up to 4 rows and would read the cache twice for 5); 16 rows 258 us
+// here; 17 rows 453 us in tiles (256 rows at the same price), about 516 here
+// in two slices.
+constexpr int DEC_ROWS_MAX = 4, ROWS_MAX = 16;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {

@@ -32,15 +32,20 @@
 // tail (a tile cut between CTAs leaves partials, merged by k_tiles_combine),
 // or a tile of its own, whichever is estimated to end first (plan_tiles).
 //
-// What bounds it: a step is 1,920 cycles of products (the key tile's 16 extra
-// rows among them); the products alone, with nothing made and no softmax,
-// take 704 us for 2,048 tokens over 32K (8 kv heads, 4 heads each), all of it
-// 835 us: the producers' and the softmax's instructions share the schedulers
-// with one another. Dequantizing to fp16 in a pass of its own instead would
-// write six times the cache's bytes and read them for every pair of tiles; three tiles of rows or a second
-// softmax set do not fit TMEM; a sixth of the tokens less per step buys exact
-// values (their zeros and scales as further rows) but sums that cancel, and
-// lost accuracy over 131K tokens to the truncating accumulators.
+// What bounds it: 2,048 tokens over 32K (8 kv heads, 4 heads each, d = 128)
+// take 820 us, 1.37 PFLOP/s of the sums that are asked for; without the
+// softmax 657 us, without unpacking 762, without either 644 (a step's products
+// are 1,920 cycles, the key tile's 16 extra rows among them). So the softmax
+// and the producers, who share the schedulers, hold the tensor cores up by a
+// fifth. With short caches a tile's fixed cost joins them: finding it and its
+// queries, the first copies, the output: 7 us. Not taken: dequantizing to
+// fp16 in a pass of its own (six times the cache's bytes written, and read
+// for every pair of tiles); three tiles of rows or a second softmax set (do
+// not fit TMEM); exact values, their zeros and scales as further rows (a
+// sixth fewer tokens per step, and sums that cancel, which lost accuracy over
+// 131K tokens to the truncating accumulators); both score sets for alternate
+// steps of a pair with one tile of rows (134 us for 128 rows of 256 heads
+// over 4K, with or without: the producers are what it waits for).
 #include <algorithm>
 #include <climits>
 #include <cmath>

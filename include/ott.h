@@ -377,8 +377,9 @@ int ott_decode_attn_window(ott_cache *c, const void *q, void *out, int window, i
  * and columns of an image; one axis for text). q, q_out: DEVICE fp16
  * [B][Hq][n][d]; k, k_out: DEVICE fp16 [B][Hkv][n][d]; pos: DEVICE int32
  * [axes][B][n], any values. Hq or Hkv may be 0 (its pointers are then
- * ignored). An output may be its input (in place) but may not overlap it
- * otherwise. d: a multiple of 16 up to 256. A call rotates all n rows.
+ * ignored). An output may be its input (in place); otherwise it lies apart
+ * from all that the call reads or writes (OTT_ERR_INVALID). d: a multiple of
+ * 16 up to 256. A call rotates all n rows.
  * The plan: sections[a] >= 1 pairs of channels turn with axis a, axis by
  * axis; half = their sum <= d / 2. Pair i is channels (i, half + i), or
  * (2i, 2i + 1) if interleaved; channels from 2 * half on are copied. Pair i

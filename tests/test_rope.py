@@ -95,6 +95,22 @@ def test_refusals():
         assert call(**kw) == pkg.OTT_ERR_INVALID, kw
 
 
+def test_outputs_apart_from_everything_else():
+    """An output on the other operand, on the other output or on the positions is refused; neighbours are not."""
+    L = pkg.load(build_if_missing=True)
+    a, nq, nk = 1 << 20, 2 * 4 * 64 * 2, 4 * 64 * 2   # two heads of four tokens, one head
+    o, pos = 1 << 24, 1 << 28
+    plan = _plan()
+
+    def call(q, qo, k, ko, pos, n=4):
+        return L.ott_rope(q, qo, 2, k, ko, 1, pos, 1, n, 64, C.byref(plan), None)
+
+    for q, qo, k, ko, ps in [(a, o, o, o, pos), (a, o, o + nq - 16, o + nq - 16, pos), (a, o, o + (1 << 20), o + nq - 16, pos),
+                             (a, a, o, a + 16, pos), (a, a, o, a + nq - 16, pos), (a, o, a + (1 << 19), a - nk + 16, pos),
+                             (a, o, o + nq, o + nq, o), (a, o, o + nq, o + nq, o + nq + nk - 4)]:
+        assert call(q, qo, k, ko, ps) == pkg.OTT_ERR_INVALID, (q, qo, k, ko, ps)
+
+
 def test_null_caches_are_refused():
     L = pkg.load(build_if_missing=True)
     assert L.ott_chunk_attn(None, None, None, None, None, 1, None, 0, 0, None) == pkg.OTT_ERR_INVALID
