@@ -717,10 +717,10 @@ int ott_append_chunk(ott_cache *c, const void *k, const void *v, int n, const in
     const __half *kh = static_cast<const __half *>(k), *vh = static_cast<const __half *>(v);
     // Two flushes or more: all of them in one pass where that is faster than
     // a round of launches each. A pass covers the whole uniform batch, or one
-    // sequence (five launches, about 25 us); a round covers every sequence (a
+    // sequence (four launches, about 25 us); a round covers every sequence (a
     // copy and a flush, about 17 us while its units fit the SMs). A prompt of
     // 8192 tokens in chunks of 1024, 8 units: 1.08 ms of appends in rounds,
-    // 0.33 ms in passes.
+    // 0.24 ms in passes.
     {
         int most = 0, active = 0;
         bool ok = true;

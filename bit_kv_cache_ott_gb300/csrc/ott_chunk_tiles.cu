@@ -1038,7 +1038,11 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
     // the tile: x = (pair of the largest sequence, 32 rows), y = kv head, z = entry
     const ChunkSeq &s = st.e[blockIdx.z];
     const int p = blockIdx.x / 8, row = 32 * (blockIdx.x % 8) + lane;
-    if (p >= s.S) return;
+    // (a CTA with nothing to merge waits, too: this grid ends behind the tiles)
+    if (p >= s.S) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     Tile t;
     long long ts = s.base + (long long)blockIdx.y * s.Iu;
     {
@@ -1052,11 +1056,10 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
         ts += before;
     }
     tile_extent(a, ta.CPT, s, p, t);
-    if (32 * (blockIdx.x % 8) >= t.rows) return;
     const int c0 = ch_warp_of(ta.W, ta.nC, ts + FIXED), c1 = ch_warp_of(ta.W, ta.nC, ts + FIXED + t.steps - 1);
-    if (c0 == c1) return;   // written whole
     const int slot0 = ch_range_start(ta.W, ta.nC, c0) < ts ? 1 : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (32 * (blockIdx.x % 8) >= t.rows || c0 == c1) return;   // no rows; written whole
     constexpr int CH = D / 8;
     float M = -CUDART_INF_F, L = 0.0f, acc[CH];
 #pragma unroll
@@ -1102,10 +1105,10 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
 }
 
 template <int D>
-cudaError_t launch_t(const TileArgs &ta, const ChunkTable &st, int pairs, cudaStream_t s) {
+cudaError_t launch_t(const TileArgs &ta, const ChunkTable &st, int rows, cudaStream_t s) {
     cudaError_t e = launch_pdl(k_chunk_tiles<D>, dim3((unsigned)ta.nC), THREADS, (size_t)TCfg<D>::SMEM, s, ta, st);
     if (e != cudaSuccess || ta.nC == 1 || ta.whole) return e;
-    return launch_pdl(k_tiles_combine<D>, dim3(8u * pairs, (unsigned)ta.a.Hkv, (unsigned)ta.a.nseq), 256, 0, s, ta, st);
+    return launch_pdl(k_tiles_combine<D>, dim3((unsigned)((rows + 31LL) / 32), (unsigned)ta.a.Hkv, (unsigned)ta.a.nseq), 256, 0, s, ta, st);
 }
 
 }  // namespace
@@ -1150,14 +1153,16 @@ bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, bool 
     // 131K-token chunk (3.14 ms without).
     const double sms = c->sm_count, W = (double)base, nT = (double)tiles;
     const long long waves = std::max<long long>(1, std::min<long long>(MAX_WAVES, (base + (long long)c->sm_count * MAX_STEPS - 1) / ((long long)c->sm_count * MAX_STEPS)));
-    // Equal runs of places, or a tile per CTA: by their estimated times. A
-    // merge costs 4 steps and 0.1 per part of a tile. 333 new tokens of five
-    // short sequences (100 tiles): 41 us in runs, 17 with a tile per CTA.
-    const double one = tiles <= c->sm_count ? FIXED + longest : W / sms + longest / 2.0;
+    // Equal runs of places, or a tile per CTA: by their estimated times. Cut
+    // tiles and their merge cost 8 steps and 0.1 per part of a tile. 333 new
+    // tokens of five short sequences (100 tiles): 41 us in runs, 17 with a
+    // tile per CTA; 1,024 tokens (128 tiles) over 2,048: 70 and 66, over
+    // 4,096: 91.3 and 90.4, over 7,168: 123 and 127.
+    const double one = std::max<double>(FIXED + longest, std::min(W / sms + longest / 2.0, std::ceil(nT / sms) * (FIXED + longest)));
     double best = 1e30;
     for (int div = 1; div <= 4; div *= 2) {
         const long long n = std::max<long long>(1, std::min<long long>((long long)c->sm_count * waves, (base - FIXED * tiles) / MIN_STEPS) / div);
-        const double run = W / n, cost = std::ceil(n / sms) * (FIXED + run) + (n > 1 ? 4 + 0.1 * (W / nT) / run : 0);
+        const double run = W / n, cost = std::ceil(n / sms) * (FIXED + run) + (n > 1 ? 8 + 0.1 * (W / nT) / run : 0);
         if (cost < best) {
             best = cost;
             nC = (int)n;
@@ -1177,9 +1182,9 @@ cudaError_t launch_tiles(const ott_cache *c, const ChunkArgs &a, const ChunkTabl
     ta.W = a.W;
     ta.part = a.part;
     ta.whole = whole;
-    int pairs = 0;
-    for (int x = 0; x < a.nseq; ++x) pairs = std::max(pairs, st.e[x].S);
-    return c->d == 128 ? launch_t<128>(ta, st, pairs, s) : launch_t<64>(ta, st, pairs, s);
+    int rows = 0;
+    for (int x = 0; x < a.nseq; ++x) rows = std::max(rows, st.e[x].nq * a.g);   // at most Hq * n
+    return c->d == 128 ? launch_t<128>(ta, st, rows, s) : launch_t<64>(ta, st, rows, s);
 }
 
 }  // namespace ott

@@ -144,8 +144,12 @@ struct ChunkFlushes {
     int off, j0, ring;
     long long T, t_first;         // t_first: first token of group j0
     const __half *rk, *rv;        // [U][ring][d]
-    const uint64_t *gtop;         // [nu][lists][P] each list's keys
-    const __half *pk, *pv;        // [nu][P][d] the old pool's rows
+    uint64_t *gtop;               // [nu][lists][P] each list's keys
+    __half *pk, *pv;              // [nu][P][d] the old pool's rows
+    int nu, np;                   // units of the pass, tokens in the old pool
+    const float *opnorm;          // the old pool: [U][P], [U][P][d]
+    const int32_t *opidx;
+    const __half *opk, *opv;
 };
 // Where token t of unit u (the uu-th of the pass) lies; `key` is its (norm, index).
 template <int D>
@@ -202,6 +206,7 @@ struct FlushArgs {
 template <int D, bool SW>
 __global__ void __launch_bounds__(FLUSH_THREADS, 2) k_flush(FlushArgs a, const __grid_constant__ FlushList fl) {
     extern __shared__ __align__(16) uint8_t smem[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // Staged rows are D halves, unpadded; the 16-byte chunks of row r are
     // permuted by XOR with r mod 8 (SWZ), so that the same chunk of 8
     // consecutive rows falls on 8 different bank groups.
@@ -624,6 +629,8 @@ inline size_t pf_group_smem_bytes(int d, int G) { return (size_t)G * (d + 8) * 2
 // summed in fp32 in channel order exactly as k_flush sums them, and the
 // group's min(P, G) smallest keys, ascending (no other group token can be in
 // the pool after this group's flush).
+// For a chunk, `nu` CTAs more take the old pools: their keys into list 0,
+// their rows aside.
 template <int D>
 __global__ void __launch_bounds__(PF_THREADS) k_pf_group(const __half *__restrict__ srcK, long long src_unit_stride,
                                                          int src_u0, int u0, int nf, int G, int P,
@@ -635,6 +642,19 @@ __global__ void __launch_bounds__(PF_THREADS) k_pf_group(const __half *__restric
     extern __shared__ __align__(16) uint8_t pf_sm[];
     __half *rows = reinterpret_cast<__half *>(pf_sm);
     uint64_t *gkey = reinterpret_cast<uint64_t *>(pf_sm + (size_t)G * RS * 2);   // [G]
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (cf.off && (int)blockIdx.x >= cf.nu * nf) {
+        const int uu = blockIdx.x - cf.nu * nf;
+        const size_t u = u0 + uu;
+        for (int k = threadIdx.x; k < cf.np; k += blockDim.x)
+            gtop[(size_t)uu * cf.lists * P + k] = ((uint64_t)__float_as_uint(cf.opnorm[u * P + k]) << 32) | (uint32_t)cf.opidx[u * P + k];
+        for (int e = threadIdx.x; e < cf.np * VPR; e += blockDim.x) {
+            reinterpret_cast<uint4 *>(cf.pk)[(size_t)uu * P * VPR + e] = reinterpret_cast<const uint4 *>(cf.opk)[u * P * VPR + e];
+            reinterpret_cast<uint4 *>(cf.pv)[(size_t)uu * P * VPR + e] = reinterpret_cast<const uint4 *>(cf.opv)[u * P * VPR + e];
+        }
+        return;
+    }
     const int uu = blockIdx.x / nf, j = blockIdx.x % nf, u = u0 + uu;
     const long long t0 = cf.t_first + (long long)j * G;
     const __half *unit = srcK + (size_t)(u - src_u0) * src_unit_stride;   // its row 0 is token T (a prompt: 0)
@@ -669,23 +689,6 @@ __global__ void __launch_bounds__(PF_THREADS) k_pf_group(const __half *__restric
         int r = 0;
         for (int q = 0; q < G; ++q) r += gkey[q] < k;
         if (r < nb) dst[r] = k;
-    }
-}
-
-
-// The old pool of every unit of a chunk's flushes: its keys into list 0, its
-// rows aside. One CTA per unit.
-__global__ void __launch_bounds__(PF_THREADS) k_cf_pool(const float *__restrict__ pnorm, const int32_t *__restrict__ pidx,
-                                                        const uint4 *__restrict__ pk, const uint4 *__restrict__ pv, int u0,
-                                                        int P, int np, int vpr, uint64_t *__restrict__ gtop, int lists,
-                                                        uint4 *__restrict__ dk, uint4 *__restrict__ dv) {
-    const int uu = blockIdx.x, u = u0 + uu;
-    for (int k = threadIdx.x; k < np; k += blockDim.x)
-        gtop[(size_t)uu * lists * P + k] =
-            ((uint64_t)__float_as_uint(pnorm[(size_t)u * P + k]) << 32) | (uint32_t)pidx[(size_t)u * P + k];
-    for (int e = threadIdx.x; e < np * vpr; e += blockDim.x) {
-        dk[(size_t)uu * P * vpr + e] = pk[(size_t)u * P * vpr + e];
-        dv[(size_t)uu * P * vpr + e] = pv[(size_t)u * P * vpr + e];
     }
 }
 
@@ -751,6 +754,8 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) k_pf_scan(const uint64_t *__r
                                                              uint64_t *__restrict__ phist, int nf_unit, int G, int P,
                                                              int cg, int C, uint64_t *__restrict__ gtot) {
     extern __shared__ uint64_t scan_sm[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const int uu = blockIdx.x / C, cc = blockIdx.x % C;
     uint64_t *A = scan_sm + (size_t)w * (2 + SCAN_AHEAD) * P, *Cn = A + P, *ring = Cn + P;
@@ -849,6 +854,8 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) k_pf_carry(uint64_t *__restri
                                                               const uint64_t *__restrict__ gtot, int nf, int G,
                                                               int P, int cg, int C) {
     extern __shared__ uint64_t car_sm[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ int cnt[2][CARRY_MAX_CHUNKS];
     const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
     const int uu = blockIdx.x / (C - 1), c = blockIdx.x % (C - 1) + 1;
@@ -973,6 +980,9 @@ __global__ void k_copy_tail(const __half *K, const __half *V, __half *rk, __half
 // One 16-byte vector of k and of v per thread and step; `per` CTAs per unit.
 __global__ void k_append_range(const uint4 *__restrict__ k, const uint4 *__restrict__ v, __half *rk, __half *rv, int n,
                                int Hkv, int d, int ring, int b0, int per, const __grid_constant__ ChunkRange r) {
+    // a call queued next may start now; it waits for this grid
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int ul = blockIdx.x / per, x = ul / Hkv, vpr = d / 8;
     const size_t u = (size_t)b0 * Hkv + ul;
     const int from = r.from[x], cnt = (r.to[x] - from) * vpr;   // at most G + R tokens
@@ -1170,13 +1180,11 @@ FlushArgs flush_args(const ott_cache *c, const __half *srcK, const __half *srcV,
 
 cudaError_t run_flush(const ott_cache *c, const FlushArgs &a, const FlushList &fl, int ctas, cudaStream_t s) {
     const int smem = flush_smem_bytes(c->d, c->G, c->P);
-    if (c->d == 128)
-        flush_swizzled(c) ? k_flush<128, true><<<ctas, FLUSH_THREADS, smem, s>>>(a, fl)
-                          : k_flush<128, false><<<ctas, FLUSH_THREADS, smem, s>>>(a, fl);
-    else
-        flush_swizzled(c) ? k_flush<64, true><<<ctas, FLUSH_THREADS, smem, s>>>(a, fl)
-                          : k_flush<64, false><<<ctas, FLUSH_THREADS, smem, s>>>(a, fl);
-    return cudaGetLastError();
+    // (a programmatic dependent: it waits for the kernel before it, and never
+    // releases its own dependents early)
+    auto kern = c->d == 128 ? (flush_swizzled(c) ? k_flush<128, true> : k_flush<128, false>)
+                            : (flush_swizzled(c) ? k_flush<64, true> : k_flush<64, false>);
+    return launch_pdl(kern, dim3((unsigned)ctas), FLUSH_THREADS, (size_t)smem, s, a, fl);
 }
 
 }  // namespace
@@ -1259,16 +1267,15 @@ static cudaError_t run_pf_scan(const ott_cache *c, const uint64_t *gtop, uint64_
     int sw = (cg + 4 - 1) / 4;
     sw = sw < 1 ? 1 : (sw > SCAN_WARPS ? SCAN_WARPS : sw);
     while (sw > 1 && scan_smem_bytes(sw, P) > (size_t)optin) --sw;
-    k_pf_scan<<<nu * C, 32 * sw, scan_smem_bytes(sw, P), s>>>(gtop, phist, nl, G, P, cg, C, gtot);
-    e = cudaGetLastError();
+    e = launch_pdl(k_pf_scan, dim3((unsigned)(nu * C)), 32 * sw, scan_smem_bytes(sw, P), s, gtop, phist, nl, G, P, cg, C, gtot);
     if (e != cudaSuccess) return e;
     if (C > 1) {
         int cw = cg < SCAN_WARPS ? cg : SCAN_WARPS;
         const size_t room = (size_t)optin - sizeof(int) * 2 * CARRY_MAX_CHUNKS;   // after the static counts
         while (cw > 1 && carry_smem_bytes(C, cw, P) > room) --cw;
         if (carry_smem_bytes(C, cw, P) > room) return cudaErrorInvalidValue;
-        k_pf_carry<<<nu * (C - 1), 32 * cw, carry_smem_bytes(C, cw, P), s>>>(phist, gtot, nl, G, P, cg, C);
-        e = cudaGetLastError();
+        e = launch_pdl(k_pf_carry, dim3((unsigned)(nu * (C - 1))), 32 * cw, carry_smem_bytes(C, cw, P), s, phist, gtot, nl, G, P,
+                       cg, C);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;
@@ -1293,7 +1300,7 @@ cudaError_t launch_chunk_flushes(const ott_cache *c, const __half *k, const __ha
     const int G = c->G, P = c->P, off = j0 > 0 && P > 0, nl = groups + off;
     uint64_t *gtop = scratch, *phist = scratch + (size_t)nu * nl * P;
     const long long ctas = (long long)nu * groups;
-    if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    if (ctas + nu > 0x7fffffffLL) return cudaErrorInvalidValue;
     // the old pool's rows: behind the lists and the scan's totals
     uint4 *rows = reinterpret_cast<uint4 *>((reinterpret_cast<uintptr_t>(scratch) + prefill_scratch_bytes(c, nu, nl) + 15) & ~(uintptr_t)15);
     ChunkFlushes cf = {};
@@ -1306,22 +1313,18 @@ cudaError_t launch_chunk_flushes(const ott_cache *c, const __half *k, const __ha
     cf.rk = c->rk;
     cf.rv = c->rv;
     cf.gtop = gtop;
-    cf.pk = reinterpret_cast<const __half *>(rows);
+    cf.pk = reinterpret_cast<__half *>(rows);
     cf.pv = cf.pk + (size_t)nu * P * c->d;
+    cf.nu = nu;
+    cf.np = pool_after(P, G, j0);
+    cf.opnorm = c->pnorm;
+    cf.opidx = c->pidx;
+    cf.opk = c->pk;
+    cf.opv = c->pv;
     cudaError_t e = cudaSuccess;
     if (P > 0) {
-        const int vpr = c->d / 8;
-        if (off)
-            k_cf_pool<<<nu, PF_THREADS, 0, s>>>(c->pnorm, c->pidx, reinterpret_cast<const uint4 *>(c->pk),
-                                                reinterpret_cast<const uint4 *>(c->pv), u0, P, pool_after(P, G, j0), vpr, gtop,
-                                                nl, rows, rows + (size_t)nu * P * vpr);
-        if (c->d == 128)
-            k_pf_group<128><<<(int)ctas, PF_THREADS, pf_group_smem_bytes(128, G), s>>>(k, (long long)n * 128, 0, u0, groups, G,
-                                                                                       P, gtop, cf);
-        else
-            k_pf_group<64><<<(int)ctas, PF_THREADS, pf_group_smem_bytes(64, G), s>>>(k, (long long)n * 64, 0, u0, groups, G, P,
-                                                                                     gtop, cf);
-        e = cudaGetLastError();
+        e = launch_pdl(c->d == 128 ? k_pf_group<128> : k_pf_group<64>, dim3((unsigned)(ctas + off * nu)), PF_THREADS,
+                       pf_group_smem_bytes(c->d, G), s, k, (long long)n * c->d, 0, u0, groups, G, P, gtop, cf);
         if (e == cudaSuccess) e = run_pf_scan(c, gtop, phist, nu, nl, s);
         if (e != cudaSuccess) return e;
     }
@@ -1398,9 +1401,8 @@ cudaError_t launch_append_range(const ott_cache *c, const __half *k, const __hal
     const int th = 256, per = std::max(1, std::min(64, (most * (c->d / 8) + th - 1) / th));
     const long long ctas = (long long)r.n * c->Hkv * per;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
-    k_append_range<<<(unsigned)ctas, th, 0, s>>>(reinterpret_cast<const uint4 *>(k), reinterpret_cast<const uint4 *>(v), c->rk,
-                                                 c->rv, n, c->Hkv, c->d, c->ring, b0, per, r);
-    return cudaGetLastError();
+    return launch_pdl(k_append_range, dim3((unsigned)ctas), th, 0, s, reinterpret_cast<const uint4 *>(k),
+                      reinterpret_cast<const uint4 *>(v), c->rk, c->rv, n, c->Hkv, c->d, c->ring, b0, per, r);
 }
 
 cudaError_t launch_copy_tail_units(const ott_cache *c, const __half *K, const __half *V, int u0, int nu,

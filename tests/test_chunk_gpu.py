@@ -60,6 +60,35 @@ CHUNKS = [
 ]
 
 
+CHUNKS += [
+    # up to four rows per kv head: every kind, some sequences with nothing, windows, listed blocks
+    ("ragged", 4, 4, 2, 128, 32, 4, 6, [0, 1, 37, 333], [2, 0, 1, 2], 0, 0),
+    ("ragged", 4, 3, 1, 64, 16, 3, 5, [90, 0, 300, 7], [1, 1, 1, 0], 40, 3),
+    ("paged", 3, 2, 2, 128, 32, 8, 8, [5, 400, 129], [4, 1, 0], 0, 0),
+    ("paged", 3, 4, 4, 64, 16, 4, 8, [50, 333, 129], [3, 4, 2], 30, 20),
+    ("cold", 2, 4, 2, 128, 32, 4, 8, 400, 2, 0, 0),
+    ("cold", 1, 4, 4, 64, 16, 4, 8, 333, 3, 90, 40),
+    ("pct", 2, 4, 2, 128, 32, 4, 16, 400, 2, 120, 3),
+    ("uniform", 2, 3, 1, 128, 17, 3, 4, 300, 1, 0, 0),           # odd group
+    ("uniform", 2, 3, 1, 64, 40, 3, 4, 500, 1, 100, 33),         # first tokens over a tile, not over the block
+    # five to sixteen
+    ("ragged", 4, 4, 2, 64, 32, 4, 6, [2, 80, 37, 533], [8, 0, 1, 5], 50, 4),
+    ("paged", 2, 8, 1, 128, 40, 8, 8, [77, 400], [2, 1], 120, 33),
+    ("cold", 2, 4, 1, 128, 32, 4, 8, 400, 4, 90, 5),
+    ("pct", 1, 10, 2, 64, 32, 4, 16, 333, 3, 0, 0),
+    ("uniform", 1, 16, 1, 128, 200, 9, 32, 900, 1, 300, 70),
+    # seventeen and more: every kind, heads that do not divide a tile, more heads than a pair of tiles has rows
+    ("paged", 2, 6, 2, 128, 40, 8, 8, [77, 400], [90, 6], 120, 33),
+    ("cold", 2, 4, 1, 128, 32, 4, 8, 400, 70, 0, 0),
+    ("pct", 1, 10, 2, 128, 32, 4, 16, 333, 61, 0, 0),
+    ("uniform", 1, 300, 1, 64, 32, 4, 6, 300, 2, 0, 0),
+    ("uniform", 1, 17, 1, 128, 100, 4, 6, 700, 1, 0, 0),
+    ("uniform", 2, 8, 2, 64, 100, 4, 6, 1500, 130, 500, 90),     # listed blocks of several groups
+    ("uniform", 19, 8, 8, 64, 32, 4, 6, 200, 17, 0, 0),          # as many equal tiles as SMs
+    ("uniform", 38, 8, 8, 64, 32, 4, 6, 200, 17, 0, 0),          # twice as many
+]
+
+
 @pytest.mark.parametrize("kind,B,Hq,Hkv,d,G,R,P,T,n,window,sinks", CHUNKS)
 def test_chunk_attn(ott, kind, B, Hq, Hkv, d, G, R, P, T, n, window, sinks):
     lens = n if isinstance(n, list) else None
