@@ -780,7 +780,16 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
         const long long T = c->ragged ? c->Tb[b] : c->T, seen = call.window > 0 ? std::min<long long>(T, (long long)call.window + nq) : T;
         blocks += (seen / c->G + 1) * c->Hkv * ((nq * (long long)c->gq + RB - 1) / RB);
     }
-    p.ipb = p.gs && blocks < (long long)c->sm_count * DEC_WARPS ? 1 : a.CPB;
+    const bool few = p.gs && blocks < (long long)c->sm_count * DEC_WARPS;
+    p.ipb = few ? 1 : a.CPB;
+    // Most slots of the list are empty (the first tokens share their first
+    // block, but any of them may have passed through the pool into a later
+    // one). With an item each, empty slots are warps' shares that others
+    // could have worked on: batch 32 x 4K, window 1,024, four first tokens,
+    // 61 us, and 56 with 8 slots an item. With warps to spare, a warp would
+    // read 8 blocks one behind the other: one sequence of 131K, window 4,096,
+    // 16 first tokens, 27 us, and 17 with an item each.
+    a.spi = few ? 1 : 8;
     const int fi = p.gs ? FP16_CHUNK : FI;
     long long base = 0, units = 0;
     int min_iu = INT_MAX;
@@ -808,7 +817,7 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
             s.nsink = std::min(a.sinks, s.jlo);
         }
         s.Sf = (int)(((long long)s.ntail + s.npool + a.C + s.nnew + fi - 1) / fi);
-        const long long iu = s.Sf + (long long)(s.nf - s.jlo + s.nsink) * p.ipb;
+        const long long iu = s.Sf + (p.gs ? (s.nsink + a.spi - 1) / a.spi : (long long)s.nsink * p.ipb) + (long long)(s.nf - s.jlo) * p.ipb;
         s.S = (int)(((long long)s.nq * c->gq + RB - 1) / RB);
         if (s.S == 0) continue;
         p.sinks |= s.nsink > 0;

@@ -44,6 +44,7 @@ struct ChunkArgs {
     int Hq, Hkv, g, NB, G, P, C, ring;
     int jfull;                 // blocks j >= jfull hold G tokens (norm criterion)
     int CPB;                   // chunks (CHUNK_TILES tiles) per block
+    int spi;           // rows mode: slots of the list of first tokens' blocks per work item
     int window, sinks;         // window 0: no limit
     long long W;               // work items
     int NWp, MAXU, RV;         // active warps, units a warp's range can touch, rows of a partial

@@ -36,9 +36,9 @@
 // block, and the listed blocks of the first tokens come before them. Batch
 // 32 x 4K, 32 heads of d = 128: four rows 129 us (427 MB, 3.3 TB/s), one row
 // without a window 100 (ott_decode_attn, which needs no masks and no table,
-// 85), one with a window of 1,024 tokens 60 (159 MB, 2.7 TB/s). The masks,
-// the products' instructions and the smaller items of a windowed unit bound
-// it, not HBM.
+// 85), one with a window of 1,024 tokens and four first ones 56 (159 MB,
+// 2.9 TB/s; without the first ones 47). The masks, the products'
+// instructions and the smaller items of a windowed unit bound it, not HBM.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -155,6 +155,7 @@ struct DecodeArgs {
     int Iu;             // work items per unit: Sf + nf * CPB
     int CPB;            // chunks (CHUNK_TILES tiles) per block
     int IPB;            // quantized work items per block: 1 (whole blocks) or CPB (chunks)
+    int SPI;            // rows mode: slots of the list of first tokens' blocks per work item
     long long W;        // U * Iu
     int NWp;            // warps in the grid
     int MAXU;           // units a warp's range can touch
@@ -390,7 +391,13 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
         int j, k, cnt;
     };
     const int CPB = a.CPB, IPB = a.IPB, KPI = CPB / IPB;   // chunks per item
-    const int jl = (q1 - 1) / IPB, kl = ((q1 - 1) % IPB + 1) * KPI - 1;   // the segment's last chunk
+    // rows mode: an item of the list is SPI slots
+    const int ns = MS ? ru.s->nsink : 0, li = MS ? (ns + a.SPI - 1) / a.SPI : 0;
+    auto slot_at = [&](int q) { return MS && q < li ? a.SPI * q : ns + (q - li) / IPB; };
+    auto chunk_at = [&](int q) { return MS && q < li ? 0 : (q - li) % IPB * KPI; };
+    // the segment's last chunk
+    const int jl = MS && q1 <= li ? min(a.SPI * q1, ns) - 1 : slot_at(q1 - 1);
+    const int kl = MS && q1 <= li ? CPB - 1 : chunk_at(q1 - 1) + KPI - 1;
     auto past = [&](const Cursor &c) { return c.j > jl || (c.j == jl && c.k > kl); };
     // move to the next chunk that holds tokens (or past the segment)
     auto settle = [&](Cursor &c) {
@@ -412,7 +419,7 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
         }
         settle(c);
     };
-    Cursor ic{q0 / IPB, (q0 % IPB) * KPI, 0};
+    Cursor ic{slot_at(q0), chunk_at(q0), 0};
     ic.cnt = cnt_at(ic.j);
     settle(ic);
     // a block's first chunk in this segment brings the block's header
@@ -1437,6 +1444,7 @@ cudaError_t launch_rows_t(const ott_cache *c, const ChunkArgs &r, const ChunkTab
     a.jfull = r.jfull;
     a.CPB = r.CPB;
     a.IPB = ipb;
+    a.SPI = r.spi;
     a.W = r.W;
     a.NWp = r.NWp;
     a.MAXU = r.MAXU;

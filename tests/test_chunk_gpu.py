@@ -71,6 +71,7 @@ CHUNKS += [
     ("pct", 2, 4, 2, 128, 32, 4, 16, 400, 2, 120, 3),
     ("uniform", 2, 3, 1, 128, 17, 3, 4, 300, 1, 0, 0),           # odd group
     ("uniform", 2, 3, 1, 64, 40, 3, 4, 500, 1, 100, 33),         # first tokens over a tile, not over the block
+    ("uniform", 64, 8, 8, 64, 16, 4, 8, 400, 2, 90, 30),         # more blocks than warps
     # five to sixteen
     ("ragged", 4, 4, 2, 64, 32, 4, 6, [2, 80, 37, 533], [8, 0, 1, 5], 50, 4),
     ("paged", 2, 8, 1, 128, 40, 8, 8, [77, 400], [2, 1], 120, 33),
@@ -126,6 +127,9 @@ WINDOWS = [
     ("cold", 2, 4, 2, 128, 32, 4, 8, 400, 100, 3),
     ("pct", 2, 4, 2, 128, 32, 4, 16, 400, 90, 3),
     ("uniform", 1, 32, 8, 128, 128, 32, 64, 5000, 1024, 16),
+    # more blocks than warps: items of several listed slots
+    ("uniform", 64, 8, 8, 64, 16, 4, 8, 200, 100, 40),
+    ("uniform", 64, 8, 8, 64, 128, 4, 8, 1100, 600, 130),
 ]
 
 
