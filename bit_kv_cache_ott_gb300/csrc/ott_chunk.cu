@@ -653,6 +653,9 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
 // block's indices ascend, so its first one decides; a token lies in one
 // block at most, so there are at most `sinks` such blocks.
 constexpr int SINK_THREADS = 256, SINK_PER = 4;   // blocks per thread and round, their loads in flight together
+// (The decode kernel's warps looking for the blocks themselves, up to 32 of
+// them, spared a windowed step of batch 32 this launch, 56 -> 54 us, and cost
+// every call of rows mode registers: verification of four tokens 129 -> 133.)
 __global__ void __launch_bounds__(SINK_THREADS)
     k_window_sinks(const __grid_constant__ ChunkArgs a, const __grid_constant__ ChunkTable st, int32_t *sel) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

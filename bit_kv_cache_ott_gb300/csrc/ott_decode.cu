@@ -33,7 +33,11 @@
 // Rows mode (MS): the same kernel for up to four query rows per kv head of a
 // chunk or a windowed step. A row is a head, to the products; its position
 // hides tokens, the chunk's new tokens are fp16 items, windows start at a
-// block, and the listed blocks of the first tokens come before them. Batch
+// block, and the listed blocks of the first tokens come before them. (Values
+// as there, w s code + w z: a code at the lowest bits of a word is a subnormal
+// of 2^-24 per unit, and the tensor cores keep 24 bits from 2^-14 down, so a
+// token's product is good to 2^-12 of w s. One token with all the weight:
+// 7e-5 rms at s = 1.3, before the rounding of the output.) Batch
 // 32 x 4K, 32 heads of d = 128: four rows 129 us (427 MB, 3.3 TB/s), one row
 // without a window 100 (ott_decode_attn, which needs no masks and no table,
 // 85), one with a window of 1,024 tokens and four first ones 56 (159 MB,

@@ -341,9 +341,10 @@ int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t 
  * appends would give it if none of them flushed. The cache is read only and
  * may be empty, in part or whole (plain causal attention over the chunk).
  * out may not alias q, k or v.
- * Softmax statistics and sums are fp32; with more than four query rows per
- * kv head (n * Hq / Hkv) the weights and the dequantized values are rounded
- * to fp16 for the tensor cores (each at most 2^-11 relative). Keys and
+ * Softmax statistics and sums are fp32. With up to four query rows per kv
+ * head (n * Hq / Hkv) the products are ott_decode_attn's; with more, the
+ * weights and the dequantized values are rounded to fp16 for the tensor cores
+ * (each at most 2^-11 relative). Keys and
  * values, the chunk's too, are finite and at most 48,000 in magnitude: a
  * value that is not finite spoils rows that do not see it as well. A call
  * gives the same bits every time.

@@ -109,7 +109,8 @@ def test_chunk_attn(ott, kind, B, Hq, Hkv, d, G, R, P, T, n, window, sinks):
         for b in range(B):
             assert bool((out[b, :, ns[b]:] == 7.0).all()), f"rows behind sequence {b}'s tokens were written"
             if ns[b]:
-                ref, tol = attend(c, b, q[b, :, :ns[b]], Ts[b], window, sinks, k[b, :, :ns[b]], v[b, :, :ns[b]])
+                ref, tol = attend(c, b, q[b, :, :ns[b]], Ts[b], window, sinks, k[b, :, :ns[b]], v[b, :, :ns[b]],
+                                  folded=max(ns) * Hq // Hkv <= 4)
                 check(out[b, :, :ns[b]], ref, tol, f"sequence {b}")
 
 
@@ -127,7 +128,11 @@ WINDOWS = [
     ("cold", 2, 4, 2, 128, 32, 4, 8, 400, 100, 3),
     ("pct", 2, 4, 2, 128, 32, 4, 16, 400, 90, 3),
     ("uniform", 1, 32, 8, 128, 128, 32, 64, 5000, 1024, 16),
+    # many blocks before the window
+    ("uniform", 2, 4, 4, 64, 16, 4, 8, 900, 100, 20),
+    ("cold", 2, 4, 2, 64, 16, 4, 8, 900, 100, 40),
     # more blocks than warps: items of several listed slots
+    ("uniform", 64, 8, 8, 64, 16, 4, 8, 900, 100, 40),
     ("uniform", 64, 8, 8, 64, 16, 4, 8, 200, 100, 40),
     ("uniform", 64, 8, 8, 64, 128, 4, 8, 1100, 600, 130),
 ]
@@ -141,7 +146,7 @@ def test_decode_attn_window(ott, kind, B, Hq, Hkv, d, G, R, P, T, window, sinks)
         out = c.decode_attn_window(q[:, :, 0].contiguous().to(DEV), window, sinks)
         c.check_device()
         for b in range(B):
-            ref, tol = attend(c, b, q[b], Ts[b] - 1, window, sinks)
+            ref, tol = attend(c, b, q[b], Ts[b] - 1, window, sinks, folded=Hq // Hkv <= 4)
             check(out[b].unsqueeze(1), ref, tol, f"sequence {b}")
 
 
@@ -244,7 +249,7 @@ def test_the_loop_of_a_serving_step(ott):
                 out = c.chunk_attn(qr, kr, vd, window=100, sinks=4)
             s.synchronize()
             for b in range(B):
-                ref, tol = attend(c, b, qr[b].cpu(), T, 100, 4, kr[b].cpu(), v[b])
+                ref, tol = attend(c, b, qr[b].cpu(), T, 100, 4, kr[b].cpu(), v[b], folded=n * Hq // Hkv <= 4)
                 check(out[b], ref, tol, f"step {step}")
             with torch.cuda.stream(s):
                 c.append_chunk(kr, vd)
@@ -253,7 +258,7 @@ def test_the_loop_of_a_serving_step(ott):
                 dec = c.decode_attn_window(qr[:, :, -1].contiguous(), 60, 4)
             s.synchronize()
             for b in range(B):
-                ref, tol = attend(c, b, qr[b, :, -1:].cpu(), T - 1, 60, 4)
+                ref, tol = attend(c, b, qr[b, :, -1:].cpu(), T - 1, 60, 4, folded=Hq // Hkv <= 4)
                 check(dec[b].unsqueeze(1), ref, tol, f"decode {step}")
         c.check_device()
 
