@@ -1038,11 +1038,10 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
     // the tile: x = (pair of the largest sequence, 32 rows), y = kv head, z = entry
     const ChunkSeq &s = st.e[blockIdx.z];
     const int p = blockIdx.x / 8, row = 32 * (blockIdx.x % 8) + lane;
-    // (a CTA with nothing to merge waits, too: this grid ends behind the tiles)
-    if (p >= s.S) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        return;
-    }
+    // A CTA with nothing to merge leaves at once, but the first one, which
+    // waits in any case: this grid ends behind the tiles.
+    const bool first = (blockIdx.x | blockIdx.y | blockIdx.z) == 0;
+    if (p >= s.S && !first) return;
     Tile t;
     long long ts = s.base + (long long)blockIdx.y * s.Iu;
     {
@@ -1056,10 +1055,12 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
         ts += before;
     }
     tile_extent(a, ta.CPT, s, p, t);
+    if (32 * (blockIdx.x % 8) >= t.rows && !first) return;
     const int c0 = ch_warp_of(ta.W, ta.nC, ts + FIXED), c1 = ch_warp_of(ta.W, ta.nC, ts + FIXED + t.steps - 1);
     const int slot0 = ch_range_start(ta.W, ta.nC, c0) < ts ? 1 : 0;
+    if (c0 == c1 && !first) return;   // written whole
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (32 * (blockIdx.x % 8) >= t.rows || c0 == c1) return;   // no rows; written whole
+    if (c0 == c1 || p >= s.S || t.rows <= 0) return;
     constexpr int CH = D / 8;
     float M = -CUDART_INF_F, L = 0.0f, acc[CH];
 #pragma unroll
