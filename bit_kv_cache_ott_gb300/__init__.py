@@ -145,45 +145,46 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, sect
     each axis; pair i is channels (i, half + i), half = sum(sections), or (2i, 2i + 1) if ``interleaved``; it turns by
     pos * base ** -e with e = i / half, or j / sections[a] for an axis's j-th pair if ``restart``. Outputs may be the
     inputs (in place). Returns (rotated q, rotated k), None for one that was not given."""
-    xs = [t for t in (q, k) if t is not None]
-    if not xs:
+    x = k if q is None else q
+    if x is None:
         raise ValueError("rope: q or k must be given")
-    if any(not isinstance(t, torch.Tensor) or t.dim() != 4 for t in xs):
-        raise ValueError("rope: expected [B][H][n][d] tensors")
-    B, _, n, d = xs[0].shape
-    sections = tuple(int(x) for x in sections)
-    if not 1 <= len(sections) <= 4:
+    for t in (q, k):
+        if t is not None and (not isinstance(t, torch.Tensor) or t.dim() != 4):
+            raise ValueError("rope: expected [B][H][n][d] tensors")
+    B, _, n, d = x.shape
+    sections = tuple(map(int, sections))
+    axes = len(sections)
+    if not 1 <= axes <= 4:
         raise ValueError("rope: one to four axes")
     if not isinstance(pos, torch.Tensor) or not pos.is_cuda or pos.dtype != torch.int32:
         raise TypeError("pos: expected a CUDA int32 tensor")
-    if tuple(pos.shape) != (len(sections), B, n) or not pos.is_contiguous():
-        raise ValueError(f"pos: expected contiguous shape {(len(sections), B, n)}, got {tuple(pos.shape)}")
-    idx = xs[0].get_device()
-    ptr, outs, heads = [], [], []
-    for name, x, o in (("q", q, out_q), ("k", k, out_k)):
-        if x is None:
-            if o is not None:
-                raise ValueError(f"out_{name} without {name}")
-            ptr += (None, None)
-            outs.append(None)
-            heads.append(0)
-            continue
-        H = x.shape[1]
-        p = _dev_ptr(x, (B, H, n, d), name)
-        if o is None:
-            o = torch.empty_like(x)
-            ptr += (p, o.data_ptr())
-        else:
-            ptr += (p, _dev_ptr(o, (B, H, n, d), f"out_{name}"))
-        outs.append(o)
-        heads.append(H)
-    _same_device(idx, pos, *xs, *[o for o in outs if o is not None])
-    if B == 0 or sum(heads) == 0 or n == 0:
-        return tuple(outs)
-    plan = _rope_plan(sections, float(base), bool(interleaved), bool(restart))
-    _on_device(idx, load().ott_rope, "ott_rope", ptr[0], ptr[1], heads[0], ptr[2], ptr[3], heads[1], pos.data_ptr(), B,
-               n, d, plan, _stream_of(stream, idx))
-    return tuple(outs)
+    if pos.shape != (axes, B, n) or not pos.is_contiguous():
+        raise ValueError(f"pos: expected contiguous shape {(axes, B, n)}, got {tuple(pos.shape)}")
+    idx = x.get_device()
+    qp, qo, out_q, Hq = _rope_operand(q, out_q, "q", B, n, d)
+    kp, ko, out_k, Hkv = _rope_operand(k, out_k, "k", B, n, d)
+    for t in (pos, q, k, out_q, out_k):
+        if t is not None and t.get_device() != idx:
+            raise ValueError(f"tensors on {t.device} and cuda:{idx}")
+    if B and n and Hq + Hkv:
+        plan = _rope_plan(sections, float(base), bool(interleaved), bool(restart))
+        _on_device(idx, load().ott_rope, "ott_rope", qp, qo, Hq, kp, ko, Hkv, pos.data_ptr(), B, n, d, plan,
+                   _stream_of(stream, idx))
+    return out_q, out_k
+
+
+def _rope_operand(x, out, name, B, n, d):
+    """(pointer, output's pointer, output, heads) of one of rope's tensors."""
+    if x is None:
+        if out is not None:
+            raise ValueError(f"out_{name} without {name}")
+        return None, None, None, 0
+    H = x.shape[1]
+    p = _dev_ptr(x, (B, H, n, d), name)
+    if out is None:
+        out = torch.empty_like(x)
+        return p, out.data_ptr(), out, H
+    return p, _dev_ptr(out, (B, H, n, d), f"out_{name}"), out, H
 
 
 @functools.lru_cache(maxsize=64)
