@@ -45,7 +45,7 @@ constexpr int CT = CHUNK_TILES * TILE;      // block slots per work item
 // then this file's kernel serve a call; the tcgen05 tiles take the rest. Batch
 // 32 x 4K, 32 heads: 4 rows 131 us in rows mode, 184 here (rows mode has one
 // slice of up to 4 rows and would read the cache twice for 5); 16 rows 258 us
-// here; 17 rows 453 us in tiles (256 rows at the same price), about 516 here
+// here; 17 rows 440 us in tiles (256 rows at the same price), about 516 here
 // in two slices.
 constexpr int DEC_ROWS_MAX = 4, ROWS_MAX = 16;
 
