@@ -601,7 +601,11 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
         float mn = M;
 #pragma unroll
         for (int x = 0; x < GRP; ++x) mn = fmaxf(mn, ms[x]);
-        if (mn == -CUDART_INF_F) continue;
+        if (mn == -CUDART_INF_F) {   // nothing seen, or scores that are NaN: then the sum is, too
+#pragma unroll
+            for (int x = 0; x < GRP; ++x) L += ls[x];
+            continue;
+        }
         const float so = ch_ex2(M - mn);
         L *= so;
 #pragma unroll
@@ -636,9 +640,9 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
             for (int c = 0; c < CPL; ++c) acc[c] = fmaf(sx, red[x][2 + lane * CPL + c], acc[c]);
         }
     }
-    // a decode step may see nothing (every token of its window discarded by a policy): zeros
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
-    __half *o = a.out + (((size_t)(a.B0 + blockIdx.y) * a.Hq + hq) * a.n + tk) * D + lane * CPL;
+    const size_t at = (((size_t)(a.B0 + blockIdx.y) * a.Hq + hq) * a.n + tk) * D;
+    const float inv = chunk_norm(L, a.k == nullptr, a.q + at, D);
+    __half *o = a.out + at + lane * CPL;
     uint32_t w[CPL / 2];
 #pragma unroll
     for (int c = 0; c < CPL; c += 2) w[c / 2] = ch_h2(__floats2half2_rn(acc[c] * inv, acc[c + 1] * inv));

@@ -92,6 +92,17 @@ __device__ __forceinline__ const __half *chunk_fp16_row(const ChunkArgs &a, cons
 // The token at t is seen from position p, whose window starts at lo.
 __device__ __forceinline__ bool chunk_sees(int t, int p, int lo, int sinks) { return t <= p && (t >= lo || t < sinks); }
 
+// What a row's output is multiplied by: one over the sum L of its weights (NaN
+// stays). A row of a chunk sees at least its own token, so that L = 0 means
+// that every score was -inf: NaN. A step may also see nothing (a policy has
+// discarded every token of its window): zeros, unless its query q is not finite.
+__device__ __forceinline__ float chunk_norm(float L, bool step, const __half *q, int D) {
+    if (L != 0.0f) return 1.0f / L;
+    bool finite = step;
+    for (int c = 0; finite && c < D; ++c) finite = fabsf(__half2float(q[c])) < CUDART_INF_F;
+    return finite ? 0.0f : CUDART_NAN_F;
+}
+
 __device__ __forceinline__ uint32_t ch_smem(const void *p) { return (uint32_t)__cvta_generic_to_shared(p); }
 __device__ __forceinline__ float ch_ex2(float x) {
     float y;

@@ -857,8 +857,9 @@ __device__ void finish(const TileArgs &ta, const Tile &t, uint32_t tmem, int til
     const int wq = (threadIdx.x >> 5) & 3, row = ROWS * tile + 32 * wq + (threadIdx.x & 31), v = 256 * t.p + row;
     const uint32_t to = tmem + C::O(tile) + ((uint32_t)(32 * wq) << 16);
     if (whole) {
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        __half *o = a.out + (((size_t)(a.B0 + t.e) * a.Hq + t.hkv * a.g + v % a.g) * a.n + v / a.g) * D;
+        const size_t at = (((size_t)(a.B0 + t.e) * a.Hq + t.hkv * a.g + v % a.g) * a.n + v / a.g) * D;
+        const float inv = row < t.rows ? chunk_norm(l, a.k == nullptr, a.q + at, D) : 0.0f;
+        __half *o = a.out + at;
 #pragma unroll 1
         for (int c = 0; c < D; c += 16) {
             float f[16];
@@ -1080,7 +1081,11 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
         float mn = M;
 #pragma unroll
         for (int z = 0; z < AHEAD; ++z) mn = fmaxf(mn, m[z]);
-        if (mn == -CUDART_INF_F) continue;
+        if (mn == -CUDART_INF_F) {   // nothing seen, or scores that are NaN: then the sum is, too
+#pragma unroll
+            for (int z = 0; z < AHEAD; ++z) L += c + z <= c1 ? l[z] : 0.0f;
+            continue;
+        }
         const float so = ch_ex2(M - mn);
         L *= so;
 #pragma unroll
@@ -1095,9 +1100,10 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
         M = mn;
     }
     if (row >= t.rows) return;
-    const float inv = L > 0.0f ? 1.0f / L : 0.0f;
     const int vv = 256 * p + row;
-    __half *o = a.out + (((size_t)(a.B0 + blockIdx.z) * a.Hq + blockIdx.y * a.g + vv % a.g) * a.n + vv / a.g) * D + CH * warp;
+    const size_t at = (((size_t)(a.B0 + blockIdx.z) * a.Hq + blockIdx.y * a.g + vv % a.g) * a.n + vv / a.g) * D;
+    const float inv = chunk_norm(L, a.k == nullptr, a.q + at, D);
+    __half *o = a.out + at + CH * warp;
 #pragma unroll
     for (int y = 0; y < CH; y += 8)
         *reinterpret_cast<uint4 *>(o + y) = make_uint4(

@@ -1175,7 +1175,13 @@ __global__ void __launch_bounds__(COMB_MAXW * 32) k_combine(DecodeArgs a, const 
         float mn = M;
 #pragma unroll
         for (int g = 0; g < GRP; ++g) mn = fmaxf(mn, ms[g]);
-        if (mn == -CUDART_INF_F) continue;
+        if (mn == -CUDART_INF_F) {
+            if constexpr (MS) {   // nothing seen, or scores that are NaN: then the sum is, too
+#pragma unroll
+                for (int g = 0; g < GRP; ++g) L += ls[g];
+            }
+            continue;
+        }
         const float so = ex2(M - mn);
         L *= so;
 #pragma unroll
@@ -1205,7 +1211,10 @@ __global__ void __launch_bounds__(COMB_MAXW * 32) k_combine(DecodeArgs a, const 
         for (int c = 0; c < CPL; ++c) acc[c] = 0.0f;
         for (int x = 0; x < cw; ++x) {
             const float mx = red[x][0];
-            if (mx == -CUDART_INF_F) continue;
+            if (mx == -CUDART_INF_F) {
+                if constexpr (MS) L += red[x][1];
+                continue;
+            }
             const float sx = ex2(mx - M);
             L = fmaf(sx, red[x][1], L);
 #pragma unroll
@@ -1214,8 +1223,9 @@ __global__ void __launch_bounds__(COMB_MAXW * 32) k_combine(DecodeArgs a, const 
     }
     __half *o = a.out + ((size_t)b * a.Hq + hq) * D + ch0;
     if constexpr (MS) {
-        o = a.out + ((size_t)a.B0 * a.Hq * a.n + bh) * D + ch0;
-        if (L == 0.0f) L = 1.0f;   // a policy has discarded every token of the window: zeros
+        const size_t at = ((size_t)a.B0 * a.Hq * a.n + bh) * D;
+        o = a.out + at + ch0;
+        if (L == 0.0f && chunk_norm(L, a.knew == nullptr, a.q + at, D) == 0.0f) L = 1.0f;   // zeros; else 0 / 0
     }
     // one vector store per lane (out may be host memory)
     if constexpr (CPL == 1) {

@@ -346,7 +346,8 @@ int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t 
  * weights and the dequantized values are rounded to fp16 for the tensor cores
  * (each at most 2^-11 relative). Keys and
  * values, the chunk's too, are finite and at most 48,000 in magnitude: a
- * value that is not finite spoils rows that do not see it as well. A call
+ * value that is not finite spoils rows that do not see it as well. A query
+ * that is not finite gets NaN in its own row and changes no other. A call
  * gives the same bits every time.
  * Partial results go to the cache's split-K scratch, or where they are
  * larger to stream-ordered scratch from the library's pool (see ott_prefill;
@@ -368,8 +369,9 @@ int ott_append_chunk(ott_cache *c, const void *k, const void *v, int n, const in
 /*
  * ott_decode_attn with a window: one query per sequence, at the position of
  * the last token appended (p = T_b - 1). q, out: DEVICE fp16 [B][Hq][d].
- * A query whose every token in sight a policy has discarded gets zeros.
- * Precision and scratch as ott_chunk_attn; OTT_ERR_STATE as ott_decode_attn.
+ * A query whose every token in sight a policy has discarded gets zeros (NaN
+ * if it is not finite). Precision and scratch as ott_chunk_attn;
+ * OTT_ERR_STATE as ott_decode_attn.
  */
 int ott_decode_attn_window(ott_cache *c, const void *q, void *out, int window, int sinks, void *stream);
 
