@@ -601,18 +601,14 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
         float mn = M;
 #pragma unroll
         for (int x = 0; x < GRP; ++x) mn = fmaxf(mn, ms[x]);
-        if (mn == -CUDART_INF_F) {   // nothing seen, or scores that are NaN: then the sum is, too
-#pragma unroll
-            for (int x = 0; x < GRP; ++x) L += ls[x];
-            continue;
-        }
-        const float so = ch_ex2(M - mn);
+        // (no maximum yet: nothing seen, or scores that are NaN, and then the sum, too, which stays)
+        const float mr = mn == -CUDART_INF_F ? 0.0f : mn, so = ch_ex2(M - mr);
         L *= so;
 #pragma unroll
         for (int c = 0; c < CPL; ++c) acc[c] *= so;
 #pragma unroll
         for (int x = 0; x < GRP; ++x) {
-            const float sn = ch_ex2(ms[x] - mn);   // 0 where nothing was seen
+            const float sn = ch_ex2(ms[x] - mr);   // 0 where nothing was seen
             L = fmaf(sn, ls[x], L);
 #pragma unroll
             for (int c = 0; c < CPL; ++c) acc[c] = fmaf(sn, vs[x][c], acc[c]);

@@ -1081,18 +1081,14 @@ __global__ void __launch_bounds__(256) k_tiles_combine(const __grid_constant__ T
         float mn = M;
 #pragma unroll
         for (int z = 0; z < AHEAD; ++z) mn = fmaxf(mn, m[z]);
-        if (mn == -CUDART_INF_F) {   // nothing seen, or scores that are NaN: then the sum is, too
-#pragma unroll
-            for (int z = 0; z < AHEAD; ++z) L += c + z <= c1 ? l[z] : 0.0f;
-            continue;
-        }
-        const float so = ch_ex2(M - mn);
+        // (no maximum yet: nothing seen, or scores that are NaN, and then the sum, too, which stays)
+        const float mr = mn == -CUDART_INF_F ? 0.0f : mn, so = ch_ex2(M - mr);
         L *= so;
 #pragma unroll
         for (int y = 0; y < CH; ++y) acc[y] *= so;
 #pragma unroll
         for (int z = 0; z < AHEAD; ++z) {
-            const float sn = ch_ex2(m[z] - mn);
+            const float sn = ch_ex2(m[z] - mr);
             L = fmaf(l[z], sn, L);
 #pragma unroll
             for (int y = 0; y < CH; ++y) acc[y] = fmaf(f[z][y], sn, acc[y]);

@@ -1175,20 +1175,15 @@ __global__ void __launch_bounds__(COMB_MAXW * 32) k_combine(DecodeArgs a, const 
         float mn = M;
 #pragma unroll
         for (int g = 0; g < GRP; ++g) mn = fmaxf(mn, ms[g]);
-        if (mn == -CUDART_INF_F) {
-            if constexpr (MS) {   // nothing seen, or scores that are NaN: then the sum is, too
-#pragma unroll
-                for (int g = 0; g < GRP; ++g) L += ls[g];
-            }
-            continue;
-        }
-        const float so = ex2(M - mn);
+        // (rows mode, no maximum yet: nothing seen, or scores that are NaN, and then the sum, too, which stays)
+        if (!MS && mn == -CUDART_INF_F) continue;
+        const float mr = MS && mn == -CUDART_INF_F ? 0.0f : mn, so = ex2(M - mr);
         L *= so;
 #pragma unroll
         for (int c = 0; c < CPL; ++c) acc[c] *= so;
 #pragma unroll
         for (int g = 0; g < GRP; ++g) {
-            const float sn = ex2(ms[g] - mn);   // 0 for an empty segment (m = -inf)
+            const float sn = ex2(ms[g] - mr);   // 0 for an empty segment (m = -inf)
             L = fmaf(sn, ls[g], L);
 #pragma unroll
             for (int c = 0; c < CPL; ++c) acc[c] = fmaf(sn, vs[g][c], acc[c]);
