@@ -9,6 +9,15 @@
 
 namespace ott {
 
+// Tokens whose weighted values the tensor cores add up on their own. They
+// truncate each product to the sum's last place, so a sum of values of one
+// sign shrinks by 5.9e-9 of itself per token (tcgen05; measured, 8,192 rows of
+// 8 heads over 2^20 tokens: 3.8e-3 of the output when runs were as long as the
+// plan made them). Sums end here and are merged in fp32: 1.5e-4 at any
+// length, a third of the output's largest rounding. 2,048 tokens over 131K:
+// 3.35 ms, and 3.29 with sums of 57,344 tokens (3.4e-4).
+constexpr int SUM_TOKENS = 25088;
+
 // One sequence of a launch.
 struct ChunkSeq {
     long long base;    // its first work item; entry [nseq] holds the total

@@ -31,6 +31,8 @@
 // all tiles, so that long caches with few rows are split and there is no
 // tail (a tile cut between CTAs leaves partials, merged by k_tiles_combine),
 // or a tile of its own, whichever is estimated to end first (plan_tiles).
+// After SUM_STEPS steps of a tile, whoever takes the next ones, its sums are
+// carried over in fp32 (finish): the tensor cores truncate.
 //
 // What bounds it: 2,048 tokens over 32K (8 kv heads, 4 heads each, d = 128)
 // take 820 us, 1.37 PFLOP/s of the sums that are asked for; without the
@@ -62,7 +64,7 @@ constexpr int THREADS = 512;
 constexpr int PROD0 = 8, MMA_WARP = 15;
 constexpr int META = 4;              // steps of group metadata in flight
 constexpr float GROW = 8.0f;         // log2: the output is rescaled when the maximum has grown by this
-constexpr int MAX_STEPS = 768, MAX_WAVES = 8;   // steps per CTA before there are more CTAs than SMs (see plan_tiles)
+constexpr int SUM_STEPS = SUM_TOKENS / STEP_TOK;   // steps whose products stay one sum in TMEM
 constexpr int MIN_STEPS = 2;         // steps per CTA at least
 constexpr int FIXED = 4;             // a tile's fixed cost (find it, queries, fill the pipeline, output) in steps of 2 us
 
@@ -849,14 +851,50 @@ __device__ void softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
     }
 }
 
-// The output of a tile's row, or its part of it. Warps of the softmax.
+// The output of a tile's row, or its part of it (the reference of its weights,
+// their sum, the output: a column of rows each). more: the part holds the
+// sums of earlier steps, which these join. Warps of the softmax.
 template <int D>
-__device__ void finish(const TileArgs &ta, const Tile &t, uint32_t tmem, int tile, bool whole, int slot, float m, float l) {
+__device__ void finish(const TileArgs &ta, const Tile &t, uint32_t tmem, int tile, bool whole, bool more, int slot, float m,
+                       float l) {
     using C = TCfg<D>;
     const ChunkArgs &a = ta.a;
     const int wq = (threadIdx.x >> 5) & 3, row = ROWS * tile + 32 * wq + (threadIdx.x & 31), v = 256 * t.p + row;
     const uint32_t to = tmem + C::O(tile) + ((uint32_t)(32 * wq) << 16);
-    if (whole) {
+    float *pb = ta.part + ((size_t)blockIdx.x * 2 + slot) * (D + 2) * 256 + row;
+    if (more) {
+        const float mo = pb[0], M = fmaxf(mo, m), mr = M == -CUDART_INF_F ? 0.0f : M;
+        const float sn = ch_ex2(m - mr), so = ch_ex2(mo - mr);
+        l = fmaf(l, sn, pb[256] * so);
+        const size_t at = (((size_t)(a.B0 + t.e) * a.Hq + t.hkv * a.g + v % a.g) * a.n + v / a.g) * D;
+        const float inv = whole && row < t.rows ? chunk_norm(l, a.k == nullptr, a.q + at, D) : 0.0f;
+        pb[0] = M;
+        pb[256] = l;
+        constexpr int CH = 32;   // channels whose loads are in flight together
+#pragma unroll 1
+        for (int c = 0; c < D; c += CH) {
+            float f[CH], o[CH];
+#pragma unroll
+            for (int y = 0; y < CH; ++y) o[y] = pb[(size_t)(2 + c + y) * 256];
+            tm_ld16(to + c, f);
+            tm_ld16(to + c + 16, f + 16);
+            wait_ld();
+            tie16(f);
+            tie16(f + 16);
+#pragma unroll
+            for (int y = 0; y < CH; ++y) o[y] = fmaf(f[(y & 24) + vrow(y & 7)], sn, o[y] * so);
+            if (!whole) {
+#pragma unroll
+                for (int y = 0; y < CH; ++y) pb[(size_t)(2 + c + y) * 256] = o[y];
+            } else if (row < t.rows) {
+#pragma unroll
+                for (int y = 0; y < CH; y += 8)
+                    *reinterpret_cast<uint4 *>(a.out + at + c + y) =
+                        make_uint4(ch_h2(__floats2half2_rn(o[y] * inv, o[y + 1] * inv)), ch_h2(__floats2half2_rn(o[y + 2] * inv, o[y + 3] * inv)),
+                                   ch_h2(__floats2half2_rn(o[y + 4] * inv, o[y + 5] * inv)), ch_h2(__floats2half2_rn(o[y + 6] * inv, o[y + 7] * inv)));
+            }
+        }
+    } else if (whole) {
         const size_t at = (((size_t)(a.B0 + t.e) * a.Hq + t.hkv * a.g + v % a.g) * a.n + v / a.g) * D;
         const float inv = row < t.rows ? chunk_norm(l, a.k == nullptr, a.q + at, D) : 0.0f;
         __half *o = a.out + at;
@@ -877,8 +915,7 @@ __device__ void finish(const TileArgs &ta, const Tile &t, uint32_t tmem, int til
                 *reinterpret_cast<uint4 *>(o + c + 8) = make_uint4(h[4], h[5], h[6], h[7]);
             }
         }
-    } else {   // maximum, sum, output: a column of rows each
-        float *pb = ta.part + ((size_t)blockIdx.x * 2 + slot) * (D + 2) * 256 + row;
+    } else {
         pb[0] = m;
         pb[256] = l;
 #pragma unroll 1
@@ -914,8 +951,11 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
         int at = 0;
         const Tile t = ta.whole ? tile_number(ta, st, blockIdx.x) : tile_at(ta, st, x0 + done, at);
         const ChunkSeq &s = st.e[t.e];
-        const int end = ta.whole ? t.steps + FIXED : min(t.steps + FIXED, at + (todo - done));
-        const int j0 = max(0, at - FIXED), j1 = max(0, end - FIXED), n = j1 - j0;
+        const int j0 = max(0, at - FIXED);
+        const int end = ta.whole ? t.steps + FIXED : min(min(t.steps, j0 + SUM_STEPS) + FIXED, at + (todo - done));
+        const int j1 = max(0, end - FIXED), n = j1 - j0;
+        const int jf = ta.whole ? 0 : max(0, at - done - FIXED);   // the CTA's first step of the tile
+        const int slot = done > at;   // a tile that the run starts in or with leaves its part in slot 0, a later one in slot 1
         done += ta.whole ? 1 : end - at;
         if (n == 0) continue;   // the run ends before the tile's steps
         const int nt = t.rows > ROWS ? 2 : 1;
@@ -926,7 +966,7 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
             const int ch = threadIdx.x % CPR, r0 = threadIdx.x / CPR;
             const __half *const q0 = a.q + (size_t)(a.B0 + t.e) * a.Hq * a.n * D + (size_t)t.hkv * a.g * a.n * D + 8 * ch;
 #pragma unroll 1
-            for (int rr = r0; rr < nt * ROWS; rr += STEP * BATCH) {
+            for (int rr = j0 > jf ? nt * ROWS : r0; rr < nt * ROWS; rr += STEP * BATCH) {   // (still there for a tile's next steps)
                 uint4 v[BATCH];
 #pragma unroll
                 for (int y = 0; y < BATCH; ++y) {
@@ -948,7 +988,7 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
                 softmax<D>(ta, s, t, sm, bar, gave_up, tmem, tile, n, it, ct[tile], m, l);
                 bar_wait(&bar[B_OFULL], run & 1u, gave_up);
                 tc_after();
-                finish<D>(ta, t, tmem, tile, n == t.steps, run > 0, m, l);
+                finish<D>(ta, t, tmem, tile, jf == 0 && j1 == t.steps, j0 > jf, slot, m, l);
             } else {
                 bar_wait(&bar[B_OFULL], run & 1u, gave_up);   // its products may still read the queries
             }
@@ -1150,12 +1190,7 @@ bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, bool 
     st.e[a.nseq] = ChunkSeq{};
     st.e[a.nseq].base = a.W = base;
     st.e[a.nseq].ubase = (int)tiles;
-    // The tensor cores truncate as they accumulate: a sum over 1,200 steps
-    // shrank by 7e-5 of itself (a third of an fp16 rounding). Runs of at most
-    // MAX_STEPS, merged in fp32, keep that below 4e-5 and cost 2-3% on a
-    // 131K-token chunk (3.14 ms without).
     const double sms = c->sm_count, W = (double)base, nT = (double)tiles;
-    const long long waves = std::max<long long>(1, std::min<long long>(MAX_WAVES, (base + (long long)c->sm_count * MAX_STEPS - 1) / ((long long)c->sm_count * MAX_STEPS)));
     // Equal runs of places, or a tile per CTA: by their estimated times. Cut
     // tiles and their merge cost 8 steps and 0.1 per part of a tile. 333 new
     // tokens of five short sequences (100 tiles): 41 us in runs, 17 with a
@@ -1164,16 +1199,17 @@ bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, bool 
     const double one = std::max<double>(FIXED + longest, std::min(W / sms + longest / 2.0, std::ceil(nT / sms) * (FIXED + longest)));
     double best = 1e30;
     for (int div = 1; div <= 4; div *= 2) {
-        const long long n = std::max<long long>(1, std::min<long long>((long long)c->sm_count * waves, (base - FIXED * tiles) / MIN_STEPS) / div);
-        const double run = W / n, cost = std::ceil(n / sms) * (FIXED + run) + (n > 1 ? 8 + 0.1 * (W / nT) / run : 0);
+        const long long n = std::max<long long>(1, std::min<long long>(c->sm_count, (base - FIXED * tiles) / MIN_STEPS) / div);
+        const double run = W / n, cost = FIXED + run + (n > 1 ? 8 + 0.1 * (W / nT) / run : 0);
+        if (div > 1 && run > INT_MAX / 2) break;   // a run's places are counted in 32 bits
         if (cost < best) {
             best = cost;
             nC = (int)n;
         }
     }
-    whole = longest <= MAX_STEPS && one <= best;
+    whole = longest <= SUM_STEPS && one <= best;
     if (whole) nC = (int)tiles;
-    part_floats = !whole && nC > 1 ? (size_t)nC * 2 * (c->d + 2) * 256 : 1;
+    part_floats = !whole && (nC > 1 || longest > SUM_STEPS) ? (size_t)nC * 2 * (c->d + 2) * 256 : 1;
     return true;
 }
 
