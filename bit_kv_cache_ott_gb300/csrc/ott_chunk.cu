@@ -19,7 +19,8 @@
 // head share its blocks, too. Work items are what one copy brings: 8 fp16
 // tokens (keys and values, 4 KB at d = 128) or a chunk of up to 64 slots of a block
 // (5.1 KB, with the block's key scales where the warp has not met them). A
-// persistent grid gives every warp an equal contiguous run of items; the
+// grid of one CTA per SM (a multiple of that for very long runs) gives every
+// warp an equal contiguous run of items; the
 // copies run ahead of the products through a ring of stages that does not
 // stop at the borders of units. A warp leaves one partial (max, sum,
 // unnormalised output) per unit that it touches; k_chunk_combine merges them.
@@ -698,11 +699,11 @@ __global__ void __launch_bounds__(SINK_THREADS)
 }
 
 template <int D, int NC>
-cudaError_t launch_rows(const ChunkArgs &a, const ChunkTable &st, int sms, cudaStream_t s) {
+cudaError_t launch_rows(const ChunkArgs &a, const ChunkTable &st, cudaStream_t s) {
     using C = RowsCfg<D, NC>;
     // CTAs only as wide as the active warps need
-    const int wpc = (a.NWp + sms - 1) / sms;
-    return launch_pdl(k_chunk_rows<D, NC>, dim3((unsigned)sms), wpc * 32, (size_t)C::WARP_SMEM * wpc, s, a, st);
+    const int wpc = (a.NWp + a.ctas - 1) / a.ctas;
+    return launch_pdl(k_chunk_rows<D, NC>, dim3((unsigned)a.ctas), wpc * 32, (size_t)C::WARP_SMEM * wpc, s, a, st);
 }
 
 template <int D, int NC>
@@ -846,7 +847,12 @@ bool make_plan(const ott_cache *c, const ChunkCall &call, int B0, Plan &p) {
         p.part_floats = 0;
         return true;
     }
-    a.NWp = (int)std::min<long long>(a.W, (long long)c->sm_count * (p.gs ? DEC_WARPS : p.NC == 1 ? 16 : 8));
+    // a warp's run is one sum per unit: where it would be longer than
+    // SUM_TOKENS, more CTAs than SMs
+    const long long slots = (long long)c->sm_count * (p.gs ? DEC_WARPS : p.NC == 1 ? 16 : 8), most = slots * (SUM_TOKENS / CT);
+    const long long waves = std::max(1LL, (a.W + most - 1) / most);
+    a.ctas = (int)(c->sm_count * waves);
+    a.NWp = (int)std::min<long long>(a.W, slots * waves);
     const long long L = (a.W + a.NWp - 1) / a.NWp;   // items of a warp's range, at most
     a.MAXU = (int)std::min<long long>(L, (L - 1) / min_iu + 2);
     p.part_floats = (size_t)a.NWp * a.MAXU * a.RV * (c->d + 2) * (p.gs ? 2 : 1);
@@ -862,7 +868,7 @@ cudaError_t launch_plan(const ott_cache *c, const Plan &p, cudaStream_t s) {
     if (e == cudaSuccess && p.gs > 0) return launch_decode_rows(c, a, p.st, p.gs, p.ipb, s);
     if (e == cudaSuccess && p.NC == 0) return launch_tiles(c, a, p.st, p.nC, p.whole, s);
     if (e == cudaSuccess)
-        e = p.NC == 1 ? launch_rows<D, 1>(a, p.st, c->sm_count, s) : launch_rows<D, 2>(a, p.st, c->sm_count, s);
+        e = p.NC == 1 ? launch_rows<D, 1>(a, p.st, s) : launch_rows<D, 2>(a, p.st, s);
     if (e != cudaSuccess) return e;
     // about two rounds of 8 partials per combine warp
     const long long per_unit = (long long)a.NWp / std::max(1, p.st.e[a.nseq].ubase) + 2;

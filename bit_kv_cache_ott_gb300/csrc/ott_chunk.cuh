@@ -13,8 +13,8 @@ namespace ott {
 // truncate each product to the sum's last place, so a sum of values of one
 // sign shrinks by 5.9e-9 of itself per token (tcgen05; measured, 8,192 rows of
 // 8 heads over 2^20 tokens: 3.8e-3 of the output when runs were as long as the
-// plan made them). Sums end here and are merged in fp32: 1.5e-4 at any
-// length, a third of the output's largest rounding. 2,048 tokens over 131K:
+// plan made them), and by 2.4 to 4.8e-9 with mma.sync. Sums end here and are
+// merged in fp32: 1.5e-4 at any length, a third of the output's largest rounding. 2,048 tokens over 131K:
 // 3.35 ms, and 3.29 with sums of 57,344 tokens (3.4e-4).
 constexpr int SUM_TOKENS = 25088;
 
@@ -56,6 +56,7 @@ struct ChunkArgs {
     int spi;           // rows mode: slots of the list of first tokens' blocks per work item
     int window, sinks;         // window 0: no limit
     long long W;               // work items
+    int ctas;                  // CTAs
     int NWp, MAXU, RV;         // active warps, units a warp's range can touch, rows of a partial
     float sl2;                 // log2(e) / sqrt(d)
 };

@@ -1476,8 +1476,8 @@ cudaError_t launch_rows_t(const ott_cache *c, const ChunkArgs &r, const ChunkTab
     a.B0 = r.B0;
     a.window = r.window;
     a.sinks = r.sinks;
-    const int wpc = (a.NWp + c->sm_count - 1) / c->sm_count;
-    cudaError_t e = launch_pdl(k_decode<D, GQ, false, false, false, true>, dim3((unsigned)c->sm_count), wpc * 32,
+    const int wpc = (a.NWp + r.ctas - 1) / r.ctas;
+    cudaError_t e = launch_pdl(k_decode<D, GQ, false, false, false, true>, dim3((unsigned)r.ctas), wpc * 32,
                                (size_t)Cfg<D, GQ>::WARP_SMEM * wpc, s, a, st);
     if (e != cudaSuccess) return e;
     // about two rounds of partials per combine warp; few heads: channels split (as launch_combine)

@@ -42,6 +42,34 @@ def test_sums_over_a_million_tokens_do_not_shrink(ott):
     assert abs(shrink) <= 2.0 ** -11 / 3, f"outputs are {shrink:.2e} too small"
 
 
+def test_sums_of_few_rows_over_many_long_caches(ott):
+    """76 x 32 units of 131,072 tokens: a unit each for the warps of up to 16 rows per kv head. The same requirement."""
+    B, H, d, T = 76, 32, 64, 131072
+    g = torch.Generator(device=DEV).manual_seed(5)
+    K = torch.randn(1, H, T, d, generator=g, device=DEV).half()
+    with ott.OTTCache(B, H, H, d, 128, 32, 32, max_tokens=T, ragged=True) as c:
+        for b in range(B):
+            c.prefill_seq(b, K[0], 2 + K[0])
+        del K
+        units, _ = unit_tokens(c, 0)
+        units = [tuple(x.to(DEV) for x in units[h][:3]) for h in range(0, H, 4)]
+        for n in (1, 4, 8, 16):
+            q, k = (torch.randn(B, H, n, d, generator=g, device=DEV).half() for _ in range(2))
+            v = 2 + k
+            out = c.chunk_attn(q, k, v)
+            c.check_device()
+            num = den = 0.0
+            for h in range(0, H, 4):
+                Kd, Vd = torch.cat([units[h // 4][0], k[0, h].double()]), torch.cat([units[h // 4][1], v[0, h].double()])
+                idx = torch.cat([units[h // 4][2], T + torch.arange(n, device=DEV)])
+                hide = idx > (T + torch.arange(n, device=DEV))[:, None]
+                ref = torch.softmax((q[0, h].double() @ Kd.t() / math.sqrt(d)).masked_fill(hide, -math.inf), 1) @ Vd
+                num += float((out[0, h].double() * ref).sum())
+                den += float((ref * ref).sum())
+            # 8 n rows of 64 channels: their roundings leave 2^-11 / sqrt(3 * 512 n), 5e-6 at n = 4 and 1.3e-5 at 1
+            assert abs(1 - num / den) <= 2.0 ** -11 / 3, f"{n} rows: outputs are {1 - num / den:.2e} too small"
+
+
 #    B  Hq  Hkv d    G    T       n     window  sinks
 LONG = [
     (1, 8, 1, 64, 128, 131072, 1100, 0, 0),         # more than 32 pairs per head, tiles over several CTAs and sums
