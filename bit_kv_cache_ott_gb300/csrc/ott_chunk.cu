@@ -39,7 +39,6 @@
 namespace ott {
 namespace {
 
-constexpr float GROW = 8.0f;                // log2: see rescale
 constexpr int FI = 8;                       // fp16 tokens per work item
 constexpr int CT = CHUNK_TILES * TILE;      // block slots per work item
 // Query rows per kv head up to which the decode kernel (its rows mode) and
@@ -305,8 +304,8 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     };
     // Scores whose largest (log2 units) are mx in this lane: the reference
     // that weights are taken against moves up, and the sums and outputs are
-    // rescaled, only when one has grown by 2^GROW (weights stay below 2^GROW,
-    // far inside fp16; the common case is one vote and no exchange).
+    // rescaled, only when one has grown by 2^GROW (the common case is one vote
+    // and no exchange).
     auto rescale = [&](float (&mx)[NC][2]) {
         bool grew = false;
 #pragma unroll
@@ -399,7 +398,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                     float p[2];
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        p[x] = ch_ex2(d[nc][x] - (m_run[nc][x] == -CUDART_INF_F ? 0.0f : m_run[nc][x]));
+                        p[x] = ch_ex2(d[nc][x] - (m_run[nc][x] == -CUDART_INF_F ? 0.0f : m_run[nc][x] - LIFT));
                         l_run[nc][x] += p[x];
                     }
                     bp[nc] = transpose8x8(ch_h2(__floats2half2_rn(p[0], p[1])));
@@ -497,7 +496,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                         float add[2];
 #pragma unroll
                         for (int x = 0; x < 2; ++x)
-                            add[x] = off2[nc][x] - (m_run[nc][x] == -CUDART_INF_F ? 0.0f : m_run[nc][x]);
+                            add[x] = off2[nc][x] - (m_run[nc][x] == -CUDART_INF_F ? 0.0f : m_run[nc][x] - LIFT);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float p[2];

@@ -176,6 +176,14 @@ __device__ __forceinline__ int ch_warp_of(long long W, int NWp, long long x) {
     return (int)(((unsigned long long)(x + 1) * (unsigned long long)NWp + (unsigned long long)W - 1) /
                  (unsigned long long)W) - 1;
 }
+// Rounded to fp16, a weight loses its last bits below 2^-14 and is gone below
+// 2^-25, while the sum of the weights, in fp32, counts all of it. A row's
+// reference lies at most GROW (log2) below its largest score, so weights are
+// taken LIFT higher: the largest is at most 2^(GROW + LIFT), inside fp16, and
+// what is lost lies 2^LIFT lower. The factor 2^LIFT is in sums and outputs
+// alike and cancels.
+constexpr float GROW = 8.0f, LIFT = 7.0f;
+
 // Entry that holds work item x (x < W): the last one whose base is <= x.
 __device__ __forceinline__ int ch_entry_of(const ChunkTable &st, int nseq, long long x) {
     int lo = 0, hi = nseq;

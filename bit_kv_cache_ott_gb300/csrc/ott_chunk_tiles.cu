@@ -63,7 +63,6 @@ constexpr int ROWS = 128;            // rows of a tile
 constexpr int THREADS = 512;
 constexpr int PROD0 = 8, MMA_WARP = 15;
 constexpr int META = 4;              // steps of group metadata in flight
-constexpr float GROW = 8.0f;         // log2: the output is rescaled when the maximum has grown by this
 constexpr int SUM_STEPS = SUM_TOKENS / STEP_TOK;   // steps whose products stay one sum in TMEM
 constexpr int MIN_STEPS = 2;         // steps per CTA at least
 constexpr int FIXED = 4;             // a tile's fixed cost (find it, queries, fill the pipeline, output) in steps of 2 us
@@ -815,7 +814,7 @@ __device__ void softmax(const TileArgs &ta, const ChunkSeq &s, const Tile &t, ui
             }
         }
         if (m_ref == -CUDART_INF_F) m_ref = mx;   // the first token that the row sees: its output is zero so far
-        const float mm = m_ref == -CUDART_INF_F ? 0.0f : m_ref;
+        const float mm = m_ref == -CUDART_INF_F ? 0.0f : m_ref - LIFT;
         float2 sum = make_float2(0.0f, 0.0f);
         auto weights = [&](int k, const float *y) {
             const float2 ad = make_float2(off[k] - mm, off[k] - mm), sc = make_float2(a.sl2, a.sl2);

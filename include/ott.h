@@ -341,14 +341,16 @@ int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t 
  * appends would give it if none of them flushed. The cache is read only and
  * may be empty, in part or whole (plain causal attention over the chunk).
  * out may not alias q, k or v.
- * Softmax statistics and sums are fp32. With up to four query rows per kv
- * head (n * Hq / Hkv) the products are ott_decode_attn's; with more, the
- * weights and the dequantized values are rounded to fp16 for the tensor cores
- * (each at most 2^-11 relative). Keys and
- * values, the chunk's too, are finite and at most 48,000 in magnitude: a
- * value that is not finite spoils rows that do not see it as well. A query
- * that is not finite gets NaN in its own row and changes no other. A call
- * gives the same bits every time.
+ * Softmax statistics and sums are fp32; the tensor cores add up at most
+ * 25,088 tokens on their own. With up to four query rows per kv head
+ * (n * Hq / Hkv) the products are ott_decode_attn's (a weight times a value's
+ * scale in two fp16 pieces, lost below 2^-25); with more, the weights and the
+ * dequantized values are rounded to fp16 for the tensor cores (each by at most
+ * 2^-11 relative, a weight also by 2^-32 of its row's largest).
+ * Keys and values, the chunk's too, are finite and at most 48,000 in
+ * magnitude: a value that is not finite spoils rows that do not see it as
+ * well. A query that is not finite gets NaN in its own row and changes no
+ * other. A call gives the same bits every time.
  * Partial results go to the cache's split-K scratch, or where they are
  * larger to stream-ordered scratch from the library's pool (see ott_prefill;
  * OTT_ERR_OOM if none can be had, before anything is queued).

@@ -81,7 +81,8 @@ LONG = [
 
 @pytest.mark.parametrize("B,Hq,Hkv,d,G,T,n,window,sinks", LONG)
 def test_rows_over_long_caches(ott, B, Hq, Hkv, d, G, T, n, window, sinks):
-    """Sampled rows, element by element: the bound of tests/chunk_util.py and the sums' 2^-11 / 3 (above); one query is NaN."""
+    """Sampled rows, element by element: the bound of tests/chunk_util.py, but 2^-32 of the row's largest weight per token
+    (twice that allowed), and the sums' 2^-11 / 3 (above); one query is NaN."""
     g = torch.Generator(device=DEV).manual_seed(9)
     K, V = (torch.randn(B, Hkv, T, d, generator=g, device=DEV).half() for _ in range(2))
     K[:, :, 17::5000] *= 0.03
@@ -109,7 +110,7 @@ def test_rows_over_long_caches(ott, B, Hq, Hkv, d, G, T, n, window, sinks):
             w = torch.softmax((qd @ Kd.t() / d ** 0.5).masked_fill(~see, -math.inf), 1)
             ref, A = w @ Vd, w @ Vd.abs()
             e = (d / 16 + 4) * 2.0 ** -22 * 2 * mag + 3 * 2.0 ** -23 * mag + 2.0 ** -21
-            tol = 2.0 ** -11 * (2 * A + ref.abs() + A / 3) * 1.01 + 2 * e * A + 2.0 ** -24 * (see.double() @ Vd.abs()) + 2.0 ** -24
+            tol = 2.0 ** -11 * (2 * A + ref.abs() + A / 3) * 1.01 + 2 * e * A + 2.0 ** -31 * (see.double() @ Vd.abs()) + 2.0 ** -24
             got = out[0, hh, rows].double()
             assert bool(got.isfinite().all()), (h, hh)
             assert bool(((got - ref).abs() <= tol).all()), (h, hh, ((got - ref).abs() - tol).max().item())
