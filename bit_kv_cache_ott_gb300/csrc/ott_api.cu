@@ -628,9 +628,11 @@ int ott_chunk_attn(ott_cache *c, const void *q, const void *k, const void *v, vo
     if (const int rc = chunk_state(c, lens)) return rc;
     if (n < 0 || window < 0 || sinks < 0 || !lens_ok(c, n, lens)) return OTT_ERR_INVALID;
     if (n == 0) return OTT_OK;
-    if (!q || !k || !v || !out || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out) || out == q ||
-        out == k || out == v)
+    if (!q || !k || !v || !out || !aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out))
         return OTT_ERR_INVALID;
+    // CTAs write rows while others still read theirs
+    const size_t nq = (size_t)c->B * c->Hq * n * c->d * 2, nk = (size_t)c->B * c->Hkv * n * c->d * 2;
+    if (overlap(out, nq, q, nq) || overlap(out, nq, k, nk) || overlap(out, nq, v, nk)) return OTT_ERR_INVALID;
     ChunkCall call = {static_cast<const __half *>(q), static_cast<const __half *>(k), static_cast<const __half *>(v),
                       static_cast<__half *>(out), n, lens, window, sinks};
     return chunk_call(c, call, stream);
@@ -640,7 +642,9 @@ int ott_decode_attn_window(ott_cache *c, const void *q, void *out, int window, i
     if (!c) return OTT_ERR_INVALID;
     if (const int rc = chunk_state(c, nullptr)) return rc;
     if (c->T < 1 || some_sequence_empty(c)) return OTT_ERR_STATE;
-    if (window < 0 || sinks < 0 || !q || !out || !aligned16(q) || !aligned16(out) || q == out) return OTT_ERR_INVALID;
+    const size_t nq = (size_t)c->B * c->Hq * c->d * 2;
+    if (window < 0 || sinks < 0 || !q || !out || !aligned16(q) || !aligned16(out) || overlap(q, nq, out, nq))
+        return OTT_ERR_INVALID;
     ChunkCall call = {static_cast<const __half *>(q), nullptr, nullptr, static_cast<__half *>(out), 1, nullptr,
                       window, sinks};
     return chunk_call(c, call, stream);

@@ -278,6 +278,11 @@ struct Scratch {
     bool owned;
     cudaStream_t stream;
 };
+// Memory ranges (na bytes at a, nb at b) that share a byte.
+inline bool overlap(const void *a, size_t na, const void *b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y ? y - x < na : x - y < nb;
+}
 // query heads per decode pass for gq query heads per kv head
 inline int slice_heads(int gq) { return (gq == 1 || gq == 2 || gq == 4) ? gq : 4; }
 

@@ -156,11 +156,6 @@ __global__ void __launch_bounds__(ROPE_THREADS) k_rope_any(const __grid_constant
     }
 }
 
-bool overlap(const void *a, size_t na, const void *b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y ? y - x < na : x - y < nb;
-}
-
 }  // namespace
 }  // namespace ott
 

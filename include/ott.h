@@ -340,7 +340,7 @@ int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t 
  * 0 .. i. out = softmax(q . K^T / sqrt(d)) V, as ott_decode_attn after i + 1
  * appends would give it if none of them flushed. The cache is read only and
  * may be empty, in part or whole (plain causal attention over the chunk).
- * out may not alias q, k or v.
+ * out may not overlap q, k or v, in part either (OTT_ERR_INVALID).
  * Softmax statistics and sums are fp32; the tensor cores add up at most
  * 25,088 tokens on their own. With up to four query rows per kv head
  * (n * Hq / Hkv) the products are ott_decode_attn's (a weight times a value's
@@ -370,7 +370,8 @@ int ott_append_chunk(ott_cache *c, const void *k, const void *v, int n, const in
 
 /*
  * ott_decode_attn with a window: one query per sequence, at the position of
- * the last token appended (p = T_b - 1). q, out: DEVICE fp16 [B][Hq][d].
+ * the last token appended (p = T_b - 1). q, out: DEVICE fp16 [B][Hq][d],
+ * apart from one another (OTT_ERR_INVALID).
  * A query whose every token in sight a policy has discarded gets zeros (NaN
  * if it is not finite). Precision and scratch as ott_chunk_attn;
  * OTT_ERR_STATE as ott_decode_attn.
