@@ -10,7 +10,7 @@
 // with z + s split into two fp16 numbers. So the logits keep fp32 accuracy;
 // a key rounded to fp16 instead would move a channel of magnitude 40 by up
 // to 2^-6 the same way for every token of the block that has that code. The
-// softmax weights (in [0, 1], relative 2^-11) and the values z + s * code
+// softmax weights (relative 2^-11) and the values z + s * code
 // are rounded to fp16: their errors differ from token to token and average
 // out in the sum.
 //
@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     uint32_t Bq[NC][NKT][2];          // queries: B operand, column r of each group
     uint32_t ks2[NKT][2];             // the block's key scales, A operand order
     float off2[NC][2];                // q . (z + s) of columns 2i, 2i + 1, in log2 units
+    bool wide = false;                // the block's key scales are halves
     float acc[NC][NKT][4], m_run[NC][2], l_run[NC][2];
     int pos[NC][2], lo[NC][2];        // the columns' positions and window starts
     int uo = 0, cnt_rows = 0;
@@ -420,14 +421,17 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                     float d[NC][4];
 #pragma unroll
                     for (int nc = 0; nc < NC; ++nc) d[nc][0] = d[nc][1] = d[nc][2] = d[nc][3] = 0.0f;
+                    uint32_t top = 0;   // the largest scales
 #pragma unroll
                     for (int kt = 0; kt < NKT; ++kt) {
                         uint32_t hi[2], lw[2];
 #pragma unroll
                         for (int o = 0; o < 2; ++o) {
                             const uint2 sz = *reinterpret_cast<const uint2 *>(stage + 4 * (16 * kt + 2 * i + 8 * o));
-                            ks2[kt][o] = __byte_perm(sz.x, sz.y, 0x5410);
-                            ch_offset(ks2[kt][o], __byte_perm(sz.x, sz.y, 0x7632), hi[o], lw[o]);
+                            const uint32_t s2 = __byte_perm(sz.x, sz.y, 0x5410);
+                            top = __vmaxu2(top, s2);
+                            ks2[kt][o] = s2;
+                            ch_offset(s2, __byte_perm(sz.x, sz.y, 0x7632), hi[o], lw[o]);
                         }
 #pragma unroll
                         for (int nc = 0; nc < NC; ++nc)
@@ -437,103 +441,117 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                     for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
                         for (int x = 0; x < 2; ++x) off2[nc][x] = (d[nc][x] + d[nc][2 + x]) * a.sl2;
+                    wide = __any_sync(0xffffffffu, ch_wide(top) || ch_wide(top >> 16));
+                    if (wide) {
+#pragma unroll
+                        for (int kt = 0; kt < NKT; ++kt)
+#pragma unroll
+                            for (int o = 0; o < 2; ++o) ks2[kt][o] = ch_h2(__hmul2(ch_as_h2(ks2[kt][o]), __float2half2_rn(0.5f)));
+                    }
                 }
                 // one tile of 16 slots at a time: a loop body that the
                 // instruction cache holds (four tiles unrolled measured twice the time)
                 const int nt = (mt_.x + TILE - 1) / TILE;
+                // (twice: scores of halved scales, in a body of their own, so that the common one stays as it is)
+                auto block_tiles = [&](auto twice) {
 #pragma unroll 1
-                for (int tau = 0; tau < nt; ++tau) {
-                    const uint8_t *tb = stage + KSZ + tau * TB;
-                    float sc[NC][4], sd[NC][4], mx[NC][2];   // two chains of products, even and odd k-tiles
+                    for (int tau = 0; tau < nt; ++tau) {
+                        const uint8_t *tb = stage + KSZ + tau * TB;
+                        float sc[NC][4], sd[NC][4], mx[NC][2];   // two chains of products, even and odd k-tiles
 #pragma unroll
-                    for (int nc = 0; nc < NC; ++nc)
+                        for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-                        for (int x = 0; x < 4; ++x) sc[nc][x] = sd[nc][x] = 0.0f;
-                    {
-                        uint32_t w[NW], w8[NW];
-                        lds_words<NW>(tb + tile_k_off(D) + lane * NW * 4, w);
+                            for (int x = 0; x < 4; ++x) sc[nc][x] = sd[nc][x] = 0.0f;
+                        {
+                            uint32_t w[NW], w8[NW];
+                            lds_words<NW>(tb + tile_k_off(D) + lane * NW * 4, w);
 #pragma unroll
-                        for (int x = 0; x < NW; ++x) w8[x] = w[x] >> 8;
+                            for (int x = 0; x < NW; ++x) w8[x] = w[x] >> 8;
 #pragma unroll
-                        for (int kt = 0; kt < NKT; ++kt) {
-                            uint32_t f4[4];   // (token r + 8 th, channels 16 kt + 8 o): f4[th + 2 o]
+                            for (int kt = 0; kt < NKT; ++kt) {
+                                uint32_t f4[4];   // (token r + 8 th, channels 16 kt + 8 o): f4[th + 2 o]
 #pragma unroll
-                            for (int o = 0; o < 2; ++o)
+                                for (int o = 0; o < 2; ++o)
 #pragma unroll
-                                for (int th = 0; th < 2; ++th) {
-                                    const int q = o * NKT + kt, wi = 2 * (q >> 3) + th;
-                                    f4[th + 2 * o] = ch_key(mg, w[wi], w8[wi], q & 7, ks2[kt][o]);
-                                }
+                                    for (int th = 0; th < 2; ++th) {
+                                        const int q = o * NKT + kt, wi = 2 * (q >> 3) + th;
+                                        f4[th + 2 * o] = ch_key(mg, w[wi], w8[wi], q & 7, ks2[kt][o]);
+                                    }
+#pragma unroll
+                                for (int nc = 0; nc < NC; ++nc)
+                                    mma16816(kt & 1 ? sd[nc] : sc[nc], f4[0], f4[1], f4[2], f4[3], Bq[nc][kt][0], Bq[nc][kt][1]);
+                            }
 #pragma unroll
                             for (int nc = 0; nc < NC; ++nc)
-                                mma16816(kt & 1 ? sd[nc] : sc[nc], f4[0], f4[1], f4[2], f4[3], Bq[nc][kt][0], Bq[nc][kt][1]);
+#pragma unroll
+                                for (int x = 0; x < 4; ++x) sc[nc][x] = decltype(twice)::value ? 2.0f * (sc[nc][x] + sd[nc][x]) : sc[nc][x] + sd[nc][x];
+                        }
+                        if (wnd || mt_.x < 16 * tau + 16) {   // a window, or the block's last tile
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int x = 16 * tau + r + 8 * h;
+                                const int t = x >= mt_.x ? INT_MAX : (wnd ? __ldg(bi + x) : 0);
+#pragma unroll
+                                for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+                                    for (int y = 0; y < 2; ++y)
+                                        if (!chunk_sees(t, pos[nc][y], lo[nc][y], a.sinks)) sc[nc][2 * h + y] = -CUDART_INF_F;
+                            }
                         }
 #pragma unroll
                         for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
-                            for (int x = 0; x < 4; ++x) sc[nc][x] += sd[nc][x];
-                    }
-                    if (wnd || mt_.x < 16 * tau + 16) {   // a window, or the block's last tile
+                            for (int x = 0; x < 2; ++x) mx[nc][x] = fmaf(fmaxf(sc[nc][x], sc[nc][2 + x]), a.sl2, off2[nc][x]);
+                        rescale(mx);
+                        uint32_t bp[NC][2];   // weights, B operand: tokens 2i, 2i + 1 (+ 8) of column r
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const int x = 16 * tau + r + 8 * h;
-                            const int t = x >= mt_.x ? INT_MAX : (wnd ? __ldg(bi + x) : 0);
+                        for (int nc = 0; nc < NC; ++nc) {
+                            float add[2];
 #pragma unroll
-                            for (int nc = 0; nc < NC; ++nc)
+                            for (int x = 0; x < 2; ++x)
+                                add[x] = off2[nc][x] - (m_run[nc][x] == -CUDART_INF_F ? 0.0f : m_run[nc][x] - LIFT);
 #pragma unroll
-                                for (int y = 0; y < 2; ++y)
-                                    if (!chunk_sees(t, pos[nc][y], lo[nc][y], a.sinks)) sc[nc][2 * h + y] = -CUDART_INF_F;
-                        }
-                    }
+                            for (int h = 0; h < 2; ++h) {
+                                float p[2];
 #pragma unroll
-                    for (int nc = 0; nc < NC; ++nc)
-#pragma unroll
-                        for (int x = 0; x < 2; ++x) mx[nc][x] = fmaf(fmaxf(sc[nc][x], sc[nc][2 + x]), a.sl2, off2[nc][x]);
-                    rescale(mx);
-                    uint32_t bp[NC][2];   // weights, B operand: tokens 2i, 2i + 1 (+ 8) of column r
-#pragma unroll
-                    for (int nc = 0; nc < NC; ++nc) {
-                        float add[2];
-#pragma unroll
-                        for (int x = 0; x < 2; ++x)
-                            add[x] = off2[nc][x] - (m_run[nc][x] == -CUDART_INF_F ? 0.0f : m_run[nc][x] - LIFT);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float p[2];
-#pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                p[x] = ch_ex2(fmaf(sc[nc][2 * h + x], a.sl2, add[x]));
-                                l_run[nc][x] += p[x];
-                            }
-                            bp[nc][h] = transpose8x8(ch_h2(__floats2half2_rn(p[0], p[1])));
-                        }
-                    }
-                    uint32_t w[NW], w8[NW];
-                    lds_words<NW>(tb + tile_v_off(D) + lane * NW * 4, w);
-#pragma unroll
-                    for (int x = 0; x < NW; ++x) w8[x] = w[x] >> 8;
-#pragma unroll
-                    for (int gm = 0; gm < NKT / 2; ++gm) {   // a value group: 32 channels, two m-tiles
-                        const uint4 sz = *reinterpret_cast<const uint4 *>(tb + tile_sz_off(D) + (gm * 4 + i) * 16);
-                        const uint32_t s2[2] = {__byte_perm(sz.x, sz.y, 0x5410), __byte_perm(sz.z, sz.w, 0x5410)};
-                        const uint32_t z2[2] = {__byte_perm(sz.x, sz.y, 0x7632), __byte_perm(sz.z, sz.w, 0x7632)};
-#pragma unroll
-                        for (int mm = 0; mm < 2; ++mm) {
-                            const int mt = 2 * gm + mm;
-                            uint32_t f4[4];   // (channels r + 8 half, tokens 2i + 8 tp): f4[half + 2 tp]
-#pragma unroll
-                            for (int tp = 0; tp < 2; ++tp)
-#pragma unroll
-                                for (int half = 0; half < 2; ++half) {
-                                    const int q = half * NKT + mt, wi = 2 * (q >> 3) + tp;
-                                    f4[half + 2 * tp] = ch_val(mg, w[wi], w8[wi], q & 7, s2[tp], z2[tp]);
+                                for (int x = 0; x < 2; ++x) {
+                                    p[x] = ch_ex2(fmaf(sc[nc][2 * h + x], a.sl2, add[x]));
+                                    l_run[nc][x] += p[x];
                                 }
+                                bp[nc][h] = transpose8x8(ch_h2(__floats2half2_rn(p[0], p[1])));
+                            }
+                        }
+                        uint32_t w[NW], w8[NW];
+                        lds_words<NW>(tb + tile_v_off(D) + lane * NW * 4, w);
 #pragma unroll
-                            for (int nc = 0; nc < NC; ++nc)
-                                mma16816(acc[nc][mt], f4[0], f4[1], f4[2], f4[3], bp[nc][0], bp[nc][1]);
+                        for (int x = 0; x < NW; ++x) w8[x] = w[x] >> 8;
+#pragma unroll
+                        for (int gm = 0; gm < NKT / 2; ++gm) {   // a value group: 32 channels, two m-tiles
+                            const uint4 sz = *reinterpret_cast<const uint4 *>(tb + tile_sz_off(D) + (gm * 4 + i) * 16);
+                            const uint32_t s2[2] = {__byte_perm(sz.x, sz.y, 0x5410), __byte_perm(sz.z, sz.w, 0x5410)};
+                            const uint32_t z2[2] = {__byte_perm(sz.x, sz.y, 0x7632), __byte_perm(sz.z, sz.w, 0x7632)};
+#pragma unroll
+                            for (int mm = 0; mm < 2; ++mm) {
+                                const int mt = 2 * gm + mm;
+                                uint32_t f4[4];   // (channels r + 8 half, tokens 2i + 8 tp): f4[half + 2 tp]
+#pragma unroll
+                                for (int tp = 0; tp < 2; ++tp)
+#pragma unroll
+                                    for (int half = 0; half < 2; ++half) {
+                                        const int q = half * NKT + mt, wi = 2 * (q >> 3) + tp;
+                                        f4[half + 2 * tp] = ch_val(mg, w[wi], w8[wi], q & 7, s2[tp], z2[tp]);
+                                    }
+#pragma unroll
+                                for (int nc = 0; nc < NC; ++nc)
+                                    mma16816(acc[nc][mt], f4[0], f4[1], f4[2], f4[3], bp[nc][0], bp[nc][1]);
+                            }
                         }
                     }
-                }
+                };
+                if (wide)
+                    block_tiles(std::true_type{});
+                else
+                    block_tiles(std::false_type{});
             }
         }
         // refill the stage, move on

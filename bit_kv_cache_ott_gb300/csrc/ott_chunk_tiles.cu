@@ -63,6 +63,8 @@ constexpr int ROWS = 128;            // rows of a tile
 constexpr int THREADS = 512;
 constexpr int PROD0 = 8, MMA_WARP = 15;
 constexpr int META = 4;              // steps of group metadata in flight
+constexpr int HIDDEN = 1, WIDE = 2;  // its flags: some row does not see some token; scores of halved scales
+constexpr unsigned long long ANY_WIDE = 0x0002020202020202ull;
 constexpr int SUM_STEPS = SUM_TOKENS / STEP_TOK;   // steps whose products stay one sum in TMEM
 constexpr int MIN_STEPS = 2;         // steps per CTA at least
 constexpr int FIXED = 4;             // a tile's fixed cost (find it, queries, fill the pipeline, output) in steps of 2 us
@@ -391,15 +393,16 @@ struct Producer {
     }
     __device__ void wait(int which) { bar_wait(&bar[which + (it & 1)], ((it >> 1) & 1u) ^ 1u, gave_up); }
     // The tile's part is written: pos (of lane < 16's token, INT_MAX: none)
-    // decides whether some row does not see it, where `ask`.
-    __device__ void key_done(bool ask, int pos) {
+    // decides whether some row does not see it, where `ask`; wide: its scores
+    // count twice.
+    __device__ void key_done(bool ask, int pos, bool wide) {
         bool hidden = false;
         if (ask) {
             hidden = __any_sync(0xffffffffu, lane < 16 && !(pos <= pmin && (pos >= lomax || pos < a.sinks)));
             if (lane < 16)
                 reinterpret_cast<volatile int *>(sm + C::OFF_POS)[(it % META) * STEP_TOK + 16 * w + slot_of(lane)] = pos;
         }
-        if (lane == 0) *reinterpret_cast<volatile uint8_t *>(sm + C::OFF_FLAG + (it % META) * 8 + w) = hidden;
+        if (lane == 0) *reinterpret_cast<volatile uint8_t *>(sm + C::OFF_FLAG + (it % META) * 8 + w) = (hidden ? HIDDEN : 0) | (wide ? WIDE : 0);
         proxy_fence();
         __syncwarp();
         if (lane == 0) bar_arrive(&bar[B_KFULL + (it & 1)]);
@@ -488,22 +491,26 @@ struct Producer {
                     zero_keys(kb);
                     fresh = 2;
                 }
-                const bool ask = g.left < 16 || a.window > 0;
+                const bool wide = *reinterpret_cast<volatile int *>(stage + 4 * D) != 0;   // (in a register, it would be spilled)
+                const bool ask = g.left < 16 || a.window > 0 || wide;
                 int pos = INT_MAX;
                 if (ask && lane < 16 && lane < g.left)
                     pos = a.window > 0 ? __ldg(a.bidx + ((size_t)u * a.NB + g.j) * a.G + 16 * g.sub + lane) : 0;
-                key_done(ask, pos);
+                key_done(ask, pos, wide);
             }
             if (enter) {   // the block's scales, through shared memory; then the next block's are fetched
                 __syncwarp();
                 if (lane < D / 4) *reinterpret_cast<uint4 *>(stage + 16 * lane) = hb;
+                const bool wide = __any_sync(0xffffffffu, lane < D / 4 && ch_wide(__vmaxu2(__vmaxu2(hb.x, hb.y), __vmaxu2(hb.z, hb.w))));
+                *reinterpret_cast<volatile int *>(stage + 4 * D) = wide;   // the same by every lane
+                const __half2 part = __float2half2_rn(wide ? 0.5f : 1.0f);
                 __syncwarp();
 #pragma unroll
                 for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
                     for (int o = 0; o < 2; ++o) {
                         const uint2 z = *reinterpret_cast<const uint2 *>(stage + 4 * (16 * kt + 2 * i + 8 * o));
-                        ks2[kt][o] = __byte_perm(z.x, z.y, 0x5410);
+                        ks2[kt][o] = ch_h2(__hmul2(ch_as_h2(__byte_perm(z.x, z.y, 0x5410)), part));
                     }
                 fresh = 2;   // both slots
                 xb = x + k + 1 - gn.sub + gn.per;
@@ -604,7 +611,7 @@ struct Producer {
             if (lane < 2 * CPR)
                 *reinterpret_cast<uint4 *>(kb + (lane % CPR / 8) * (ROWS * 128) + (STEP_TOK + 2 * w + lane / CPR) * 128 +
                                            (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
-            key_done(true, pos);
+            key_done(true, pos, false);
             asm volatile("cp.async.wait_all;" ::: "memory");
             wait(B_VEMPTY);   // (its __syncwarp covers the copies)
             uint8_t *vb = value_at();
@@ -669,6 +676,21 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
             mma_ss(tmem + C::S(t), dq + t * (C::QB / 16) + off, dk + slot * (C::KB / 16) + off, HI, instr_desc(128), k > 0);
         }
     };
+    // groups whose keys are halves: their 16 columns once more
+    auto scores_again = [&](int t, int slot, uint32_t it) {
+        unsigned long long flags = *reinterpret_cast<const volatile unsigned long long *>(sm + C::OFF_FLAG + (it % META) * 8);
+        if (!(flags & ANY_WIDE)) return;
+#pragma unroll 1
+        for (int w = 0; w < GRPS; ++w, flags >>= 8)
+            if (flags & WIDE) {
+#pragma unroll 1
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint32_t off = ((k / 4) * (ROWS * 128) + (k & 3) * 32) / 16;
+                    mma_ss(tmem + C::S(t) + 16 * w, dq + t * (C::QB / 16) + off, dk + slot * (C::KB / 16) + off + w * (16 * 128 / 16),
+                           desc_hi(1024, 2), instr_desc(16), true);
+                }
+            }
+    };
     auto values = [&](int t, int slot, bool acc) {
 #pragma unroll
         for (int k = 0; k < GRPS; ++k) {
@@ -686,6 +708,7 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
         tc_after();
         if (elect_one()) {
             scores(0, slot);
+            scores_again(0, slot, it);
             tc_commit(&bar[B_SFULL]);
         }
         __syncwarp();
@@ -698,6 +721,7 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
                     tc_commit(&bar[B_VEMPTY + prev]);
                 }
                 scores(1, slot);
+                scores_again(1, slot, it);
                 tc_commit(&bar[B_SFULL + 1]);
                 tc_commit(&bar[B_KEMPTY + slot]);
             }

@@ -347,9 +347,9 @@ int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t 
  * scale in two fp16 pieces, lost below 2^-25); with more, the weights and the
  * dequantized values are rounded to fp16 for the tensor cores (each by at most
  * 2^-11 relative, a weight also by 2^-32 of its row's largest).
- * Keys and values, the chunk's too, are finite and at most 48,000 in
- * magnitude: a value that is not finite spoils rows that do not see it as
- * well. A query that is not finite gets NaN in its own row and changes no
+ * Keys and values, the chunk's too, are finite; values are at most 65,440 in
+ * magnitude (dequantized, a larger one may round to infinity). One that is
+ * not finite spoils rows that do not see it as well. A query that is not finite gets NaN in its own row and changes no
  * other. A call gives the same bits every time.
  * Partial results go to the cache's split-K scratch, or where they are
  * larger to stream-ordered scratch from the library's pool (see ott_prefill;
