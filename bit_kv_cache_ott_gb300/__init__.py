@@ -189,7 +189,16 @@ def _rope_operand(x, out, name, B, n, d):
 
 @functools.lru_cache(maxsize=64)
 def _rope_plan(sections, base, interleaved, restart):
-    return C.byref(RopePlan(len(sections), (C.c_int * 4)(*sections), base, int(interleaved), int(restart)))
+    sec = (C.c_int * 4)(*[_int32(x, "sections") for x in sections])
+    return C.byref(RopePlan(len(sections), sec, base, int(interleaved), int(restart)))
+
+
+def _int32(x, name: str) -> int:
+    """x as the C ABI's int (ctypes would drop the bits that do not fit)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
 
 
 def _same_device(idx, *tensors):
@@ -346,7 +355,7 @@ class OTTCache:
             return None
         if len(lens) != self.B:
             raise ValueError("lens must hold one length per sequence")
-        return (C.c_int * self.B)(*[int(x) for x in lens])
+        return (C.c_int * self.B)(*[_int32(x, "lens") for x in lens])
 
     def chunk_attn(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens=None, window: int = 0, sinks: int = 0,
                    out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
@@ -361,8 +370,8 @@ class OTTCache:
             out = torch.empty_like(q)
         ptr.append(_dev_ptr(out, shp, "out"))
         _same_device(self._dev, q, k, v, out)
-        _on_device(self._dev, load().ott_chunk_attn, "ott_chunk_attn", self._h, *ptr, n, self._lens(lens), int(window),
-                   int(sinks), _stream_of(stream, self._dev))
+        _on_device(self._dev, load().ott_chunk_attn, "ott_chunk_attn", self._h, *ptr, n, self._lens(lens),
+                   _int32(window, "window"), _int32(sinks, "sinks"), _stream_of(stream, self._dev))
         return out
 
     def append_chunk(self, k: torch.Tensor, v: torch.Tensor, lens=None, stream=None):
@@ -384,8 +393,8 @@ class OTTCache:
             out = torch.empty_like(q)
         op = _dev_ptr(out, shp, "out")
         _same_device(self._dev, q, out)
-        _on_device(self._dev, load().ott_decode_attn_window, "ott_decode_attn_window", self._h, qp, op, int(window),
-                   int(sinks), _stream_of(stream, self._dev))
+        _on_device(self._dev, load().ott_decode_attn_window, "ott_decode_attn_window", self._h, qp, op,
+                   _int32(window, "window"), _int32(sinks, "sinks"), _stream_of(stream, self._dev))
         return out
 
     def counts(self):
