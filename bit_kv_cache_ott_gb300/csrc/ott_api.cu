@@ -241,6 +241,7 @@ int create_cache(int B, int Hq, int Hkv, int d, int G, int R, int P, int max_tok
     c->device = dev;
     c->sm_count = sms;
     c->flush_smem = fsmem;
+    c->smem_optin = smem_optin;
     // the decode grid's warps split the work items evenly; a warp's range
     // (at most W/NW + 1 items) touches at most U*S/NW + 2 units (kv-head slices)
     const int nwarps = sms * DEC_WARPS;

@@ -1210,11 +1210,16 @@ bool prefill_parallel_ok(const ott_cache *c, int nf, int shared_units) {
     return c->cold < 0 && c->pct < 0 && nf >= 2 && shared_units < c->sm_count;
 }
 
+// Shared memory of k_pf_carry's lists, after the static counts.
+static size_t carry_room(const ott_cache *c) { return (size_t)c->smem_optin - sizeof(int) * 2 * CARRY_MAX_CHUNKS; }
+
 // Chunks per unit of the pool scan: enough CTAs to cover the SMs twice, at
-// most CARRY_MAX_CHUNKS, and chunks of at least SCAN_WARPS groups.
+// most CARRY_MAX_CHUNKS, chunks of at least SCAN_WARPS groups, and no more
+// lists than a carry's CTA can hold (a pool of 447 tokens or more).
 static int scan_chunks(const ott_cache *c, int nu, int nf) {
     long long C = std::min<long long>(CARRY_MAX_CHUNKS, (nf + SCAN_WARPS - 1) / SCAN_WARPS);
     C = std::min<long long>(C, (2LL * c->sm_count + nu - 1) / nu);
+    while (C > 1 && carry_smem_bytes((int)C, 1, c->P) > carry_room(c)) --C;
     return C < 1 ? 1 : (int)C;
 }
 
@@ -1259,21 +1264,16 @@ static cudaError_t run_pf_scan(const ott_cache *c, const uint64_t *gtop, uint64_
     // C chunks per unit, one CTA each; a warp per 4 groups of a chunk (fewer,
     // smaller CTAs cover the SMs in one wave), at most SCAN_WARPS, within
     // the shared memory
-    int optin = 0;
-    e = cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, c->device);
-    if (e != cudaSuccess) return e;
     const int C = scan_chunks(c, nu, nl), cg = (nl + C - 1) / C;
     uint64_t *gtot = C > 1 ? phist + (size_t)nu * nl * P : nullptr;
     int sw = (cg + 4 - 1) / 4;
     sw = sw < 1 ? 1 : (sw > SCAN_WARPS ? SCAN_WARPS : sw);
-    while (sw > 1 && scan_smem_bytes(sw, P) > (size_t)optin) --sw;
+    while (sw > 1 && scan_smem_bytes(sw, P) > (size_t)c->smem_optin) --sw;
     e = launch_pdl(k_pf_scan, dim3((unsigned)(nu * C)), 32 * sw, scan_smem_bytes(sw, P), s, gtop, phist, nl, G, P, cg, C, gtot);
     if (e != cudaSuccess) return e;
     if (C > 1) {
         int cw = cg < SCAN_WARPS ? cg : SCAN_WARPS;
-        const size_t room = (size_t)optin - sizeof(int) * 2 * CARRY_MAX_CHUNKS;   // after the static counts
-        while (cw > 1 && carry_smem_bytes(C, cw, P) > room) --cw;
-        if (carry_smem_bytes(C, cw, P) > room) return cudaErrorInvalidValue;
+        while (cw > 1 && carry_smem_bytes(C, cw, P) > carry_room(c)) --cw;
         e = launch_pdl(k_pf_carry, dim3((unsigned)(nu * (C - 1))), 32 * cw, carry_smem_bytes(C, cw, P), s, phist, gtot, nl, G, P,
                        cg, C);
         if (e != cudaSuccess) return e;

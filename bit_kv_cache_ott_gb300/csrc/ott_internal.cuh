@@ -141,6 +141,7 @@ struct ott_cache {
     int device;
     int sm_count;
     int flush_smem;
+    int smem_optin;         // shared memory that a CTA can have
     int maxu;               // units (kv-head slices) one decode warp's item range can touch
     // device memory (one allocation)
     void *mem;
