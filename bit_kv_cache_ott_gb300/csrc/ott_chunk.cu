@@ -1,6 +1,8 @@
 // ott_chunk.cu -- attention of several query rows per kv head over the OTT
 // stores: a chunk of new tokens (ott_chunk_attn) or one query with a window
-// (ott_decode_attn_window), few rows at a time.
+// (ott_decode_attn_window). The plan of every such call, and the kernel for 5
+// to 16 rows (up to four go to the decode kernel, ott_decode.cu, more than 16
+// to ott_chunk_tiles.cu).
 //
 // Mathematics. A block's key channel is z + s * code. With code - 1 in
 // {-1, 0, 1, 2}, s * (code - 1) is an exact fp16 number, and
@@ -10,25 +12,25 @@
 // with z + s split into two fp16 numbers. So the logits keep fp32 accuracy;
 // a key rounded to fp16 instead would move a channel of magnitude 40 by up
 // to 2^-6 the same way for every token of the block that has that code. The
-// softmax weights (relative 2^-11) and the values z + s * code
-// are rounded to fp16: their errors differ from token to token and average
-// out in the sum.
+// softmax weights (relative 2^-11) and the values z + s * code are rounded to
+// fp16: their errors differ from token to token and average out in the sum.
 //
 // Layout of the work. A unit is (sequence, kv head, slice of 8 or 16 query
 // rows); row v = token * g + head, so that the g query heads that share a kv
 // head share its blocks, too. Work items are what one copy brings: 8 fp16
-// tokens (keys and values, 4 KB at d = 128) or a chunk of up to 64 slots of a block
-// (5.1 KB, with the block's key scales where the warp has not met them). A
-// grid of one CTA per SM (a multiple of that for very long runs) gives every
-// warp an equal contiguous run of items; the
-// copies run ahead of the products through a ring of stages that does not
-// stop at the borders of units. A warp leaves one partial (max, sum,
-// unnormalised output) per unit that it touches; k_chunk_combine merges them.
+// tokens (keys and values, 4 KB at d = 128) or a chunk of up to 64 slots of a
+// block (5.1 KB, with the block's key scales where the warp has not met them).
+// A grid of one CTA per SM (a multiple of that for very long runs) gives every
+// warp an equal contiguous run of items; the copies run ahead of the products
+// through a ring of stages that does not stop at the borders of units. A warp
+// leaves one partial (max, sum, unnormalised output) per unit that it touches;
+// k_chunk_combine merges them.
 //
 // What bounds it: the instructions that unpack codes into operands, of which
 // 8 or 16 columns of products do not make enough use; the copies run ahead
-// and HBM waits. Batch 32 x 4K, 32 heads of d = 128 (405 MB of cache): 184 us
-// with 4 rows (NC = 1) and 188 with 8, 2.2 TB/s; 258 with 16 rows (NC = 2).
+// and HBM waits. Batch 32 x 4K, 32 heads of d = 128 (405 MB of cache): 188 us
+// with 8 rows (NC = 1, 128 registers and 80 bytes spilled), 2.2 TB/s; 256 with
+// 16 (NC = 2, 236 registers).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -43,10 +45,9 @@ constexpr int FI = 8;                       // fp16 tokens per work item
 constexpr int CT = CHUNK_TILES * TILE;      // block slots per work item
 // Query rows per kv head up to which the decode kernel (its rows mode) and
 // then this file's kernel serve a call; the tcgen05 tiles take the rest. Batch
-// 32 x 4K, 32 heads: 4 rows 131 us in rows mode, 184 here (rows mode has one
-// slice of up to 4 rows and would read the cache twice for 5); 16 rows 258 us
-// here; 17 rows 440 us in tiles (256 rows at the same price), about 516 here
-// in two slices.
+// 32 x 4K, 32 heads: 4 rows 129 us in rows mode, 184 here (rows mode has one
+// slice of up to 4 rows and would read the cache twice for 5); 16 rows 256 us
+// here; 17 rows 441 us in tiles (64 rows 443), about 511 here in two slices.
 constexpr int DEC_ROWS_MAX = 4, ROWS_MAX = 16;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,

@@ -35,11 +35,12 @@
 // carried over in fp32 (finish): the tensor cores truncate.
 //
 // What bounds it: 2,048 tokens over 32K (8 kv heads, 4 heads each, d = 128)
-// take 820 us, 1.37 PFLOP/s of the sums that are asked for; without the
-// softmax 657 us, without unpacking 762, without either 644 (a step's products
-// are 1,920 cycles, the key tile's 16 extra rows among them). So the softmax
-// and the producers, who share the schedulers, hold the tensor cores up by a
-// fifth. With short caches a tile's fixed cost joins them: finding it and its
+// take 840 us, 1.34 PFLOP/s of the sums that are asked for. An earlier build
+// took 820; without the softmax 657 us, without unpacking 762, without either
+// 644 (a step's products are 1,920 cycles, the key tile's 16 extra rows among
+// them). So the softmax and the producers, who share the schedulers, hold the
+// tensor cores up by a fifth; sums carried over add 1 to 4% to long caches.
+// With short caches a tile's fixed cost joins them: finding it and its
 // queries, the first copies, the output: 7 us. Not taken: dequantizing to
 // fp16 in a pass of its own (six times the cache's bytes written, and read
 // for every pair of tiles); three tiles of rows or a second softmax set (do
@@ -1218,7 +1219,8 @@ bool plan_tiles(const ott_cache *c, ChunkArgs &a, ChunkTable &st, int &nC, bool 
     // tiles and their merge cost 8 steps and 0.1 per part of a tile. 333 new
     // tokens of five short sequences (100 tiles): 41 us in runs, 17 with a
     // tile per CTA; 1,024 tokens (128 tiles) over 2,048: 70 and 66, over
-    // 4,096: 91.3 and 90.4, over 7,168: 123 and 127.
+    // 4,096: 91.3 and 90.4, over 7,168: 123 and 127. (Fitted to shapes of 8 kv
+    // heads; elsewhere an estimate.)
     const double one = std::max<double>(FIXED + longest, std::min(W / sms + longest / 2.0, std::ceil(nT / sms) * (FIXED + longest)));
     double best = 1e30;
     for (int div = 1; div <= 4; div *= 2) {

@@ -39,9 +39,9 @@
 // token's product is good to 2^-12 of w s. One token with all the weight:
 // 7e-5 rms at s = 1.3, before the rounding of the output.) Batch
 // 32 x 4K, 32 heads of d = 128: four rows 129 us (427 MB, 3.3 TB/s), one row
-// without a window 100 (ott_decode_attn, which needs no masks and no table,
+// without a window 99 (ott_decode_attn, which needs no masks and no table,
 // 85), one with a window of 1,024 tokens and four first ones 56 (159 MB,
-// 2.9 TB/s; without the first ones 47). The masks, the products'
+// 2.9 TB/s; without the first ones 45). The masks, the products'
 // instructions and the smaller items of a windowed unit bound it, not HBM.
 #include <math_constants.h>
 

@@ -4,10 +4,10 @@
 // Pair i of a head's channels turns by the angle pos[axis(i)] * f_i with
 // f_i = base^-e_i. The angle of a far position (10^6 radians and more) has
 // no fractional digits left in 32 bits, so it is never formed: with
-// F_i = round(2^64 f_i / 2 pi) the 64-bit product pos * F_i, wrapped modulo
-// 2^64, is the turn's fraction in units of 2^-64, whole turns dropped
-// exactly. Its upper 32 bits, as a signed number of half turns in [-1, 1),
-// go to sincospif. The products and sums of a pair are taken in 32 bits and
+// F_i = 2^64 f_i / 2 pi, cut to a whole number, the 64-bit product pos * F_i,
+// wrapped modulo 2^64, is the turn's fraction in units of 2^-64, whole turns
+// dropped exactly. Its upper 32 bits, as a signed number of half turns in
+// [-1, 1), go to sincospif. The products and sums of a pair are taken in 32 bits and
 // rounded once to fp16.
 //
 // The pass reads and writes every element once and nothing else of size, so

@@ -42,8 +42,9 @@
  * ott_ex2_probe).
  *
  * Kernels of consecutive calls on one stream are chained by programmatic
- * dependent launches: an append or a decode may start while the kernel
- * before it finishes, and waits for it before reading its inputs.
+ * dependent launches: an append (its flushes too), a decode or a chunk's
+ * attention may start while the kernel before it finishes, and waits for it
+ * before reading its inputs.
  *
  * Conventions for every call:
  *   - Device pointers are CUDA device addresses of fp16 data (IEEE binary16),
@@ -87,7 +88,8 @@ enum {
  * G=128, R=32, P=32). max_tokens bounds T; all device memory is allocated
  * here (blocks, residual ring, pool, split-K scratch). The other calls
  * allocate nothing, except ott_export_state's staging buffer and the
- * parallel prefill's stream-ordered scratch (see ott_prefill).
+ * stream-ordered scratch of parallel prefills (see ott_prefill), of chunk
+ * appends and of chunk attention beyond the split-K scratch.
  * Supported: d in {64, 128}; Hq % Hkv == 0 (any ratio g = Hq/Hkv); G >= 1;
  * R >= 0; P >= 0; (P + G) * (d + 8) * 4 bytes of flush staging must fit in
  * one CTA's shared memory. Uses the current CUDA device.
@@ -350,7 +352,9 @@ int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t 
  * Keys and values, the chunk's too, are finite; values are at most 65,440 in
  * magnitude (dequantized, a larger one may round to infinity). One that is
  * not finite spoils rows that do not see it as well. A query that is not finite gets NaN in its own row and changes no
- * other. A call gives the same bits every time.
+ * other. A call gives the same bits every time; the kernel and the order of
+ * its sums go by the largest lens of up to 64 sequences and by the GPU's SMs,
+ * so a sequence's bits may differ beside other sequences.
  * Partial results go to the cache's split-K scratch, or where they are
  * larger to stream-ordered scratch from the library's pool (see ott_prefill;
  * OTT_ERR_OOM if none can be had, before anything is queued).
@@ -364,7 +368,8 @@ int ott_chunk_attn(ott_cache *c, const void *q, const void *k, const void *v, vo
  * they make due included, in every variant). k, v: DEVICE fp16
  * [B][Hkv][n][d]. An empty sequence may be filled this way.
  * OTT_ERR_CAPACITY if a sequence would outgrow max_tokens or a paged pool
- * lacks the blocks, before anything is queued.
+ * lacks the blocks, before anything is queued. Several flushes at once use
+ * stream-ordered scratch (see ott_prefill); without it they go one by one.
  */
 int ott_append_chunk(ott_cache *c, const void *k, const void *v, int n, const int *lens, void *stream);
 
