@@ -77,7 +77,7 @@ enum {
     OTT_ERR_STATE = -2,     /* not allowed now: prefill on a non-empty cache,
                                decode on an empty one, poisoned handle */
     OTT_ERR_CAPACITY = -3,  /* would exceed max_tokens */
-    OTT_ERR_OOM = -4,       /* device allocation failed in ott_create */
+    OTT_ERR_OOM = -4,       /* a device allocation failed (ott_create, ott_chunk_attn) */
     OTT_ERR_CUDA = -5,      /* a CUDA call or kernel failed; handle poisoned */
     OTT_ERR_DEVICE = -6     /* a kernel reported a bounded wait that timed out */
 };
@@ -351,10 +351,11 @@ int ott_decode_attn_topk(ott_cache *c, const void *q, void *out, int K, int32_t 
  * 2^-11 relative, a weight also by 2^-32 of its row's largest).
  * Keys and values, the chunk's too, are finite; values are at most 65,440 in
  * magnitude (dequantized, a larger one may round to infinity). One that is
- * not finite spoils rows that do not see it as well. A query that is not finite gets NaN in its own row and changes no
- * other. A call gives the same bits every time; the kernel and the order of
- * its sums go by the largest lens of up to 64 sequences and by the GPU's SMs,
- * so a sequence's bits may differ beside other sequences.
+ * not finite spoils rows that do not see it as well. A query that is not
+ * finite gets NaN in its own row and changes no other.
+ * A call gives the same bits every time; the kernel and the order of its sums
+ * go by the largest lens of up to 64 sequences and by the GPU's SMs, so a
+ * sequence's bits may differ beside other sequences.
  * Partial results go to the cache's split-K scratch, or where they are
  * larger to stream-ordered scratch from the library's pool (see ott_prefill;
  * OTT_ERR_OOM if none can be had, before anything is queued).
