@@ -14,8 +14,9 @@ namespace ott {
 // sign shrinks by 5.9e-9 of itself per token (tcgen05; measured, 8,192 rows of
 // 8 heads over 2^20 tokens: 3.8e-3 of the output when runs were as long as the
 // plan made them), and by 2.4 to 4.8e-9 with mma.sync. Sums end here and are
-// merged in fp32: 1.5e-4 at any length, a third of the output's largest rounding. 2,048 tokens over 131K:
-// 3.35 ms, and 3.29 with sums of 57,344 tokens (3.4e-4).
+// merged in fp32: 1.5e-4 at any length, a third of the output's largest
+// rounding. 2,048 tokens over 131K: 3.35 ms, and 3.29 with sums of 57,344
+// tokens (3.4e-4).
 constexpr int SUM_TOKENS = 25088;
 
 // One sequence of a launch.
