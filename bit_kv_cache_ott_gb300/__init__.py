@@ -17,7 +17,7 @@ import torch
 
 from . import synth  # noqa: F401  (seeded workloads)
 
-__all__ = ["OTTCache", "OTTError", "load", "status_str", "lib_path", "hbm_copy", "rope"]
+__all__ = ["OTTCache", "ByteCache", "OTTError", "load", "status_str", "lib_path", "hbm_copy", "rope"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "_build", "libott.so")
@@ -47,7 +47,10 @@ SYMBOLS = ("ott_create", "ott_create_ragged", "ott_create_paged", "ott_release_s
            "ott_free_blocks", "ott_create_cold", "ott_create_pct", "ott_export_cold", "ott_destroy", "ott_prefill", "ott_prefill_lens", "ott_append", "ott_step_host",
            "ott_decode_attn", "ott_decode_attn_static", "ott_decode_attn_topk",
            "ott_chunk_attn", "ott_append_chunk", "ott_decode_attn_window", "ott_rope", "ott_get_counts", "ott_get_seq_counts", "ott_block_count",
-           "ott_export_state", "ott_check_device", "ott_device_bytes", "ott_status_str", "ott_hbm_copy", "ott_ex2_probe")
+           "ott_export_state", "ott_check_device", "ott_device_bytes", "ott_status_str", "ott_hbm_copy", "ott_ex2_probe",
+           "ott_byte_create", "ott_byte_destroy", "ott_byte_append", "ott_byte_append_seq", "ott_byte_read", "ott_byte_decode",
+           "ott_byte_attn", "ott_byte_release", "ott_byte_reset", "ott_byte_counts", "ott_byte_free_blocks", "ott_byte_check",
+           "ott_byte_bytes")
 
 
 def lib_path() -> str:
@@ -99,6 +102,21 @@ def load(build_if_missing: bool = False):
     L.ott_status_str.restype = C.c_char_p
     L.ott_hbm_copy.argtypes = [P, P, i64, P]
     L.ott_ex2_probe.argtypes = [P, P, i32, P]
+    L.ott_byte_create.argtypes = [i32] * 7 + [i64, C.POINTER(P)]
+    L.ott_byte_destroy.argtypes = [P]
+    L.ott_byte_append.argtypes = [P, P, P, i32, C.POINTER(i32), P]
+    L.ott_byte_append_seq.argtypes = [P, i32, P, P, i32, P]
+    L.ott_byte_read.argtypes = [P, P, P, i32, i32, P]
+    L.ott_byte_decode.argtypes = [P, P, P, i32, P, P]
+    L.ott_byte_attn.argtypes = [P, P, P, P, P, i32, C.POINTER(i32), i32, P, P]
+    L.ott_byte_release.argtypes = [P, i32, P]
+    L.ott_byte_reset.argtypes = [P, P]
+    L.ott_byte_counts.argtypes = [P, i32, C.POINTER(i64), C.POINTER(i32)]
+    L.ott_byte_free_blocks.argtypes = [P]
+    L.ott_byte_free_blocks.restype = i64
+    L.ott_byte_check.argtypes = [P]
+    L.ott_byte_bytes.argtypes = [P]
+    L.ott_byte_bytes.restype = i64
     _lib = L
     return L
 
@@ -479,3 +497,184 @@ class OTTCache:
             e.update(bcount=bc[:, :nf], ncold=nc, cidx=ci[:, :Cc], ck=ck[:, :Cc], cv=cv[:, :Cc])
         e.update(T=T, nf=nf, tail=nt, npool=npool)
         return e
+
+
+class ByteCache:
+    """One cache (one attention layer) held in 8 bits, for layers that 2 bits hurt (``ott_byte_*``): keys and values of
+    complete blocks of G tokens (32, 64 or 128) as codes of one byte with one scale for the keys and one for the values
+    of each block and kv head, the tokens of the open block in fp16. ``fmt``: "int8" or "e4m3". Every sequence keeps
+    its own length. ``pool_blocks``: the complete blocks of all (sequence, kv head) units come from one pool.
+
+    Calls go to the given stream, or to the current one of the cache's device, on which all tensors lie; they are made
+    one after another on one stream, or ordered by events."""
+
+    FORMATS = {"int8": 0, "e4m3": 1}
+
+    def __init__(self, B, Hq, Hkv, d, G=64, fmt="int8", max_tokens=8192, pool_blocks=None):
+        L = load()
+        if fmt not in self.FORMATS:
+            raise ValueError(f"fmt: expected one of {tuple(self.FORMATS)}, got {fmt!r}")
+        if pool_blocks is not None and int(pool_blocks) < 1:
+            raise ValueError("pool_blocks: at least one block")
+        self.B, self.Hq, self.Hkv, self.d, self.G, self.fmt, self.max_tokens = B, Hq, Hkv, d, G, fmt, max_tokens
+        self._h = C.c_void_p()
+        self._dev = torch.cuda.current_device()
+        sizes = [_int32(x, n) for x, n in ((B, "B"), (Hq, "Hq"), (Hkv, "Hkv"), (d, "d"), (G, "G"))]
+        _check(L.ott_byte_create(*sizes, self.FORMATS[fmt], _int32(max_tokens, "max_tokens"), int(pool_blocks or 0),
+                                 C.byref(self._h)), "ott_byte_create")
+
+    def close(self):
+        if getattr(self, "_h", None) and self._h.value:
+            load().ott_byte_destroy(self._h)
+            self._h = C.c_void_p()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+    @property
+    def handle(self) -> int:
+        return self._h.value
+
+    def _call(self, fn, what, *args, stream):
+        _on_device(self._dev, fn, what, self._h, *args, _stream_of(stream, self._dev))
+
+    def _ptr(self, t, shape, name) -> int:
+        p = _dev_ptr(t, shape, name)
+        if t.get_device() != self._dev:
+            raise ValueError(f"{name}: on {t.device}, the cache is on cuda:{self._dev}")
+        return p
+
+    def _lens(self, lens):
+        if lens is None:
+            return None
+        if len(lens) != self.B:
+            raise ValueError("lens must hold one length per sequence")
+        return (C.c_int * self.B)(*[_int32(x, "lens") for x in lens])
+
+    def _append(self, k, v, n, shape, lens, stream):
+        self._call(load().ott_byte_append, "ott_byte_append", self._ptr(k, shape, "k"), self._ptr(v, shape, "v"), n,
+                   self._lens(lens), stream=stream)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, stream=None):
+        """One token to every sequence: k, v fp16 [B][Hkv][d]."""
+        self._append(k, v, 1, (self.B, self.Hkv, self.d), None, stream)
+
+    def append_chunk(self, k: torch.Tensor, v: torch.Tensor, lens=None, stream=None):
+        """n tokens per sequence, k, v fp16 [B][Hkv][n][d] (ott_byte_append); ``lens``: sequence b takes its first lens[b],
+        0 included. What the cache holds does not depend on how the tokens are cut into calls."""
+        n = k.shape[2] if isinstance(k, torch.Tensor) and k.dim() == 4 else -1
+        self._append(k, v, n, (self.B, self.Hkv, n, self.d), lens, stream)
+
+    def prefill(self, K: torch.Tensor, V: torch.Tensor, stream=None):
+        """A prompt of L tokens for every sequence of an empty cache: K, V fp16 [B][Hkv][L][d]."""
+        self.prefill_lens(K, V, None, stream)
+
+    def prefill_lens(self, K: torch.Tensor, V: torch.Tensor, lens, stream=None):
+        """The same with lens[b] tokens for sequence b."""
+        if any(self.seq_counts(b)[0] for b in range(self.B)):
+            raise OTTError(OTT_ERR_STATE, "prefill of a cache that holds tokens")
+        self.append_chunk(K, V, lens, stream)
+
+    def prefill_seq(self, b: int, K: torch.Tensor, V: torch.Tensor, stream=None):
+        """A prompt for the empty sequence b: K, V fp16 [Hkv][L][d]."""
+        if self.seq_counts(b)[0]:
+            raise OTTError(OTT_ERR_STATE, "prefill of a sequence that holds tokens")
+        n = K.shape[1] if isinstance(K, torch.Tensor) and K.dim() == 3 else -1
+        shp = (self.Hkv, n, self.d)
+        self._call(load().ott_byte_append_seq, "ott_byte_append_seq", _int32(b, "b"), self._ptr(K, shp, "K"),
+                   self._ptr(V, shp, "V"), n, stream=stream)
+
+    def read(self, start: int, n: int, out_k: torch.Tensor | None = None, out_v: torch.Tensor | None = None, stream=None):
+        """Tokens start .. start + n - 1 of every sequence as the cache holds them (ott_byte_read): keys and values, fp16
+        [B][Hkv][n][d]. Rows of tokens that a sequence does not hold stay as they are (zero in a new tensor)."""
+        n = _int32(n, "n")
+        shp = (self.B, self.Hkv, n, self.d)
+        if out_k is None:
+            out_k = torch.zeros(shp, dtype=torch.float16, device=f"cuda:{self._dev}")
+        if out_v is None:
+            out_v = torch.zeros(shp, dtype=torch.float16, device=f"cuda:{self._dev}")
+        self._call(load().ott_byte_read, "ott_byte_read", self._ptr(out_k, shp, "out_k"), self._ptr(out_v, shp, "out_v"),
+                   _int32(start, "start"), n, stream=stream)
+        return out_k, out_v
+
+    def decode_attn(self, q: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """One query per sequence over all its tokens: q fp16 [B][Hq][d] -> [B][Hq][d]."""
+        return self.decode_attn_topk(q, 0, out, None, stream)
+
+    def decode_attn_topk(self, q: torch.Tensor, K: int, out: torch.Tensor | None = None, sel: torch.Tensor | None = None,
+                         stream=None) -> torch.Tensor:
+        """decode_attn over the K complete blocks with the largest bound of each (sequence, kv head) and the open block
+        (ott_byte_decode; K = 0: all). ``sel``: int32 [B][1][Hkv][min(K, most blocks of a sequence)] (or without the
+        1), receives the blocks."""
+        shp = (self.B, self.Hq, self.d)
+        qp = self._ptr(q, shp, "q")
+        if out is None:
+            out = torch.empty_like(q)
+        self._call(load().ott_byte_decode, "ott_byte_decode", qp, self._ptr(out, shp, "out"), _int32(K, "K"),
+                   self._sel(sel, 1, K), stream=stream)
+        return out
+
+    def chunk_attn(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens=None, out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+        """n new tokens per sequence over the cache and, causally, one another (ott_byte_attn): q fp16 [B][Hq][n][d], k, v
+        fp16 [B][Hkv][n][d], not yet in the cache; it is not changed. ``lens``: the new tokens of each sequence; rows
+        behind them are neither read nor written."""
+        return self.chunk_attn_topk(q, k, v, 0, lens, out, None, stream)
+
+    def chunk_attn_topk(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, K: int, lens=None,
+                        out: torch.Tensor | None = None, sel: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+        """chunk_attn in which every token attends, for each kv head, the K complete blocks with its largest bounds, the
+        open block, and new tokens up to itself. ``sel``: int32 [B][n][Hkv][min(K, most blocks of a sequence)], receives
+        the blocks."""
+        n = q.shape[2] if isinstance(q, torch.Tensor) and q.dim() == 4 else -1
+        shp, kshp = (self.B, self.Hq, n, self.d), (self.B, self.Hkv, n, self.d)
+        ptr = [self._ptr(q, shp, "q"), self._ptr(k, kshp, "k"), self._ptr(v, kshp, "v")]
+        if out is None:
+            out = torch.empty_like(q)
+        self._call(load().ott_byte_attn, "ott_byte_attn", *ptr, self._ptr(out, shp, "out"), n, self._lens(lens),
+                   _int32(K, "K"), self._sel(sel, n, K), stream=stream)
+        return out
+
+    def _sel(self, sel, n, K):
+        if sel is None:
+            return None
+        slots = min(int(K), max(self.seq_counts(b)[1] for b in range(self.B)))
+        shapes = [(self.B, n, self.Hkv, slots)] + ([(self.B, self.Hkv, slots)] if n == 1 else [])
+        if not isinstance(sel, torch.Tensor) or not sel.is_cuda or sel.dtype != torch.int32:
+            raise TypeError("sel: expected a CUDA int32 tensor")
+        if tuple(sel.shape) not in shapes or not sel.is_contiguous() or sel.get_device() != self._dev:
+            raise ValueError(f"sel: expected contiguous shape {shapes[0]} on cuda:{self._dev}, got {tuple(sel.shape)}")
+        return sel.data_ptr()
+
+    def release_seq(self, b: int, stream=None):
+        """Sequence b drops its tokens (and its pool blocks)."""
+        self._call(load().ott_byte_release, "ott_byte_release", _int32(b, "b"), stream=stream)
+
+    def reset(self, stream=None):
+        """Every sequence drops its tokens."""
+        self._call(load().ott_byte_reset, "ott_byte_reset", stream=stream)
+
+    def seq_counts(self, b: int):
+        """(tokens of sequence b, its complete blocks per kv head)."""
+        T, nb = C.c_longlong(), C.c_int()
+        _check(load().ott_byte_counts(self._h, _int32(b, "b"), C.byref(T), C.byref(nb)), "ott_byte_counts")
+        return T.value, nb.value
+
+    def free_blocks(self) -> int:
+        """Free blocks of the pool (-1 without one)."""
+        return int(load().ott_byte_free_blocks(self._h))
+
+    def device_bytes(self) -> int:
+        return int(load().ott_byte_bytes(self._h))
+
+    def check_device(self):
+        _check(load().ott_byte_check(self._h), "ott_byte_check")

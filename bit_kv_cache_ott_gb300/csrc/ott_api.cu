@@ -106,9 +106,11 @@ cudaMemPool_t scratch_pool(int dev) {
     return pools[dev];
 }
 
+}  // namespace
+
 // Stream-ordered device memory from the library's pool, or else the device's
 // default pool; null if neither has it.
-void *stream_alloc(int dev, size_t bytes, cudaStream_t s) {
+void *ott::stream_alloc(int dev, size_t bytes, cudaStream_t s) {
     void *p = nullptr;
     const cudaMemPool_t pool = scratch_pool(dev);
     if (pool && cudaMallocFromPoolAsync(&p, bytes, pool, s) == cudaSuccess) return p;
@@ -117,6 +119,8 @@ void *stream_alloc(int dev, size_t bytes, cudaStream_t s) {
     cudaGetLastError();
     return nullptr;
 }
+
+namespace {
 
 bool try_prefill_parallel(const ott_cache *c, const __half *K, const __half *V, long long unit_stride, int src_u0,
                           int u0, int nu, int nf, int shared_units, cudaStream_t s, cudaError_t &err) {
@@ -134,11 +138,14 @@ bool try_prefill_parallel(const ott_cache *c, const __half *K, const __half *V, 
 
 namespace ott {
 
-Scratch::Scratch(const ott_cache *c, size_t floats, cudaStream_t s) : ptr(c->part), owned(false), stream(s) {
-    if (floats <= c->part_floats) return;
-    ptr = stream_alloc(c->device, floats * sizeof(float), s);
+Scratch::Scratch(float *own, size_t own_floats, int dev, size_t floats, cudaStream_t s)
+    : ptr(own), owned(false), stream(s) {
+    if (floats <= own_floats) return;
+    ptr = stream_alloc(dev, floats * sizeof(float), s);
     owned = ptr != nullptr;
 }
+Scratch::Scratch(const ott_cache *c, size_t floats, cudaStream_t s)
+    : Scratch(c->part, c->part_floats, c->device, floats, s) {}
 
 cudaError_t Scratch::release() {
     if (!owned) return cudaSuccess;

@@ -1,0 +1,863 @@
+// ott_byte_rows.cu -- attention of few query rows per kv head over the cache
+// held in 8 bits, over all its blocks or over those that a bound selects; the
+// plan of every such call (more than 16 rows go to ott_byte_tiles.cu).
+//
+// Mathematics. A code is an exact fp16 number, so the tensor cores get the
+// codes themselves: scores are (q . code) * ks, one multiplication in fp32. The
+// values' scale goes into the weight: with lv = log2(vs),
+//     z = (q . code) ks log2(e) / sqrt(d) + lv,   w = 2^(z - m),
+//     out = sum w code / sum (w / vs),
+// where m runs with the largest z (not the largest score). So a block costs
+// no operation per element for its scales, and a weight is rounded once, to
+// fp16, where its product with the codes counts most; what falls below fp16's
+// range is small beside the row's largest w * code, whatever its scale.
+//
+// Layout of the work, as ott_chunk.cu's: a unit is a (sequence, kv head, slice
+// of 8 or 16 query rows), row v = token * g + head; with selected blocks, a
+// slice of one token's heads. Work items are what a copy brings: 16 fp16
+// tokens, or 32 tokens of a block (64 d bytes, contiguous, as the lanes'
+// fragments: 16-byte loads from shared memory, no transposition; and the
+// block's record). Every warp gets an equal contiguous run of the items of all
+// units, with a ring of stages of its own that its copies fill ahead, and
+// leaves one partial per unit that it touches; k_byte_combine merges them.
+#include <algorithm>
+#include <climits>
+#include <cmath>
+
+#include "ott_byte.cuh"
+#include "ott_select.cuh"
+
+namespace ott {
+namespace {
+
+constexpr int ROWS_MAX = 16;   // rows per kv head up to which this file's kernel serves a call
+constexpr int QT = 32, FT = 16;   // tokens of a work item: of a block, fp16
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t (&r)[4], const void *p) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(ch_smem(p)));
+}
+__device__ __forceinline__ void expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(ch_smem(bar)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_copy(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(ch_smem(dst)),
+        "l"(src), "r"(bytes), "r"(ch_smem(bar))
+        : "memory");
+}
+// Bounded wait: gives up after a fixed number of polls instead of hanging.
+__device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
+    for (int it = 0; it < (1 << 22); ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(ch_smem(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    return false;
+}
+
+// NC groups of 8 query rows (the columns of an MMA).
+template <int D, int NC>
+struct RowsCfg {
+    static constexpr int NKS = D / 16, PP = D / 64;
+    static constexpr int WARPS = 8, NST = 3;
+    static constexpr int RS = D + 8;                       // padded fp16 row (halves)
+    static constexpr int ITEM = QT * 2 * D;                // bytes of a block's item
+    static constexpr int STAGE = 2 * FT * RS * 2;          // fp16 rows; a block's item and its record fit, too
+    static constexpr int WARP_SMEM = NST * STAGE + 128;    // stages, barriers, what each stage holds
+    static_assert(ITEM + 16 <= STAGE && STAGE % 128 == 0 && NST * 8 <= 64, "stages");
+    static_assert(WARP_SMEM * WARPS <= 227 * 1024, "shared memory");
+};
+
+// A work item: its unit (entry, kv head, slice of rows), its number in the
+// unit, and for one of a block the block's place and the part.
+struct Cursor {
+    long long x;
+    int e, hkv, sl, off, jp, k;
+    int Sf, Iu;   // of the entry
+    __device__ __forceinline__ void unit(const ByteTable &st) {
+        off = jp = k = 0;
+        Sf = st.e[e].Sf;
+        Iu = st.e[e].Iu;
+    }
+    // true: the next item is another unit's
+    __device__ __forceinline__ bool next(const ByteArgs &a, const ByteTable &st) {
+        ++x;
+        if (off++ >= Sf && ++k == a.IPB) {
+            k = 0;
+            ++jp;
+        }
+        if (off < Iu) return false;
+        if (++sl == st.e[e].S) {
+            sl = 0;
+            if (++hkv == a.Hkv) {
+                hkv = 0;
+                do ++e;
+                while (e < a.nseq && st.e[e].S == 0);
+            }
+        }
+        if (e < a.nseq) unit(st);
+        return true;
+    }
+};
+
+__device__ __forceinline__ int entry_of(const ByteTable &st, int nseq, long long x) {   // the last one whose base is <= x
+    int lo = 0, hi = nseq;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (st.e[mid].base <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+// Rows of slice sl of an entry: first row, number of rows (a row is token * g + head).
+__device__ __forceinline__ void slice_rows(const ByteArgs &a, const ByteSeq &s, int sl, int &v0, int &cnt) {
+    if (a.sel) {
+        const int h0 = sl % a.SG * a.RB;
+        v0 = sl / a.SG * a.g + h0;
+        cnt = min(a.RB, a.g - h0);
+    } else {
+        v0 = sl * a.RB;
+        cnt = min(a.RB, s.nq * a.g - v0);
+    }
+}
+
+template <int D, int NC, int FMT>
+__global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
+    k_byte_rows(const __grid_constant__ ByteArgs a, const __grid_constant__ ByteTable st) {
+    using C = RowsCfg<D, NC>;
+    constexpr int NKS = C::NKS, PP = C::PP, NST = C::NST, RS = C::RS;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, i = lane & 3;
+    const int rot = D == 128 ? 8 * (i >> 1) : 0;
+    uint8_t *stg = smem + (size_t)warp * C::WARP_SMEM;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(stg + NST * C::STAGE);
+    int *meta = reinterpret_cast<int *>(stg + NST * C::STAGE + 64);   // valid tokens of each stage
+    if (lane < NST) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(ch_smem(&bars[lane])) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    __syncwarp();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int gw = warp * gridDim.x + blockIdx.x;   // warp indices dealt across the CTAs first
+    if (gw >= a.NWp) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const long long x0 = ch_range_start(a.W, a.NWp, gw), x1 = ch_range_start(a.W, a.NWp, gw + 1);
+
+    Cursor ic;
+    ic.x = x0;
+    ic.e = entry_of(st, a.nseq, x0);
+    {
+        const ByteSeq &s = st.e[ic.e];
+        const unsigned rel = (unsigned)(x0 - s.base);   // a sequence's items fit 32 bits (checked on the host)
+        const int h = (int)(rel / (unsigned)s.Iu), off = (int)(rel % (unsigned)s.Iu);
+        ic.hkv = h / s.S;
+        ic.sl = h % s.S;
+        ic.unit(st);
+        ic.off = off;
+        if (off > s.Sf) {
+            ic.jp = (off - s.Sf) / a.IPB;
+            ic.k = (off - s.Sf) % a.IPB;
+        }
+    }
+    Cursor cc = ic;
+
+    // Slots of the next 32 blocks of the issuing cursor's unit, a lane each.
+    int slots = -1, slots_from = INT_MIN;
+    auto issue = [&](const Cursor &c, int sg) {
+        const ByteSeq &s = st.e[c.e];
+        const int b = a.B0 + c.e, u = b * a.Hkv + c.hkv;
+        uint8_t *dst = stg + sg * C::STAGE;
+        int m;
+        if (c.off < c.Sf) {
+            const bool fresh = c.off >= s.Ft;
+            const int f0 = (fresh ? c.off - s.Ft : c.off) * FT;
+            m = min(FT, (fresh ? s.nq : s.T % a.G) - f0);
+            const __half *src = fresh ? (lane < FT ? a.k : a.v) + ((size_t)u * a.n + f0) * D
+                                      : (lane < FT ? a.tk : a.tv) + ((size_t)u * a.G + f0) * D;
+            if (lane == 0) expect_tx(&bars[sg], 2 * FT * D * 2);
+            __syncwarp();
+            // rows past the end repeat the first (finite values under a zero weight)
+            const int x = lane & (FT - 1);
+            bulk_copy(dst + (size_t)lane * RS * 2, src + (size_t)(x < m ? x : 0) * D, D * 2, &bars[sg]);
+        } else {
+            if (c.jp < slots_from || c.jp >= slots_from + 32) {
+                slots_from = c.jp;
+                const int jp = c.jp + lane;
+                slots = -1;
+                if (jp < s.nb) {
+                    int j = jp;
+                    if (a.sel) j = __ldg(a.sel + (((size_t)b * a.n + c.sl / a.SG) * a.Hkv + c.hkv) * a.Kc + jp);
+                    const size_t own = (size_t)u * a.NB + j;
+                    if (j >= 0) slots = a.bt ? __ldg(a.bt + own) : (int)own;
+                }
+            }
+            const int slot = __shfl_sync(0xffffffffu, slots, c.jp - slots_from);
+            m = slot < 0 ? 0 : QT;
+            if (slot >= 0 && lane == 0) {
+                expect_tx(&bars[sg], C::ITEM + 16);
+                bulk_copy(dst, a.blk + (size_t)slot * a.blk_bytes + (size_t)c.k * C::ITEM, C::ITEM, &bars[sg]);
+                bulk_copy(dst + C::ITEM, a.rec + slot, 16, &bars[sg]);
+            }
+        }
+        if (lane == 0) meta[sg] = m;
+    };
+    auto advance = [&](Cursor &c) {
+        if (c.next(a, st)) slots_from = INT_MIN;
+    };
+
+    uint32_t Bq[NC][NKS][2];          // queries: B operand, column r of each group
+    float acc[NC][NKS][4], m_run[NC][2], l_run[NC][2];
+    int tok[NC][2];                   // the columns' tokens (of the chunk)
+    int uo = 0, cnt_rows = 0;
+
+    auto begin_unit = [&](const Cursor &c) {
+        const ByteSeq &s = st.e[c.e];
+        const int b = a.B0 + c.e;
+        int v0;
+        slice_rows(a, s, c.sl, v0, cnt_rows);
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+            const int v = v0 + min(8 * nc + r, cnt_rows - 1);   // rows past the last repeat it, unused
+            const __half *qp = a.q + (((size_t)b * a.Hq + c.hkv * a.g + v % a.g) * a.n + v / a.g) * D + (D / 4) * i;
+#pragma unroll
+            for (int ks = 0; ks < NKS; ++ks) {
+                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(qp + 16 * (ks >> 2) + ((4 * (ks & 3)) ^ rot)));
+                Bq[nc][ks][0] = w.x;
+                Bq[nc][ks][1] = w.y;
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                tok[nc][x] = (v0 + min(8 * nc + 2 * i + x, cnt_rows - 1)) / a.g;
+                m_run[nc][x] = -CUDART_INF_F;
+                l_run[nc][x] = 0.0f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < NKS; ++mt) acc[nc][mt][0] = acc[nc][mt][1] = acc[nc][mt][2] = acc[nc][mt][3] = 0.0f;
+        }
+    };
+    auto end_unit = [&]() {
+        if (uo >= a.MAXU) {   // never with the host's bound; recorded instead of writing out of bounds
+            if (lane == 0) atomicExch(&a.ctl[1], 1);
+            return;
+        }
+        float *pb = a.part + ((size_t)gw * a.MAXU + uo) * a.RV * (D + 2);
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float l = l_run[nc][x];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                const int col = 8 * nc + 2 * i + x;
+                if (col < cnt_rows) {
+                    float *p = pb + (size_t)col * (D + 2);
+                    if (r == 0) *reinterpret_cast<float2 *>(p) = make_float2(m_run[nc][x], l);
+#pragma unroll
+                    for (int mt = 0; mt < NKS; ++mt) {
+                        p[2 + 16 * mt + r] = acc[nc][mt][x];
+                        p[2 + 16 * mt + r + 8] = acc[nc][mt][2 + x];
+                    }
+                }
+            }
+        ++uo;
+    };
+    // z values whose largest is mx in this lane: the reference moves up, and
+    // sums and outputs are rescaled, only when one has grown by 2^GROW.
+    auto rescale = [&](float (&mx)[NC][2]) {
+        bool grew = false;
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) grew |= mx[nc][x] > m_run[nc][x] + GROW;
+        if (!__any_sync(0xffffffffu, grew)) return;
+#pragma unroll
+        for (int nc = 0; nc < NC; ++nc) {
+            float al[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float v = fmaxf(mx[nc][x], m_run[nc][x]);
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                al[x] = v > m_run[nc][x] ? ch_ex2(m_run[nc][x] - v) : 1.0f;
+                l_run[nc][x] *= al[x];
+                m_run[nc][x] = v;
+            }
+#pragma unroll
+            for (int mt = 0; mt < NKS; ++mt) {
+                acc[nc][mt][0] *= al[0];
+                acc[nc][mt][1] *= al[1];
+                acc[nc][mt][2] *= al[0];
+                acc[nc][mt][3] *= al[1];
+            }
+        }
+    };
+    // Weights of 16 tokens from their z (d[nc]: tokens r, r + 8, columns 2i,
+    // 2i + 1): sums, and the B operand of the values' product.
+    auto weights = [&](const float (&d)[4], int nc, float iv, uint32_t &b0, uint32_t &b1) {
+        float p[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            const float m = m_run[nc][y & 1];
+            p[y] = ch_ex2(d[y] - (m == -CUDART_INF_F ? 0.0f : m - LIFT));
+        }
+        l_run[nc][0] = fmaf(p[0] + p[2], iv, l_run[nc][0]);
+        l_run[nc][1] = fmaf(p[1] + p[3], iv, l_run[nc][1]);
+        b0 = transpose8x8(ch_h2(__floats2half2_rn(p[0], p[1])));
+        b1 = transpose8x8(ch_h2(__floats2half2_rn(p[2], p[3])));
+    };
+
+    // prime the ring
+    int st_issue = 0;
+    for (int k = 0; k < NST && ic.x < x1; ++k) {
+        issue(ic, st_issue);
+        advance(ic);
+        st_issue = st_issue + 1 == NST ? 0 : st_issue + 1;
+    }
+    begin_unit(cc);
+    __syncwarp();
+
+    uint32_t phase = 0;
+    int sg = 0;
+    while (cc.x < x1) {
+        const ByteSeq &s = st.e[cc.e];
+        const int valid = meta[sg];
+        uint8_t *stage = stg + sg * C::STAGE;
+        if (valid > 0) {
+            if (!mbar_wait(&bars[sg], (phase >> sg) & 1u)) {
+                if (lane == 0) atomicExch(&a.ctl[1], 1);
+                // let the other copies in flight land before giving up the buffers
+                for (int x = 0; x < NST; ++x)
+                    if (x != sg) mbar_wait(&bars[x], (phase >> x) & 1u);
+                return;
+            }
+            phase ^= 1u << sg;
+            if (cc.off < cc.Sf) {
+                // 16 fp16 tokens: of the open block, or new ones (causal)
+                const bool fresh = cc.off >= s.Ft;
+                const int f0 = (fresh ? cc.off - s.Ft : cc.off) * FT;
+                const __half *kr = reinterpret_cast<const __half *>(stage), *vr = kr + FT * RS;
+                float d[NC][4], mx[NC][2];
+#pragma unroll
+                for (int nc = 0; nc < NC; ++nc) d[nc][0] = d[nc][1] = d[nc][2] = d[nc][3] = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < NKS; ks += 2) {
+                    const int ch = (D / 4) * i + 16 * (ks >> 2) + ((4 * (ks & 3)) ^ rot);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(kr + r * RS + ch);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(kr + (r + 8) * RS + ch);
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc) {
+                        mma16816(d[nc], x.x, y.x, x.y, y.y, Bq[nc][ks][0], Bq[nc][ks][1]);
+                        mma16816(d[nc], x.z, y.z, x.w, y.w, Bq[nc][ks + 1][0], Bq[nc][ks + 1][1]);
+                    }
+                }
+#pragma unroll
+                for (int nc = 0; nc < NC; ++nc) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int t = r + 8 * (y >> 1);
+                        const bool see = t < valid && (!fresh || f0 + t <= tok[nc][y & 1]);
+                        d[nc][y] = see ? d[nc][y] * a.sl2 : -CUDART_INF_F;
+                    }
+                    mx[nc][0] = fmaxf(d[nc][0], d[nc][2]);
+                    mx[nc][1] = fmaxf(d[nc][1], d[nc][3]);
+                }
+                rescale(mx);
+                uint32_t bp[NC][2];
+#pragma unroll
+                for (int nc = 0; nc < NC; ++nc) weights(d[nc], nc, 1.0f, bp[nc][0], bp[nc][1]);
+#pragma unroll
+                for (int mt = 0; mt < NKS; ++mt) {
+                    uint32_t f[4];   // (channels, tokens): (0..7, 0..7), (8..15, 0..7), (0..7, 8..15), (8..15, 8..15)
+                    ldsm_x4_t(f, vr + ((lane & 7) + 8 * (lane >> 4)) * RS + 16 * mt + 8 * (lane >> 3 & 1));
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc) mma16816(acc[nc][mt], f[0], f[1], f[2], f[3], bp[nc][0], bp[nc][1]);
+                }
+            } else {
+                const float4 rec = *reinterpret_cast<const float4 *>(stage + C::ITEM);   // ks, vs, lv, iv
+                const float sc = rec.x * a.sl2;
+                float d[2][NC][4], mx[NC][2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const uint4 *kp = reinterpret_cast<const uint4 *>(stage + t * (C::ITEM / 2)) + lane;
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc) d[t][nc][0] = d[t][nc][1] = d[t][nc][2] = d[t][nc][3] = 0.0f;
+#pragma unroll
+                    for (int pp = 0; pp < PP; ++pp) {
+                        const uint4 x = kp[pp * 32], y = kp[(pp + PP) * 32];
+                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            uint32_t a0, a1, a2, a3;
+                            byte_unpack<FMT>(xw[w], a0, a2);
+                            byte_unpack<FMT>(yw[w], a1, a3);
+#pragma unroll
+                            for (int nc = 0; nc < NC; ++nc)
+                                mma16816(d[t][nc], a0, a1, a2, a3, Bq[nc][4 * pp + w][0], Bq[nc][4 * pp + w][1]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int nc = 0; nc < NC; ++nc) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) d[t][nc][y] = fmaf(d[t][nc][y], sc, rec.z);
+                    mx[nc][0] = fmaxf(fmaxf(d[0][nc][0], d[0][nc][2]), fmaxf(d[1][nc][0], d[1][nc][2]));
+                    mx[nc][1] = fmaxf(fmaxf(d[0][nc][1], d[0][nc][3]), fmaxf(d[1][nc][1], d[1][nc][3]));
+                }
+                rescale(mx);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t bp[NC][2];
+#pragma unroll
+                    for (int nc = 0; nc < NC; ++nc) weights(d[t][nc], nc, rec.w, bp[nc][0], bp[nc][1]);
+                    const uint4 *vp = reinterpret_cast<const uint4 *>(stage + t * (C::ITEM / 2) + C::ITEM / 4) + lane;
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        const uint4 x = vp[c * 32];
+                        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t a0, a1, a2, a3;
+                            byte_unpack<FMT>(xw[2 * h], a0, a2);
+                            byte_unpack<FMT>(xw[2 * h + 1], a1, a3);
+#pragma unroll
+                            for (int nc = 0; nc < NC; ++nc)
+                                mma16816(acc[nc][2 * c + h], a0, a1, a2, a3, bp[nc][0], bp[nc][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+        // the stage's reads (generic proxy) come before the copy that refills it
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        if (ic.x < x1) {
+            issue(ic, sg);
+            advance(ic);
+            __syncwarp();
+        }
+        const bool other = cc.next(a, st);
+        sg = sg + 1 == NST ? 0 : sg + 1;
+        if (other || cc.x >= x1) {
+            end_unit();
+            if (cc.x < x1) begin_unit(cc);
+        }
+    }
+}
+
+// Merge a row's partials: a CTA of cw warps per (sequence, query head,
+// token), the warps' shares merged through shared memory.
+constexpr int CMB_MAXW = 16;
+template <int D>
+__global__ void __launch_bounds__(CMB_MAXW * 32)
+    k_byte_combine(const __grid_constant__ ByteArgs a, const __grid_constant__ ByteTable st) {
+    constexpr int CPL = D / 32, GRP = 8;
+    __shared__ float red[CMB_MAXW][D + 2];
+    const int cw = blockDim.x >> 5, wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const ByteSeq &s = st.e[blockIdx.y];
+    const int hq = blockIdx.x / a.n, tk = blockIdx.x % a.n;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (tk >= s.nq || s.S == 0) return;
+    const int hd = hq % a.g, v = a.sel ? hd : tk * a.g + hd;
+    const int sl = a.sel ? tk * a.SG + hd / a.RB : v / a.RB, h = hq / a.g * s.S + sl, col = v % a.RB;
+    const long long ub = s.base + (long long)h * s.Iu, ue = ub + s.Iu;
+    const int wa = ch_warp_of(a.W, a.NWp, ub), wb = ch_warp_of(a.W, a.NWp, ue - 1);
+    // the unit's place among those of warp wa
+    const long long xa = ch_range_start(a.W, a.NWp, wa);
+    const int ea = entry_of(st, a.nseq, xa);
+    const int uo_a = s.ubase + h - (st.e[ea].ubase + (int)((unsigned)(xa - st.e[ea].base) / (unsigned)st.e[ea].Iu));
+    float M = -CUDART_INF_F, L = 0.0f, acc[CPL];
+#pragma unroll
+    for (int c = 0; c < CPL; ++c) acc[c] = 0.0f;
+    for (int k0 = wa + wi * GRP; k0 <= wb; k0 += cw * GRP) {
+        float ms[GRP], ls[GRP], vs[GRP][CPL];
+#pragma unroll
+        for (int x = 0; x < GRP; ++x) {
+            ms[x] = -CUDART_INF_F;
+            ls[x] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) vs[x][c] = 0.0f;
+            const int w = k0 + x;
+            if (w <= wb) {
+                const float *p = a.part + (((size_t)w * a.MAXU + (w == wa ? uo_a : 0)) * a.RV + col) * (D + 2);
+                ms[x] = p[0];
+                ls[x] = p[1];
+#pragma unroll
+                for (int c = 0; c < CPL; c += 2) {
+                    const float2 t = *reinterpret_cast<const float2 *>(p + 2 + lane * CPL + c);
+                    vs[x][c] = t.x;
+                    vs[x][c + 1] = t.y;
+                }
+            }
+        }
+        float mn = M;
+#pragma unroll
+        for (int x = 0; x < GRP; ++x) mn = fmaxf(mn, ms[x]);
+        // (no maximum yet: nothing seen, or scores that are NaN, and then the sum, too, which stays)
+        const float mr = mn == -CUDART_INF_F ? 0.0f : mn, so = ch_ex2(M - mr);
+        L *= so;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) acc[c] *= so;
+#pragma unroll
+        for (int x = 0; x < GRP; ++x) {
+            const float sn = ch_ex2(ms[x] - mr);   // 0 where nothing was seen
+            L = fmaf(sn, ls[x], L);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) acc[c] = fmaf(sn, vs[x][c], acc[c]);
+        }
+        M = mn;
+    }
+    if (cw > 1) {
+        if (lane == 0) {
+            red[wi][0] = M;
+            red[wi][1] = L;
+        }
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) red[wi][2 + lane * CPL + c] = acc[c];
+        __syncthreads();
+        if (wi != 0) return;
+        M = -CUDART_INF_F;
+        for (int x = 0; x < cw; ++x) M = fmaxf(M, red[x][0]);
+        const float mr = M == -CUDART_INF_F ? 0.0f : M;
+        L = 0.0f;
+#pragma unroll
+        for (int c = 0; c < CPL; ++c) acc[c] = 0.0f;
+        for (int x = 0; x < cw; ++x) {
+            const float sx = ch_ex2(red[x][0] - mr);
+            L = fmaf(sx, red[x][1], L);
+#pragma unroll
+            for (int c = 0; c < CPL; ++c) acc[c] = fmaf(sx, red[x][2 + lane * CPL + c], acc[c]);
+        }
+    }
+    // a row sees a token at least, so that L = 0 means scores of -inf or NaN alone: NaN
+    const float inv = 1.0f / L;
+    __half *o = a.out + (((size_t)(a.B0 + blockIdx.y) * a.Hq + hq) * a.n + tk) * D + lane * CPL;
+    uint32_t w[CPL / 2];
+#pragma unroll
+    for (int c = 0; c < CPL; c += 2) w[c / 2] = ch_h2(__floats2half2_rn(acc[c] * inv, acc[c + 1] * inv));
+    if constexpr (CPL == 4)
+        *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t *>(o) = w[0];
+}
+
+// ---------------------------------------------------------------- selection
+constexpr int BND_BLOCKS = 32, BND_THREADS = 128;
+
+struct BoundArgs {
+    const __half2 *dig;
+    const int32_t *bt;
+    const __half *q;
+    float *bound;       // [nseq][n][Hkv][stride]
+    int32_t *sel;       // [B][n][Hkv][Kc]
+    int n, B0, Hq, Hkv, g, NB, K, Kc, stride;
+};
+struct BoundTable {
+    int nb[CHUNK_SEQS], nq[CHUNK_SEQS];
+};
+
+// Bounds of 32 blocks for the queries of one (sequence, kv head): the blocks'
+// channel ranges in shared memory (rows padded by one word, so that threads
+// that read one channel of their own blocks meet different banks), then four
+// query rows at a time, a thread per (block, row).
+template <int D>
+__global__ void __launch_bounds__(BND_THREADS) k_byte_bounds(const __grid_constant__ BoundArgs a, const __grid_constant__ BoundTable t) {
+    constexpr int RW = D + 1, V4 = D / 4, PER = BND_BLOCKS * V4 / BND_THREADS, RPI = BND_THREADS / BND_BLOCKS;
+    __shared__ uint32_t dg[BND_BLOCKS * RW];
+    __shared__ float qs[RPI][D];
+    __shared__ float part[RPI][BND_BLOCKS];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int e = blockIdx.y / a.Hkv, hkv = blockIdx.y % a.Hkv, j0 = blockIdx.x * BND_BLOCKS, tid = threadIdx.x;
+    const int u = (a.B0 + e) * a.Hkv + hkv, nb = min(BND_BLOCKS, t.nb[e] - j0), nq = t.nq[e];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (nb <= 0 || nq == 0) return;   // the whole CTA
+    uint4 buf[PER];
+#pragma unroll
+    for (int y = 0; y < PER; ++y) {
+        const int z = tid + y * BND_THREADS, row = z / V4;
+        if (row < nb) {
+            const size_t own = (size_t)u * a.NB + j0 + row, slot = a.bt ? (size_t)__ldg(a.bt + own) : own;
+            buf[y] = __ldg(reinterpret_cast<const uint4 *>(a.dig + slot * D) + z % V4);
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < PER; ++y) {
+        const int z = tid + y * BND_THREADS, row = z / V4;
+        if (row < nb) {
+            uint32_t *w = dg + row * RW + 4 * (z % V4);
+            w[0] = buf[y].x;
+            w[1] = buf[y].y;
+            w[2] = buf[y].z;
+            w[3] = buf[y].w;
+        }
+    }
+    const int row = tid % BND_BLOCKS, h = tid / BND_BLOCKS;
+    for (int tk = 0; tk < nq; ++tk) {
+        float best = -CUDART_INF_F;
+        for (int s0 = 0; s0 < a.g; s0 += RPI) {   // a short last round repeats its last head
+            __syncthreads();
+            for (int z = tid; z < RPI * D; z += BND_THREADS)
+                qs[z / D][z % D] = __half2float(
+                    __ldg(a.q + (((size_t)(a.B0 + e) * a.Hq + hkv * a.g + min(s0 + z / D, a.g - 1)) * a.n + tk) * D + z % D));
+            __syncthreads();
+            float sum = 0.0f;
+            if (row < nb) {
+#pragma unroll 8
+                for (int c = 0; c < D; ++c) {
+                    const float2 f = __half22float2(ch_as_h2(dg[row * RW + c]));
+                    const float lo = __fmul_rn(qs[h][c], f.x), up = __fmul_rn(qs[h][c], f.y);
+                    sum = __fadd_rn(sum, up > lo ? up : lo);
+                }
+            }
+            part[h][row] = sum;
+            __syncthreads();
+            if (tid < nb)
+#pragma unroll
+                for (int x = 0; x < RPI; ++x) best = part[x][tid] > best ? part[x][tid] : best;
+        }
+        if (tid < nb) a.bound[(((size_t)e * a.n + tk) * a.Hkv + hkv) * a.stride + j0 + tid] = best;
+    }
+}
+
+__global__ void __launch_bounds__(SORT_THREADS) k_byte_pick(const __grid_constant__ BoundArgs a, const __grid_constant__ BoundTable t) {
+    extern __shared__ uint32_t key[];
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int hkv = blockIdx.x % a.Hkv, tk = blockIdx.x / a.Hkv % a.n, e = blockIdx.x / a.Hkv / a.n;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tk >= t.nq[e]) return;   // the whole CTA
+    const size_t at = ((size_t)e * a.n + tk) * a.Hkv + hkv;
+    pick_blocks(a.bound + at * a.stride, t.nb[e], a.K, a.Kc, a.sel + ((size_t)a.B0 * a.n * a.Hkv + at) * a.Kc, key);
+}
+
+// ---------------------------------------------------------------- plans
+struct Plan {
+    ByteArgs a;
+    ByteTable st;
+    BoundArgs ba;
+    BoundTable bt;
+    bool any, pick;
+    int NC;        // groups of 8 rows; 0: tiles
+    int ctas, wpc;
+    int nC;        // tiles: CTAs
+    bool whole;    // ... each with a tile of its own
+    size_t part_floats, bound_floats;
+    int cw, nbmax;
+};
+
+// Kc: slots of a list of selected blocks. false: sizes beyond the kernels' 32-bit counters.
+bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Plan &p) {
+    ByteArgs &a = p.a;
+    a.blk = c->blk;
+    a.rec = c->rec;
+    a.bt = c->paged ? c->bt : nullptr;
+    a.tk = c->tk;
+    a.tv = c->tv;
+    a.q = call.q;
+    a.k = call.k;
+    a.v = call.v;
+    a.out = call.out;
+    a.ctl = c->ctl;
+    a.sel = nullptr;
+    a.blk_bytes = c->blk_bytes;
+    a.n = call.n;
+    a.B0 = B0;
+    a.nseq = std::min(c->B - B0, CHUNK_SEQS);
+    a.Hq = c->Hq;
+    a.Hkv = c->Hkv;
+    a.g = c->g;
+    a.NB = c->NB;
+    a.G = c->G;
+    a.Kc = Kc;
+    a.IPB = c->G / QT;
+    a.sl2 = (float)(1.4426950408889634 / std::sqrt((double)c->d));
+    int nq_max = 0;
+    p.nbmax = 0;
+    for (int x = 0; x < a.nseq; ++x) {
+        ByteSeq &s = p.st.e[x];
+        const int T = c->T[B0 + x], nq = call.lens ? call.lens[B0 + x] : call.n;
+        s.T = T;
+        s.nq = nq;
+        s.nb = call.topk > 0 ? std::min(call.topk, T / c->G) : T / c->G;
+        s.Ft = (T % c->G + FT - 1) / FT;
+        s.Sf = s.Ft + (call.k ? (nq + FT - 1) / FT : 0);
+        nq_max = std::max(nq_max, nq);
+        if (nq > 0) p.nbmax = std::max(p.nbmax, T / c->G);
+        p.bt.nb[x] = T / c->G;
+        p.bt.nq[x] = nq;
+    }
+    p.any = nq_max > 0;
+    p.pick = call.topk > 0;
+    p.part_floats = p.bound_floats = 0;
+    p.NC = 0;
+    if (!p.any) return true;
+    const bool pick = p.pick;
+    const long long rows = pick ? c->g : (long long)nq_max * c->g;
+    if (!pick && rows > ROWS_MAX) return plan_byte_tiles(c, a, p.st, p.nC, p.whole, p.part_floats);
+    p.NC = rows <= 8 ? 1 : 2;
+    a.RB = 8 * p.NC;
+    a.SG = pick ? (c->g + a.RB - 1) / a.RB : 1;
+    a.RV = (int)std::min<long long>(rows, a.RB);
+    long long base = 0, units = 0, iu_min = LLONG_MAX;
+    for (int x = 0; x < a.nseq; ++x) {
+        ByteSeq &s = p.st.e[x];
+        s.base = base;
+        s.ubase = (int)units;
+        const long long S = s.nq == 0 ? 0 : pick ? (long long)s.nq * a.SG : ((long long)s.nq * c->g + a.RB - 1) / a.RB;
+        const long long Iu = s.Sf + (long long)s.nb * a.IPB;
+        if (S * c->Hkv * Iu > INT_MAX || units + S * c->Hkv > INT_MAX) return false;
+        s.S = (int)S;
+        s.Iu = (int)Iu;
+        base += S * c->Hkv * Iu;
+        units += S * c->Hkv;
+        if (S > 0) iu_min = std::min(iu_min, Iu);
+    }
+    p.st.e[a.nseq] = ByteSeq{};
+    p.st.e[a.nseq].base = a.W = base;
+    p.st.e[a.nseq].ubase = (int)units;
+    // Equal runs, at least two items each; sums end after SUM_TOKENS tokens.
+    constexpr int WARPS = 8;
+    const long long W = base;
+    int ctas = c->sm_count;
+    while (ctas < (1 << 20) && W / ((long long)ctas * WARPS) >= SUM_TOKENS / QT) ctas += c->sm_count;
+    a.NWp = (int)std::max<long long>(1, std::min<long long>((long long)ctas * WARPS, W / 2));
+    p.ctas = (int)std::min<long long>(ctas, a.NWp);
+    p.wpc = (a.NWp + p.ctas - 1) / p.ctas;
+    const long long run = (W + a.NWp - 1) / a.NWp;
+    a.MAXU = (int)std::min<long long>((run - 1) / iu_min + 2, run);
+    p.part_floats = (size_t)a.NWp * a.MAXU * a.RV * (c->d + 2);
+    // merge: warps per row by the partials of a unit
+    const long long longest = [&] {
+        long long m = 0;
+        for (int x = 0; x < a.nseq; ++x) m = std::max<long long>(m, p.st.e[x].S ? p.st.e[x].Iu : 0);
+        return m;
+    }();
+    const long long parts = longest * a.NWp / W + 2;
+    p.cw = (int)std::min<long long>(CMB_MAXW, (parts + 7) / 8);
+    if (pick) {
+        p.ba = {c->dig, a.bt, call.q, nullptr, nullptr, call.n, B0, c->Hq, c->Hkv, c->g, c->NB, call.topk, Kc, p.nbmax};
+        p.bound_floats = (size_t)a.nseq * call.n * c->Hkv * p.nbmax;
+    }
+    return true;
+}
+
+template <int D, int NC, int FMT>
+cudaError_t launch_rows(const Plan &p, cudaStream_t s) {
+    using C = RowsCfg<D, NC>;
+    return launch_pdl(k_byte_rows<D, NC, FMT>, dim3((unsigned)p.ctas), p.wpc * 32, (size_t)C::WARP_SMEM * p.wpc, s, p.a, p.st);
+}
+
+template <int D>
+cudaError_t launch_plan(const ott_byte_cache *c, const Plan &p, cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (p.NC == 0) return launch_byte_tiles(c, p.a, p.st, p.nC, p.whole, s);
+    if (p.pick) {
+        if (p.nbmax > 0)
+            e = launch_pdl(k_byte_bounds<D>, dim3((unsigned)((p.nbmax + BND_BLOCKS - 1) / BND_BLOCKS), (unsigned)(p.a.nseq * c->Hkv)),
+                           BND_THREADS, 0, s, p.ba, p.bt);
+        int th = ((p.nbmax + 1) / 2 + 31) / 32 * 32;
+        th = std::min(std::max(th, 32), SORT_THREADS);
+        if (e == cudaSuccess)
+            e = launch_pdl(k_byte_pick, dim3((unsigned)(p.a.nseq * p.a.n * c->Hkv)), th, (size_t)p.nbmax * 4, s, p.ba, p.bt);
+    }
+    const bool i8 = c->format == OTT_BYTE_INT;
+    if (e == cudaSuccess)
+        e = p.NC == 1 ? (i8 ? launch_rows<D, 1, OTT_BYTE_INT>(p, s) : launch_rows<D, 1, OTT_BYTE_FLOAT>(p, s))
+                      : (i8 ? launch_rows<D, 2, OTT_BYTE_INT>(p, s) : launch_rows<D, 2, OTT_BYTE_FLOAT>(p, s));
+    if (e == cudaSuccess)
+        e = launch_pdl(k_byte_combine<D>, dim3((unsigned)(c->Hq * p.a.n), (unsigned)p.a.nseq), 32 * p.cw, 0, s, p.a, p.st);
+    return e;
+}
+
+template <int D, int NC, int FMT>
+cudaError_t rows_attribute() {
+    return cudaFuncSetAttribute(k_byte_rows<D, NC, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                RowsCfg<D, NC>::WARP_SMEM * RowsCfg<D, NC>::WARPS);
+}
+template <int D>
+cudaError_t set_attributes(int format) {
+    if (format == OTT_BYTE_INT) {
+        const cudaError_t e = rows_attribute<D, 1, OTT_BYTE_INT>();
+        return e != cudaSuccess ? e : rows_attribute<D, 2, OTT_BYTE_INT>();
+    }
+    const cudaError_t e = rows_attribute<D, 1, OTT_BYTE_FLOAT>();
+    return e != cudaSuccess ? e : rows_attribute<D, 2, OTT_BYTE_FLOAT>();
+}
+
+// shared memory of the selection that a launch may ask for
+int pick_smem(const ott_byte_cache *c) { return c->smem_optin - 2048; }
+
+}  // namespace
+
+cudaError_t set_byte_attributes(const ott_byte_cache *c) {
+    cudaError_t e = c->d == 128 ? set_attributes<128>(c->format) : set_attributes<64>(c->format);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_byte_pick, cudaFuncAttributeMaxDynamicSharedMemorySize, pick_smem(c));
+    return e == cudaSuccess ? set_byte_tiles_attributes(c->d, c->format) : e;
+}
+
+// err: the CUDA error behind OTT_ERR_CUDA.
+int run_byte_attn(const ott_byte_cache *c, const ByteCall &call, cudaStream_t s, cudaError_t &err) {
+    err = cudaSuccess;
+    int nb_all = 0;   // the most blocks of any sequence: the width of the lists that a caller gets
+    for (int b = 0; b < c->B; ++b) nb_all = std::max(nb_all, c->T[b] / c->G);
+    const int Kc = std::min(call.topk, nb_all);
+    if (Kc > 0 && (long long)nb_all * 4 > pick_smem(c)) return OTT_ERR_INVALID;
+    // With nothing to select, the call is the one over every block.
+    ByteCall cl = call;
+    if (Kc == 0) cl.topk = 0;
+    if ((long long)c->Hq * cl.n > INT_MAX || (cl.topk > 0 && (long long)CHUNK_SEQS * c->Hkv * cl.n > INT_MAX))
+        return OTT_ERR_INVALID;
+    const int passes = (c->B + CHUNK_SEQS - 1) / CHUNK_SEQS;
+    size_t floats = 0, parts = 0, bounds = 0;
+    auto plan = [&](int x, Plan &p) { return make_plan(c, cl, x * CHUNK_SEQS, Kc, p); };
+    Plan p;
+    for (int x = 0; x < passes; ++x) {   // every pass is checked before the first is queued
+        if (!plan(x, p)) return OTT_ERR_INVALID;
+        if (p.NC > 0 && ((long long)p.a.nseq * c->Hkv > 65535 && cl.topk > 0)) return OTT_ERR_INVALID;   // a grid dimension
+        parts = std::max(parts, p.part_floats);
+        bounds = std::max(bounds, p.bound_floats);
+    }
+    const size_t lists = cl.topk > 0 && !cl.sel ? (size_t)c->U * cl.n * Kc : 0;
+    parts = (parts + 63) / 64 * 64;
+    bounds = (bounds + 63) / 64 * 64;
+    floats = parts + bounds + lists;
+    Scratch scratch(c->part, c->part_floats, c->device, floats, s);
+    if (!scratch.ptr) return OTT_ERR_OOM;
+    float *base = static_cast<float *>(scratch.ptr);
+    for (int x = 0; x < passes && err == cudaSuccess; ++x) {
+        if (passes > 1) plan(x, p);
+        if (!p.any) continue;
+        p.a.part = base;
+        if (cl.topk > 0) {
+            p.ba.bound = base + parts;
+            p.ba.sel = cl.sel ? cl.sel : reinterpret_cast<int32_t *>(base + parts + bounds);
+            p.a.sel = p.ba.sel;
+        }
+        err = c->d == 128 ? launch_plan<128>(c, p, s) : launch_plan<64>(c, p, s);
+    }
+    const cudaError_t e2 = scratch.release();
+    if (err == cudaSuccess) err = e2;
+    return err == cudaSuccess ? OTT_OK : OTT_ERR_CUDA;
+}
+
+}  // namespace ott

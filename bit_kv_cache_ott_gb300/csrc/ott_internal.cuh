@@ -270,10 +270,14 @@ struct ChunkRange {
 };
 cudaError_t launch_append_range(const ott_cache *c, const __half *k, const __half *v, int n, int b0,
                                 const ChunkRange &r, cudaStream_t s);
+// Stream-ordered device memory from the library's pool, or else the device's
+// default pool; null if neither has it.
+void *stream_alloc(int dev, size_t bytes, cudaStream_t s);
 // `floats` floats for the duration of a call: the cache's split-K scratch
 // where they fit, else stream-ordered memory (ptr null: none to be had).
 struct Scratch {
     Scratch(const ott_cache *c, size_t floats, cudaStream_t s);
+    Scratch(float *own, size_t own_floats, int dev, size_t floats, cudaStream_t s);
     cudaError_t release();
     void *ptr;
     bool owned;

@@ -411,6 +411,126 @@ typedef struct {
 int ott_rope(const void *q, void *q_out, int Hq, const void *k, void *k_out, int Hkv, const int32_t *pos,
              int B, int n, int d, const ott_rope_plan *plan, void *stream);
 
+/*
+ * A cache held in 8 bits: the kind for layers and models that 2 bits hurt,
+ * with the same loop (append, decode, chunks, Top-K, a paged pool). Every
+ * sequence keeps its own length. A unit is a (sequence, kv head); its tokens
+ * are cut into blocks of G, token t in block t / G. The tokens of the block
+ * that is still open stay fp16. A block that is complete is held as codes of
+ * one byte with one fp32 scale for its keys and one for its values: with
+ * a = max |x| over the block's G x d keys (or values), all finite,
+ *   OTT_BYTE_INT:   code = rint(127 x / a), scale = a / 127;
+ *   OTT_BYTE_FLOAT: code = the e4m3 number nearest 448 x / a, scale = a / 448,
+ * ties to even, both decided by the exact quotient; a = 0 gives codes and
+ * scale 0. A code stands for code * scale. The smallest and largest key of
+ * each channel are kept beside it, in fp16, for the Top-K calls' bounds.
+ * What the cache holds does not depend on how its tokens were cut into calls.
+ *
+ * All of these calls need the cache's device to be the current one
+ * (OTT_ERR_STATE), and follow the conventions above. Calls on one cache are
+ * made one after another on one stream (or ordered by events): they share its
+ * tables and its scratch, captured graphs of them too. A graph repeats its
+ * calls at the lengths that the cache had when they were captured.
+ *
+ * ott_byte_create: d in {64, 128}; G in {32, 64, 128}; Hq % Hkv == 0;
+ * B <= 256; max_tokens bounds each sequence. pool_blocks = 0: room for
+ * max_tokens in every unit; else the complete blocks of all units come from
+ * one pool of that many, taken as they fill up and returned by
+ * ott_byte_release and ott_byte_reset.
+ */
+typedef struct ott_byte_cache ott_byte_cache;
+enum { OTT_BYTE_INT = 0, OTT_BYTE_FLOAT = 1 };
+
+int ott_byte_create(int B, int Hq, int Hkv, int d, int G, int format, int max_tokens, long long pool_blocks,
+                    ott_byte_cache **out);
+
+/* Free everything. NULL-safe. Waits for the device to finish. */
+int ott_byte_destroy(ott_byte_cache *c);
+
+/*
+ * Append a chunk (a prompt, a part of one, one token): sequence b receives
+ * its lens[b] tokens (HOST int32[B], read during the call, 0 <= lens[b] <= n;
+ * NULL: n each), the first rows of its room. k, v: DEVICE fp16 [B][Hkv][n][d];
+ * rows behind them are not read. Blocks that become complete are quantized
+ * in the same kernel. OTT_ERR_CAPACITY if a sequence would outgrow max_tokens
+ * or the pool lacks the blocks, before anything is queued.
+ */
+int ott_byte_append(ott_byte_cache *c, const void *k, const void *v, int n, const int *lens, void *stream);
+
+/* The same for sequence b alone: k, v DEVICE fp16 [Hkv][n][d]. */
+int ott_byte_append_seq(ott_byte_cache *c, int b, const void *k, const void *v, int n, void *stream);
+
+/*
+ * Read back: tokens start .. start + n - 1 of every sequence into K, V
+ * (DEVICE fp16 [B][Hkv][n][d], apart from one another). A token of a complete
+ * block is its code times its scale (one fp32 product), rounded to fp16; one
+ * of the open block is as it was given. Rows of tokens that a sequence does not hold
+ * are left as they are. start, n >= 0.
+ */
+int ott_byte_read(ott_byte_cache *c, void *K, void *V, int start, int n, void *stream);
+
+/*
+ * Decode-step attention, one query per sequence over all its tokens: q, out
+ * DEVICE fp16 [B][Hq][d], apart from one another. Every sequence must hold a
+ * token (OTT_ERR_STATE).
+ * topk > 0: of the complete blocks each kv head attends the min(topk, T_b / G)
+ * with the largest bound (ties to the lower block), next to the open block's
+ * tokens. A block's bound for query head h is sum over channels of
+ * max(q*lo, q*hi) with the block's smallest and largest key of the channel, in
+ * fp32 (the products are exact; sums in channel order, each rounded); for the
+ * kv head it is the largest over its query heads. sel: NULL, or DEVICE
+ * int32 [B][Hkv][min(topk, nb)] (nb: the most complete blocks of any
+ * sequence), which receives the selected blocks in ascending order, -1 behind
+ * them. topk = 0: every block; sel is ignored.
+ * OTT_ERR_INVALID also if a sequence holds too many blocks for the
+ * selection's shared memory (4 bytes each).
+ */
+int ott_byte_decode(ott_byte_cache *c, const void *q, void *out, int topk, int32_t *sel, void *stream);
+
+/*
+ * Attention of a chunk of new tokens over the cache and, causally, one
+ * another: as ott_chunk_attn without a window, over this kind of cache.
+ * q, out: DEVICE fp16 [B][Hq][n][d]; k, v: DEVICE fp16 [B][Hkv][n][d], not in
+ * the cache yet; lens as in ott_byte_append. out lies apart from q, k and v.
+ * topk > 0: query i of a sequence attends the topk blocks that it selects for
+ * each kv head, as in ott_byte_decode, the open block's tokens, and new tokens
+ * 0 .. i. sel: NULL, or DEVICE int32 [B][n][Hkv][min(topk, nb)], written for
+ * the tokens that lens counts. (Every query reads its own blocks: meant for
+ * drafts of some tokens, not for prompts.)
+ *
+ * Precision of both calls: keys' and values' codes enter the tensor cores
+ * exactly; softmax statistics and sums are fp32; a weight times its block's
+ * value scale is rounded to fp16 (2^-11 relative, gone below 2^-32 of its
+ * row's largest such product). The tensor cores add up at most 25,088 tokens
+ * on their own. Keys and values are finite; one that is not spoils rows that
+ * do not see it as well. A query that is not finite gets NaN in its own row
+ * (with topk the selection of its kv head is then any) and changes no other
+ * row's attention. A call gives the same bits every time; the kernel and the
+ * order of its sums go by the largest lens of up to 64 sequences and the
+ * GPU's SMs. Larger scratch than the cache's own comes from the library's
+ * stream-ordered pool (OTT_ERR_OOM before anything is queued).
+ */
+int ott_byte_attn(ott_byte_cache *c, const void *q, const void *k, const void *v, void *out, int n, const int *lens,
+                  int topk, int32_t *sel, void *stream);
+
+/* Sequence b drops its tokens; its blocks return to the pool. */
+int ott_byte_release(ott_byte_cache *c, int b, void *stream);
+
+/* Every sequence drops its tokens. */
+int ott_byte_reset(ott_byte_cache *c, void *stream);
+
+/* Tokens of sequence b and its complete blocks per kv head. Host-side. */
+int ott_byte_counts(const ott_byte_cache *c, int b, long long *T, int *blocks);
+
+/* Free blocks of the pool (host-side), -1 without one. */
+long long ott_byte_free_blocks(const ott_byte_cache *c);
+
+/* As ott_check_device. */
+int ott_byte_check(ott_byte_cache *c);
+
+/* Bytes of device memory the cache holds. Host-side. */
+long long ott_byte_bytes(const ott_byte_cache *c);
+
 /* Counts (same for every sequence and kv head): tokens seen, blocks (flushes),
  * residual tokens, pool tokens. Host-side, no device access. After
  * ott_prefill_lens the counts differ per sequence; this then reports
