@@ -430,7 +430,8 @@ int ott_rope(const void *q, void *q_out, int Hq, const void *k, void *k_out, int
  * (OTT_ERR_STATE), and follow the conventions above. Calls on one cache are
  * made one after another on one stream (or ordered by events): they share its
  * tables and its scratch, captured graphs of them too. A graph repeats its
- * calls at the lengths that the cache had when they were captured.
+ * calls at the lengths that the cache had when they were captured; one that
+ * appends or releases is replayed once, on the state that it was captured for.
  *
  * ott_byte_create: d in {64, 128}; G in {32, 64, 128}; Hq % Hkv == 0;
  * B <= 256; max_tokens bounds each sequence. pool_blocks = 0: room for
