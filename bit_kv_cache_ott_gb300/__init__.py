@@ -230,6 +230,11 @@ def _stream_of(stream, idx: int) -> int:
     return (torch.cuda.current_stream(idx) if stream is None else stream).cuda_stream
 
 
+# (torch.cuda.current_stream and current_device without their objects and checks)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda idx: torch.cuda.current_stream(idx).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", lambda: torch.cuda.current_device())
+
+
 def _on_device(idx: int, fn, what: str, *args):
     """fn(*args) with device idx current (a context manager per call costs more than most of these kernels)."""
     prev = torch.cuda.current_device()
@@ -511,7 +516,7 @@ class ByteCache:
     FORMATS = {"int8": 0, "e4m3": 1}
 
     def __init__(self, B, Hq, Hkv, d, G=64, fmt="int8", max_tokens=8192, pool_blocks=None):
-        L = load()
+        self._L = L = load()
         if fmt not in self.FORMATS:
             raise ValueError(f"fmt: expected one of {tuple(self.FORMATS)}, got {fmt!r}")
         if pool_blocks is not None and int(pool_blocks) < 1:
@@ -519,6 +524,7 @@ class ByteCache:
         self.B, self.Hq, self.Hkv, self.d, self.G, self.fmt, self.max_tokens = B, Hq, Hkv, d, G, fmt, max_tokens
         self._h = C.c_void_p()
         self._dev = torch.cuda.current_device()
+        self._qshape, self._kshape = (B, Hq, d), (B, Hkv, d)
         sizes = [_int32(x, n) for x, n in ((B, "B"), (Hq, "Hq"), (Hkv, "Hkv"), (d, "d"), (G, "G"))]
         _check(L.ott_byte_create(*sizes, self.FORMATS[fmt], _int32(max_tokens, "max_tokens"), int(pool_blocks or 0),
                                  C.byref(self._h)), "ott_byte_create")
@@ -544,14 +550,24 @@ class ByteCache:
     def handle(self) -> int:
         return self._h.value
 
+    # (Small calls end on the device before the next one is queued: checks are one expression, and the current stream
+    # and device come from the calls that torch's own wrappers make: a decode step's call 15 -> 8 us.)
     def _call(self, fn, what, *args, stream):
-        _on_device(self._dev, fn, what, self._h, *args, _stream_of(stream, self._dev))
+        dev = self._dev
+        s = _raw_stream(dev) if stream is None else stream.cuda_stream
+        if _raw_device() == dev:
+            rc = fn(self._h, *args, s)
+            if rc:
+                _check(rc, what)
+        else:
+            _on_device(dev, fn, what, self._h, *args, s)
 
     def _ptr(self, t, shape, name) -> int:
-        p = _dev_ptr(t, shape, name)
-        if t.get_device() != self._dev:
-            raise ValueError(f"{name}: on {t.device}, the cache is on cuda:{self._dev}")
-        return p
+        if isinstance(t, torch.Tensor) and t.dtype is torch.float16 and t.get_device() == self._dev and t.shape == shape \
+                and t.is_contiguous():
+            return t.data_ptr()
+        _dev_ptr(t, shape, name)   # says what is wrong, but for the device
+        raise ValueError(f"{name}: on {t.device}, the cache is on cuda:{self._dev}")
 
     def _lens(self, lens):
         if lens is None:
@@ -561,12 +577,12 @@ class ByteCache:
         return (C.c_int * self.B)(*[_int32(x, "lens") for x in lens])
 
     def _append(self, k, v, n, shape, lens, stream):
-        self._call(load().ott_byte_append, "ott_byte_append", self._ptr(k, shape, "k"), self._ptr(v, shape, "v"), n,
+        self._call(self._L.ott_byte_append, "ott_byte_append", self._ptr(k, shape, "k"), self._ptr(v, shape, "v"), n,
                    self._lens(lens), stream=stream)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, stream=None):
         """One token to every sequence: k, v fp16 [B][Hkv][d]."""
-        self._append(k, v, 1, (self.B, self.Hkv, self.d), None, stream)
+        self._append(k, v, 1, self._kshape, None, stream)
 
     def append_chunk(self, k: torch.Tensor, v: torch.Tensor, lens=None, stream=None):
         """n tokens per sequence, k, v fp16 [B][Hkv][n][d] (ott_byte_append); ``lens``: sequence b takes its first lens[b],
@@ -590,7 +606,7 @@ class ByteCache:
             raise OTTError(OTT_ERR_STATE, "prefill of a sequence that holds tokens")
         n = K.shape[1] if isinstance(K, torch.Tensor) and K.dim() == 3 else -1
         shp = (self.Hkv, n, self.d)
-        self._call(load().ott_byte_append_seq, "ott_byte_append_seq", _int32(b, "b"), self._ptr(K, shp, "K"),
+        self._call(self._L.ott_byte_append_seq, "ott_byte_append_seq", _int32(b, "b"), self._ptr(K, shp, "K"),
                    self._ptr(V, shp, "V"), n, stream=stream)
 
     def read(self, start: int, n: int, out_k: torch.Tensor | None = None, out_v: torch.Tensor | None = None, stream=None):
@@ -602,7 +618,7 @@ class ByteCache:
             out_k = torch.zeros(shp, dtype=torch.float16, device=f"cuda:{self._dev}")
         if out_v is None:
             out_v = torch.zeros(shp, dtype=torch.float16, device=f"cuda:{self._dev}")
-        self._call(load().ott_byte_read, "ott_byte_read", self._ptr(out_k, shp, "out_k"), self._ptr(out_v, shp, "out_v"),
+        self._call(self._L.ott_byte_read, "ott_byte_read", self._ptr(out_k, shp, "out_k"), self._ptr(out_v, shp, "out_v"),
                    _int32(start, "start"), n, stream=stream)
         return out_k, out_v
 
@@ -615,11 +631,10 @@ class ByteCache:
         """decode_attn over the K complete blocks with the largest bound of each (sequence, kv head) and the open block
         (ott_byte_decode; K = 0: all). ``sel``: int32 [B][1][Hkv][min(K, most blocks of a sequence)] (or without the
         1), receives the blocks."""
-        shp = (self.B, self.Hq, self.d)
-        qp = self._ptr(q, shp, "q")
+        qp = self._ptr(q, self._qshape, "q")
         if out is None:
             out = torch.empty_like(q)
-        self._call(load().ott_byte_decode, "ott_byte_decode", qp, self._ptr(out, shp, "out"), _int32(K, "K"),
+        self._call(self._L.ott_byte_decode, "ott_byte_decode", qp, self._ptr(out, self._qshape, "out"), _int32(K, "K"),
                    self._sel(sel, 1, K), stream=stream)
         return out
 
@@ -640,7 +655,7 @@ class ByteCache:
         ptr = [self._ptr(q, shp, "q"), self._ptr(k, kshp, "k"), self._ptr(v, kshp, "v")]
         if out is None:
             out = torch.empty_like(q)
-        self._call(load().ott_byte_attn, "ott_byte_attn", *ptr, self._ptr(out, shp, "out"), n, self._lens(lens),
+        self._call(self._L.ott_byte_attn, "ott_byte_attn", *ptr, self._ptr(out, shp, "out"), n, self._lens(lens),
                    _int32(K, "K"), self._sel(sel, n, K), stream=stream)
         return out
 
@@ -657,24 +672,24 @@ class ByteCache:
 
     def release_seq(self, b: int, stream=None):
         """Sequence b drops its tokens (and its pool blocks)."""
-        self._call(load().ott_byte_release, "ott_byte_release", _int32(b, "b"), stream=stream)
+        self._call(self._L.ott_byte_release, "ott_byte_release", _int32(b, "b"), stream=stream)
 
     def reset(self, stream=None):
         """Every sequence drops its tokens."""
-        self._call(load().ott_byte_reset, "ott_byte_reset", stream=stream)
+        self._call(self._L.ott_byte_reset, "ott_byte_reset", stream=stream)
 
     def seq_counts(self, b: int):
         """(tokens of sequence b, its complete blocks per kv head)."""
         T, nb = C.c_longlong(), C.c_int()
-        _check(load().ott_byte_counts(self._h, _int32(b, "b"), C.byref(T), C.byref(nb)), "ott_byte_counts")
+        _check(self._L.ott_byte_counts(self._h, _int32(b, "b"), C.byref(T), C.byref(nb)), "ott_byte_counts")
         return T.value, nb.value
 
     def free_blocks(self) -> int:
         """Free blocks of the pool (-1 without one)."""
-        return int(load().ott_byte_free_blocks(self._h))
+        return int(self._L.ott_byte_free_blocks(self._h))
 
     def device_bytes(self) -> int:
-        return int(load().ott_byte_bytes(self._h))
+        return int(self._L.ott_byte_bytes(self._h))
 
     def check_device(self):
-        _check(load().ott_byte_check(self._h), "ott_byte_check")
+        _check(self._L.ott_byte_check(self._h), "ott_byte_check")

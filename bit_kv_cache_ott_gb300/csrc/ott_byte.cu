@@ -28,7 +28,11 @@ using namespace ott;
 
 namespace {
 
-constexpr int APP_THREADS = 256, READ_WARPS = 8;
+constexpr int READ_WARPS = 8;
+// Threads of an append CTA: eight 16-byte pieces of one block each (with four,
+// the fixed part of a thread's work took as many instructions as its pieces:
+// PLACEHOLDER).
+__host__ __device__ constexpr int app_threads(int d, int g) { return g * d / 64; }
 
 struct AppendArgs {
     uint8_t *blk;
@@ -55,32 +59,29 @@ __device__ __forceinline__ uint32_t h2max(uint32_t a, uint32_t b) { return ch_h2
 template <int FMT>
 __device__ __forceinline__ uint32_t encode2(uint32_t x, float a, float inv) {
     constexpr float TOP = FMT == OTT_BYTE_INT ? 127.0f : 448.0f;
-    const float2 f = __half22float2(ch_as_h2(x));
-    float r[2];
-#pragma unroll
-    for (int y = 0; y < 2; ++y) {
-        const float p = (y ? f.y : f.x) * TOP;
-        const float q = p * inv;
-        r[y] = fmaf(fmaf(-q, a, p), inv, q);
-    }
+    const float2 p = __fmul2_rn(__half22float2(ch_as_h2(x)), make_float2(TOP, TOP)), i2 = make_float2(inv, inv);
+    const float2 q = __fmul2_rn(p, i2);
+    // p - q a: exact
+    const float2 r = __ffma2_rn(__ffma2_rn(q, make_float2(-a, -a), p), i2, q);
     if constexpr (FMT == OTT_BYTE_INT) {
         // r + 1.5 * 2^23 + 128: the sum rounds r to an integer (ties to even), its low byte is 128 + code
-        const float big = 12583040.0f;
-        return __byte_perm(__float_as_uint(__fadd_rn(r[0], big)), __float_as_uint(__fadd_rn(r[1], big)), 0x0040);
+        const float2 c = __fadd2_rn(r, make_float2(12583040.0f, 12583040.0f));
+        return __byte_perm(__float_as_uint(c.x), __float_as_uint(c.y), 0x0040);
     } else {
         uint16_t c;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(r[1]), "f"(r[0]));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(r.y), "f"(r.x));
         return c;
     }
 }
 
 template <int D, int G, int FMT>
-__global__ void __launch_bounds__(APP_THREADS)
+__global__ void __launch_bounds__(app_threads(D, G))
     k_byte_append(const __grid_constant__ AppendArgs a, const __grid_constant__ AppendTable t) {
+    constexpr int APP_THREADS = app_threads(D, G);
     constexpr int CPR = D / 8;                          // 16-byte pieces of a token
     constexpr int PER = G * CPR / APP_THREADS;          // pieces per thread: tokens TPI apart, the same channels
     constexpr int TPI = APP_THREADS / CPR, WARPS = APP_THREADS / 32;
-    static_assert(G * CPR % APP_THREADS == 0 && APP_THREADS % CPR == 0, "whole pieces");
+    static_assert(PER * APP_THREADS == G * CPR && TPI * CPR == APP_THREADS && WARPS * 32 == APP_THREADS, "whole pieces");
     constexpr float TOP = FMT == OTT_BYTE_INT ? 127.0f : 448.0f;
     constexpr int RS = D + 4;                           // row of codes in shared memory
     __shared__ uint32_t rng[2][WARPS][D / 2];           // smallest and largest, by warp
@@ -142,18 +143,18 @@ __global__ void __launch_bounds__(APP_THREADS)
         }
         __syncthreads();
         float m = 0.0f;
-        if (tid < D / 2) {
-            uint32_t l = rng[0][0][tid], h = rng[1][0][tid];
+        for (int z = tid; z < D / 2; z += APP_THREADS) {
+            uint32_t l = rng[0][0][z], h = rng[1][0][z];
 #pragma unroll
             for (int w = 1; w < WARPS; ++w) {
-                l = h2min(l, rng[0][w][tid]);
-                h = h2max(h, rng[1][w][tid]);
+                l = h2min(l, rng[0][w][z]);
+                h = h2max(h, rng[1][w][z]);
             }
             if (!val)
-                *reinterpret_cast<uint2 *>(a.dig + slot * D + 2 * tid) =
+                *reinterpret_cast<uint2 *>(a.dig + slot * D + 2 * z) =
                     make_uint2(__byte_perm(l, h, 0x5410), __byte_perm(l, h, 0x7632));
             const float2 fl = __half22float2(ch_as_h2(l)), fh = __half22float2(ch_as_h2(h));
-            m = fmaxf(fmaxf(fabsf(fl.x), fabsf(fl.y)), fmaxf(fabsf(fh.x), fabsf(fh.y)));
+            m = fmaxf(m, fmaxf(fmaxf(fabsf(fl.x), fabsf(fl.y)), fmaxf(fabsf(fh.x), fabsf(fh.y))));
         }
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -343,7 +344,7 @@ int state_of(const ott_byte_cache *c) {
 template <int D, int G>
 cudaError_t append_t(const AppendArgs &a, const AppendTable &t, int format, int ctas, cudaStream_t s) {
     auto *kern = format == OTT_BYTE_INT ? k_byte_append<D, G, OTT_BYTE_INT> : k_byte_append<D, G, OTT_BYTE_FLOAT>;
-    return launch_pdl(kern, dim3((unsigned)ctas, 2), APP_THREADS, 0, s, a, t);
+    return launch_pdl(kern, dim3((unsigned)ctas, 2), app_threads(D, G), 0, s, a, t);
 }
 
 // Sequences [b0, b0 + nb): m[x] tokens each from k, v [nb][Hkv][n][d]; m null: n.

@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 
 // Merge a row's partials: a CTA of cw warps per (sequence, query head,
 // token), the warps' shares merged through shared memory.
-constexpr int CMB_MAXW = 16;
+constexpr int CMB_MAXW = 8;   // (small enough to wait beside the rows kernel's CTAs)
 template <int D>
 __global__ void __launch_bounds__(CMB_MAXW * 32)
     k_byte_combine(const __grid_constant__ ByteArgs a, const __grid_constant__ ByteTable st) {
@@ -476,17 +476,23 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
     const int cw = blockDim.x >> 5, wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const ByteSeq &s = st.e[blockIdx.y];
     const int hq = blockIdx.x / a.n, tk = blockIdx.x % a.n;
+    const bool row = tk < s.nq;
+    int wa = 0, wb = -1, uo_a = 0, col = 0;
+    if (row) {   // the plan, while the rows kernel still runs
+        const int hd = hq % a.g, v = a.sel ? hd : tk * a.g + hd;
+        const int sl = a.sel ? tk * a.SG + hd / a.RB : v / a.RB, h = hq / a.g * s.S + sl;
+        col = v % a.RB;
+        const long long ub = s.base + (long long)h * s.Iu, ue = ub + s.Iu;
+        wa = ch_warp_of(a.W, a.NWp, ub);
+        wb = ch_warp_of(a.W, a.NWp, ue - 1);
+        // the unit's place among those of warp wa
+        const long long xa = ch_range_start(a.W, a.NWp, wa);
+        const int ea = entry_of(st, a.nseq, xa);
+        uo_a = s.ubase + h - (st.e[ea].ubase + (int)((unsigned)(xa - st.e[ea].base) / (unsigned)st.e[ea].Iu));
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (tk >= s.nq || s.S == 0) return;
-    const int hd = hq % a.g, v = a.sel ? hd : tk * a.g + hd;
-    const int sl = a.sel ? tk * a.SG + hd / a.RB : v / a.RB, h = hq / a.g * s.S + sl, col = v % a.RB;
-    const long long ub = s.base + (long long)h * s.Iu, ue = ub + s.Iu;
-    const int wa = ch_warp_of(a.W, a.NWp, ub), wb = ch_warp_of(a.W, a.NWp, ue - 1);
-    // the unit's place among those of warp wa
-    const long long xa = ch_range_start(a.W, a.NWp, wa);
-    const int ea = entry_of(st, a.nseq, xa);
-    const int uo_a = s.ubase + h - (st.e[ea].ubase + (int)((unsigned)(xa - st.e[ea].base) / (unsigned)st.e[ea].Iu));
+    if (!row) return;
     float M = -CUDART_INF_F, L = 0.0f, acc[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) acc[c] = 0.0f;
