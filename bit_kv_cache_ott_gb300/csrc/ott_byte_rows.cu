@@ -569,99 +569,116 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
 }
 
 // ---------------------------------------------------------------- selection
-constexpr int BND_BLOCKS = 32, BND_THREADS = 128;
+// A cluster of up to 8 CTAs per (sequence, kv head) takes the bounds of its
+// blocks for every token of the sequence, and then, one token per CTA, the
+// selection.
+// A slab is 32 blocks' channel ranges in shared memory (16-byte pieces turned
+// by the block, so that 8 lanes that read one piece of their own blocks meet
+// all banks). A warp takes a (slab, token): lane = block, four query heads
+// at a time as two packed pairs. max(q lo, q hi) is (q > 0 ? q hi : q lo), which
+// two multiply-adds with the positive and the negative part of q give with
+// one rounding, the sum's (products of two fp16 numbers are exact, and one
+// of the two is zero): two operations per channel for two heads.
+constexpr int SEL_THREADS = 256, SLABS = 8, SEL_CLUSTER = 8;
 
-struct BoundArgs {
+struct SelectArgs {
     const __half2 *dig;
     const int32_t *bt;
     const __half *q;
     float *bound;       // [nseq][n][Hkv][stride]
     int32_t *sel;       // [B][n][Hkv][Kc]
     int n, B0, Hq, Hkv, g, NB, K, Kc, stride;
+    int cluster, slabs;   // CTAs per (sequence, kv head), slabs in shared memory at a time
 };
-struct BoundTable {
+struct SelectTable {
     int nb[CHUNK_SEQS], nq[CHUNK_SEQS];
 };
-
-// Bounds of 32 blocks for the queries of one (sequence, kv head): the blocks'
-// channel ranges in shared memory (rows padded by one word, so that threads
-// that read one channel of their own blocks meet different banks), then four
-// query rows at a time, a thread per (block, row).
 template <int D>
-__global__ void __launch_bounds__(BND_THREADS) k_byte_bounds(const __grid_constant__ BoundArgs a, const __grid_constant__ BoundTable t) {
-    constexpr int RW = D + 1, V4 = D / 4, PER = BND_BLOCKS * V4 / BND_THREADS, RPI = BND_THREADS / BND_BLOCKS;
-    __shared__ uint32_t dg[BND_BLOCKS * RW];
-    __shared__ float qs[RPI][D];
-    __shared__ float part[RPI][BND_BLOCKS];
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int e = blockIdx.y / a.Hkv, hkv = blockIdx.y % a.Hkv, j0 = blockIdx.x * BND_BLOCKS, tid = threadIdx.x;
-    const int u = (a.B0 + e) * a.Hkv + hkv, nb = min(BND_BLOCKS, t.nb[e] - j0), nq = t.nq[e];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (nb <= 0 || nq == 0) return;   // the whole CTA
-    uint4 buf[PER];
-#pragma unroll
-    for (int y = 0; y < PER; ++y) {
-        const int z = tid + y * BND_THREADS, row = z / V4;
-        if (row < nb) {
-            const size_t own = (size_t)u * a.NB + j0 + row, slot = a.bt ? (size_t)__ldg(a.bt + own) : own;
-            buf[y] = __ldg(reinterpret_cast<const uint4 *>(a.dig + slot * D) + z % V4);
-        }
-    }
-#pragma unroll
-    for (int y = 0; y < PER; ++y) {
-        const int z = tid + y * BND_THREADS, row = z / V4;
-        if (row < nb) {
-            uint32_t *w = dg + row * RW + 4 * (z % V4);
-            w[0] = buf[y].x;
-            w[1] = buf[y].y;
-            w[2] = buf[y].z;
-            w[3] = buf[y].w;
-        }
-    }
-    const int row = tid % BND_BLOCKS, h = tid / BND_BLOCKS;
-    for (int tk = 0; tk < nq; ++tk) {
-        float best = -CUDART_INF_F;
-        for (int s0 = 0; s0 < a.g; s0 += RPI) {   // a short last round repeats its last head
-            __syncthreads();
-            for (int z = tid; z < RPI * D; z += BND_THREADS)
-                qs[z / D][z % D] = __half2float(
-                    __ldg(a.q + (((size_t)(a.B0 + e) * a.Hq + hkv * a.g + min(s0 + z / D, a.g - 1)) * a.n + tk) * D + z % D));
-            __syncthreads();
-            float sum = 0.0f;
-            if (row < nb) {
-#pragma unroll 8
-                for (int c = 0; c < D; ++c) {
-                    const float2 f = __half22float2(ch_as_h2(dg[row * RW + c]));
-                    const float lo = __fmul_rn(qs[h][c], f.x), up = __fmul_rn(qs[h][c], f.y);
-                    sum = __fadd_rn(sum, up > lo ? up : lo);
-                }
-            }
-            part[h][row] = sum;
-            __syncthreads();
-            if (tid < nb)
-#pragma unroll
-                for (int x = 0; x < RPI; ++x) best = part[x][tid] > best ? part[x][tid] : best;
-        }
-        if (tid < nb) a.bound[(((size_t)e * a.n + tk) * a.Hkv + hkv) * a.stride + j0 + tid] = best;
-    }
-}
+__host__ __device__ constexpr int slab_bytes() { return 32 * D * 4; }
+template <int D>
+__host__ __device__ constexpr int heads_bytes() { return 2 * D * 16; }   // four heads: (q0+, q1+, q0-, q1-) per channel, twice
 
-__global__ void __launch_bounds__(SORT_THREADS) k_byte_pick(const __grid_constant__ BoundArgs a, const __grid_constant__ BoundTable t) {
-    extern __shared__ uint32_t key[];
+template <int D>
+__global__ void __launch_bounds__(SEL_THREADS)
+    k_byte_select(const __grid_constant__ SelectArgs a, const __grid_constant__ SelectTable t) {
+    constexpr int V4 = D / 4, WARPS = SEL_THREADS / 32;
+    extern __shared__ __align__(128) uint8_t smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int hkv = blockIdx.x % a.Hkv, tk = blockIdx.x / a.Hkv % a.n, e = blockIdx.x / a.Hkv / a.n;
+    const int rank = blockIdx.x % a.cluster, unit = blockIdx.x / a.cluster, e = unit / a.Hkv, hkv = unit % a.Hkv;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int u = (a.B0 + e) * a.Hkv + hkv, nb = t.nb[e], nq = t.nq[e];
+    const int all = (nb + 31) / 32, per = (all + a.cluster - 1) / a.cluster, s0 = min(all, rank * per),
+              s1 = nq > 0 ? min(all, s0 + per) : s0;
+    float4 *const heads = reinterpret_cast<float4 *>(smem + a.slabs * slab_bytes<D>() + warp * heads_bytes<D>());
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (tk >= t.nq[e]) return;   // the whole CTA
-    const size_t at = ((size_t)e * a.n + tk) * a.Hkv + hkv;
-    pick_blocks(a.bound + at * a.stride, t.nb[e], a.K, a.Kc, a.sel + ((size_t)a.B0 * a.n * a.Hkv + at) * a.Kc, key);
+    for (int sb = s0; sb < s1; sb += a.slabs) {
+        const int ns = min(a.slabs, s1 - sb);
+        if (sb > s0) __syncthreads();   // the slabs before are read
+        for (int z = threadIdx.x; z < ns * 32 * V4; z += SEL_THREADS) {
+            const int x = z / V4, v = z % V4, j = sb * 32 + x;
+            if (j < nb) {
+                const size_t own = (size_t)u * a.NB + j, slot = a.bt ? (size_t)__ldg(a.bt + own) : own;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ch_smem(smem + x * (D * 4) + ((v ^ (x & 7)) << 4))),
+                             "l"(a.dig + slot * D + 4 * v)
+                             : "memory");
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        for (int task = warp; task < ns * nq; task += WARPS) {
+            const int x = task % ns, tk = task / ns, j = (sb + x) * 32 + lane;
+            const uint4 *row = reinterpret_cast<const uint4 *>(smem + (x * 32 + lane) * (D * 4));
+            const __half *q = a.q + (((size_t)(a.B0 + e) * a.Hq + hkv * a.g) * a.n + tk) * D;
+            float best = -CUDART_INF_F;
+            for (int h0 = 0; h0 < a.g; h0 += 4) {   // a short last round repeats its last head
+                __syncwarp();
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const __half *q0 = q + (size_t)min(h0 + 2 * p, a.g - 1) * a.n * D, *q1 = q + (size_t)min(h0 + 2 * p + 1, a.g - 1) * a.n * D;
+#pragma unroll
+                    for (int c = lane; c < D; c += 32) {
+                        const float f0 = __half2float(__ldg(q0 + c)), f1 = __half2float(__ldg(q1 + c));
+                        heads[p * D + c] = make_float4(fmaxf(f0, 0.0f), fmaxf(f1, 0.0f), fminf(f0, 0.0f), fminf(f1, 0.0f));
+                    }
+                }
+                __syncwarp();
+                float2 s01 = make_float2(0.0f, 0.0f), s23 = s01;
+#pragma unroll 4
+                for (int c4 = 0; c4 < V4; ++c4) {
+                    const uint4 d = row[c4 ^ (lane & 7)];
+                    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const float2 f = __half22float2(ch_as_h2(w[y])), lo = make_float2(f.x, f.x), up = make_float2(f.y, f.y);
+                        const float4 p = heads[4 * c4 + y], r = heads[D + 4 * c4 + y];
+                        s01 = __ffma2_rn(make_float2(p.z, p.w), lo, __ffma2_rn(make_float2(p.x, p.y), up, s01));
+                        s23 = __ffma2_rn(make_float2(r.z, r.w), lo, __ffma2_rn(make_float2(r.x, r.y), up, s23));
+                    }
+                }
+                best = s01.x > best ? s01.x : best;
+                best = s01.y > best ? s01.y : best;
+                best = s23.x > best ? s23.x : best;
+                best = s23.y > best ? s23.y : best;
+            }
+            if (j < nb) a.bound[(((size_t)e * a.n + tk) * a.Hkv + hkv) * a.stride + j] = best;
+        }
+    }
+    // every CTA of the cluster comes by here; the bounds are visible to all of them behind it
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    for (int tk = rank; tk < nq; tk += a.cluster) {
+        const size_t at = ((size_t)e * a.n + tk) * a.Hkv + hkv;
+        pick_blocks(a.bound + at * a.stride, nb, a.K, a.Kc, a.sel + ((size_t)a.B0 * a.n * a.Hkv + at) * a.Kc,
+                    reinterpret_cast<uint32_t *>(smem));
+        __syncthreads();
+    }
 }
 
 // ---------------------------------------------------------------- plans
 struct Plan {
     ByteArgs a;
     ByteTable st;
-    BoundArgs ba;
-    BoundTable bt;
+    SelectArgs ba;
+    SelectTable bt;
     bool any, pick;
     int NC;        // groups of 8 rows; 0: tiles
     int ctas, wpc;
@@ -761,7 +778,12 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
     const long long parts = longest * a.NWp / W + 2;
     p.cw = (int)std::min<long long>(CMB_MAXW, (parts + 7) / 8);
     if (pick) {
-        p.ba = {c->dig, a.bt, call.q, nullptr, nullptr, call.n, B0, c->Hq, c->Hkv, c->g, c->NB, call.topk, Kc, p.nbmax};
+        // CTAs per (sequence, kv head): as many as give every SM one, but a slab each
+        const int slabs = std::max(1, (p.nbmax + 31) / 32);
+        int cluster = 1;
+        while (cluster < SEL_CLUSTER && 2 * cluster <= slabs && (long long)a.nseq * c->Hkv * cluster < c->sm_count) cluster *= 2;
+        p.ba = {c->dig, a.bt, call.q, nullptr, nullptr, call.n, B0, c->Hq, c->Hkv, c->g, c->NB, call.topk, Kc, p.nbmax,
+                cluster, std::min(SLABS, (slabs + cluster - 1) / cluster)};
         p.bound_floats = (size_t)a.nseq * call.n * c->Hkv * p.nbmax;
     }
     return true;
@@ -774,18 +796,33 @@ cudaError_t launch_rows(const Plan &p, cudaStream_t s) {
 }
 
 template <int D>
+int select_smem(int slabs, int nb) {
+    return std::max(slabs * slab_bytes<D>() + SEL_THREADS / 32 * heads_bytes<D>(), pick_words(nb) * 4);
+}
+
+template <int D>
+cudaError_t launch_select(const ott_byte_cache *c, const Plan &p, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(p.a.nseq * c->Hkv * p.ba.cluster));
+    cfg.blockDim = dim3(SEL_THREADS);
+    cfg.dynamicSmemBytes = (size_t)select_smem<D>(p.ba.slabs, p.nbmax);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.ba.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, k_byte_select<D>, p.ba, p.bt);
+}
+
+template <int D>
 cudaError_t launch_plan(const ott_byte_cache *c, const Plan &p, cudaStream_t s) {
     cudaError_t e = cudaSuccess;
     if (p.NC == 0) return launch_byte_tiles(c, p.a, p.st, p.nC, p.whole, s);
-    if (p.pick) {
-        if (p.nbmax > 0)
-            e = launch_pdl(k_byte_bounds<D>, dim3((unsigned)((p.nbmax + BND_BLOCKS - 1) / BND_BLOCKS), (unsigned)(p.a.nseq * c->Hkv)),
-                           BND_THREADS, 0, s, p.ba, p.bt);
-        int th = ((p.nbmax + 1) / 2 + 31) / 32 * 32;
-        th = std::min(std::max(th, 32), SORT_THREADS);
-        if (e == cudaSuccess)
-            e = launch_pdl(k_byte_pick, dim3((unsigned)(p.a.nseq * p.a.n * c->Hkv)), th, (size_t)p.nbmax * 4, s, p.ba, p.bt);
-    }
+    if (p.pick) e = launch_select<D>(c, p, s);
     const bool i8 = c->format == OTT_BYTE_INT;
     if (e == cudaSuccess)
         e = p.NC == 1 ? (i8 ? launch_rows<D, 1, OTT_BYTE_INT>(p, s) : launch_rows<D, 1, OTT_BYTE_FLOAT>(p, s))
@@ -817,7 +854,9 @@ int pick_smem(const ott_byte_cache *c) { return c->smem_optin - 2048; }
 
 cudaError_t set_byte_attributes(const ott_byte_cache *c) {
     cudaError_t e = c->d == 128 ? set_attributes<128>(c->format) : set_attributes<64>(c->format);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_byte_pick, cudaFuncAttributeMaxDynamicSharedMemorySize, pick_smem(c));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(c->d == 128 ? k_byte_select<128> : k_byte_select<64>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, pick_smem(c));
     return e == cudaSuccess ? set_byte_tiles_attributes(c->d, c->format) : e;
 }
 
@@ -827,11 +866,11 @@ int run_byte_attn(const ott_byte_cache *c, const ByteCall &call, cudaStream_t s,
     int nb_all = 0;   // the most blocks of any sequence: the width of the lists that a caller gets
     for (int b = 0; b < c->B; ++b) nb_all = std::max(nb_all, c->T[b] / c->G);
     const int Kc = std::min(call.topk, nb_all);
-    if (Kc > 0 && (long long)nb_all * 4 > pick_smem(c)) return OTT_ERR_INVALID;
+    if (Kc > 0 && (nb_all > (1 << 20) || pick_words(nb_all) * 4 > pick_smem(c))) return OTT_ERR_INVALID;
     // With nothing to select, the call is the one over every block.
     ByteCall cl = call;
     if (Kc == 0) cl.topk = 0;
-    if ((long long)c->Hq * cl.n > INT_MAX || (cl.topk > 0 && (long long)CHUNK_SEQS * c->Hkv * cl.n > INT_MAX))
+    if ((long long)c->Hq * cl.n > INT_MAX || (cl.topk > 0 && (long long)CHUNK_SEQS * c->Hkv * SEL_CLUSTER > INT_MAX))
         return OTT_ERR_INVALID;
     const int passes = (c->B + CHUNK_SEQS - 1) / CHUNK_SEQS;
     size_t floats = 0, parts = 0, bounds = 0;
@@ -839,7 +878,6 @@ int run_byte_attn(const ott_byte_cache *c, const ByteCall &call, cudaStream_t s,
     Plan p;
     for (int x = 0; x < passes; ++x) {   // every pass is checked before the first is queued
         if (!plan(x, p)) return OTT_ERR_INVALID;
-        if (p.NC > 0 && ((long long)p.a.nseq * c->Hkv > 65535 && cl.topk > 0)) return OTT_ERR_INVALID;   // a grid dimension
         parts = std::max(parts, p.part_floats);
         bounds = std::max(bounds, p.bound_floats);
     }

@@ -16,127 +16,146 @@ __device__ __forceinline__ uint32_t ordered(float f) {
     return (x & 0x80000000u) ? ~x : (x | 0x80000000u);
 }
 
-// Exclusive prefix sum of v over the threads of the CTA (in thread order);
-// `total` receives the sum over all threads. ws: 32 ints of shared memory.
-__device__ __forceinline__ int block_exscan(int v, int *ws, int &total) {
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
-    int x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) ws[wid] = x;
-    __syncthreads();
-    if (wid == 0) {
-        int t = lane < nw ? ws[lane] : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, t, o);
-            if (lane >= o) t += y;
-        }
-        ws[lane] = t;
-    }
-    __syncthreads();
-    total = ws[nw - 1];
-    const int r = (wid > 0 ? ws[wid - 1] : 0) + x - v;
-    __syncthreads();   // ws is reused by the next call
-    return r;
-}
-
-// The selection among n bounds (-inf: an empty block), by a CTA: the first min(K,
-// non-empty) into out[0 .. Kc), -1 behind them, by an exact radix select: key_j = the bit-inverted ordered
-// bound (smallest key = largest bound). Four rounds over 8-bit digits, most
-// significant first, each a histogram of the keys that still match the
-// digits found so far, give the key tau of the need-th smallest key and the
-// number `take` of keys equal to tau that belong to the selection. The
-// selection is every key below tau and the `take` lowest-indexed keys equal
-// to tau: exactly the first min(K, non-empty) blocks under (bound
-// descending, index ascending). A prefix count gives each its slot in
-// ascending block order.
 constexpr uint32_t EMPTY = 0xffffffffu;           // key of an empty block
 
-// key: n words of shared memory.
+// Words of shared memory for a selection among n blocks.
+__host__ __device__ constexpr int pick_words(int n) { return n + 2 * ((n + 31) / 32); }
+
+// The selection among n bounds (-inf: an empty block), by a CTA of whole
+// warps: the first min(K, non-empty) under (bound descending, index ascending),
+// into out[0 .. Kc) in ascending order, -1 behind them. An exact radix select:
+// key_j = the bit-inverted ordered bound (smallest key = largest bound). The
+// bits above the highest one in which keys differ are known (bounds are of
+// one magnitude: a first histogram over sign and exponent would put all keys
+// into a few bins, whose atomics go one after another). Rounds over 8-bit
+// digits below them, each a histogram of the keys that match the digits found
+// so far, end when every key that still matches is selected. Two counts
+// per 32 keys (selected, and equal to the last prefix) and their prefix sums
+// give each selected block its place.
 __device__ __forceinline__ void pick_blocks(const float *bd, int n, int K, int Kc, int32_t *out, uint32_t *key) {
     __shared__ int hist[256];
-    __shared__ int ws[32];
-    __shared__ int s_digit, s_below;
-    const int tid = threadIdx.x, nth = blockDim.x;
-    // a contiguous chunk of blocks per thread, so that prefix counts follow block order
-    const int chunk = (n + nth - 1) / nth, jb = min(n, tid * chunk), je = min(n, jb + chunk);
-    int ne_local = 0;
-    for (int j = jb; j < je; ++j) {
+    __shared__ uint32_t red[3][SORT_THREADS / 32];
+    __shared__ int s_digit, s_below, s_count;
+    const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, wid = tid >> 5, nseg = (n + 31) / 32;
+    int *const below = reinterpret_cast<int *>(key + n), *const equal = below + nseg;
+    uint32_t all = EMPTY, any = 0;
+    int ne = 0;
+    for (int j = tid; j < n; j += nth) {
         const float f = bd[j];
-        const bool nonempty = f != -CUDART_INF_F;
-        key[j] = nonempty ? ~ordered(f) : EMPTY;   // a finite bound never maps to EMPTY
-        ne_local += nonempty;
+        uint32_t k = EMPTY;
+        if (f != -CUDART_INF_F) {
+            k = ~ordered(f);   // a finite bound never maps to EMPTY
+            all &= k;
+            any |= k;
+            ++ne;
+        }
+        key[j] = k;
     }
-    int ne;
-    block_exscan(ne_local, ws, ne);
+    all = __reduce_and_sync(0xffffffffu, all);
+    any = __reduce_or_sync(0xffffffffu, any);
+    ne = __reduce_add_sync(0xffffffffu, ne);
+    if (lane == 0) {
+        red[0][wid] = all;
+        red[1][wid] = any;
+        red[2][wid] = (uint32_t)ne;
+    }
+    __syncthreads();
+    ne = 0;
+    for (int w = 0; w < nth / 32; ++w) {
+        all &= red[0][w];
+        any |= red[1][w];
+        ne += (int)red[2][w];
+    }
     const int want = min(K, ne);
-    uint32_t prefix = 0, mask = 0;
-    int need = want;
-    for (int shift = 24; shift >= 0 && want > 0; shift -= 8) {
+    int left = 32 - __clz(all ^ any);   // bits that are not known yet
+    uint32_t mask = left == 32 ? 0u : 0xffffffffu << left, prefix = all & mask;
+    // the first `need` of the `cnt` keys that match the prefix are selected, and all keys below it
+    int need = want, cnt = ne;
+    while (left > 0 && need < cnt) {
+        const int bits = min(8, left), shift = left - bits;
+        const uint32_t digit = (1u << bits) - 1u;
         for (int i = tid; i < 256; i += nth) hist[i] = 0;
         __syncthreads();
-        for (int j = jb; j < je; ++j) {
+        for (int j = tid; j < n; j += nth) {
             const uint32_t k = key[j];
-            if (k != EMPTY && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+            if (k != EMPTY && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1);
         }
         __syncthreads();
-        if (tid < 32) {
+        if (wid == 0) {
             // lane l owns digits 8l .. 8l+7
-            int cnt[8], sum = 0;
+            int c[8], sum = 0;
 #pragma unroll
             for (int x = 0; x < 8; ++x) {
-                cnt[x] = hist[8 * tid + x];
-                sum += cnt[x];
+                c[x] = hist[8 * lane + x];
+                sum += c[x];
             }
             int incl = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                if (tid >= o) incl += y;
+                if (lane >= o) incl += y;
             }
-            const int excl = incl - sum;
-            if (excl < need && need <= incl) {   // exactly one lane
-                int c = excl, dg = 8 * tid;
+            int run = incl - sum;
+            if (run < need && need <= incl) {   // exactly one lane
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    if (c + cnt[x] >= need) {
-                        dg = 8 * tid + x;
-                        break;
+                    if (run < need && need <= run + c[x]) {
+                        s_digit = 8 * lane + x;
+                        s_below = run;
+                        s_count = c[x];
                     }
-                    c += cnt[x];
+                    run += c[x];
                 }
-                s_digit = dg;
-                s_below = c;
             }
         }
         __syncthreads();
         prefix |= (uint32_t)s_digit << shift;
-        mask |= 255u << shift;
+        mask |= digit << shift;
         need -= s_below;
-        __syncthreads();
+        cnt = s_count;
+        left = shift;
     }
-    // keys equal to tau = prefix: the `need` lowest-indexed ones are taken
-    int eq_local = 0;
-    for (int j = jb; j < je; ++j) eq_local += want > 0 && key[j] != EMPTY && key[j] == prefix;
-    int eq_total;
-    int eq_before = block_exscan(eq_local, ws, eq_total);
-    int sel_local = 0;
-    for (int j = jb; j < je; ++j) {
-        const uint32_t k = key[j];
-        const bool ok = want > 0 && k != EMPTY;
-        const bool take = ok && (k < prefix || (k == prefix && eq_before++ < need));
-        key[j] = take ? 1u : 0u;                   // reused as the selection mark
-        sel_local += take;
+    // (all threads of a warp together: nth and the segments are multiples of 32)
+    for (int j = tid; j < 32 * nseg; j += nth) {
+        const uint32_t k = j < n ? key[j] : EMPTY, m = k & mask;
+        const unsigned lt = __ballot_sync(0xffffffffu, k != EMPTY && m < prefix), eq = __ballot_sync(0xffffffffu, k != EMPTY && m == prefix);
+        if (lane == 0) {
+            below[j / 32] = __popc(lt);
+            equal[j / 32] = __popc(eq);
+        }
     }
-    int nsel;
-    int pos = block_exscan(sel_local, ws, nsel);
-    for (int j = jb; j < je; ++j)
-        if (key[j]) out[pos++] = j;
-    for (int i = nsel + tid; i < Kc; i += nth) out[i] = -1;
+    __syncthreads();
+    if (wid == 0) {
+        int lt0 = 0, eq0 = 0;
+        for (int x = 0; x < nseg; x += 32) {
+            const int lt = x + lane < nseg ? below[x + lane] : 0, eq = x + lane < nseg ? equal[x + lane] : 0;
+            int a = lt, b = eq;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, a, o), z = __shfl_up_sync(0xffffffffu, b, o);
+                if (lane >= o) {
+                    a += y;
+                    b += z;
+                }
+            }
+            if (x + lane < nseg) {
+                below[x + lane] = lt0 + a - lt;
+                equal[x + lane] = eq0 + b - eq;
+            }
+            lt0 += __shfl_sync(0xffffffffu, a, 31);
+            eq0 += __shfl_sync(0xffffffffu, b, 31);
+        }
+    }
+    __syncthreads();
+    const unsigned before = (1u << lane) - 1u;
+    for (int j = tid; j < 32 * nseg; j += nth) {
+        const uint32_t k = j < n ? key[j] : EMPTY, m = k & mask;
+        const bool l = k != EMPTY && m < prefix, e = k != EMPTY && m == prefix;
+        const unsigned lt = __ballot_sync(0xffffffffu, l), eq = __ballot_sync(0xffffffffu, e);
+        const int nl = below[j / 32] + __popc(lt & before), nq = equal[j / 32] + __popc(eq & before);
+        if (l || (e && nq < need)) out[nl + min(nq, need)] = j;
+    }
+    for (int i = want + tid; i < Kc; i += nth) out[i] = -1;
 }
 
 }  // namespace

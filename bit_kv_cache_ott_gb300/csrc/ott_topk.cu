@@ -21,9 +21,9 @@
 //     threads of a warp, each reading one channel of its own block, hit
 //     different banks. Thread (block, head) then sums its bound in channel
 //     order; the block's bound is the largest over its heads.
-//   k_topk_pick: a CTA per unit. An exact radix select over the bounds (four
-//     8-bit histogram rounds) finds the first min(K, non-empty blocks) under
-//     (bound descending, index ascending); a prefix count writes them to
+//   k_topk_pick: a CTA per unit. An exact radix select over the bounds
+//     (ott_select.cuh) finds the first min(K, non-empty blocks) under (bound
+//     descending, index ascending); a prefix count writes them to
 //     sel[u][0..Kc) in ascending block order (-1 in the slots left over).
 #include <math_constants.h>
 
@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(BND_THREADS) k_topk_bounds(TopkArgs a, const _
 }
 
 __global__ void __launch_bounds__(SORT_THREADS) k_topk_pick(TopkArgs a, const __grid_constant__ NfTable nt) {
-    extern __shared__ uint32_t key[];              // [nf]
+    extern __shared__ uint32_t key[];              // pick_words(nf)
     // the decode may be scheduled now; it waits for the selection
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int u = blockIdx.x;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(SORT_THREADS) k_topk_pick(TopkArgs a, const __
 int topk_smem_bytes(int d, int gs, int nf) {
     (void)d;
     (void)gs;
-    return (nf > 1 ? nf : 1) * 4;
+    return pick_words(nf > 1 ? nf : 1) * 4;
 }
 
 cudaError_t launch_topk_select(const ott_cache *c, const __half *q, int K, int Kc, cudaStream_t s) {
