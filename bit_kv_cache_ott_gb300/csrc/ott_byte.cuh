@@ -99,7 +99,7 @@ struct ByteArgs {
     int SG;                    // selected blocks: slices of heads per token
     int RB;                    // rows per slice
     long long W;               // work items
-    int NWp, MAXU, RV;         // active warps, units that a warp's range can touch, rows of a partial
+    int NWp, wpc, MAXU, RV;    // active warps, warps per CTA, units that a warp's range can touch, rows of a partial
     float sl2;                 // log2(e) / sqrt(d)
 };
 

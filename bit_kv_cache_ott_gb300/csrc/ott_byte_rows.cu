@@ -78,11 +78,11 @@ template <int D, int NC>
 struct RowsCfg {
     static constexpr int NKS = D / 16, PP = D / 64;
     static constexpr int WARPS = 8, NST = 3;
-    static constexpr int RS = D + 8;                       // padded fp16 row (halves)
     static constexpr int ITEM = QT * 2 * D;                // bytes of a block's item
-    static constexpr int STAGE = 2 * FT * RS * 2;          // fp16 rows; a block's item and its record fit, too
+    static constexpr int STAGE = ITEM + 128;               // with its record; 16 fp16 tokens fit, too
+    static_assert(2 * FT * D * 2 <= ITEM, "fp16 items");
     static constexpr int WARP_SMEM = NST * STAGE + 128;    // stages, barriers, what each stage holds
-    static_assert(ITEM + 16 <= STAGE && STAGE % 128 == 0 && NST * 8 <= 64, "stages");
+    static_assert(STAGE % 128 == 0 && NST * 8 <= 64, "stages");
     static_assert(WARP_SMEM * WARPS <= 227 * 1024, "shared memory");
 };
 
@@ -128,6 +128,13 @@ __device__ __forceinline__ int entry_of(const ByteTable &st, int nseq, long long
     return lo;
 }
 
+// Items x0 .. x1 - 1 (x0 < x1) are of one unit.
+__device__ __forceinline__ bool one_unit(const ByteArgs &a, const ByteTable &st, long long x0, long long x1) {
+    const int e = entry_of(st, a.nseq, x0);
+    const unsigned Iu = (unsigned)st.e[e].Iu, rel = (unsigned)(x0 - st.e[e].base);
+    return x1 <= st.e[e].base + (long long)(rel / Iu + 1) * Iu;
+}
+
 // Rows of slice sl of an entry: first row, number of rows (a row is token * g + head).
 __device__ __forceinline__ void slice_rows(const ByteArgs &a, const ByteSeq &s, int sl, int &v0, int &cnt) {
     if (a.sel) {
@@ -144,7 +151,7 @@ template <int D, int NC, int FMT>
 __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     k_byte_rows(const __grid_constant__ ByteArgs a, const __grid_constant__ ByteTable st) {
     using C = RowsCfg<D, NC>;
-    constexpr int NKS = C::NKS, PP = C::PP, NST = C::NST, RS = C::RS;
+    constexpr int NKS = C::NKS, PP = C::PP, NST = C::NST;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, i = lane & 3;
     const int rot = D == 128 ? 8 * (i >> 1) : 0;
@@ -155,9 +162,18 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int gw = warp * gridDim.x + blockIdx.x;   // warp indices dealt across the CTAs first
-    if (gw >= a.NWp) return;
+    const int wpc = blockDim.x >> 5, gw = blockIdx.x * wpc + warp;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // A CTA whose warps all work for one unit merges their results.
+    bool merge = false;
+    if (wpc > 1) {
+        const int g1 = min(a.NWp, (int)(blockIdx.x + 1) * wpc);
+        merge = g1 > (int)blockIdx.x * wpc && one_unit(a, st, ch_range_start(a.W, a.NWp, blockIdx.x * wpc), ch_range_start(a.W, a.NWp, g1));
+    }
+    if (gw >= a.NWp) {   // the last CTA may have warps to spare
+        if (merge) __syncthreads();
+        return;
+    }
     const long long x0 = ch_range_start(a.W, a.NWp, gw), x1 = ch_range_start(a.W, a.NWp, gw + 1);
 
     Cursor ic;
@@ -189,13 +205,14 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
             const bool fresh = c.off >= s.Ft;
             const int f0 = (fresh ? c.off - s.Ft : c.off) * FT;
             m = min(FT, (fresh ? s.nq : s.T % a.G) - f0);
-            const __half *src = fresh ? (lane < FT ? a.k : a.v) + ((size_t)u * a.n + f0) * D
-                                      : (lane < FT ? a.tk : a.tv) + ((size_t)u * a.G + f0) * D;
-            if (lane == 0) expect_tx(&bars[sg], 2 * FT * D * 2);
-            __syncwarp();
-            // rows past the end repeat the first (finite values under a zero weight)
-            const int x = lane & (FT - 1);
-            bulk_copy(dst + (size_t)lane * RS * 2, src + (size_t)(x < m ? x : 0) * D, D * 2, &bars[sg]);
+            // Two copies; the rows past the end keep what the stage held, and are masked where they are read. (A copy per
+            // row, to padded rows, spared bank conflicts and cost a warp about 5,000 cycles an item.)
+            if (lane == 0) {
+                const size_t at = (fresh ? (size_t)u * a.n + f0 : (size_t)u * a.G + f0) * D;
+                expect_tx(&bars[sg], (uint32_t)m * (2 * D * 2));
+                bulk_copy(dst, (fresh ? a.k : a.tk) + at, (uint32_t)m * (D * 2), &bars[sg]);
+                bulk_copy(dst + FT * D * 2, (fresh ? a.v : a.tv) + at, (uint32_t)m * (D * 2), &bars[sg]);
+            }
         } else {
             if (c.jp < slots_from || c.jp >= slots_from + 32) {
                 slots_from = c.jp;
@@ -347,6 +364,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 // let the other copies in flight land before giving up the buffers
                 for (int x = 0; x < NST; ++x)
                     if (x != sg) mbar_wait(&bars[x], (phase >> x) & 1u);
+                if (merge) __syncthreads();   // the others' barrier
                 return;
             }
             phase ^= 1u << sg;
@@ -354,15 +372,15 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 // 16 fp16 tokens: of the open block, or new ones (causal)
                 const bool fresh = cc.off >= s.Ft;
                 const int f0 = (fresh ? cc.off - s.Ft : cc.off) * FT;
-                const __half *kr = reinterpret_cast<const __half *>(stage), *vr = kr + FT * RS;
+                const __half *kr = reinterpret_cast<const __half *>(stage), *vr = kr + FT * D;
                 float d[NC][4], mx[NC][2];
 #pragma unroll
                 for (int nc = 0; nc < NC; ++nc) d[nc][0] = d[nc][1] = d[nc][2] = d[nc][3] = 0.0f;
 #pragma unroll
                 for (int ks = 0; ks < NKS; ks += 2) {
                     const int ch = (D / 4) * i + 16 * (ks >> 2) + ((4 * (ks & 3)) ^ rot);
-                    const uint4 x = *reinterpret_cast<const uint4 *>(kr + r * RS + ch);
-                    const uint4 y = *reinterpret_cast<const uint4 *>(kr + (r + 8) * RS + ch);
+                    const uint4 x = *reinterpret_cast<const uint4 *>(kr + r * D + ch);
+                    const uint4 y = *reinterpret_cast<const uint4 *>(kr + (r + 8) * D + ch);
 #pragma unroll
                     for (int nc = 0; nc < NC; ++nc) {
                         mma16816(d[nc], x.x, y.x, x.y, y.y, Bq[nc][ks][0], Bq[nc][ks][1]);
@@ -384,10 +402,17 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 uint32_t bp[NC][2];
 #pragma unroll
                 for (int nc = 0; nc < NC; ++nc) weights(d[nc], nc, 1.0f, bp[nc][0], bp[nc][1]);
+                // values of tokens 2i, 2i + 1 (+ 8) that there are
+                auto halves = [&](int t) { return (t < valid ? 0xffffu : 0u) | (t + 1 < valid ? 0xffff0000u : 0u); };
+                const uint32_t keep0 = halves(2 * i), keep1 = halves(2 * i + 8);
 #pragma unroll
                 for (int mt = 0; mt < NKS; ++mt) {
                     uint32_t f[4];   // (channels, tokens): (0..7, 0..7), (8..15, 0..7), (0..7, 8..15), (8..15, 8..15)
-                    ldsm_x4_t(f, vr + ((lane & 7) + 8 * (lane >> 4)) * RS + 16 * mt + 8 * (lane >> 3 & 1));
+                    ldsm_x4_t(f, vr + ((lane & 7) + 8 * (lane >> 4)) * D + 16 * mt + 8 * (lane >> 3 & 1));
+                    f[0] &= keep0;
+                    f[1] &= keep0;
+                    f[2] &= keep1;
+                    f[3] &= keep1;
 #pragma unroll
                     for (int nc = 0; nc < NC; ++nc) mma16816(acc[nc][mt], f[0], f[1], f[2], f[3], bp[nc][0], bp[nc][1]);
                 }
@@ -458,10 +483,52 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
         }
         const bool other = cc.next(a, st);
         sg = sg + 1 == NST ? 0 : sg + 1;
+        if (merge) continue;
         if (other || cc.x >= x1) {
             end_unit();
             if (cc.x < x1) begin_unit(cc);
         }
+    }
+    if (!merge) return;
+    // Every warp's largest z and sum, then its output at the common reference,
+    // in its first stage (its copies have all been read).
+    float *const own = reinterpret_cast<float *>(stg);
+#pragma unroll
+    for (int nc = 0; nc < NC; ++nc)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            float l = l_run[nc][x];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const int col = 8 * nc + 2 * i + x;
+            if (r == 0) *reinterpret_cast<float2 *>(own + col * (D + 2)) = make_float2(m_run[nc][x], l);
+#pragma unroll
+            for (int mt = 0; mt < NKS; ++mt) {
+                own[col * (D + 2) + 2 + 16 * mt + r] = acc[nc][mt][x];
+                own[col * (D + 2) + 2 + 16 * mt + r + 8] = acc[nc][mt][2 + x];
+            }
+        }
+    __syncthreads();
+    const int nw = min(wpc, a.NWp - (int)blockIdx.x * wpc);
+    float *const pb = a.part + (size_t)(blockIdx.x * wpc) * a.MAXU * a.RV * (D + 2);
+    for (int col = warp; col < cnt_rows; col += nw) {
+        float M = -CUDART_INF_F, L = 0.0f, o[D / 32];
+        for (int w = 0; w < nw; ++w) M = fmaxf(M, reinterpret_cast<const float *>(smem + (size_t)w * C::WARP_SMEM)[col * (D + 2)]);
+        const float mr = M == -CUDART_INF_F ? 0.0f : M;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) o[c] = 0.0f;
+        for (int w = 0; w < nw; ++w) {
+            const float *p = reinterpret_cast<const float *>(smem + (size_t)w * C::WARP_SMEM) + col * (D + 2);
+            const float sw = ch_ex2(p[0] - mr);   // 0 where nothing was seen
+            L = fmaf(sw, p[1], L);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) o[c] = fmaf(sw, p[2 + 32 * c + lane], o[c]);
+        }
+        float *p = pb + (size_t)col * (D + 2);
+        if (lane == 0) *reinterpret_cast<float2 *>(p) = make_float2(M, L);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) p[2 + 32 * c + lane] = o[c];
     }
 }
 
@@ -477,7 +544,8 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
     const ByteSeq &s = st.e[blockIdx.y];
     const int hq = blockIdx.x / a.n, tk = blockIdx.x % a.n;
     const bool row = tk < s.nq;
-    int wa = 0, wb = -1, uo_a = 0, col = 0;
+    int wa = 0, wb = -1, uo_a = 0, col = 0, n0 = 0, n01 = 0, parts = 0;
+    int first = 0, inner = 0, last = 0;   // where the parts of the unit's first CTA, of the inner ones, and of the last begin
     if (row) {   // the plan, while the rows kernel still runs
         const int hd = hq % a.g, v = a.sel ? hd : tk * a.g + hd;
         const int sl = a.sel ? tk * a.SG + hd / a.RB : v / a.RB, h = hq / a.g * s.S + sl;
@@ -489,6 +557,20 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
         const long long xa = ch_range_start(a.W, a.NWp, wa);
         const int ea = entry_of(st, a.nseq, xa);
         uo_a = s.ubase + h - (st.e[ea].ubase + (int)((unsigned)(xa - st.e[ea].base) / (unsigned)st.e[ea].Iu));
+        // The unit's parts: one of each CTA that merged its warps (all of whose items are the unit's), else one of each warp.
+        const int ca = wa / a.wpc, cb = wb / a.wpc;
+        auto merged = [&](int c) {
+            return a.wpc > 1 && ch_range_start(a.W, a.NWp, (long long)c * a.wpc) >= ub &&
+                   ch_range_start(a.W, a.NWp, min(a.NWp, (c + 1) * a.wpc)) <= ue;
+        };
+        const bool ma = merged(ca), mb = ca == cb ? ma : merged(cb);
+        first = ma ? ca * a.wpc : wa;
+        inner = (ca + 1) * a.wpc;
+        last = cb * a.wpc;
+        if (ma) uo_a = 0;
+        n0 = ma ? 1 : min(wb + 1, inner) - wa;
+        n01 = n0 + max(0, cb - ca - 1);
+        parts = n01 + (ca == cb ? 0 : mb ? 1 : wb - last + 1);
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -496,7 +578,7 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
     float M = -CUDART_INF_F, L = 0.0f, acc[CPL];
 #pragma unroll
     for (int c = 0; c < CPL; ++c) acc[c] = 0.0f;
-    for (int k0 = wa + wi * GRP; k0 <= wb; k0 += cw * GRP) {
+    for (int k0 = wi * GRP; k0 < parts; k0 += cw * GRP) {
         float ms[GRP], ls[GRP], vs[GRP][CPL];
 #pragma unroll
         for (int x = 0; x < GRP; ++x) {
@@ -504,9 +586,10 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
             ls[x] = 0.0f;
 #pragma unroll
             for (int c = 0; c < CPL; ++c) vs[x][c] = 0.0f;
-            const int w = k0 + x;
-            if (w <= wb) {
-                const float *p = a.part + (((size_t)w * a.MAXU + (w == wa ? uo_a : 0)) * a.RV + col) * (D + 2);
+            const int k = k0 + x;
+            if (k < parts) {
+                const int w = k < n0 ? first + k : k < n01 ? inner + (k - n0) * a.wpc : last + (k - n01);
+                const float *p = a.part + (((size_t)w * a.MAXU + (k == 0 ? uo_a : 0)) * a.RV + col) * (D + 2);
                 ms[x] = p[0];
                 ls[x] = p[1];
 #pragma unroll
@@ -569,34 +652,35 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
 }
 
 // ---------------------------------------------------------------- selection
-// A cluster of up to 8 CTAs per (sequence, kv head) takes the bounds of its
+// A cluster of up to 16 CTAs per (sequence, kv head) takes the bounds of its
 // blocks for every token of the sequence, and then, one token per CTA, the
 // selection.
 // A slab is 32 blocks' channel ranges in shared memory (16-byte pieces turned
 // by the block, so that 8 lanes that read one piece of their own blocks meet
-// all banks). A warp takes a (slab, token): lane = block, four query heads
-// at a time as two packed pairs. max(q lo, q hi) is (q > 0 ? q hi : q lo), which
-// two multiply-adds with the positive and the negative part of q give with
-// one rounding, the sum's (products of two fp16 numbers are exact, and one
-// of the two is zero): two operations per channel for two heads.
-constexpr int SEL_THREADS = 256, SLABS = 8, SEL_CLUSTER = 8;
+// all banks). A warp takes a (slab, token, four of its heads): a lane per
+// block. max(q lo, q hi) is q hi for positive q, else q lo, and products of
+// two fp16 numbers are exact: a selection and a multiply-add, which rounds
+// once, as the sum does. A warp alone on its scheduler needs some 30 cycles
+// per channel; with few tasks that latency is what counts (two blocks per
+// lane: fewer operations in all, but 55 cycles), with many the operations.
+constexpr int SEL_THREADS = 512, SLAB = 32, SLABS = 8, SEL_CLUSTER = 16;
 
 struct SelectArgs {
     const __half2 *dig;
     const int32_t *bt;
     const __half *q;
-    float *bound;       // [nseq][n][Hkv][stride]
+    float *bound;       // [nseq][n][Hkv][groups][stride]: by four heads
     int32_t *sel;       // [B][n][Hkv][Kc]
     int n, B0, Hq, Hkv, g, NB, K, Kc, stride;
-    int cluster, slabs;   // CTAs per (sequence, kv head), slabs in shared memory at a time
+    int groups, cluster, slabs;   // groups of four heads per kv head; CTAs per (sequence, kv head), slabs in shared memory at a time
 };
 struct SelectTable {
     int nb[CHUNK_SEQS], nq[CHUNK_SEQS];
 };
 template <int D>
-__host__ __device__ constexpr int slab_bytes() { return 32 * D * 4; }
+__host__ __device__ constexpr int slab_bytes() { return SLAB * D * 4; }
 template <int D>
-__host__ __device__ constexpr int heads_bytes() { return 2 * D * 16; }   // four heads: (q0+, q1+, q0-, q1-) per channel, twice
+__host__ __device__ constexpr int heads_bytes() { return D * 16; }   // four heads per channel
 
 template <int D>
 __global__ void __launch_bounds__(SEL_THREADS)
@@ -607,15 +691,15 @@ __global__ void __launch_bounds__(SEL_THREADS)
     const int rank = blockIdx.x % a.cluster, unit = blockIdx.x / a.cluster, e = unit / a.Hkv, hkv = unit % a.Hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int u = (a.B0 + e) * a.Hkv + hkv, nb = t.nb[e], nq = t.nq[e];
-    const int all = (nb + 31) / 32, per = (all + a.cluster - 1) / a.cluster, s0 = min(all, rank * per),
+    const int all = (nb + SLAB - 1) / SLAB, per = (all + a.cluster - 1) / a.cluster, s0 = min(all, rank * per),
               s1 = nq > 0 ? min(all, s0 + per) : s0;
     float4 *const heads = reinterpret_cast<float4 *>(smem + a.slabs * slab_bytes<D>() + warp * heads_bytes<D>());
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int sb = s0; sb < s1; sb += a.slabs) {
         const int ns = min(a.slabs, s1 - sb);
         if (sb > s0) __syncthreads();   // the slabs before are read
-        for (int z = threadIdx.x; z < ns * 32 * V4; z += SEL_THREADS) {
-            const int x = z / V4, v = z % V4, j = sb * 32 + x;
+        for (int z = threadIdx.x; z < ns * SLAB * V4; z += SEL_THREADS) {
+            const int x = z / V4, v = z % V4, j = sb * SLAB + x;
             if (j < nb) {
                 const size_t own = (size_t)u * a.NB + j, slot = a.bt ? (size_t)__ldg(a.bt + own) : own;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ch_smem(smem + x * (D * 4) + ((v ^ (x & 7)) << 4))),
@@ -625,49 +709,45 @@ __global__ void __launch_bounds__(SEL_THREADS)
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
-        for (int task = warp; task < ns * nq; task += WARPS) {
-            const int x = task % ns, tk = task / ns, j = (sb + x) * 32 + lane;
-            const uint4 *row = reinterpret_cast<const uint4 *>(smem + (x * 32 + lane) * (D * 4));
+        for (int task = warp; task < ns * nq * a.groups; task += WARPS) {
+            const int x = task % ns, tk = task / ns / a.groups, grp = task / ns % a.groups, j = (sb + x) * SLAB + lane;
+            const uint4 *row = reinterpret_cast<const uint4 *>(smem + (x * SLAB + lane) * (D * 4));
             const __half *q = a.q + (((size_t)(a.B0 + e) * a.Hq + hkv * a.g) * a.n + tk) * D;
-            float best = -CUDART_INF_F;
-            for (int h0 = 0; h0 < a.g; h0 += 4) {   // a short last round repeats its last head
-                __syncwarp();
+            __half qv[4][D / 32];   // a short last group repeats its last head
 #pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const __half *q0 = q + (size_t)min(h0 + 2 * p, a.g - 1) * a.n * D, *q1 = q + (size_t)min(h0 + 2 * p + 1, a.g - 1) * a.n * D;
+            for (int p = 0; p < 4; ++p)
 #pragma unroll
-                    for (int c = lane; c < D; c += 32) {
-                        const float f0 = __half2float(__ldg(q0 + c)), f1 = __half2float(__ldg(q1 + c));
-                        heads[p * D + c] = make_float4(fmaxf(f0, 0.0f), fmaxf(f1, 0.0f), fminf(f0, 0.0f), fminf(f1, 0.0f));
-                    }
-                }
-                __syncwarp();
-                float2 s01 = make_float2(0.0f, 0.0f), s23 = s01;
+                for (int y = 0; y < D / 32; ++y) qv[p][y] = __ldg(q + (size_t)min(4 * grp + p, a.g - 1) * a.n * D + 32 * y + lane);
+            __syncwarp();
+#pragma unroll
+            for (int y = 0; y < D / 32; ++y)
+                heads[32 * y + lane] = make_float4(__half2float(qv[0][y]), __half2float(qv[1][y]), __half2float(qv[2][y]), __half2float(qv[3][y]));
+            __syncwarp();
+            float sum[4] = {};
 #pragma unroll 4
-                for (int c4 = 0; c4 < V4; ++c4) {
-                    const uint4 d = row[c4 ^ (lane & 7)];
-                    const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+            for (int c4 = 0; c4 < V4; ++c4) {
+                const uint4 d = row[c4 ^ (lane & 7)];
+                const uint32_t w[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        const float2 f = __half22float2(ch_as_h2(w[y])), lo = make_float2(f.x, f.x), up = make_float2(f.y, f.y);
-                        const float4 p = heads[4 * c4 + y], r = heads[D + 4 * c4 + y];
-                        s01 = __ffma2_rn(make_float2(p.z, p.w), lo, __ffma2_rn(make_float2(p.x, p.y), up, s01));
-                        s23 = __ffma2_rn(make_float2(r.z, r.w), lo, __ffma2_rn(make_float2(r.x, r.y), up, s23));
-                    }
+                for (int y = 0; y < 4; ++y) {
+                    const float4 q4 = heads[4 * c4 + y];
+                    const float qs[4] = {q4.x, q4.y, q4.z, q4.w};
+                    const float2 f = __half22float2(ch_as_h2(w[y]));
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) sum[p] = __fmaf_rn(qs[p], qs[p] > 0.0f ? f.y : f.x, sum[p]);
                 }
-                best = s01.x > best ? s01.x : best;
-                best = s01.y > best ? s01.y : best;
-                best = s23.x > best ? s23.x : best;
-                best = s23.y > best ? s23.y : best;
             }
-            if (j < nb) a.bound[(((size_t)e * a.n + tk) * a.Hkv + hkv) * a.stride + j] = best;
+            float best = -CUDART_INF_F;
+#pragma unroll
+            for (int p = 0; p < 4; ++p) best = sum[p] > best ? sum[p] : best;
+            if (j < nb) a.bound[((((size_t)e * a.n + tk) * a.Hkv + hkv) * a.groups + grp) * a.stride + j] = best;
         }
     }
     // every CTA of the cluster comes by here; the bounds are visible to all of them behind it
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
     for (int tk = rank; tk < nq; tk += a.cluster) {
         const size_t at = ((size_t)e * a.n + tk) * a.Hkv + hkv;
-        pick_blocks(a.bound + at * a.stride, nb, a.K, a.Kc, a.sel + ((size_t)a.B0 * a.n * a.Hkv + at) * a.Kc,
+        pick_blocks(a.bound + at * a.groups * a.stride, a.groups, a.stride, nb, a.K, a.Kc, a.sel + ((size_t)a.B0 * a.n * a.Hkv + at) * a.Kc,
                     reinterpret_cast<uint32_t *>(smem));
         __syncthreads();
     }
@@ -681,7 +761,7 @@ struct Plan {
     SelectTable bt;
     bool any, pick;
     int NC;        // groups of 8 rows; 0: tiles
-    int ctas, wpc;
+    int ctas;
     int nC;        // tiles: CTAs
     bool whole;    // ... each with a tile of its own
     size_t part_floats, bound_floats;
@@ -765,7 +845,8 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
     while (ctas < (1 << 20) && W / ((long long)ctas * WARPS) >= SUM_TOKENS / QT) ctas += c->sm_count;
     a.NWp = (int)std::max<long long>(1, std::min<long long>((long long)ctas * WARPS, W / 2));
     p.ctas = (int)std::min<long long>(ctas, a.NWp);
-    p.wpc = (a.NWp + p.ctas - 1) / p.ctas;
+    a.wpc = (a.NWp + p.ctas - 1) / p.ctas;
+    p.ctas = (a.NWp + a.wpc - 1) / a.wpc;
     const long long run = (W + a.NWp - 1) / a.NWp;
     a.MAXU = (int)std::min<long long>((run - 1) / iu_min + 2, run);
     p.part_floats = (size_t)a.NWp * a.MAXU * a.RV * (c->d + 2);
@@ -775,16 +856,17 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
         for (int x = 0; x < a.nseq; ++x) m = std::max<long long>(m, p.st.e[x].S ? p.st.e[x].Iu : 0);
         return m;
     }();
-    const long long parts = longest * a.NWp / W + 2;
+    const long long parts = longest * a.NWp / W / a.wpc + 2 * a.wpc;
     p.cw = (int)std::min<long long>(CMB_MAXW, (parts + 7) / 8);
     if (pick) {
-        // CTAs per (sequence, kv head): as many as give every SM one, but a slab each
-        const int slabs = std::max(1, (p.nbmax + 31) / 32);
+        // CTAs per (sequence, kv head): as many as give every SM two, but a slab each
+        const int slabs = std::max(1, (p.nbmax + SLAB - 1) / SLAB);
         int cluster = 1;
-        while (cluster < SEL_CLUSTER && 2 * cluster <= slabs && (long long)a.nseq * c->Hkv * cluster < c->sm_count) cluster *= 2;
+        while (cluster < SEL_CLUSTER && 2 * cluster <= slabs && (long long)a.nseq * c->Hkv * cluster < 2 * c->sm_count)
+            cluster *= 2;
         p.ba = {c->dig, a.bt, call.q, nullptr, nullptr, call.n, B0, c->Hq, c->Hkv, c->g, c->NB, call.topk, Kc, p.nbmax,
-                cluster, std::min(SLABS, (slabs + cluster - 1) / cluster)};
-        p.bound_floats = (size_t)a.nseq * call.n * c->Hkv * p.nbmax;
+                (c->g + 3) / 4, cluster, std::min(SLABS, (slabs + cluster - 1) / cluster)};
+        p.bound_floats = (size_t)a.nseq * call.n * c->Hkv * ((c->g + 3) / 4) * p.nbmax;
     }
     return true;
 }
@@ -792,7 +874,7 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
 template <int D, int NC, int FMT>
 cudaError_t launch_rows(const Plan &p, cudaStream_t s) {
     using C = RowsCfg<D, NC>;
-    return launch_pdl(k_byte_rows<D, NC, FMT>, dim3((unsigned)p.ctas), p.wpc * 32, (size_t)C::WARP_SMEM * p.wpc, s, p.a, p.st);
+    return launch_pdl(k_byte_rows<D, NC, FMT>, dim3((unsigned)p.ctas), p.a.wpc * 32, (size_t)C::WARP_SMEM * p.a.wpc, s, p.a, p.st);
 }
 
 template <int D>
@@ -854,9 +936,9 @@ int pick_smem(const ott_byte_cache *c) { return c->smem_optin - 2048; }
 
 cudaError_t set_byte_attributes(const ott_byte_cache *c) {
     cudaError_t e = c->d == 128 ? set_attributes<128>(c->format) : set_attributes<64>(c->format);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(c->d == 128 ? k_byte_select<128> : k_byte_select<64>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, pick_smem(c));
+    auto *select = c->d == 128 ? k_byte_select<128> : k_byte_select<64>;
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, pick_smem(c));
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);   // 16 CTAs
     return e == cudaSuccess ? set_byte_tiles_attributes(c->d, c->format) : e;
 }
 

@@ -32,7 +32,8 @@ __host__ __device__ constexpr int pick_words(int n) { return n + 2 * ((n + 31) /
 // so far, end when every key that still matches is selected. Two counts
 // per 32 keys (selected, and equal to the last prefix) and their prefix sums
 // give each selected block its place.
-__device__ __forceinline__ void pick_blocks(const float *bd, int n, int K, int Kc, int32_t *out, uint32_t *key) {
+// The bounds: the largest of bd[j], bd[stride + j] .. of `groups` of them.
+__device__ __forceinline__ void pick_blocks(const float *bd, int groups, int stride, int n, int K, int Kc, int32_t *out, uint32_t *key) {
     __shared__ int hist[256];
     __shared__ uint32_t red[3][SORT_THREADS / 32];
     __shared__ int s_digit, s_below, s_count;
@@ -40,16 +41,29 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int n, int K, int K
     int *const below = reinterpret_cast<int *>(key + n), *const equal = below + nseg;
     uint32_t all = EMPTY, any = 0;
     int ne = 0;
-    for (int j = tid; j < n; j += nth) {
-        const float f = bd[j];
-        uint32_t k = EMPTY;
-        if (f != -CUDART_INF_F) {
-            k = ~ordered(f);   // a finite bound never maps to EMPTY
-            all &= k;
-            any |= k;
-            ++ne;
+    constexpr int BATCH = 8;   // bounds in flight per thread
+    for (int j0 = tid; j0 < n; j0 += BATCH * nth) {
+        float f[BATCH];
+#pragma unroll
+        for (int x = 0; x < BATCH; ++x) f[x] = j0 + x * nth < n ? bd[j0 + x * nth] : -CUDART_INF_F;
+        for (int y = 1; y < groups; ++y) {
+            float v[BATCH];
+#pragma unroll
+            for (int x = 0; x < BATCH; ++x) v[x] = j0 + x * nth < n ? bd[(size_t)y * stride + j0 + x * nth] : -CUDART_INF_F;
+#pragma unroll
+            for (int x = 0; x < BATCH; ++x) f[x] = v[x] > f[x] ? v[x] : f[x];
         }
-        key[j] = k;
+#pragma unroll
+        for (int x = 0; x < BATCH; ++x) {
+            uint32_t k = EMPTY;
+            if (f[x] != -CUDART_INF_F) {
+                k = ~ordered(f[x]);   // a finite bound never maps to EMPTY
+                all &= k;
+                any |= k;
+                ++ne;
+            }
+            if (j0 + x * nth < n) key[j0 + x * nth] = k;
+        }
     }
     all = __reduce_and_sync(0xffffffffu, all);
     any = __reduce_or_sync(0xffffffffu, any);
@@ -60,12 +74,10 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int n, int K, int K
         red[2][wid] = (uint32_t)ne;
     }
     __syncthreads();
-    ne = 0;
-    for (int w = 0; w < nth / 32; ++w) {
-        all &= red[0][w];
-        any |= red[1][w];
-        ne += (int)red[2][w];
-    }
+    const bool has = lane < nth / 32;
+    all = __reduce_and_sync(0xffffffffu, has ? red[0][lane] : EMPTY);
+    any = __reduce_or_sync(0xffffffffu, has ? red[1][lane] : 0u);
+    ne = __reduce_add_sync(0xffffffffu, has ? (int)red[2][lane] : 0);
     const int want = min(K, ne);
     int left = 32 - __clz(all ^ any);   // bits that are not known yet
     uint32_t mask = left == 32 ? 0u : 0xffffffffu << left, prefix = all & mask;
@@ -76,6 +88,7 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int n, int K, int K
         const uint32_t digit = (1u << bits) - 1u;
         for (int i = tid; i < 256; i += nth) hist[i] = 0;
         __syncthreads();
+#pragma unroll 4
         for (int j = tid; j < n; j += nth) {
             const uint32_t k = key[j];
             if (k != EMPTY && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1);
@@ -116,6 +129,7 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int n, int K, int K
         left = shift;
     }
     // (all threads of a warp together: nth and the segments are multiples of 32)
+#pragma unroll 4
     for (int j = tid; j < 32 * nseg; j += nth) {
         const uint32_t k = j < n ? key[j] : EMPTY, m = k & mask;
         const unsigned lt = __ballot_sync(0xffffffffu, k != EMPTY && m < prefix), eq = __ballot_sync(0xffffffffu, k != EMPTY && m == prefix);
@@ -148,6 +162,7 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int n, int K, int K
     }
     __syncthreads();
     const unsigned before = (1u << lane) - 1u;
+#pragma unroll 4
     for (int j = tid; j < 32 * nseg; j += nth) {
         const uint32_t k = j < n ? key[j] : EMPTY, m = k & mask;
         const bool l = k != EMPTY && m < prefix, e = k != EMPTY && m == prefix;

@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(SORT_THREADS) k_topk_pick(TopkArgs a, const __
     const int u = blockIdx.x;
     // the bounds are the previous grid's results
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    pick_blocks(a.bound + (size_t)u * a.NB, unit_nf(a, nt, u), a.K, a.Kc, a.sel + (size_t)u * a.Kc, key);
+    pick_blocks(a.bound + (size_t)u * a.NB, 1, 0, unit_nf(a, nt, u), a.K, a.Kc, a.sel + (size_t)u * a.Kc, key);
 }
 
 }  // namespace
