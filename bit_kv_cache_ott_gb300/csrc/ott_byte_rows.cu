@@ -859,10 +859,10 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
     const long long parts = longest * a.NWp / W / a.wpc + 2 * a.wpc;
     p.cw = (int)std::min<long long>(CMB_MAXW, (parts + 7) / 8);
     if (pick) {
-        // CTAs per (sequence, kv head): as many as give every SM two, but a slab each
+        // CTAs per (sequence, kv head): as many as give every SM one, but a slab each (two each: five drafts 38 -> 43 us)
         const int slabs = std::max(1, (p.nbmax + SLAB - 1) / SLAB);
         int cluster = 1;
-        while (cluster < SEL_CLUSTER && 2 * cluster <= slabs && (long long)a.nseq * c->Hkv * cluster < 2 * c->sm_count)
+        while (cluster < SEL_CLUSTER && 2 * cluster <= slabs && (long long)a.nseq * c->Hkv * cluster < c->sm_count)
             cluster *= 2;
         p.ba = {c->dig, a.bt, call.q, nullptr, nullptr, call.n, B0, c->Hq, c->Hkv, c->g, c->NB, call.topk, Kc, p.nbmax,
                 (c->g + 3) / 4, cluster, std::min(SLABS, (slabs + cluster - 1) / cluster)};

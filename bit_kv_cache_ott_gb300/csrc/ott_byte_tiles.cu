@@ -12,7 +12,8 @@
 // step of 112 tokens:
 //   warps 0-3, 4-7  softmax of tile 0 and 1: a thread per row. S from TMEM,
 //                   running maximum (the output is rescaled only when it has
-//                   grown by 2^8), weights back into S's columns as fp16.
+//                   grown by 2^8), weights back into S's columns as fp16, those of
+//                   four groups first, whose product starts under the others.
 //   warps 8-14      producers: warp w turns group w of each step from codes into
 //                   the swizzled key tile and value tile (V transposed; both
 //                   K-major), the lanes' pieces being cut for stores that meet all banks.
@@ -25,6 +26,20 @@
 // k_byte_tiles_combine), or a tile of its own, whichever is estimated to end
 // first (plan_byte_tiles). After SUM_STEPS steps of a tile, whoever takes the
 // next ones, its sums are carried over in fp32 (finish): the tensor cores truncate.
+//
+// What bounds it: 512 tokens of four sequences over 32K (8 kv heads, 4 heads
+// each, d = 128) take 850 us, 1.31 PFLOP/s; 2,048 over 131K 3.12 ms, 1.42. A step is some 2,900 cycles, 1,920 of
+// them products (a score product takes as long for 112 keys as for 128: its
+// queries are read at 64 bytes a cycle). The rest is the chain that a tile
+// goes through, since S(j+1) takes the place of P(j): softmax about 1,500, then O
+// and S, 450 each, and the handing over; no part of it alone (with fewer
+// products, no exponentials, no unpacking, or no stores of the producers the same
+// call takes 3 to 7% less). Weights handed over in one part: 875 us. Not taken, all
+// measured on that call: steps of 80 tokens whose S(j+1) has columns of its own, so that
+// the softmax never waits (1,040: a score product costs the same for 80 keys); that with a
+// warp of products per tile (957); a warp of products per tile and six
+// producers, with steps of 112 (988); exponentials of one group under the conversions of the one before
+// (885: registers spill); loops over the groups (910 to 980).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -40,6 +55,7 @@ constexpr int STEP_TOK = 16 * GRPS;
 constexpr int ROWS = 128;            // rows of a tile
 constexpr int THREADS = 512;
 constexpr int PROD0 = 8, MMA_WARP = 15;
+constexpr int HALF = 4;              // groups whose weights are handed over first
 constexpr int META = 4;              // steps of group metadata in flight
 constexpr int HIDDEN = 1;            // its flag: some row does not see some token
 constexpr int SUM_STEPS = SUM_TOKENS / STEP_TOK;   // steps whose products stay one sum in TMEM
@@ -61,7 +77,7 @@ struct TCfg {
     __host__ __device__ static constexpr uint32_t O(int t) { return 256u + (uint32_t)D * t; }
 };
 
-enum { B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_SFULL = 8, B_PFULL = 10, B_OFULL = 12, B_COUNT = 13 };
+enum { B_KFULL = 0, B_KEMPTY = 2, B_VFULL = 4, B_VEMPTY = 6, B_SFULL = 8, B_PFULL = 10, B_PHALF = 12, B_OFULL = 14, B_COUNT = 15 };
 
 struct TileArgs {
     ByteArgs a;
@@ -390,9 +406,9 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
             mma_ss(tmem + C::S(t), dq + t * (C::QB / 16) + off, dk + slot * (C::KB / 16) + off, HI, instr_desc(STEP_TOK), k > 0);
         }
     };
-    auto values = [&](int t, int slot, bool acc) {
+    auto values = [&](int t, int slot, bool acc, int k0, int k1) {
 #pragma unroll
-        for (int k = 0; k < GRPS; ++k) {
+        for (int k = k0; k < k1; ++k) {
             constexpr uint32_t HI = desc_hi(1024, 2);
             mma_ts(tmem + C::O(t), tmem + C::S(t) + 8 * k, dv + slot * (C::VB / 16) + ((k / 4) * (D * 128) + (k & 3) * 32) / 16, HI, instr_desc(D),
                    acc || k > 0);
@@ -411,11 +427,17 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
         }
         __syncwarp();
         if (nt == 2) {
-            if (j > 0) bar_wait(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up);
+            if (j > 0) {
+                bar_wait(&bar[B_PHALF + 1], (c1 - 1) & 1u, gave_up);
+                tc_after();
+                if (elect_one()) values(1, prev, j > 1, 0, HALF);
+                __syncwarp();
+                bar_wait(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up);
+            }
             tc_after();
             if (elect_one()) {
                 if (j > 0) {
-                    values(1, prev, j > 1);
+                    values(1, prev, true, HALF, GRPS);
                     tc_commit(&bar[B_VEMPTY + prev]);
                 }
                 scores(1, slot);
@@ -428,21 +450,28 @@ __device__ void multiply(uint8_t *sm, uint64_t *bar, volatile int *gave_up, uint
         }
         __syncwarp();
         bar_wait(&bar[B_VFULL + slot], par, gave_up);
+        bar_wait(&bar[B_PHALF], c0 & 1u, gave_up);
+        tc_after();
+        if (elect_one()) values(0, slot, j > 0, 0, HALF);
+        __syncwarp();
         bar_wait(&bar[B_PFULL], c0 & 1u, gave_up);
         ++c0;
         tc_after();
         if (elect_one()) {
-            values(0, slot, j > 0);
+            values(0, slot, true, HALF, GRPS);
             if (nt == 1) tc_commit(&bar[B_VEMPTY + slot]);
         }
         __syncwarp();
     }
     const int last = (it - 1) & 1;
-    if (nt == 2) bar_wait(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up);
+    if (nt == 2) {
+        bar_wait(&bar[B_PHALF + 1], (c1 - 1) & 1u, gave_up);
+        bar_wait(&bar[B_PFULL + 1], (c1 - 1) & 1u, gave_up);
+    }
     tc_after();
     if (elect_one()) {
         if (nt == 2) {
-            values(1, last, steps > 1);
+            values(1, last, steps > 1, 0, GRPS);
             tc_commit(&bar[B_VEMPTY + last]);
         }
         tc_commit(&bar[B_OFULL]);
@@ -559,7 +588,11 @@ __device__ void softmax(const TileArgs &ta, const ByteSeq &s, const Tile &t, uin
         tm_ld16(ts + 80, x + 16);
         tm_ld16(ts + 96, x + 32);
         weights(3, x + 48);
+        wait_st();
         wait_ld();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&bar[B_PHALF + tile]);
         tie16(x);
         tie16(x + 16);
         tie16(x + 32);
@@ -735,8 +768,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (ch_smem(smem_raw) & 1023u)) & 1023u);
     uint64_t *bar = reinterpret_cast<uint64_t *>(sm + C::OFF_BAR);
-    uint32_t *tm = reinterpret_cast<uint32_t *>(sm + C::OFF_BAR + 128);
-    volatile int *gave_up = reinterpret_cast<volatile int *>(sm + C::OFF_BAR + 132);
+    uint32_t *tm = reinterpret_cast<uint32_t *>(sm + C::OFF_BAR + 192);
+    volatile int *gave_up = reinterpret_cast<volatile int *>(sm + C::OFF_BAR + 196);
     const ByteArgs &a = ta.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
@@ -747,6 +780,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             bar_init(&bar[B_VEMPTY + k], 1);
             bar_init(&bar[B_SFULL + k], 1);
             bar_init(&bar[B_PFULL + k], ROWS / 32);
+            bar_init(&bar[B_PHALF + k], ROWS / 32);
         }
         bar_init(&bar[B_OFULL], 1);
         *gave_up = 0;
