@@ -163,7 +163,6 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     __syncwarp();
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int wpc = blockDim.x >> 5, gw = blockIdx.x * wpc + warp;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     // A CTA whose warps all work for one unit merges their results.
     bool merge = false;
     if (wpc > 1) {
@@ -173,7 +172,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     if (gw >= a.NWp) {   // the last CTA may have warps to spare
         if (merge) __syncthreads();
         return;
-    }
+    }   // (the others wait for the kernel before this one below, and so does the grid)
     const long long x0 = ch_range_start(a.W, a.NWp, gw), x1 = ch_range_start(a.W, a.NWp, gw + 1);
 
     Cursor ic;
@@ -342,6 +341,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
         b1 = transpose8x8(ch_h2(__floats2half2_rn(p[2], p[3])));
     };
 
+    asm volatile("griddepcontrol.wait;" ::: "memory");   // (the place in the plan is found while the kernel before runs)
     // prime the ring
     int st_issue = 0;
     for (int k = 0; k < NST && ic.x < x1; ++k) {
