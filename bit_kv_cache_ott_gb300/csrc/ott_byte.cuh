@@ -50,7 +50,7 @@ struct ott_byte_cache {
     int32_t *fstack;    // [pool_blocks] free slots, free_blocks of them (the host counts)
     float *part;        // partial results, bounds and selections of a call
     size_t part_floats;
-    int *ctl;           // [1]: a bounded wait gave up
+    int *ctl;           // [1]: a bounded wait gave up; [2]: runs of B items claimed (0 between calls)
     std::vector<int> T;
 };
 
@@ -72,13 +72,13 @@ cudaError_t set_byte_attributes(const ott_byte_cache *c);
 
 // One sequence of an attention launch.
 struct ByteSeq {
-    long long base;    // first work item; entry [nseq] holds the total
+    long long base, base2;   // first work item (A, B); entry [nseq] holds the totals
     int ubase;         // first work unit
     int S;             // slices of query rows per kv head, or pairs of tiles (0: no queries)
     int T, nq;         // tokens in the cache, query tokens
     int nb;            // blocks that a query attends
     int Ft, Sf;        // work items of the open block; and with the new tokens'
-    int Iu;            // work items of a unit
+    int Iu, Ia;        // work items of a unit, the A items among them
 };
 struct ByteTable {
     ByteSeq e[CHUNK_SEQS + 1];
@@ -98,8 +98,9 @@ struct ByteArgs {
     int IPB;                   // work items per block
     int SG;                    // selected blocks: slices of heads per token
     int RB;                    // rows per slice
-    long long W;               // work items
-    int NWp, wpc, MAXU, RV;    // active warps, warps per CTA, units that a warp's range can touch, rows of a partial
+    long long W, Wb;           // work items: A, B
+    int NWp, wpc, MAXU, RV;    // active warps, warps per CTA, units that a warp's run of A items can touch, rows of a partial
+    int NQ, MAXU2;             // runs of B items, units that one can touch
     float sl2;                 // log2(e) / sqrt(d)
 };
 

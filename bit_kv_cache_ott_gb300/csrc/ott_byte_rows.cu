@@ -18,8 +18,16 @@
 // tokens, or 32 tokens of a block (64 d bytes, contiguous, as the lanes'
 // fragments: 16-byte loads from shared memory, no transposition; and the
 // block's record). Every warp gets an equal contiguous run of the items of all
-// units, with a ring of stages of its own that its copies fill ahead, and
-// leaves one partial per unit that it touches; k_byte_combine merges them.
+// units, with a ring of stages of its own that its copies fill ahead.
+//
+// SMs do not get equal shares of HBM: with equal runs alone, the warps of batch
+// 32 x 4K, 32 heads, ended between 133 and 168 us.
+// So of a unit's items in long calls only the first seven eighths (its A items) are cut into equal runs, one per
+// warp; the rest (B items) are cut into short runs, about three per warp,
+// which warps claim from a counter when they have nothing else to copy. A run leaves
+// one partial per unit that it touches, in a place that goes by the run's number: who took
+// it does not show in the result. k_byte_combine merges the partials of a row.
+// (Short calls have A items only; a CTA whose warps then all work for one unit merges their results.)
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -81,58 +89,82 @@ struct RowsCfg {
     static constexpr int ITEM = QT * 2 * D;                // bytes of a block's item
     static constexpr int STAGE = ITEM + 128;               // with its record; 16 fp16 tokens fit, too
     static_assert(2 * FT * D * 2 <= ITEM, "fp16 items");
-    static constexpr int WARP_SMEM = NST * STAGE + 128;    // stages, barriers, what each stage holds
+    static constexpr int WARP_SMEM = NST * STAGE + 256;    // stages, barriers, what each stage holds
     static_assert(STAGE % 128 == 0 && NST * 8 <= 64, "stages");
     static_assert(WARP_SMEM * WARPS <= 227 * 1024, "shared memory");
 };
 
-// A work item: its unit (entry, kv head, slice of rows), its number in the
-// unit, and for one of a block the block's place and the part.
-struct Cursor {
-    long long x;
-    int e, hkv, sl, off, jp, k;
-    int Sf, Iu;   // of the entry
-    __device__ __forceinline__ void unit(const ByteTable &st) {
-        off = jp = k = 0;
-        Sf = st.e[e].Sf;
-        Iu = st.e[e].Iu;
-    }
-    // true: the next item is another unit's
-    __device__ __forceinline__ bool next(const ByteArgs &a, const ByteTable &st) {
-        ++x;
-        if (off++ >= Sf && ++k == a.IPB) {
-            k = 0;
-            ++jp;
-        }
-        if (off < Iu) return false;
-        if (++sl == st.e[e].S) {
-            sl = 0;
-            if (++hkv == a.Hkv) {
-                hkv = 0;
-                do ++e;
-                while (e < a.nseq && st.e[e].S == 0);
-            }
-        }
-        if (e < a.nseq) unit(st);
-        return true;
-    }
-};
-
-__device__ __forceinline__ int entry_of(const ByteTable &st, int nseq, long long x) {   // the last one whose base is <= x
+// The entry that holds work item x: the last one whose base (of A or B items) is <= x.
+template <bool B>
+__device__ __forceinline__ int entry_of(const ByteTable &st, int nseq, long long x) {
     int lo = 0, hi = nseq;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (st.e[mid].base <= x) lo = mid;
+        if ((B ? st.e[mid].base2 : st.e[mid].base) <= x) lo = mid;
         else hi = mid;
     }
     return lo;
 }
 
-// Items x0 .. x1 - 1 (x0 < x1) are of one unit.
+// A work item: its unit (entry, kv head, slice of rows), its number in the
+// unit, and for one of a block the block's place and the part.
+struct Cursor {
+    int e, hkv, sl, off, jp, k;
+    int lo, hi, Sf;   // of the entry: the unit's items of this kind, its fp16 items
+    bool b;           // B items
+    __device__ __forceinline__ void unit(const ByteArgs &a, const ByteTable &st, int skip) {
+        const ByteSeq &s = st.e[e];
+        lo = b ? s.Ia : 0;
+        hi = b ? s.Iu : s.Ia;
+        Sf = s.Sf;
+        off = lo + skip;
+        const int x = max(0, off - Sf);
+        jp = x / a.IPB;
+        k = x % a.IPB;
+    }
+    __device__ __forceinline__ void seek(const ByteArgs &a, const ByteTable &st, bool b_, long long x) {
+        b = b_;
+        e = b ? entry_of<true>(st, a.nseq, x) : entry_of<false>(st, a.nseq, x);
+        const ByteSeq &s = st.e[e];
+        const unsigned rel = (unsigned)(x - (b ? s.base2 : s.base)), len = (unsigned)(b ? s.Iu - s.Ia : s.Ia);   // (32 bits: checked on the host)
+        const int h = (int)(rel / len);
+        hkv = h / s.S;
+        sl = h % s.S;
+        unit(a, st, (int)(rel % len));
+    }
+    // true: the next item is another unit's
+    __device__ __forceinline__ bool next(const ByteArgs &a, const ByteTable &st) {
+        if (off++ >= Sf && ++k == a.IPB) {
+            k = 0;
+            ++jp;
+        }
+        if (off < hi) return false;
+        if (++sl == st.e[e].S) {
+            sl = 0;
+            if (++hkv == a.Hkv) {
+                hkv = 0;
+                do ++e;
+                while (e < a.nseq && (st.e[e].S == 0 || (b && st.e[e].Iu == st.e[e].Ia)));
+            }
+        }
+        if (e < a.nseq) unit(a, st, 0);
+        return true;
+    }
+};
+
+// What a stage holds: valid tokens (0: none, nothing to wait for; -1: no more
+// items), the unit, first fp16 token (of the new ones: + FRESH; -1: a block's
+// item), whether it is the first of its unit in the run, and if it is the last the partial's place, else -1.
+struct Desc {
+    int valid, e, hkv, sl, f0, first, part, pad;
+};
+constexpr int FRESH = 1 << 30;
+
+// A items x0 .. x1 - 1 (x0 < x1) are of one unit.
 __device__ __forceinline__ bool one_unit(const ByteArgs &a, const ByteTable &st, long long x0, long long x1) {
-    const int e = entry_of(st, a.nseq, x0);
-    const unsigned Iu = (unsigned)st.e[e].Iu, rel = (unsigned)(x0 - st.e[e].base);
-    return x1 <= st.e[e].base + (long long)(rel / Iu + 1) * Iu;
+    const int e = entry_of<false>(st, a.nseq, x0);
+    const unsigned Ia = (unsigned)st.e[e].Ia, rel = (unsigned)(x0 - st.e[e].base);
+    return x1 <= st.e[e].base + (long long)(rel / Ia + 1) * Ia;
 }
 
 // Rows of slice sl of an entry: first row, number of rows (a row is token * g + head).
@@ -157,7 +189,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     const int rot = D == 128 ? 8 * (i >> 1) : 0;
     uint8_t *stg = smem + (size_t)warp * C::WARP_SMEM;
     uint64_t *bars = reinterpret_cast<uint64_t *>(stg + NST * C::STAGE);
-    int *meta = reinterpret_cast<int *>(stg + NST * C::STAGE + 64);   // valid tokens of each stage
+    Desc *desc = reinterpret_cast<Desc *>(stg + NST * C::STAGE + 64);
     if (lane < NST) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(ch_smem(&bars[lane])) : "memory");
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     __syncwarp();
@@ -165,7 +197,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     const int wpc = blockDim.x >> 5, gw = blockIdx.x * wpc + warp;
     // A CTA whose warps all work for one unit merges their results.
     bool merge = false;
-    if (wpc > 1) {
+    if (wpc > 1 && a.Wb == 0) {
         const int g1 = min(a.NWp, (int)(blockIdx.x + 1) * wpc);
         merge = g1 > (int)blockIdx.x * wpc && one_unit(a, st, ch_range_start(a.W, a.NWp, blockIdx.x * wpc), ch_range_start(a.W, a.NWp, g1));
     }
@@ -173,36 +205,30 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
         if (merge) __syncthreads();
         return;
     }   // (the others wait for the kernel before this one below, and so does the grid)
-    const long long x0 = ch_range_start(a.W, a.NWp, gw), x1 = ch_range_start(a.W, a.NWp, gw + 1);
-
+    // the run at hand: the next item, how many are left, the places of its partials
+    const long long x0 = ch_range_start(a.W, a.NWp, gw);
+    int left = (int)(ch_range_start(a.W, a.NWp, gw + 1) - x0);
     Cursor ic;
-    ic.x = x0;
-    ic.e = entry_of(st, a.nseq, x0);
-    {
-        const ByteSeq &s = st.e[ic.e];
-        const unsigned rel = (unsigned)(x0 - s.base);   // a sequence's items fit 32 bits (checked on the host)
-        const int h = (int)(rel / (unsigned)s.Iu), off = (int)(rel % (unsigned)s.Iu);
-        ic.hkv = h / s.S;
-        ic.sl = h % s.S;
-        ic.unit(st);
-        ic.off = off;
-        if (off > s.Sf) {
-            ic.jp = (off - s.Sf) / a.IPB;
-            ic.k = (off - s.Sf) % a.IPB;
-        }
-    }
-    Cursor cc = ic;
+    ic.seek(a, st, false, x0);
+    size_t place = (size_t)gw * a.MAXU;
+    int room = a.MAXU;
+    bool first = true, more = a.Wb > 0;
+    int claimed = 0;        // lane 0: the run claimed last
+    constexpr int CLAIM = 2;   // items before the end of a run when the next one is claimed
+    auto claim = [&]() {
+        if (more && lane == 0) claimed = atomicAdd(&a.ctl[2], 1);
+    };
 
     // Slots of the next 32 blocks of the issuing cursor's unit, a lane each.
     int slots = -1, slots_from = INT_MIN;
-    auto issue = [&](const Cursor &c, int sg) {
+    auto issue = [&](const Cursor &c, int sg, int &f0) {
         const ByteSeq &s = st.e[c.e];
         const int b = a.B0 + c.e, u = b * a.Hkv + c.hkv;
         uint8_t *dst = stg + sg * C::STAGE;
         int m;
         if (c.off < c.Sf) {
             const bool fresh = c.off >= s.Ft;
-            const int f0 = (fresh ? c.off - s.Ft : c.off) * FT;
+            f0 = (fresh ? c.off - s.Ft : c.off) * FT;
             m = min(FT, (fresh ? s.nq : s.T % a.G) - f0);
             // Two copies; the rows past the end keep what the stage held, and are masked where they are read. (A copy per
             // row, to padded rows, spared bank conflicts and cost a warp about 5,000 cycles an item.)
@@ -212,7 +238,9 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 bulk_copy(dst, (fresh ? a.k : a.tk) + at, (uint32_t)m * (D * 2), &bars[sg]);
                 bulk_copy(dst + FT * D * 2, (fresh ? a.v : a.tv) + at, (uint32_t)m * (D * 2), &bars[sg]);
             }
+            if (fresh) f0 += FRESH;
         } else {
+            f0 = -1;
             if (c.jp < slots_from || c.jp >= slots_from + 32) {
                 slots_from = c.jp;
                 const int jp = c.jp + lane;
@@ -232,18 +260,57 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 bulk_copy(dst + C::ITEM, a.rec + slot, 16, &bars[sg]);
             }
         }
-        if (lane == 0) meta[sg] = m;
+        return m;
     };
-    auto advance = [&](Cursor &c) {
-        if (c.next(a, st)) slots_from = INT_MIN;
+    // The next item into stage sg (whose reads are done).
+    auto feed = [&](int sg) {
+        if (left == 0) {
+            int q = 0;
+            if (more) {
+                q = __shfl_sync(0xffffffffu, claimed, 0);
+                more = q < a.NQ;
+            }
+            if (!more) {
+                if (lane == 0) desc[sg].valid = -1;
+                return;
+            }
+            const long long x = ch_range_start(a.Wb, a.NQ, q);
+            left = (int)(ch_range_start(a.Wb, a.NQ, q + 1) - x);
+            ic.seek(a, st, true, x);
+            slots_from = INT_MIN;
+            place = (size_t)a.NWp * a.MAXU + (size_t)q * a.MAXU2;
+            room = a.MAXU2;
+            first = true;
+            if (left <= CLAIM) claim();
+        }
+        Desc d;
+        d.e = ic.e;
+        d.hkv = ic.hkv;
+        d.sl = ic.sl;
+        d.valid = issue(ic, sg, d.f0);
+        d.first = first;
+        const bool other = ic.next(a, st);
+        --left;
+        first = other || left == 0;
+        d.part = -1;
+        if (other) slots_from = INT_MIN;
+        if (first && !merge) {
+            d.part = (int)place++;
+            if (--room < 0) {   // never with the host's bound; recorded instead of writing out of bounds
+                if (lane == 0) atomicExch(&a.ctl[1], 1);
+                d.part = -1;
+            }
+        }
+        if (lane == 0) desc[sg] = d;
+        if (left == CLAIM) claim();
     };
 
     uint32_t Bq[NC][NKS][2];          // queries: B operand, column r of each group
     float acc[NC][NKS][4], m_run[NC][2], l_run[NC][2];
     int tok[NC][2];                   // the columns' tokens (of the chunk)
-    int uo = 0, cnt_rows = 0;
+    int cnt_rows = 0;
 
-    auto begin_unit = [&](const Cursor &c) {
+    auto begin_unit = [&](const Desc &c) {
         const ByteSeq &s = st.e[c.e];
         const int b = a.B0 + c.e;
         int v0;
@@ -268,12 +335,8 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
             for (int mt = 0; mt < NKS; ++mt) acc[nc][mt][0] = acc[nc][mt][1] = acc[nc][mt][2] = acc[nc][mt][3] = 0.0f;
         }
     };
-    auto end_unit = [&]() {
-        if (uo >= a.MAXU) {   // never with the host's bound; recorded instead of writing out of bounds
-            if (lane == 0) atomicExch(&a.ctl[1], 1);
-            return;
-        }
-        float *pb = a.part + ((size_t)gw * a.MAXU + uo) * a.RV * (D + 2);
+    auto end_unit = [&](int part) {
+        float *pb = a.part + (size_t)part * a.RV * (D + 2);
 #pragma unroll
         for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
@@ -293,7 +356,6 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                     }
                 }
             }
-        ++uo;
     };
     // z values whose largest is mx in this lane: the reference moves up, and
     // sums and outputs are rescaled, only when one has grown by 2^GROW.
@@ -342,21 +404,17 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     };
 
     asm volatile("griddepcontrol.wait;" ::: "memory");   // (the place in the plan is found while the kernel before runs)
-    // prime the ring
-    int st_issue = 0;
-    for (int k = 0; k < NST && ic.x < x1; ++k) {
-        issue(ic, st_issue);
-        advance(ic);
-        st_issue = st_issue + 1 == NST ? 0 : st_issue + 1;
-    }
-    begin_unit(cc);
+    if (left <= CLAIM) claim();
+    for (int k = 0; k < NST; ++k) feed(k);
     __syncwarp();
 
     uint32_t phase = 0;
     int sg = 0;
-    while (cc.x < x1) {
-        const ByteSeq &s = st.e[cc.e];
-        const int valid = meta[sg];
+    for (;;) {
+        const Desc dc = desc[sg];
+        const int valid = dc.valid;
+        if (valid < 0) break;
+        if (dc.first) begin_unit(dc);
         uint8_t *stage = stg + sg * C::STAGE;
         if (valid > 0) {
             if (!mbar_wait(&bars[sg], (phase >> sg) & 1u)) {
@@ -368,10 +426,10 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 return;
             }
             phase ^= 1u << sg;
-            if (cc.off < cc.Sf) {
+            if (dc.f0 >= 0) {
                 // 16 fp16 tokens: of the open block, or new ones (causal)
-                const bool fresh = cc.off >= s.Ft;
-                const int f0 = (fresh ? cc.off - s.Ft : cc.off) * FT;
+                const bool fresh = dc.f0 >= FRESH;
+                const int f0 = fresh ? dc.f0 - FRESH : dc.f0;
                 const __half *kr = reinterpret_cast<const __half *>(stage), *vr = kr + FT * D;
                 float d[NC][4], mx[NC][2];
 #pragma unroll
@@ -472,22 +530,14 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                     }
                 }
             }
-            __syncwarp();
         }
+        __syncwarp();
         // the stage's reads (generic proxy) come before the copy that refills it
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        if (ic.x < x1) {
-            issue(ic, sg);
-            advance(ic);
-            __syncwarp();
-        }
-        const bool other = cc.next(a, st);
+        feed(sg);
+        __syncwarp();
+        if (dc.part >= 0) end_unit(dc.part);
         sg = sg + 1 == NST ? 0 : sg + 1;
-        if (merge) continue;
-        if (other || cc.x >= x1) {
-            end_unit();
-            if (cc.x < x1) begin_unit(cc);
-        }
     }
     if (!merge) return;
     // Every warp's largest z and sum, then its output at the common reference,
@@ -532,48 +582,72 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     }
 }
 
-// Merge a row's partials: a CTA of cw warps per (sequence, query head,
-// token), the warps' shares merged through shared memory.
+// Merge a row's partials: a CTA of cw warps per (sequence, query head, token),
+// the warps' shares merged through shared memory.
 constexpr int CMB_MAXW = 8;   // (small enough to wait beside the rows kernel's CTAs)
 template <int D>
 __global__ void __launch_bounds__(CMB_MAXW * 32)
     k_byte_combine(const __grid_constant__ ByteArgs a, const __grid_constant__ ByteTable st) {
     constexpr int CPL = D / 32, GRP = 8;
     __shared__ float red[CMB_MAXW][D + 2];
-    const int cw = blockDim.x >> 5, wi = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cw = blockDim.x >> 5, wi = threadIdx.x >> 5, lane = threadIdx.x & 31, ch = lane * CPL;
     const ByteSeq &s = st.e[blockIdx.y];
     const int hq = blockIdx.x / a.n, tk = blockIdx.x % a.n;
     const bool row = tk < s.nq;
-    int wa = 0, wb = -1, uo_a = 0, col = 0, n0 = 0, n01 = 0, parts = 0;
-    int first = 0, inner = 0, last = 0;   // where the parts of the unit's first CTA, of the inner ones, and of the last begin
+    int wa = 0, uo_a = 0, col = 0, n0 = 0, n01 = 0, na = 0, parts = 0;
+    int first = 0, inner = 0, last = 0;   // A: where the parts of the unit's first CTA, of the inner ones, and of the last begin
+    size_t qa = 0;                        // B: the first part's place
+    int uo_b = 0;
     if (row) {   // the plan, while the rows kernel still runs
         const int hd = hq % a.g, v = a.sel ? hd : tk * a.g + hd;
         const int sl = a.sel ? tk * a.SG + hd / a.RB : v / a.RB, h = hq / a.g * s.S + sl;
         col = v % a.RB;
-        const long long ub = s.base + (long long)h * s.Iu, ue = ub + s.Iu;
+        const long long ub = s.base + (long long)h * s.Ia, ue = ub + s.Ia;
         wa = ch_warp_of(a.W, a.NWp, ub);
-        wb = ch_warp_of(a.W, a.NWp, ue - 1);
+        const int wb = ch_warp_of(a.W, a.NWp, ue - 1);
         // the unit's place among those of warp wa
         const long long xa = ch_range_start(a.W, a.NWp, wa);
-        const int ea = entry_of(st, a.nseq, xa);
-        uo_a = s.ubase + h - (st.e[ea].ubase + (int)((unsigned)(xa - st.e[ea].base) / (unsigned)st.e[ea].Iu));
+        const int ea = entry_of<false>(st, a.nseq, xa);
+        uo_a = s.ubase + h - (st.e[ea].ubase + (int)((unsigned)(xa - st.e[ea].base) / (unsigned)st.e[ea].Ia));
         // The unit's parts: one of each CTA that merged its warps (all of whose items are the unit's), else one of each warp.
         const int ca = wa / a.wpc, cb = wb / a.wpc;
         auto merged = [&](int c) {
-            return a.wpc > 1 && ch_range_start(a.W, a.NWp, (long long)c * a.wpc) >= ub &&
+            return a.wpc > 1 && a.Wb == 0 && ch_range_start(a.W, a.NWp, (long long)c * a.wpc) >= ub &&
                    ch_range_start(a.W, a.NWp, min(a.NWp, (c + 1) * a.wpc)) <= ue;
         };
-        const bool ma = merged(ca), mb = ca == cb ? ma : merged(cb);
-        first = ma ? ca * a.wpc : wa;
-        inner = (ca + 1) * a.wpc;
-        last = cb * a.wpc;
-        if (ma) uo_a = 0;
-        n0 = ma ? 1 : min(wb + 1, inner) - wa;
-        n01 = n0 + max(0, cb - ca - 1);
-        parts = n01 + (ca == cb ? 0 : mb ? 1 : wb - last + 1);
+        if (a.Wb == 0) {
+            const bool ma = merged(ca), mb = ca == cb ? ma : merged(cb);
+            first = ma ? ca * a.wpc : wa;
+            inner = (ca + 1) * a.wpc;
+            last = cb * a.wpc;
+            if (ma) uo_a = 0;
+            n0 = ma ? 1 : min(wb + 1, inner) - wa;
+            n01 = n0 + max(0, cb - ca - 1);
+            na = n01 + (ca == cb ? 0 : mb ? 1 : wb - last + 1);
+        } else {
+            first = wa;
+            n0 = n01 = na = wb - wa + 1;
+        }
+        parts = na;
+        if (s.Iu > s.Ia) {
+            const int Ib = s.Iu - s.Ia;
+            const long long b0 = s.base2 + (long long)h * Ib;
+            const int r0 = ch_warp_of(a.Wb, a.NQ, b0), r1 = ch_warp_of(a.Wb, a.NQ, b0 + Ib - 1);
+            const long long xb = ch_range_start(a.Wb, a.NQ, r0);
+            // the unit's place among those of run r0 (entries may have no B items: counted by walking)
+            int e = entry_of<true>(st, a.nseq, xb);
+            int u0 = (int)((unsigned)(xb - st.e[e].base2) / (unsigned)(st.e[e].Iu - st.e[e].Ia));
+            for (uo_b = -u0; e < (int)blockIdx.y; ++e)
+                if (st.e[e].Iu > st.e[e].Ia) uo_b += st.e[e].S * a.Hkv;
+            uo_b += h;
+            qa = (size_t)a.NWp * a.MAXU + (size_t)r0 * a.MAXU2;
+            parts = na + r1 - r0 + 1;
+        }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the next call's runs are claimed from the start
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) a.ctl[2] = 0;
     if (!row) return;
     float M = -CUDART_INF_F, L = 0.0f, acc[CPL];
 #pragma unroll
@@ -588,13 +662,19 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
             for (int c = 0; c < CPL; ++c) vs[x][c] = 0.0f;
             const int k = k0 + x;
             if (k < parts) {
-                const int w = k < n0 ? first + k : k < n01 ? inner + (k - n0) * a.wpc : last + (k - n01);
-                const float *p = a.part + (((size_t)w * a.MAXU + (k == 0 ? uo_a : 0)) * a.RV + col) * (D + 2);
+                size_t at;
+                if (k < na) {
+                    const int w = k < n0 ? first + k : k < n01 ? inner + (k - n0) * a.wpc : last + (k - n01);
+                    at = (size_t)w * a.MAXU + (k == 0 ? uo_a : 0);
+                } else {
+                    at = qa + (size_t)(k - na) * a.MAXU2 + (k == na ? uo_b : 0);
+                }
+                const float *p = a.part + (at * a.RV + col) * (D + 2);
                 ms[x] = p[0];
                 ls[x] = p[1];
 #pragma unroll
                 for (int c = 0; c < CPL; c += 2) {
-                    const float2 t = *reinterpret_cast<const float2 *>(p + 2 + lane * CPL + c);
+                    const float2 t = *reinterpret_cast<const float2 *>(p + 2 + ch + c);
                     vs[x][c] = t.x;
                     vs[x][c + 1] = t.y;
                 }
@@ -641,14 +721,9 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
     }
     // a row sees a token at least, so that L = 0 means scores of -inf or NaN alone: NaN
     const float inv = 1.0f / L;
-    __half *o = a.out + (((size_t)(a.B0 + blockIdx.y) * a.Hq + hq) * a.n + tk) * D + lane * CPL;
-    uint32_t w[CPL / 2];
+    __half *o = a.out + (((size_t)(a.B0 + blockIdx.y) * a.Hq + hq) * a.n + tk) * D + ch;
 #pragma unroll
-    for (int c = 0; c < CPL; c += 2) w[c / 2] = ch_h2(__floats2half2_rn(acc[c] * inv, acc[c + 1] * inv));
-    if constexpr (CPL == 4)
-        *reinterpret_cast<uint2 *>(o) = make_uint2(w[0], w[1]);
-    else
-        *reinterpret_cast<uint32_t *>(o) = w[0];
+    for (int c = 0; c < CPL; c += 2) *reinterpret_cast<__half2 *>(o + c) = __floats2half2_rn(acc[c] * inv, acc[c + 1] * inv);
 }
 
 // ---------------------------------------------------------------- selection
@@ -821,42 +896,64 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
     a.RB = 8 * p.NC;
     a.SG = pick ? (c->g + a.RB - 1) / a.RB : 1;
     a.RV = (int)std::min<long long>(rows, a.RB);
-    long long base = 0, units = 0, iu_min = LLONG_MAX;
+    constexpr int WARPS = 8;
+    long long W = 0, units = 0, longest = 0;
     for (int x = 0; x < a.nseq; ++x) {
         ByteSeq &s = p.st.e[x];
-        s.base = base;
         s.ubase = (int)units;
         const long long S = s.nq == 0 ? 0 : pick ? (long long)s.nq * a.SG : ((long long)s.nq * c->g + a.RB - 1) / a.RB;
         const long long Iu = s.Sf + (long long)s.nb * a.IPB;
         if (S * c->Hkv * Iu > INT_MAX || units + S * c->Hkv > INT_MAX) return false;
         s.S = (int)S;
-        s.Iu = (int)Iu;
-        base += S * c->Hkv * Iu;
+        s.Iu = s.Ia = (int)Iu;
+        if (S > 0) longest = std::max(longest, Iu);
+        W += S * c->Hkv * Iu;
         units += S * c->Hkv;
-        if (S > 0) iu_min = std::min(iu_min, Iu);
     }
-    p.st.e[a.nseq] = ByteSeq{};
-    p.st.e[a.nseq].base = a.W = base;
-    p.st.e[a.nseq].ubase = (int)units;
-    // Equal runs, at least two items each; sums end after SUM_TOKENS tokens.
-    constexpr int WARPS = 8;
-    const long long W = base;
+    // A items in equal runs, at least two items each, sums ending after
+    // SUM_TOKENS tokens. An eighth of the units as B items where a warp has 64 items or more and
+    // a unit 16 runs at most; elsewhere their partials cost more than they even out.
+    // Without and with them: batch 32 x 4K, 32 heads (108 items a warp, 1.2 runs a unit) 166 and
+    // 161 us, four queries each 182 and 165; batch 16 x 32K, 8 kv heads (9.5 runs)
+    // 164 and 162; 4 x 131K (38 runs) 161 and 163; 600K tokens, 8 kv heads (152 runs) 183
+    // and 193; 131K (27 items a warp) 46 and 51 to 60.
     int ctas = c->sm_count;
     while (ctas < (1 << 20) && W / ((long long)ctas * WARPS) >= SUM_TOKENS / QT) ctas += c->sm_count;
     a.NWp = (int)std::max<long long>(1, std::min<long long>((long long)ctas * WARPS, W / 2));
+    const bool claims = W / a.NWp >= 64 && longest * a.NWp / W <= 16;
+    long long base = 0, base2 = 0, ia_min = LLONG_MAX, ib_min = LLONG_MAX;
+    for (int x = 0; x < a.nseq; ++x) {
+        ByteSeq &s = p.st.e[x];
+        if (claims) s.Ia = s.Iu - s.Iu / 8;
+        s.base = base;
+        s.base2 = base2;
+        base += (long long)s.S * c->Hkv * s.Ia;
+        base2 += (long long)s.S * c->Hkv * (s.Iu - s.Ia);
+        if (s.S == 0) continue;
+        ia_min = std::min<long long>(ia_min, s.Ia);
+        if (s.Iu > s.Ia) ib_min = std::min<long long>(ib_min, s.Iu - s.Ia);
+    }
+    p.st.e[a.nseq] = ByteSeq{};
+    p.st.e[a.nseq].base = a.W = base;
+    p.st.e[a.nseq].base2 = a.Wb = base2;
+    p.st.e[a.nseq].ubase = (int)units;
     p.ctas = (int)std::min<long long>(ctas, a.NWp);
     a.wpc = (a.NWp + p.ctas - 1) / p.ctas;
     p.ctas = (a.NWp + a.wpc - 1) / a.wpc;
-    const long long run = (W + a.NWp - 1) / a.NWp;
-    a.MAXU = (int)std::min<long long>((run - 1) / iu_min + 2, run);
-    p.part_floats = (size_t)a.NWp * a.MAXU * a.RV * (c->d + 2);
+    const long long run = (base + a.NWp - 1) / a.NWp;
+    a.MAXU = (int)std::min<long long>((run - 1) / ia_min + 2, run);
+    a.NQ = 0;
+    a.MAXU2 = 0;
+    if (base2 > 0) {
+        a.NQ = (int)std::max<long long>(1, std::min<long long>(base2 / 4, 3LL * a.NWp));
+        const long long run2 = (base2 + a.NQ - 1) / a.NQ;
+        a.MAXU2 = (int)std::min<long long>((run2 - 1) / ib_min + 2, run2);
+    }
+    const long long places = (long long)a.NWp * a.MAXU + (long long)a.NQ * a.MAXU2;
+    if (places > INT_MAX) return false;
+    p.part_floats = (size_t)places * a.RV * (c->d + 2);
     // merge: warps per row by the partials of a unit
-    const long long longest = [&] {
-        long long m = 0;
-        for (int x = 0; x < a.nseq; ++x) m = std::max<long long>(m, p.st.e[x].S ? p.st.e[x].Iu : 0);
-        return m;
-    }();
-    const long long parts = longest * a.NWp / W / a.wpc + 2 * a.wpc;
+    const long long all = W, parts = (base2 > 0 ? longest * a.NWp / all + longest * a.NQ / all : longest * a.NWp / all / a.wpc + 2 * a.wpc) + 2;
     p.cw = (int)std::min<long long>(CMB_MAXW, (parts + 7) / 8);
     if (pick) {
         // CTAs per (sequence, kv head): as many as give every SM one, but a slab each (two each: five drafts 38 -> 43 us)
