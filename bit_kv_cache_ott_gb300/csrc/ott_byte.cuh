@@ -101,6 +101,7 @@ struct ByteArgs {
     long long W, Wb;           // work items: A, B
     int NWp, wpc, MAXU, RV;    // active warps, warps per CTA, units that a warp's run of A items can touch, rows of a partial
     int NQ, MAXU2;             // runs of B items, units that one can touch
+    bool direct;               // a CTA per unit, which writes its rows
     float sl2;                 // log2(e) / sqrt(d)
 };
 

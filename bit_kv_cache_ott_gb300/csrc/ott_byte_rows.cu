@@ -27,7 +27,9 @@
 // which warps claim from a counter when they have nothing else to copy. A run leaves
 // one partial per unit that it touches, in a place that goes by the run's number: who took
 // it does not show in the result. k_byte_combine merges the partials of a row.
-// (Short calls have A items only; a CTA whose warps then all work for one unit merges their results.)
+// (Other calls have A items only; a CTA whose warps then all work for one unit
+// merges their results. The shortest calls, units of up to 1,024 tokens and no more of them than
+// SMs, give every unit a CTA, which writes its rows: no second kernel.)
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -40,6 +42,7 @@ namespace {
 
 constexpr int ROWS_MAX = 16;   // rows per kv head up to which this file's kernel serves a call
 constexpr int QT = 32, FT = 16;   // tokens of a work item: of a block, fp16
+constexpr int DIRECT_ITEMS = 32;  // items of a unit that a CTA of its own serves
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -196,20 +199,37 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int wpc = blockDim.x >> 5, gw = blockIdx.x * wpc + warp;
     // A CTA whose warps all work for one unit merges their results.
-    bool merge = false;
-    if (wpc > 1 && a.Wb == 0) {
+    bool merge = a.direct;
+    if (!a.direct && wpc > 1 && a.Wb == 0) {
         const int g1 = min(a.NWp, (int)(blockIdx.x + 1) * wpc);
         merge = g1 > (int)blockIdx.x * wpc && one_unit(a, st, ch_range_start(a.W, a.NWp, blockIdx.x * wpc), ch_range_start(a.W, a.NWp, g1));
     }
-    if (gw >= a.NWp) {   // the last CTA may have warps to spare
+    if (!a.direct && gw >= a.NWp) {   // the last CTA may have warps to spare
         if (merge) __syncthreads();
         return;
     }   // (the others wait for the kernel before this one below, and so does the grid)
     // the run at hand: the next item, how many are left, the places of its partials
-    const long long x0 = ch_range_start(a.W, a.NWp, gw);
-    int left = (int)(ch_range_start(a.W, a.NWp, gw + 1) - x0);
     Cursor ic;
-    ic.seek(a, st, false, x0);
+    int left;
+    if (a.direct) {   // this CTA's unit, this warp's share of it (there may be none)
+        int e = 0;
+        for (int hi = a.nseq; hi - e > 1;) {
+            const int mid = (e + hi) >> 1;
+            if (st.e[mid].ubase <= (int)blockIdx.x) e = mid;
+            else hi = mid;
+        }
+        const int h = (int)blockIdx.x - st.e[e].ubase, from = st.e[e].Iu * warp / wpc;
+        ic.b = false;
+        ic.e = e;
+        ic.hkv = h / st.e[e].S;
+        ic.sl = h % st.e[e].S;
+        ic.unit(a, st, from);
+        left = st.e[e].Iu * (warp + 1) / wpc - from;
+    } else {
+        const long long x0 = ch_range_start(a.W, a.NWp, gw);
+        left = (int)(ch_range_start(a.W, a.NWp, gw + 1) - x0);
+        ic.seek(a, st, false, x0);
+    }
     size_t place = (size_t)gw * a.MAXU;
     int room = a.MAXU;
     bool first = true, more = a.Wb > 0;
@@ -405,7 +425,15 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 
     asm volatile("griddepcontrol.wait;" ::: "memory");   // (the place in the plan is found while the kernel before runs)
     if (left <= CLAIM) claim();
+    const Cursor start = ic;
     for (int k = 0; k < NST; ++k) feed(k);
+    if (a.direct) {   // the rows of a warp without items, too
+        Desc d;
+        d.e = start.e;
+        d.hkv = start.hkv;
+        d.sl = start.sl;
+        begin_unit(d);
+    }
     __syncwarp();
 
     uint32_t phase = 0;
@@ -414,7 +442,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
         const Desc dc = desc[sg];
         const int valid = dc.valid;
         if (valid < 0) break;
-        if (dc.first) begin_unit(dc);
+        if (dc.first && !a.direct) begin_unit(dc);
         uint8_t *stage = stg + sg * C::STAGE;
         if (valid > 0) {
             if (!mbar_wait(&bars[sg], (phase >> sg) & 1u)) {
@@ -560,7 +588,9 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
             }
         }
     __syncthreads();
-    const int nw = min(wpc, a.NWp - (int)blockIdx.x * wpc);
+    const int nw = a.direct ? wpc : min(wpc, a.NWp - (int)blockIdx.x * wpc);
+    int v0, rows;
+    slice_rows(a, st.e[start.e], start.sl, v0, rows);
     float *const pb = a.part + (size_t)(blockIdx.x * wpc) * a.MAXU * a.RV * (D + 2);
     for (int col = warp; col < cnt_rows; col += nw) {
         float M = -CUDART_INF_F, L = 0.0f, o[D / 32];
@@ -574,6 +604,15 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
             L = fmaf(sw, p[1], L);
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) o[c] = fmaf(sw, p[2 + 32 * c + lane], o[c]);
+        }
+        if (a.direct) {
+            // a row sees a token at least, so that L = 0 means scores of -inf or NaN alone: NaN
+            const int v = v0 + col;
+            const float inv = 1.0f / L;
+            __half *out = a.out + (((size_t)(a.B0 + start.e) * a.Hq + start.hkv * a.g + v % a.g) * a.n + v / a.g) * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) out[32 * c + lane] = __float2half_rn(o[c] * inv);
+            continue;
         }
         float *p = pb + (size_t)col * (D + 2);
         if (lane == 0) *reinterpret_cast<float2 *>(p) = make_float2(M, L);
@@ -940,6 +979,13 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
     p.ctas = (int)std::min<long long>(ctas, a.NWp);
     a.wpc = (a.NWp + p.ctas - 1) / p.ctas;
     p.ctas = (a.NWp + a.wpc - 1) / a.wpc;
+    a.direct = false;
+    if (units <= c->sm_count && longest <= DIRECT_ITEMS) {
+        a.direct = true;
+        a.wpc = (int)std::min<long long>(WARPS, longest);
+        p.ctas = (int)units;
+        a.NWp = p.ctas * a.wpc;
+    }
     const long long run = (base + a.NWp - 1) / a.NWp;
     a.MAXU = (int)std::min<long long>((run - 1) / ia_min + 2, run);
     a.NQ = 0;
@@ -949,7 +995,7 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
         const long long run2 = (base2 + a.NQ - 1) / a.NQ;
         a.MAXU2 = (int)std::min<long long>((run2 - 1) / ib_min + 2, run2);
     }
-    const long long places = (long long)a.NWp * a.MAXU + (long long)a.NQ * a.MAXU2;
+    const long long places = a.direct ? 0 : (long long)a.NWp * a.MAXU + (long long)a.NQ * a.MAXU2;
     if (places > INT_MAX) return false;
     p.part_floats = (size_t)places * a.RV * (c->d + 2);
     // merge: warps per row by the partials of a unit
@@ -1006,7 +1052,7 @@ cudaError_t launch_plan(const ott_byte_cache *c, const Plan &p, cudaStream_t s) 
     if (e == cudaSuccess)
         e = p.NC == 1 ? (i8 ? launch_rows<D, 1, OTT_BYTE_INT>(p, s) : launch_rows<D, 1, OTT_BYTE_FLOAT>(p, s))
                       : (i8 ? launch_rows<D, 2, OTT_BYTE_INT>(p, s) : launch_rows<D, 2, OTT_BYTE_FLOAT>(p, s));
-    if (e == cudaSuccess)
+    if (e == cudaSuccess && !p.a.direct)
         e = launch_pdl(k_byte_combine<D>, dim3((unsigned)(c->Hq * p.a.n), (unsigned)p.a.nseq), 32 * p.cw, 0, s, p.a, p.st);
     return e;
 }

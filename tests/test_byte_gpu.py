@@ -470,6 +470,56 @@ def test_places_beyond_32_bits(ott):
     torch.cuda.empty_cache()
 
 
+@pytest.mark.parametrize("fmt,n", [("int8", 1), ("e4m3", 3)])
+def test_long_batches_share_their_last_items(ott, fmt, n):
+    """Calls long enough that warps claim the last items of every unit: sequences of every length, the same bits every
+    time, several units of several sequences against the 64-bit form."""
+    B, Hkv, d, G = 20, 32, 128, 64
+    Ts = [9000, 1, 70, 5000, 64, 9000, 33, 7777, 3, 8200, 9000, 640, 9000, 129, 6500, 9000, 2, 8888, 9000, 4096]
+    g = torch.Generator(device=DEV).manual_seed(5)
+    K = torch.randn(B, Hkv, max(Ts), d, generator=g, device=DEV, dtype=torch.float16)
+    V = torch.randn(B, Hkv, max(Ts), d, generator=g, device=DEV, dtype=torch.float16)
+    q = draw(6, B, Hkv, n, d, outliers=False)
+    k, v = _kv(7, B, Hkv, n, d)
+    with ott.ByteCache(B, Hkv, Hkv, d, G, fmt, max_tokens=max(Ts)) as c:
+        c.append_chunk(K, V, lens=Ts)
+        if n == 1:
+            outs = [c.decode_attn(q[:, :, 0].contiguous().to(DEV)).unsqueeze(2) for _ in range(3)]
+        else:
+            outs = [c.chunk_attn(q.to(DEV), k.to(DEV), v.to(DEV)) for _ in range(3)]
+        c.check_device()
+        assert all(torch.equal(outs[0], o) for o in outs[1:])
+        for b in (0, 1, 2, 4, 8, 9, 13, 19):
+            for h in (0, 13, 31):
+                Kx, Vx = K[b, h:h + 1, :Ts[b]].cpu(), V[b, h:h + 1, :Ts[b]].cpu()
+                new = (k[b, h:h + 1], v[b, h:h + 1]) if n > 1 else ()
+                check(outs[0][b, h:h + 1], *bu.attend(q[b, h:h + 1], Kx, Vx, fmt, G, *new), f"{b} {h}")
+    del K, V, outs
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T", [1, 40, 1000, 1024, 1025, 1100, 5000])
+def test_units_of_a_cta_and_of_several(ott, T):
+    """Calls on both sides of the size up to which a CTA serves a unit alone; more warps than items; ragged."""
+    B, Hq, Hkv, d, G = 3, 6, 2, 128, 32
+    Ts = [T, max(1, T // 3), 1]
+    K, V = _kv(31, B, Hkv, T, d)
+    q = draw(33, B, Hq, 4, d, outliers=False)
+    k, v = _kv(34, B, Hkv, 4, d)
+    with ott.ByteCache(B, Hq, Hkv, d, G, "e4m3", max_tokens=T) as c:
+        _fill(c, K, V, Ts)
+        one = c.decode_attn(q[:, :, 0].contiguous().to(DEV))
+        ns = [4, 0, 2]
+        out = c.chunk_attn(q.to(DEV), k.to(DEV), v.to(DEV), lens=ns)
+        for b in range(B):
+            Kb, Vb = K[b, :, :Ts[b]], V[b, :, :Ts[b]]
+            check(one[b].unsqueeze(1), *bu.attend(q[b, :, :1], Kb, Vb, "e4m3", G))
+            m = ns[b]
+            if m:
+                check(out[b, :, :m], *bu.attend(q[b, :, :m], Kb, Vb, "e4m3", G, k[b, :, :m], v[b, :, :m]))
+        c.check_device()
+
+
 def test_beside_an_ott_cache(ott):
     """A model whose first layer is kept in 8 bits and the second in 2: the same loop over both kinds."""
     B, Hq, Hkv, d, T, n = 2, 8, 2, 128, 300, 20
