@@ -2,16 +2,17 @@
 // checks, the host's counts), and the kernels that write it and read it back.
 //
 // Writing. A CTA quantizes the keys or the values of one block: it holds them
-// in registers, finds each channel's smallest and largest value (the keys'
-// are stored for the Top-K bounds), from them a = max |x|, and stores the
-// codes in the pieces that the attention kernels load. It reads a token's 4 d
-// bytes and writes 2 d once each; HBM bounds it.
+// in registers, finds each channel's smallest and largest value (the keys' are
+// stored for the Top-K bounds), from them a = max |x|, and stores the codes in
+// the pieces that the attention kernels load. It reads a token's 4 d bytes and
+// writes 2 d once each; HBM bounds it (32 prompts of 4,096 tokens, 32 heads, d
+// = 128, written and read back, 6.5 GB: 984 us, 6.6 TB/s).
 // The quotient 127 x / a (or 448 x / a) decides a rounding, so it has to fall
 // on the right side of every tie: 127 x is exact in fp32; the quotient differs
-// from a tie by 0 or by more than 2^-19 of itself (both are ratios of integers
+// from a tie by 0 or by more than 2^-20 of itself (both are ratios of integers
 // of at most 18 and 11 bits); and a product with 1 / a, corrected once by its
-// exact residual (Markstein's division), is off by less than 2^-23, and exact where
-// the quotient is a number that fp32 holds.
+// exact residual (Markstein's division), is off by less than 2^-23, and exact
+// where the quotient is a number that fp32 holds.
 //
 // Reading back. A warp takes a group of 16 tokens: codes times the scale in
 // fp32, rounded to fp16, to rows in shared memory (the values transposed by
@@ -29,9 +30,10 @@ using namespace ott;
 namespace {
 
 constexpr int READ_WARPS = 8;
-// Threads of an append CTA: eight 16-byte pieces of one block each (with four,
-// the fixed part of a thread's work took as many instructions as its pieces:
-// PLACEHOLDER).
+// Threads of an append CTA: eight 16-byte pieces of one block each. (With four,
+// and scalar arithmetic, a thread's fixed work was half of its instructions:
+// 131K tokens of 8 units in blocks of 64 took 136 us, now 118, in blocks of 32
+// 100 us per 400 MB, now 60.)
 __host__ __device__ constexpr int app_threads(int d, int g) { return g * d / 64; }
 
 struct AppendArgs {

@@ -18,18 +18,26 @@
 // tokens, or 32 tokens of a block (64 d bytes, contiguous, as the lanes'
 // fragments: 16-byte loads from shared memory, no transposition; and the
 // block's record). Every warp gets an equal contiguous run of the items of all
-// units, with a ring of stages of its own that its copies fill ahead.
-//
+// units, with a ring of stages of its own that its copies fill ahead. It leaves
+// one partial per unit that it touches, in a place that goes by the run;
+// k_byte_combine merges the partials of a row. A CTA whose warps all work for
+// one unit merges their results first (131K tokens of 8 kv heads: 33 partials a
+// row instead of 152, the merge 8 -> 5 us).
 // SMs do not get equal shares of HBM: with equal runs alone, the warps of batch
-// 32 x 4K, 32 heads, ended between 133 and 168 us.
-// So of a unit's items in long calls only the first seven eighths (its A items) are cut into equal runs, one per
-// warp; the rest (B items) are cut into short runs, about three per warp,
-// which warps claim from a counter when they have nothing else to copy. A run leaves
-// one partial per unit that it touches, in a place that goes by the run's number: who took
-// it does not show in the result. k_byte_combine merges the partials of a row.
-// (Other calls have A items only; a CTA whose warps then all work for one unit
-// merges their results. The shortest calls, units of up to 1,024 tokens and no more of them than
-// SMs, give every unit a CTA, which writes its rows: no second kernel.)
+// 32 x 4K, 32 heads, ended between 133 and 168 us. So in long calls only the
+// first seven eighths of a unit's items (its A items) are cut into equal runs,
+// one per warp; the rest (B items) are cut into short runs, about three per
+// warp, which warps claim from a counter when they have nothing else to copy.
+// Who took a run does not show in the result.
+// The shortest calls, units of up to 1,024 tokens and no more of them than SMs,
+// give every unit a CTA, which writes its rows: no second kernel.
+//
+// What bounds it: HBM. Batch 32 x 4K, 32 heads of d = 128 (1.07 GB of cache)
+// takes 161 us, 6.7 TB/s; with four queries each, 165. Calls of a few ten us
+// add the start of the copies and the merge: 131K tokens, 8 kv heads (269 MB),
+// 46 us, 5.8 TB/s; 32 sequences of 1K to 7K from a paged pool (272 MB) 50.5. 12
+// warps with two stages each instead of 8 with three: 161 and 50.5 us became
+// 160 and 53.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -157,7 +165,8 @@ struct Cursor {
 
 // What a stage holds: valid tokens (0: none, nothing to wait for; -1: no more
 // items), the unit, first fp16 token (of the new ones: + FRESH; -1: a block's
-// item), whether it is the first of its unit in the run, and if it is the last the partial's place, else -1.
+// item), whether it is the first of its unit in the run, and if it is the last
+// the partial's place, else -1.
 struct Desc {
     int valid, e, hkv, sl, f0, first, part, pad;
 };
@@ -772,11 +781,11 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
 // A slab is 32 blocks' channel ranges in shared memory (16-byte pieces turned
 // by the block, so that 8 lanes that read one piece of their own blocks meet
 // all banks). A warp takes a (slab, token, four of its heads): a lane per
-// block. max(q lo, q hi) is q hi for positive q, else q lo, and products of
-// two fp16 numbers are exact: a selection and a multiply-add, which rounds
-// once, as the sum does. A warp alone on its scheduler needs some 30 cycles
-// per channel; with few tasks that latency is what counts (two blocks per
-// lane: fewer operations in all, but 55 cycles), with many the operations.
+// block. max(q lo, q hi) is q hi for positive q, else q lo, and products of two
+// fp16 numbers are exact: a selection and a multiply-add, which rounds once, as
+// the sum does. A warp alone on its scheduler needs some 30 cycles per channel;
+// with few tasks that latency is what counts (two blocks per lane: fewer
+// operations in all, but 55 cycles), with many the operations.
 constexpr int SEL_THREADS = 512, SLAB = 32, SLABS = 8, SEL_CLUSTER = 16;
 
 struct SelectArgs {
@@ -949,13 +958,11 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
         W += S * c->Hkv * Iu;
         units += S * c->Hkv;
     }
-    // A items in equal runs, at least two items each, sums ending after
-    // SUM_TOKENS tokens. An eighth of the units as B items where a warp has 64 items or more and
-    // a unit 16 runs at most; elsewhere their partials cost more than they even out.
-    // Without and with them: batch 32 x 4K, 32 heads (108 items a warp, 1.2 runs a unit) 166 and
-    // 161 us, four queries each 182 and 165; batch 16 x 32K, 8 kv heads (9.5 runs)
-    // 164 and 162; 4 x 131K (38 runs) 161 and 163; 600K tokens, 8 kv heads (152 runs) 183
-    // and 193; 131K (27 items a warp) 46 and 51 to 60.
+    // A items in equal runs, at least two items each, sums ending after SUM_TOKENS tokens. An eighth of the units
+    // as B items where a warp has 64 items or more and a unit 16 runs at most; elsewhere their partials cost more
+    // than they even out. Without and with them: batch 32 x 4K, 32 heads (108 items a warp, 1.2 runs a unit) 166
+    // and 161 us, four queries each 182 and 165; batch 16 x 32K, 8 kv heads (9.5 runs) 164 and 162; 4 x 131K (38
+    // runs) 161 and 163; 600K tokens, 8 kv heads (152 runs) 183 and 193; 131K (27 items a warp) 46 and 51 to 60.
     int ctas = c->sm_count;
     while (ctas < (1 << 20) && W / ((long long)ctas * WARPS) >= SUM_TOKENS / QT) ctas += c->sm_count;
     a.NWp = (int)std::max<long long>(1, std::min<long long>((long long)ctas * WARPS, W / 2));

@@ -25,21 +25,23 @@
 // all tiles (a tile cut between CTAs leaves partials, merged by
 // k_byte_tiles_combine), or a tile of its own, whichever is estimated to end
 // first (plan_byte_tiles). After SUM_STEPS steps of a tile, whoever takes the
-// next ones, its sums are carried over in fp32 (finish): the tensor cores truncate.
+// next ones, its sums are carried over in fp32 (finish): the tensor cores
+// truncate.
 //
 // What bounds it: 512 tokens of four sequences over 32K (8 kv heads, 4 heads
-// each, d = 128) take 850 us, 1.31 PFLOP/s; 2,048 over 131K 3.12 ms, 1.42. A step is some 2,900 cycles, 1,920 of
-// them products (a score product takes as long for 112 keys as for 128: its
-// queries are read at 64 bytes a cycle). The rest is the chain that a tile
-// goes through, since S(j+1) takes the place of P(j): softmax about 1,500, then O
-// and S, 450 each, and the handing over; no part of it alone (with fewer
-// products, no exponentials, no unpacking, or no stores of the producers the same
-// call takes 3 to 7% less). Weights handed over in one part: 875 us. Not taken, all
-// measured on that call: steps of 80 tokens whose S(j+1) has columns of its own, so that
-// the softmax never waits (1,040: a score product costs the same for 80 keys); that with a
-// warp of products per tile (957); a warp of products per tile and six
-// producers, with steps of 112 (988); exponentials of one group under the conversions of the one before
-// (885: registers spill); loops over the groups (910 to 980).
+// each, d = 128) take 850 us, 1.31 PFLOP/s; 2,048 over 131K 3.12 ms, 1.42. A
+// step is some 2,900 cycles, 1,920 of them products (a score product takes as
+// long for 112 keys as for 128: its queries are read at 64 bytes a cycle). The
+// rest is the chain that a tile goes through, since S(j+1) takes the place of
+// P(j): softmax about 1,500, then O and S, 450 each, and the handing over; no
+// part of it alone (with fewer products, no exponentials, no unpacking, or no
+// stores of the producers the same call takes 3 to 7% less). Weights handed
+// over in one part: 875 us. Not taken, all measured on that call: steps of 80
+// tokens whose S(j+1) has columns of its own, so that the softmax never waits
+// (1,040: a score product costs the same for 80 keys); that with a warp of
+// products per tile (957); a warp of products per tile and six producers, with
+// steps of 112 (988); exponentials of one group under the conversions of the
+// one before (885: registers spill); loops over the groups (910 to 980).
 #include <algorithm>
 #include <climits>
 #include <cmath>

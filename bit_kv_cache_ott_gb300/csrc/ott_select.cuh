@@ -21,18 +21,18 @@ constexpr uint32_t EMPTY = 0xffffffffu;           // key of an empty block
 // Words of shared memory for a selection among n blocks.
 __host__ __device__ constexpr int pick_words(int n) { return n + 2 * ((n + 31) / 32); }
 
-// The selection among n bounds (-inf: an empty block), by a CTA of whole
-// warps: the first min(K, non-empty) under (bound descending, index ascending),
-// into out[0 .. Kc) in ascending order, -1 behind them. An exact radix select:
-// key_j = the bit-inverted ordered bound (smallest key = largest bound). The
-// bits above the highest one in which keys differ are known (bounds are of
-// one magnitude: a first histogram over sign and exponent would put all keys
-// into a few bins, whose atomics go one after another). Rounds over 8-bit
-// digits below them, each a histogram of the keys that match the digits found
-// so far, end when every key that still matches is selected. Two counts
-// per 32 keys (selected, and equal to the last prefix) and their prefix sums
-// give each selected block its place.
-// The bounds: the largest of bd[j], bd[stride + j] .. of `groups` of them.
+// The selection among n bounds (-inf: an empty block), by a CTA of whole warps:
+// the first min(K, non-empty) under (bound descending, index ascending), into
+// out[0 .. Kc) in ascending order, -1 behind them. An exact radix select: key_j
+// = the bit-inverted ordered bound (smallest key = largest bound). The bits
+// above the highest one in which keys differ are known (bounds are of one
+// magnitude: a first histogram over sign and exponent would put all keys into a
+// few bins, whose atomics go one after another). Rounds over 8-bit digits below
+// them, each a histogram of the keys that match the digits found so far, end
+// when every key that still matches is selected. Two counts per 32 keys
+// (selected, and equal to the last prefix) and their prefix sums give each
+// selected block its place. The bounds: the largest of bd[j], bd[stride + j] ..
+// of `groups` of them.
 __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int stride, int n, int K, int Kc, int32_t *out, uint32_t *key) {
     __shared__ int hist[256];
     __shared__ uint32_t red[3][SORT_THREADS / 32];
