@@ -38,6 +38,7 @@ struct ott_byte_cache {
     int U, g, NB;
     long long blk_bytes;
     int poisoned, device, sm_count, smem_optin;
+    int max_cluster;    // CTAs of a cluster that selects blocks
     void *mem;
     size_t mem_bytes;
     uint8_t *blk;
@@ -68,7 +69,7 @@ struct ByteCall {
     int32_t *sel;      // [B][n][Hkv][Kc] or null
 };
 int run_byte_attn(const ott_byte_cache *c, const ByteCall &call, cudaStream_t s, cudaError_t &err);
-cudaError_t set_byte_attributes(const ott_byte_cache *c);
+cudaError_t set_byte_attributes(ott_byte_cache *c);
 
 // One sequence of an attention launch.
 struct ByteSeq {

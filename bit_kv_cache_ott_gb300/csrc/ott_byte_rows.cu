@@ -1012,7 +1012,7 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
         // CTAs per (sequence, kv head): as many as give every SM one, but a slab each (two each: five drafts 38 -> 43 us)
         const int slabs = std::max(1, (p.nbmax + SLAB - 1) / SLAB);
         int cluster = 1;
-        while (cluster < SEL_CLUSTER && 2 * cluster <= slabs && (long long)a.nseq * c->Hkv * cluster < c->sm_count)
+        while (cluster < c->max_cluster && 2 * cluster <= slabs && (long long)a.nseq * c->Hkv * cluster < c->sm_count)
             cluster *= 2;
         p.ba = {c->dig, a.bt, call.q, nullptr, nullptr, call.n, B0, c->Hq, c->Hkv, c->g, c->NB, call.topk, Kc, p.nbmax,
                 (c->g + 3) / 4, cluster, std::min(SLABS, (slabs + cluster - 1) / cluster)};
@@ -1029,7 +1029,7 @@ cudaError_t launch_rows(const Plan &p, cudaStream_t s) {
 
 template <int D>
 int select_smem(int slabs, int nb) {
-    return std::max(slabs * slab_bytes<D>() + SEL_THREADS / 32 * heads_bytes<D>(), pick_words(nb) * 4);
+    return std::max(slabs * slab_bytes<D>() + SEL_THREADS / 32 * heads_bytes<D>(), nb * 4);
 }
 
 template <int D>
@@ -1084,11 +1084,28 @@ int pick_smem(const ott_byte_cache *c) { return c->smem_optin - 2048; }
 
 }  // namespace
 
-cudaError_t set_byte_attributes(const ott_byte_cache *c) {
+cudaError_t set_byte_attributes(ott_byte_cache *c) {
     cudaError_t e = c->d == 128 ? set_attributes<128>(c->format) : set_attributes<64>(c->format);
     auto *select = c->d == 128 ? k_byte_select<128> : k_byte_select<64>;
     if (e == cudaSuccess) e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, pick_smem(c));
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);   // 16 CTAs
+    // clusters of 16 CTAs where this GPU has room for them, else of 8
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    c->max_cluster = 8;
+    if (e == cudaSuccess) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(SEL_CLUSTER);
+        cfg.blockDim = dim3(SEL_THREADS);
+        cfg.dynamicSmemBytes = (size_t)pick_smem(c);
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = SEL_CLUSTER;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int fit = 0;
+        if (cudaOccupancyMaxActiveClusters(&fit, select, &cfg) == cudaSuccess && fit > 0) c->max_cluster = SEL_CLUSTER;
+        else cudaGetLastError();
+    }
     return e == cudaSuccess ? set_byte_tiles_attributes(c->d, c->format) : e;
 }
 
@@ -1098,7 +1115,7 @@ int run_byte_attn(const ott_byte_cache *c, const ByteCall &call, cudaStream_t s,
     int nb_all = 0;   // the most blocks of any sequence: the width of the lists that a caller gets
     for (int b = 0; b < c->B; ++b) nb_all = std::max(nb_all, c->T[b] / c->G);
     const int Kc = std::min(call.topk, nb_all);
-    if (Kc > 0 && (nb_all > (1 << 20) || pick_words(nb_all) * 4 > pick_smem(c))) return OTT_ERR_INVALID;
+    if (Kc > 0 && (long long)nb_all * 4 > pick_smem(c)) return OTT_ERR_INVALID;
     // With nothing to select, the call is the one over every block.
     ByteCall cl = call;
     if (Kc == 0) cl.topk = 0;

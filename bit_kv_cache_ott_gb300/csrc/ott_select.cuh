@@ -18,9 +18,6 @@ __device__ __forceinline__ uint32_t ordered(float f) {
 
 constexpr uint32_t EMPTY = 0xffffffffu;           // key of an empty block
 
-// Words of shared memory for a selection among n blocks.
-__host__ __device__ constexpr int pick_words(int n) { return n + 2 * ((n + 31) / 32); }
-
 // The selection among n bounds (-inf: an empty block), by a CTA of whole warps:
 // the first min(K, non-empty) under (bound descending, index ascending), into
 // out[0 .. Kc) in ascending order, -1 behind them. An exact radix select: key_j
@@ -29,16 +26,18 @@ __host__ __device__ constexpr int pick_words(int n) { return n + 2 * ((n + 31) /
 // magnitude: a first histogram over sign and exponent would put all keys into a
 // few bins, whose atomics go one after another). Rounds over 8-bit digits below
 // them, each a histogram of the keys that match the digits found so far, end
-// when every key that still matches is selected. Two counts per 32 keys
-// (selected, and equal to the last prefix) and their prefix sums give each
-// selected block its place. The bounds: the largest of bd[j], bd[stride + j] ..
-// of `groups` of them.
+// when every key that still matches is selected. Then 32 keys at a time give
+// way to two masks (below the last prefix, equal to it) and their counts, whose
+// prefix sums give each selected block its place. The bounds: the largest of
+// bd[j], bd[stride + j] .. of `groups` of them. key: n words of shared memory.
 __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int stride, int n, int K, int Kc, int32_t *out, uint32_t *key) {
     __shared__ int hist[256];
     __shared__ uint32_t red[3][SORT_THREADS / 32];
     __shared__ int s_digit, s_below, s_count;
     const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, wid = tid >> 5, nseg = (n + 31) / 32;
-    int *const below = reinterpret_cast<int *>(key + n), *const equal = below + nseg;
+    // masks and counts of segment x take the place of its keys, the last one's, which may be fewer than four, a place of their own
+    __shared__ uint32_t tail[4];
+    auto seg = [&](int x) { return x + 1 < nseg ? key + 32 * x : tail; };
     uint32_t all = EMPTY, any = 0;
     int ne = 0;
     constexpr int BATCH = 8;   // bounds in flight per thread
@@ -133,16 +132,21 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int str
     for (int j = tid; j < 32 * nseg; j += nth) {
         const uint32_t k = j < n ? key[j] : EMPTY, m = k & mask;
         const unsigned lt = __ballot_sync(0xffffffffu, k != EMPTY && m < prefix), eq = __ballot_sync(0xffffffffu, k != EMPTY && m == prefix);
-        if (lane == 0) {
-            below[j / 32] = __popc(lt);
-            equal[j / 32] = __popc(eq);
+        if (lane == 0) {   // (behind the votes all lanes have read their keys)
+            uint32_t *w = seg(j / 32);
+            w[0] = lt;
+            w[1] = eq;
+            w[2] = __popc(lt);
+            w[3] = __popc(eq);
         }
     }
     __syncthreads();
     if (wid == 0) {
         int lt0 = 0, eq0 = 0;
         for (int x = 0; x < nseg; x += 32) {
-            const int lt = x + lane < nseg ? below[x + lane] : 0, eq = x + lane < nseg ? equal[x + lane] : 0;
+            const bool in = x + lane < nseg;
+            uint32_t *w = seg(in ? x + lane : nseg - 1);
+            const int lt = in ? (int)w[2] : 0, eq = in ? (int)w[3] : 0;
             int a = lt, b = eq;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -152,9 +156,9 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int str
                     b += z;
                 }
             }
-            if (x + lane < nseg) {
-                below[x + lane] = lt0 + a - lt;
-                equal[x + lane] = eq0 + b - eq;
+            if (in) {
+                w[2] = lt0 + a - lt;
+                w[3] = eq0 + b - eq;
             }
             lt0 += __shfl_sync(0xffffffffu, a, 31);
             eq0 += __shfl_sync(0xffffffffu, b, 31);
@@ -164,11 +168,10 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int str
     const unsigned before = (1u << lane) - 1u;
 #pragma unroll 4
     for (int j = tid; j < 32 * nseg; j += nth) {
-        const uint32_t k = j < n ? key[j] : EMPTY, m = k & mask;
-        const bool l = k != EMPTY && m < prefix, e = k != EMPTY && m == prefix;
-        const unsigned lt = __ballot_sync(0xffffffffu, l), eq = __ballot_sync(0xffffffffu, e);
-        const int nl = below[j / 32] + __popc(lt & before), nq = equal[j / 32] + __popc(eq & before);
-        if (l || (e && nq < need)) out[nl + min(nq, need)] = j;
+        const uint32_t *w = seg(j / 32);
+        const unsigned lt = w[0], eq = w[1];
+        const int nl = (int)w[2] + __popc(lt & before), nq = (int)w[3] + __popc(eq & before);
+        if ((lt >> lane & 1u) || ((eq >> lane & 1u) && nq < need)) out[nl + min(nq, need)] = j;
     }
     for (int i = want + tid; i < Kc; i += nth) out[i] = -1;
 }

@@ -154,6 +154,29 @@ def test_selected_blocks(ott, fmt, B, Hq, Hkv, d, G, Ts, n, topk):
         c.check_device()
 
 
+@pytest.mark.parametrize("T,K", [(300000, 700), (40000, 1249), (32 * 33, 5), (32 * 2, 1), (32 * 34 + 5, 34)])
+def test_selected_among_many_blocks(ott, T, K):
+    """More blocks than a cluster's shared memory holds at once, every number of blocks in the last 32, ties throughout
+    (keys repeat), selections of nearly all of them."""
+    d, G, Hq = 64, 32, 3
+    g = torch.Generator().manual_seed(T)
+    Kx = torch.randn(1, 1, 997 * G, d, generator=g).half().repeat(1, 1, T // (997 * G) + 1, 1)[:, :, :T].contiguous()
+    V = torch.randn(1, 1, T, d, generator=g).half()
+    q = torch.randn(1, Hq, d, generator=g).half()
+    with ott.ByteCache(1, Hq, 1, d, G, max_tokens=T, pool_blocks=T // G) as c:
+        _fill(c, Kx, V, [T])
+        sel = torch.full((1, 1, min(K, T // G)), 7, dtype=torch.int32, device=DEV)
+        out = c.decode_attn_topk(q.to(DEV), K, sel=sel)
+        ch = bu.choose(q[0].unsqueeze(1), Kx[0], G, K)
+        assert sel[0, 0].tolist() == ch[0][0]
+        see = torch.ones(T, dtype=torch.bool)
+        see[:T // G * G] = torch.zeros(T // G, dtype=torch.bool).index_fill_(0, torch.tensor(ch[0][0]), True).repeat_interleave(G)
+        Kh, Vh = (bu.held(x[0], "int8", G)[0][0][see] for x in (Kx, V))
+        ref = torch.softmax(q[0].double() @ Kh.t() / d ** 0.5, 1) @ Vh
+        assert (out[0].double().cpu() - ref).abs().max().item() <= 2e-3   # outputs below 1: two roundings of 2^-11
+        c.check_device()
+
+
 def test_more_blocks_than_there_are_is_every_block(ott):
     B, Hq, Hkv, d, G, T = 2, 4, 2, 128, 32, 500
     K, V = _kv(8, B, Hkv, T, d)
