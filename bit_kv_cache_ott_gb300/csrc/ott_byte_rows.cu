@@ -806,7 +806,7 @@ template <int D>
 __host__ __device__ constexpr int heads_bytes() { return D * 16; }   // four heads per channel
 
 template <int D>
-__global__ void __launch_bounds__(SEL_THREADS)
+__global__ void __launch_bounds__(SEL_THREADS, 2)
     k_byte_select(const __grid_constant__ SelectArgs a, const __grid_constant__ SelectTable t) {
     constexpr int V4 = D / 4, WARPS = SEL_THREADS / 32;
     extern __shared__ __align__(128) uint8_t smem[];
