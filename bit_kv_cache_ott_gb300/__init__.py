@@ -596,7 +596,7 @@ class ByteCache:
 
     def prefill_lens(self, K: torch.Tensor, V: torch.Tensor, lens, stream=None):
         """The same with lens[b] tokens for sequence b."""
-        if any(self.seq_counts(b)[0] for b in range(self.B)):
+        if self.seq_counts(-1)[0]:
             raise OTTError(OTT_ERR_STATE, "prefill of a cache that holds tokens")
         self.append_chunk(K, V, lens, stream)
 
@@ -662,7 +662,7 @@ class ByteCache:
     def _sel(self, sel, n, K):
         if sel is None:
             return None
-        slots = min(int(K), max(self.seq_counts(b)[1] for b in range(self.B)))
+        slots = min(int(K), self.seq_counts(-1)[1])
         shapes = [(self.B, n, self.Hkv, slots)] + ([(self.B, self.Hkv, slots)] if n == 1 else [])
         if not isinstance(sel, torch.Tensor) or not sel.is_cuda or sel.dtype != torch.int32:
             raise TypeError("sel: expected a CUDA int32 tensor")
@@ -679,7 +679,7 @@ class ByteCache:
         self._call(self._L.ott_byte_reset, "ott_byte_reset", stream=stream)
 
     def seq_counts(self, b: int):
-        """(tokens of sequence b, its complete blocks per kv head)."""
+        """(tokens of sequence b, its complete blocks per kv head); b = -1: of the longest sequence."""
         T, nb = C.c_longlong(), C.c_int()
         _check(self._L.ott_byte_counts(self._h, _int32(b, "b"), C.byref(T), C.byref(nb)), "ott_byte_counts")
         return T.value, nb.value

@@ -634,9 +634,10 @@ int ott_byte_reset(ott_byte_cache *c, void *stream) {
 }
 
 int ott_byte_counts(const ott_byte_cache *c, int b, long long *T, int *blocks) {
-    if (!c || b < 0 || b >= c->B) return OTT_ERR_INVALID;
-    if (T) *T = c->T[b];
-    if (blocks) *blocks = c->T[b] / c->G;
+    if (!c || b < -1 || b >= c->B) return OTT_ERR_INVALID;
+    const int t = b < 0 ? *std::max_element(c->T.begin(), c->T.end()) : c->T[b];
+    if (T) *T = t;
+    if (blocks) *blocks = t / c->G;
     return OTT_OK;
 }
 

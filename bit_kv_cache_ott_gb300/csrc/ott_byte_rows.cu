@@ -778,15 +778,17 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
 // A cluster of up to 16 CTAs per (sequence, kv head) takes the bounds of its
 // blocks for every token of the sequence, and then, one token per CTA, the
 // selection.
-// A slab is 32 blocks' channel ranges in shared memory (16-byte pieces turned
-// by the block, so that 8 lanes that read one piece of their own blocks meet
-// all banks). A warp takes a (slab, token, four of its heads): a lane per
-// block. max(q lo, q hi) is q hi for positive q, else q lo, and products of two
-// fp16 numbers are exact: a selection and a multiply-add, which rounds once, as
-// the sum does. A warp alone on its scheduler needs some 30 cycles per channel;
-// with few tasks that latency is what counts (two blocks per lane: fewer
-// operations in all, but 55 cycles), with many the operations.
-constexpr int SEL_THREADS = 512, SLAB = 32, SLABS = 8, SEL_CLUSTER = 16;
+// A slab is 32 BPL blocks' channel ranges in shared memory (16-byte pieces
+// turned by the block, so that 8 lanes that read one piece of their own blocks
+// meet all banks). A warp takes a (slab, token, four of its heads): BPL blocks
+// per lane. max(q lo, q hi) is q hi for positive q, else q lo, and products of
+// two fp16 numbers are exact: a selection and a multiply-add, which rounds
+// once, as the sum does. A warp alone on its scheduler needs some 30 cycles per
+// channel (BPL = 1; 55 with 2), which counts where a CTA has no more tasks than
+// warps; elsewhere shared memory bounds it, 4 cycles per channel for the
+// queries of a task and one for a lane's block, so two blocks per lane share
+// the queries (drafts of five tokens over 512 blocks, seven heads: 35.4 -> 33.5 us in all).
+constexpr int SEL_THREADS = 512, SEL_BLOCKS = 256, SEL_CLUSTER = 16;   // blocks in shared memory at a time
 
 struct SelectArgs {
     const __half2 *dig;
@@ -795,20 +797,18 @@ struct SelectArgs {
     float *bound;       // [nseq][n][Hkv][groups][stride]: by four heads
     int32_t *sel;       // [B][n][Hkv][Kc]
     int n, B0, Hq, Hkv, g, NB, K, Kc, stride;
-    int groups, cluster, slabs;   // groups of four heads per kv head; CTAs per (sequence, kv head), slabs in shared memory at a time
+    int groups, cluster, slabs;   // (of 32 blocks, even where BPL is 2) groups of four heads per kv head; CTAs per (sequence, kv head), slabs in shared memory at a time
 };
 struct SelectTable {
     int nb[CHUNK_SEQS], nq[CHUNK_SEQS];
 };
 template <int D>
-__host__ __device__ constexpr int slab_bytes() { return SLAB * D * 4; }
-template <int D>
 __host__ __device__ constexpr int heads_bytes() { return D * 16; }   // four heads per channel
 
-template <int D>
+template <int D, int BPL>
 __global__ void __launch_bounds__(SEL_THREADS, 2)
     k_byte_select(const __grid_constant__ SelectArgs a, const __grid_constant__ SelectTable t) {
-    constexpr int V4 = D / 4, WARPS = SEL_THREADS / 32;
+    constexpr int V4 = D / 4, WARPS = SEL_THREADS / 32, SLAB = 32 * BPL;
     extern __shared__ __align__(128) uint8_t smem[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int rank = blockIdx.x % a.cluster, unit = blockIdx.x / a.cluster, e = unit / a.Hkv, hkv = unit % a.Hkv;
@@ -816,10 +816,10 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
     const int u = (a.B0 + e) * a.Hkv + hkv, nb = t.nb[e], nq = t.nq[e];
     const int all = (nb + SLAB - 1) / SLAB, per = (all + a.cluster - 1) / a.cluster, s0 = min(all, rank * per),
               s1 = nq > 0 ? min(all, s0 + per) : s0;
-    float4 *const heads = reinterpret_cast<float4 *>(smem + a.slabs * slab_bytes<D>() + warp * heads_bytes<D>());
+    float4 *const heads = reinterpret_cast<float4 *>(smem + a.slabs * (32 * D * 4) + warp * heads_bytes<D>());
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int sb = s0; sb < s1; sb += a.slabs) {
-        const int ns = min(a.slabs, s1 - sb);
+    for (int sb = s0; sb < s1; sb += a.slabs / BPL) {
+        const int ns = min(a.slabs / BPL, s1 - sb);
         if (sb > s0) __syncthreads();   // the slabs before are read
         for (int z = threadIdx.x; z < ns * SLAB * V4; z += SEL_THREADS) {
             const int x = z / V4, v = z % V4, j = sb * SLAB + x;
@@ -846,24 +846,35 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
             for (int y = 0; y < D / 32; ++y)
                 heads[32 * y + lane] = make_float4(__half2float(qv[0][y]), __half2float(qv[1][y]), __half2float(qv[2][y]), __half2float(qv[3][y]));
             __syncwarp();
-            float sum[4] = {};
-#pragma unroll 4
+            float sum[BPL][4] = {};
+#pragma unroll(4 / BPL)
             for (int c4 = 0; c4 < V4; ++c4) {
-                const uint4 d = row[c4 ^ (lane & 7)];
-                const uint32_t w[4] = {d.x, d.y, d.z, d.w};
+                uint32_t w[BPL][4];
+#pragma unroll
+                for (int o = 0; o < BPL; ++o) {
+                    const uint4 d = row[o * (32 * V4) + (c4 ^ (lane & 7))];
+                    w[o][0] = d.x; w[o][1] = d.y; w[o][2] = d.z; w[o][3] = d.w;
+                }
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     const float4 q4 = heads[4 * c4 + y];
                     const float qs[4] = {q4.x, q4.y, q4.z, q4.w};
-                    const float2 f = __half22float2(ch_as_h2(w[y]));
 #pragma unroll
-                    for (int p = 0; p < 4; ++p) sum[p] = __fmaf_rn(qs[p], qs[p] > 0.0f ? f.y : f.x, sum[p]);
+                    for (int o = 0; o < BPL; ++o) {
+                        const float2 f = __half22float2(ch_as_h2(w[o][y]));
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) sum[o][p] = __fmaf_rn(qs[p], qs[p] > 0.0f ? f.y : f.x, sum[o][p]);
+                    }
                 }
             }
-            float best = -CUDART_INF_F;
 #pragma unroll
-            for (int p = 0; p < 4; ++p) best = sum[p] > best ? sum[p] : best;
-            if (j < nb) a.bound[((((size_t)e * a.n + tk) * a.Hkv + hkv) * a.groups + grp) * a.stride + j] = best;
+            for (int o = 0; o < BPL; ++o) {
+                float best = -CUDART_INF_F;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) best = sum[o][p] > best ? sum[o][p] : best;
+                if (j + 32 * o < nb)
+                    a.bound[((((size_t)e * a.n + tk) * a.Hkv + hkv) * a.groups + grp) * a.stride + j + 32 * o] = best;
+            }
         }
     }
     // every CTA of the cluster comes by here; the bounds are visible to all of them behind it
@@ -883,6 +894,7 @@ struct Plan {
     SelectArgs ba;
     SelectTable bt;
     bool any, pick;
+    bool two;      // bounds: two blocks per lane
     int NC;        // groups of 8 rows; 0: tiles
     int ctas;
     int nC;        // tiles: CTAs
@@ -1010,12 +1022,14 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
     p.cw = (int)std::min<long long>(CMB_MAXW, (parts + 7) / 8);
     if (pick) {
         // CTAs per (sequence, kv head): as many as give every SM one, but a slab each (two each: five drafts 38 -> 43 us)
-        const int slabs = std::max(1, (p.nbmax + SLAB - 1) / SLAB);
+        const int slabs = std::max(1, (p.nbmax + 31) / 32);
         int cluster = 1;
         while (cluster < c->max_cluster && 2 * cluster <= slabs && (long long)a.nseq * c->Hkv * cluster < c->sm_count)
             cluster *= 2;
+        const int groups = (c->g + 3) / 4, own = (slabs + cluster - 1) / cluster;   // slabs of a CTA
+        p.two = (long long)own * nq_max * groups > SEL_THREADS / 32;
         p.ba = {c->dig, a.bt, call.q, nullptr, nullptr, call.n, B0, c->Hq, c->Hkv, c->g, c->NB, call.topk, Kc, p.nbmax,
-                (c->g + 3) / 4, cluster, std::min(SLABS, (slabs + cluster - 1) / cluster)};
+                groups, cluster, std::min(SEL_BLOCKS / 32, p.two ? (own + 1) / 2 * 2 : own)};
         p.bound_floats = (size_t)a.nseq * call.n * c->Hkv * ((c->g + 3) / 4) * p.nbmax;
     }
     return true;
@@ -1029,7 +1043,7 @@ cudaError_t launch_rows(const Plan &p, cudaStream_t s) {
 
 template <int D>
 int select_smem(int slabs, int nb) {
-    return std::max(slabs * slab_bytes<D>() + SEL_THREADS / 32 * heads_bytes<D>(), nb * 4);
+    return std::max(slabs * (32 * D * 4) + SEL_THREADS / 32 * heads_bytes<D>(), nb * 4);
 }
 
 template <int D>
@@ -1047,7 +1061,7 @@ cudaError_t launch_select(const ott_byte_cache *c, const Plan &p, cudaStream_t s
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, k_byte_select<D>, p.ba, p.bt);
+    return cudaLaunchKernelEx(&cfg, p.two ? k_byte_select<D, 2> : k_byte_select<D, 1>, p.ba, p.bt);
 }
 
 template <int D>
@@ -1086,12 +1100,13 @@ int pick_smem(const ott_byte_cache *c) { return c->smem_optin - 2048; }
 
 cudaError_t set_byte_attributes(ott_byte_cache *c) {
     cudaError_t e = c->d == 128 ? set_attributes<128>(c->format) : set_attributes<64>(c->format);
-    auto *select = c->d == 128 ? k_byte_select<128> : k_byte_select<64>;
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, pick_smem(c));
     // clusters of 16 CTAs where this GPU has room for them, else of 8
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    c->max_cluster = 8;
-    if (e == cudaSuccess) {
+    c->max_cluster = SEL_CLUSTER;
+    for (int two = 0; two < 2 && e == cudaSuccess; ++two) {
+        auto *select = c->d == 128 ? (two ? k_byte_select<128, 2> : k_byte_select<128, 1>)
+                                   : (two ? k_byte_select<64, 2> : k_byte_select<64, 1>);
+        e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize, pick_smem(c));
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(SEL_CLUSTER);
         cfg.blockDim = dim3(SEL_THREADS);
@@ -1103,8 +1118,10 @@ cudaError_t set_byte_attributes(ott_byte_cache *c) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int fit = 0;
-        if (cudaOccupancyMaxActiveClusters(&fit, select, &cfg) == cudaSuccess && fit > 0) c->max_cluster = SEL_CLUSTER;
-        else cudaGetLastError();
+        if (cudaOccupancyMaxActiveClusters(&fit, select, &cfg) != cudaSuccess || fit < 1) {
+            cudaGetLastError();
+            c->max_cluster = 8;
+        }
     }
     return e == cudaSuccess ? set_byte_tiles_attributes(c->d, c->format) : e;
 }

@@ -520,7 +520,7 @@ int ott_byte_release(ott_byte_cache *c, int b, void *stream);
 /* Every sequence drops its tokens. */
 int ott_byte_reset(ott_byte_cache *c, void *stream);
 
-/* Tokens of sequence b and its complete blocks per kv head. Host-side. */
+/* Tokens of sequence b (-1: of the longest one) and its complete blocks per kv head. Host-side. */
 int ott_byte_counts(const ott_byte_cache *c, int b, long long *T, int *blocks);
 
 /* Free blocks of the pool (host-side), -1 without one. */
