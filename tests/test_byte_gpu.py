@@ -127,6 +127,7 @@ def test_attention(ott, fmt, case):
 @pytest.mark.parametrize("B,Hq,Hkv,d,G,Ts,n,topk", [
     (2, 2, 2, 128, 32, [500, 333], 1, 3), (1, 8, 2, 64, 32, [1999], 4, 1), (3, 9, 1, 128, 64, [10, 64, 700], 2, 4),
     (1, 20, 1, 64, 32, [640], 3, 5), (2, 4, 4, 128, 128, [1280, 127], 2, 100), (1, 4, 1, 128, 32, [4000], 2, 60),
+    (2, 4, 2, 64, 32, [700, 90], 100, 3),
 ])
 def test_selected_blocks(ott, fmt, B, Hq, Hkv, d, G, Ts, n, topk):
     K, V = _kv(5, B, Hkv, max(Ts), d)
@@ -325,7 +326,9 @@ def test_capacity_and_refusals(ott):
         assert code(c.append_chunk, K, V, lens=[0, 70]) == ott.OTT_ERR_CAPACITY   # 4 blocks, 3 free
         assert code(c.append_chunk, K, V, lens=[0, 71]) == ott.OTT_ERR_INVALID
         assert code(c.append_chunk, K, V, lens=[-1, 0]) == ott.OTT_ERR_INVALID
-        assert c.seq_counts(0) == (40, 1) and c.seq_counts(1) == (0, 0) and c.free_blocks() == 3
+        assert c.seq_counts(0) == c.seq_counts(-1) == (40, 1) and c.seq_counts(1) == (0, 0) and c.free_blocks() == 3
+        for b in (-2, 2):
+            assert code(c.seq_counts, b) == ott.OTT_ERR_INVALID
         assert all(torch.equal(x, y) for x, y in zip(before, c.read(0, 70)))
         c.append_chunk(K, V, lens=[0, 33])
         assert code(c.decode_attn_topk, q, -1) == ott.OTT_ERR_INVALID
