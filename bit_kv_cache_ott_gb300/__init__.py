@@ -9,6 +9,7 @@ kernels. There is no CPU fallback: if the library is missing or cannot load,
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import functools
 import os
@@ -104,11 +105,11 @@ def load(build_if_missing: bool = False):
     L.ott_ex2_probe.argtypes = [P, P, i32, P]
     L.ott_byte_create.argtypes = [i32] * 7 + [i64, C.POINTER(P)]
     L.ott_byte_destroy.argtypes = [P]
-    L.ott_byte_append.argtypes = [P, P, P, i32, C.POINTER(i32), P]
+    L.ott_byte_append.argtypes = [P, P, P, i32, P, P]
     L.ott_byte_append_seq.argtypes = [P, i32, P, P, i32, P]
     L.ott_byte_read.argtypes = [P, P, P, i32, i32, P]
     L.ott_byte_decode.argtypes = [P, P, P, i32, P, P]
-    L.ott_byte_attn.argtypes = [P, P, P, P, P, i32, C.POINTER(i32), i32, P, P]
+    L.ott_byte_attn.argtypes = [P, P, P, P, P, i32, P, i32, P, P]
     L.ott_byte_release.argtypes = [P, i32, P]
     L.ott_byte_reset.argtypes = [P, P]
     L.ott_byte_counts.argtypes = [P, i32, C.POINTER(i64), C.POINTER(i32)]
@@ -574,11 +575,15 @@ class ByteCache:
             return None
         if len(lens) != self.B:
             raise ValueError("lens must hold one length per sequence")
-        return (C.c_int * self.B)(*[_int32(x, "lens") for x in lens])
+        try:
+            return array.array("i", lens)
+        except OverflowError:
+            raise ValueError("lens: a length does not fit 32 bits") from None
 
     def _append(self, k, v, n, shape, lens, stream):
+        lens = self._lens(lens)   # alive during the call
         self._call(self._L.ott_byte_append, "ott_byte_append", self._ptr(k, shape, "k"), self._ptr(v, shape, "v"), n,
-                   self._lens(lens), stream=stream)
+                   lens and lens.buffer_info()[0], stream=stream)
 
     def append(self, k: torch.Tensor, v: torch.Tensor, stream=None):
         """One token to every sequence: k, v fp16 [B][Hkv][d]."""
@@ -655,8 +660,9 @@ class ByteCache:
         ptr = [self._ptr(q, shp, "q"), self._ptr(k, kshp, "k"), self._ptr(v, kshp, "v")]
         if out is None:
             out = torch.empty_like(q)
-        self._call(self._L.ott_byte_attn, "ott_byte_attn", *ptr, self._ptr(out, shp, "out"), n, self._lens(lens),
-                   _int32(K, "K"), self._sel(sel, n, K), stream=stream)
+        lens = self._lens(lens)
+        self._call(self._L.ott_byte_attn, "ott_byte_attn", *ptr, self._ptr(out, shp, "out"), n,
+                   lens and lens.buffer_info()[0], _int32(K, "K"), self._sel(sel, n, K), stream=stream)
         return out
 
     def _sel(self, sel, n, K):

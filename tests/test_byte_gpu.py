@@ -344,8 +344,11 @@ def test_capacity_and_refusals(ott):
         for at in (8, nq - 8, nq + nk - 8, nq + 2 * nk - 8):                    # out overlaps an input
             assert code(c.chunk_attn, qq, kk, vv, out=buf[at:at + nq].view(B, Hq, 8, d)) == ott.OTT_ERR_INVALID
         c.chunk_attn(qq, kk, vv, out=buf[nq + 2 * nk:2 * nq + 2 * nk].view(B, Hq, 8, d))
-        with pytest.raises(ValueError):
-            c.append_chunk(K, V, lens=[1])
+        for bad in ([1], [1, 2 ** 32], [1, -2 ** 31 - 1]):
+            with pytest.raises(ValueError):
+                c.append_chunk(K, V, lens=bad)
+        with pytest.raises(TypeError):
+            c.append_chunk(K, V, lens=[1, 1.5])
         with pytest.raises(ValueError):
             c.append_chunk(K, V[:, :, :5])
         with pytest.raises(ValueError):
