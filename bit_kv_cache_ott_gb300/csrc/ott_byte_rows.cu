@@ -781,13 +781,15 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
 // A slab is 32 BPL blocks' channel ranges in shared memory (16-byte pieces
 // turned by the block, so that 8 lanes that read one piece of their own blocks
 // meet all banks). A warp takes a (slab, token, four of its heads): BPL blocks
-// per lane. max(q lo, q hi) is q hi for positive q, else q lo, and products of
-// two fp16 numbers are exact: a selection and a multiply-add, which rounds
-// once, as the sum does. A warp alone on its scheduler needs some 30 cycles per
-// channel (BPL = 1; 55 with 2), which counts where a CTA has no more tasks than
-// warps; elsewhere shared memory bounds it, 4 cycles per channel for the
-// queries of a task and one for a lane's block, so two blocks per lane share
-// the queries (drafts of five tokens over 512 blocks, seven heads: 35.4 -> 33.5 us in all).
+// per lane. max(q lo, q hi) is q hi for positive q, else q lo. Products of two
+// fp16 numbers are exact, so a multiply-add of fp16 factors into an fp32 sum
+// rounds once, as the sum does: two of them, of (q or 0) lo and (0 or q) hi, and
+// the ranges need no conversion. (Conversions, a selection and an fp32
+// multiply-add: 131K tokens 22.4 -> 23.6 us in all, drafts of five tokens over
+// 512 blocks, seven heads, 30.2 -> 33.5; the half selected by its byte, then
+// one multiply-add: 22.6, 31.5.) Where a CTA has no more tasks than warps, a
+// warp alone on its scheduler, some 30 cycles per channel, decides; elsewhere
+// two blocks per lane share the queries' loads.
 constexpr int SEL_THREADS = 512, SEL_BLOCKS = 256, SEL_CLUSTER = 16;   // blocks in shared memory at a time
 
 struct SelectArgs {
@@ -805,6 +807,19 @@ struct SelectTable {
 template <int D>
 __host__ __device__ constexpr int heads_bytes() { return D * 16; }   // four heads per channel
 
+// (q, 0) of a q that is not positive, (0, q) of one that is
+__device__ __forceinline__ uint32_t by_sign(__half q) {
+    const uint32_t x = __half_as_ushort(q);
+    return __hgt(q, __ushort_as_half(0)) ? x << 16 : x;
+}
+// sum + q.x lo + q.y hi, of which one is 0
+__device__ __forceinline__ void add_bound(float &sum, uint32_t q, uint32_t range) {
+    asm("{\n .reg .b16 l, h, n, p;\n mov.b32 {l, h}, %1;\n mov.b32 {n, p}, %2;\n fma.rn.f32.f16 %0, n, l, %0;\n"
+        " fma.rn.f32.f16 %0, p, h, %0;\n}"
+        : "+f"(sum)
+        : "r"(range), "r"(q));
+}
+
 template <int D, int BPL>
 __global__ void __launch_bounds__(SEL_THREADS, 2)
     k_byte_select(const __grid_constant__ SelectArgs a, const __grid_constant__ SelectTable t) {
@@ -816,7 +831,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
     const int u = (a.B0 + e) * a.Hkv + hkv, nb = t.nb[e], nq = t.nq[e];
     const int all = (nb + SLAB - 1) / SLAB, per = (all + a.cluster - 1) / a.cluster, s0 = min(all, rank * per),
               s1 = nq > 0 ? min(all, s0 + per) : s0;
-    float4 *const heads = reinterpret_cast<float4 *>(smem + a.slabs * (32 * D * 4) + warp * heads_bytes<D>());
+    uint4 *const heads = reinterpret_cast<uint4 *>(smem + a.slabs * (32 * D * 4) + warp * heads_bytes<D>());
     asm volatile("griddepcontrol.wait;" ::: "memory");
     for (int sb = s0; sb < s1; sb += a.slabs / BPL) {
         const int ns = min(a.slabs / BPL, s1 - sb);
@@ -844,7 +859,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
             __syncwarp();
 #pragma unroll
             for (int y = 0; y < D / 32; ++y)
-                heads[32 * y + lane] = make_float4(__half2float(qv[0][y]), __half2float(qv[1][y]), __half2float(qv[2][y]), __half2float(qv[3][y]));
+                heads[32 * y + lane] = make_uint4(by_sign(qv[0][y]), by_sign(qv[1][y]), by_sign(qv[2][y]), by_sign(qv[3][y]));
             __syncwarp();
             float sum[BPL][4] = {};
 #pragma unroll(4 / BPL)
@@ -857,14 +872,12 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
                 }
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
-                    const float4 q4 = heads[4 * c4 + y];
-                    const float qs[4] = {q4.x, q4.y, q4.z, q4.w};
+                    const uint4 q4 = heads[4 * c4 + y];
+                    const uint32_t qs[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-                    for (int o = 0; o < BPL; ++o) {
-                        const float2 f = __half22float2(ch_as_h2(w[o][y]));
+                    for (int o = 0; o < BPL; ++o)
 #pragma unroll
-                        for (int p = 0; p < 4; ++p) sum[o][p] = __fmaf_rn(qs[p], qs[p] > 0.0f ? f.y : f.x, sum[o][p]);
-                    }
+                        for (int p = 0; p < 4; ++p) add_bound(sum[o][p], qs[p], w[o][y]);
                 }
             }
 #pragma unroll
