@@ -1056,7 +1056,7 @@ cudaError_t launch_rows(const Plan &p, cudaStream_t s) {
 
 template <int D>
 int select_smem(int slabs, int nb) {
-    return std::max(slabs * (32 * D * 4) + SEL_THREADS / 32 * heads_bytes<D>(), nb * 4);
+    return std::max(slabs * (32 * D * 4) + SEL_THREADS / 32 * heads_bytes<D>(), (nb + 3) / 4 * 16);
 }
 
 template <int D>
@@ -1145,7 +1145,7 @@ int run_byte_attn(const ott_byte_cache *c, const ByteCall &call, cudaStream_t s,
     int nb_all = 0;   // the most blocks of any sequence: the width of the lists that a caller gets
     for (int b = 0; b < c->B; ++b) nb_all = std::max(nb_all, c->T[b] / c->G);
     const int Kc = std::min(call.topk, nb_all);
-    if (Kc > 0 && (long long)nb_all * 4 > pick_smem(c)) return OTT_ERR_INVALID;
+    if (Kc > 0 && ((long long)nb_all + 3) / 4 * 16 > pick_smem(c)) return OTT_ERR_INVALID;
     // With nothing to select, the call is the one over every block.
     ByteCall cl = call;
     if (Kc == 0) cl.topk = 0;

@@ -26,25 +26,29 @@ constexpr uint32_t EMPTY = 0xffffffffu;           // key of an empty block
 // magnitude: a first histogram over sign and exponent would put all keys into a
 // few bins, whose atomics go one after another). Rounds over 8-bit digits below
 // them, each a histogram of the keys that match the digits found so far, end
-// when every key that still matches is selected. Then 32 keys at a time give
-// way to two masks (below the last prefix, equal to it) and their counts, whose
-// prefix sums give each selected block its place. The bounds: the largest of
-// bd[j], bd[stride + j] .. of `groups` of them. key: n words of shared memory.
+// when every key that still matches is selected. Then threads count, in four
+// keys each, those below the last prefix and those equal to it; the sums over
+// the threads before give each selected block its place. Latency bounds all of
+// it: instructions that are run once, and are loaded for it (loops unrolled
+// four and eight times cost a 131K layer's call 0.4 us), barriers, votes.
+// The bounds: the largest of bd[j], bd[stride + j] .. of `groups` of them.
+// key: n words of shared memory and up to the next multiple of four.
 __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int stride, int n, int K, int Kc, int32_t *out, uint32_t *key) {
-    __shared__ int hist[256];
-    __shared__ uint32_t red[3][SORT_THREADS / 32];
+    __shared__ __align__(16) int hist[256];
+    __shared__ uint32_t red[3][SORT_THREADS / 32], tot[2][SORT_THREADS / 32];
     __shared__ int s_digit, s_below, s_count;
-    const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, wid = tid >> 5, nseg = (n + 31) / 32;
-    // masks and counts of segment x take the place of its keys, the last one's, which may be fewer than four, a place of their own
-    __shared__ uint32_t tail[4];
-    auto seg = [&](int x) { return x + 1 < nseg ? key + 32 * x : tail; };
+    const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, wid = tid >> 5, n4 = (n + 3) / 4;
+    const uint4 *const key4 = reinterpret_cast<const uint4 *>(key);
+    for (int i = tid; i < 256; i += nth) hist[i] = 0;
     uint32_t all = EMPTY, any = 0;
     int ne = 0;
-    constexpr int BATCH = 8;   // bounds in flight per thread
-    for (int j0 = tid; j0 < n; j0 += BATCH * nth) {
+    constexpr int BATCH = 4;   // bounds in flight per thread
+#pragma unroll 1
+    for (int j0 = tid; j0 < 4 * n4; j0 += BATCH * nth) {
         float f[BATCH];
 #pragma unroll
         for (int x = 0; x < BATCH; ++x) f[x] = j0 + x * nth < n ? bd[j0 + x * nth] : -CUDART_INF_F;
+#pragma unroll 1
         for (int y = 1; y < groups; ++y) {
             float v[BATCH];
 #pragma unroll
@@ -61,7 +65,7 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int str
                 any |= k;
                 ++ne;
             }
-            if (j0 + x * nth < n) key[j0 + x * nth] = k;
+            if (j0 + x * nth < 4 * n4) key[j0 + x * nth] = k;
         }
     }
     all = __reduce_and_sync(0xffffffffu, all);
@@ -85,22 +89,22 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int str
     while (left > 0 && need < cnt) {
         const int bits = min(8, left), shift = left - bits;
         const uint32_t digit = (1u << bits) - 1u;
-        for (int i = tid; i < 256; i += nth) hist[i] = 0;
-        __syncthreads();
-#pragma unroll 4
-        for (int j = tid; j < n; j += nth) {
-            const uint32_t k = key[j];
-            if (k != EMPTY && (k & mask) == prefix) atomicAdd(&hist[(k >> shift) & digit], 1);
+#pragma unroll 1
+        for (int j = tid; j < n4; j += nth) {
+            const uint4 k4 = key4[j];
+            const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                if (k[x] != EMPTY && (k[x] & mask) == prefix) atomicAdd(&hist[(k[x] >> shift) & digit], 1);
         }
         __syncthreads();
         if (wid == 0) {
-            // lane l owns digits 8l .. 8l+7
-            int c[8], sum = 0;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                c[x] = hist[8 * lane + x];
-                sum += c[x];
-            }
+            // lane l owns digits 8l .. 8l+7, and clears them for the next round
+            int4 *const h = reinterpret_cast<int4 *>(hist) + 2 * lane;
+            const int4 ha = h[0], hb = h[1];
+            h[0] = h[1] = make_int4(0, 0, 0, 0);
+            const int c[8] = {ha.x, ha.y, ha.z, ha.w, hb.x, hb.y, hb.z, hb.w};
+            const int sum = ha.x + ha.y + ha.z + ha.w + hb.x + hb.y + hb.z + hb.w;
             int incl = sum;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -127,51 +131,40 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int str
         cnt = s_count;
         left = shift;
     }
-    // (all threads of a warp together: nth and the segments are multiples of 32)
-#pragma unroll 4
-    for (int j = tid; j < 32 * nseg; j += nth) {
-        const uint32_t k = j < n ? key[j] : EMPTY, m = k & mask;
-        const unsigned lt = __ballot_sync(0xffffffffu, k != EMPTY && m < prefix), eq = __ballot_sync(0xffffffffu, k != EMPTY && m == prefix);
-        if (lane == 0) {   // (behind the votes all lanes have read their keys)
-            uint32_t *w = seg(j / 32);
-            w[0] = lt;
-            w[1] = eq;
-            w[2] = __popc(lt);
-            w[3] = __popc(eq);
-        }
-    }
-    __syncthreads();
-    if (wid == 0) {
-        int lt0 = 0, eq0 = 0;
-        for (int x = 0; x < nseg; x += 32) {
-            const bool in = x + lane < nseg;
-            uint32_t *w = seg(in ? x + lane : nseg - 1);
-            const int lt = in ? (int)w[2] : 0, eq = in ? (int)w[3] : 0;
-            int a = lt, b = eq;
+    int lt0 = 0, eq0 = 0;   // below the prefix, equal to it, so far
+#pragma unroll 1
+    for (int c0 = 0, turn = 0; c0 < n4; c0 += nth, turn ^= 1) {
+        const int j = c0 + tid;
+        const uint4 k4 = j < n4 ? key4[j] : make_uint4(EMPTY, EMPTY, EMPTY, EMPTY);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        bool lt[4], eq[4];
+        uint32_t own = 0;   // low half: below; high half: equal
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, a, o), z = __shfl_up_sync(0xffffffffu, b, o);
-                if (lane >= o) {
-                    a += y;
-                    b += z;
-                }
-            }
-            if (in) {
-                w[2] = lt0 + a - lt;
-                w[3] = eq0 + b - eq;
-            }
-            lt0 += __shfl_sync(0xffffffffu, a, 31);
-            eq0 += __shfl_sync(0xffffffffu, b, 31);
+        for (int x = 0; x < 4; ++x) {
+            lt[x] = k[x] != EMPTY && (k[x] & mask) < prefix;
+            eq[x] = k[x] != EMPTY && (k[x] & mask) == prefix;
+            own += (lt[x] ? 1u : 0u) + (eq[x] ? 0x10000u : 0u);
         }
-    }
-    __syncthreads();
-    const unsigned before = (1u << lane) - 1u;
-#pragma unroll 4
-    for (int j = tid; j < 32 * nseg; j += nth) {
-        const uint32_t *w = seg(j / 32);
-        const unsigned lt = w[0], eq = w[1];
-        const int nl = (int)w[2] + __popc(lt & before), nq = (int)w[3] + __popc(eq & before);
-        if ((lt >> lane & 1u) || ((eq >> lane & 1u) && nq < need)) out[nl + min(nq, need)] = j;
+        uint32_t incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) tot[turn][wid] = incl;
+        __syncthreads();
+        const uint32_t t = lane < nth / 32 ? tot[turn][lane] : 0u;
+        const uint32_t before = __reduce_add_sync(0xffffffffu, lane < wid ? t : 0u) + incl - own;
+        int nl = lt0 + (int)(before & 0xffffu), nq = eq0 + (int)(before >> 16);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (lt[x] || (eq[x] && nq < need)) out[nl + min(nq, need)] = 4 * j + x;
+            nl += lt[x];
+            nq += eq[x];
+        }
+        const uint32_t more = __reduce_add_sync(0xffffffffu, t);
+        lt0 += (int)(more & 0xffffu);
+        eq0 += (int)(more >> 16);
     }
     for (int i = want + tid; i < Kc; i += nth) out[i] = -1;
 }

@@ -143,7 +143,7 @@ __global__ void __launch_bounds__(BND_THREADS) k_topk_bounds(TopkArgs a, const _
 }
 
 __global__ void __launch_bounds__(SORT_THREADS) k_topk_pick(TopkArgs a, const __grid_constant__ NfTable nt) {
-    extern __shared__ uint32_t key[];              // [nf]
+    extern __shared__ __align__(16) uint32_t key[];   // [nf], to the next multiple of four
     // the decode may be scheduled now; it waits for the selection
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int u = blockIdx.x;
@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(SORT_THREADS) k_topk_pick(TopkArgs a, const __
 int topk_smem_bytes(int d, int gs, int nf) {
     (void)d;
     (void)gs;
-    return (nf > 1 ? nf : 1) * 4;
+    return (nf > 1 ? (nf + 3) / 4 : 1) * 16;
 }
 
 cudaError_t launch_topk_select(const ott_cache *c, const __half *q, int K, int Kc, cudaStream_t s) {
