@@ -791,12 +791,16 @@ __global__ void __launch_bounds__(CMB_MAXW * 32)
 // warp alone on its scheduler, some 30 cycles per channel, decides; elsewhere
 // two blocks per lane share the queries' loads.
 constexpr int SEL_THREADS = 512, SEL_BLOCKS = 256, SEL_CLUSTER = 16;   // blocks in shared memory at a time
+// Bounds go to the shared memory of the CTA that selects by them where they
+// take no more than this (131K tokens 19.5 us in all, by way of L2 20.0; not
+// more than the slabs and heads before them: the selection's keys lie there).
+constexpr size_t KEPT_BYTES = 16384;
 
 struct SelectArgs {
     const __half2 *dig;
     const int32_t *bt;
     const __half *q;
-    float *bound;       // [nseq][n][Hkv][groups][stride]: by four heads
+    float *bound;       // [nseq][n][Hkv][groups][stride]: by four heads; null: the token's CTA has them, behind its heads
     int32_t *sel;       // [B][n][Hkv][Kc]
     int n, B0, Hq, Hkv, g, NB, K, Kc, stride;
     int groups, cluster, slabs;   // (of 32 blocks, even where BPL is 2) groups of four heads per kv head; CTAs per (sequence, kv head), slabs in shared memory at a time
@@ -806,7 +810,14 @@ struct SelectTable {
 };
 template <int D>
 __host__ __device__ constexpr int heads_bytes() { return D * 16; }   // four heads per channel
+static_assert(KEPT_BYTES <= SEL_THREADS / 32 * heads_bytes<64>(), "keys end before the bounds");
 
+// The place of own shared memory in the CTA of that rank of the cluster.
+__device__ __forceinline__ float *of_rank(float *own, int rank) {
+    uint64_t at;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(at) : "l"(own), "r"(rank));
+    return reinterpret_cast<float *>(at);
+}
 // (q, 0) of a q that is not positive, (0, q) of one that is
 __device__ __forceinline__ uint32_t by_sign(__half q) {
     const uint32_t x = __half_as_ushort(q);
@@ -832,7 +843,11 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
     const int all = (nb + SLAB - 1) / SLAB, per = (all + a.cluster - 1) / a.cluster, s0 = min(all, rank * per),
               s1 = nq > 0 ? min(all, s0 + per) : s0;
     uint4 *const heads = reinterpret_cast<uint4 *>(smem + a.slabs * (32 * D * 4) + warp * heads_bytes<D>());
+    float *const kept = reinterpret_cast<float *>(smem + a.slabs * (32 * D * 4) + WARPS * heads_bytes<D>());
+    // (the cluster's CTAs run once this barrier is through: bounds may be stored into their shared memory)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    bool running = false;
     for (int sb = s0; sb < s1; sb += a.slabs / BPL) {
         const int ns = min(a.slabs / BPL, s1 - sb);
         if (sb > s0) __syncthreads();   // the slabs before are read
@@ -847,6 +862,8 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         __syncthreads();
+        if (!running) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        running = true;
         for (int task = warp; task < ns * nq * a.groups; task += WARPS) {
             const int x = task % ns, tk = task / ns / a.groups, grp = task / ns % a.groups, j = (sb + x) * SLAB + lane;
             const uint4 *row = reinterpret_cast<const uint4 *>(smem + (x * SLAB + lane) * (D * 4));
@@ -880,21 +897,24 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
                         for (int p = 0; p < 4; ++p) add_bound(sum[o][p], qs[p], w[o][y]);
                 }
             }
+            float *to;
+            if (a.bound) to = a.bound + ((((size_t)e * a.n + tk) * a.Hkv + hkv) * a.groups + grp) * a.stride;
+            else to = of_rank(kept + (tk / a.cluster * a.groups + grp) * a.stride, tk % a.cluster);
 #pragma unroll
             for (int o = 0; o < BPL; ++o) {
                 float best = -CUDART_INF_F;
 #pragma unroll
                 for (int p = 0; p < 4; ++p) best = sum[o][p] > best ? sum[o][p] : best;
-                if (j + 32 * o < nb)
-                    a.bound[((((size_t)e * a.n + tk) * a.Hkv + hkv) * a.groups + grp) * a.stride + j + 32 * o] = best;
+                if (j + 32 * o < nb) to[j + 32 * o] = best;
             }
         }
     }
+    if (!running) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     // every CTA of the cluster comes by here; the bounds are visible to all of them behind it
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
     for (int tk = rank; tk < nq; tk += a.cluster) {
         const size_t at = ((size_t)e * a.n + tk) * a.Hkv + hkv;
-        pick_blocks(a.bound + at * a.groups * a.stride, a.groups, a.stride, nb, a.K, a.Kc, a.sel + ((size_t)a.B0 * a.n * a.Hkv + at) * a.Kc,
+        pick_blocks(a.bound ? a.bound + at * a.groups * a.stride : kept + tk / a.cluster * a.groups * a.stride, a.groups, a.stride, nb, a.K, a.Kc, a.sel + ((size_t)a.B0 * a.n * a.Hkv + at) * a.Kc,
                     reinterpret_cast<uint32_t *>(smem));
         __syncthreads();
     }
@@ -914,6 +934,7 @@ struct Plan {
     bool whole;    // ... each with a tile of its own
     size_t part_floats, bound_floats;
     int cw, nbmax;
+    size_t kept;   // bytes of bounds that a CTA which selects keeps
 };
 
 // Kc: slots of a list of selected blocks. false: sizes beyond the kernels' 32-bit counters.
@@ -1043,7 +1064,11 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
         p.two = (long long)own * nq_max * groups > SEL_THREADS / 32;
         p.ba = {c->dig, a.bt, call.q, nullptr, nullptr, call.n, B0, c->Hq, c->Hkv, c->g, c->NB, call.topk, Kc, p.nbmax,
                 groups, cluster, std::min(SEL_BLOCKS / 32, p.two ? (own + 1) / 2 * 2 : own)};
-        p.bound_floats = (size_t)a.nseq * call.n * c->Hkv * ((c->g + 3) / 4) * p.nbmax;
+        p.kept = (size_t)((nq_max + cluster - 1) / cluster) * groups * p.nbmax * 4;
+        if (p.kept > KEPT_BYTES) {
+            p.kept = 0;
+            p.bound_floats = (size_t)a.nseq * call.n * c->Hkv * groups * p.nbmax;
+        }
     }
     return true;
 }
@@ -1055,8 +1080,8 @@ cudaError_t launch_rows(const Plan &p, cudaStream_t s) {
 }
 
 template <int D>
-int select_smem(int slabs, int nb) {
-    return std::max(slabs * (32 * D * 4) + SEL_THREADS / 32 * heads_bytes<D>(), (nb + 3) / 4 * 16);
+int select_smem(int slabs, int nb, int kept) {
+    return std::max(slabs * (32 * D * 4) + SEL_THREADS / 32 * heads_bytes<D>() + kept, (nb + 3) / 4 * 16);
 }
 
 template <int D>
@@ -1064,7 +1089,7 @@ cudaError_t launch_select(const ott_byte_cache *c, const Plan &p, cudaStream_t s
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(p.a.nseq * c->Hkv * p.ba.cluster));
     cfg.blockDim = dim3(SEL_THREADS);
-    cfg.dynamicSmemBytes = (size_t)select_smem<D>(p.ba.slabs, p.nbmax);
+    cfg.dynamicSmemBytes = (size_t)select_smem<D>(p.ba.slabs, p.nbmax, (int)p.kept);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1172,7 +1197,7 @@ int run_byte_attn(const ott_byte_cache *c, const ByteCall &call, cudaStream_t s,
         if (!p.any) continue;
         p.a.part = base;
         if (cl.topk > 0) {
-            p.ba.bound = base + parts;
+            p.ba.bound = p.bound_floats ? base + parts : nullptr;
             p.ba.sel = cl.sel ? cl.sel : reinterpret_cast<int32_t *>(base + parts + bounds);
             p.a.sel = p.ba.sel;
         }
