@@ -29,14 +29,15 @@ constexpr uint32_t EMPTY = 0xffffffffu;           // key of an empty block
 // when every key that still matches is selected. Then threads count, in four
 // keys each, those below the last prefix and those equal to it; the sums over
 // the threads before give each selected block its place. Latency bounds all of
-// it: instructions that are run once, and are loaded for it (loops unrolled
-// four and eight times cost a 131K layer's call 0.4 us), barriers, votes.
+// it (2,047 bounds, 256 selected, in cycles: bounds and common bits 2,000, a
+// round 1,400, places 1,000); loops unrolled four and eight times cost a 131K
+// layer's call 0.4 us, a key at a time with votes for the places 1.5 us.
 // The bounds: the largest of bd[j], bd[stride + j] .. of `groups` of them.
 // key: n words of shared memory and up to the next multiple of four.
 __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int stride, int n, int K, int Kc, int32_t *out, uint32_t *key) {
     __shared__ __align__(16) int hist[256];
     __shared__ uint32_t red[3][SORT_THREADS / 32], tot[2][SORT_THREADS / 32];
-    __shared__ int s_digit, s_below, s_count;
+    __shared__ int4 found;   // a round's digit, the keys below it, those that have it
     const int tid = threadIdx.x, nth = blockDim.x, lane = tid & 31, wid = tid >> 5, n4 = (n + 3) / 4;
     const uint4 *const key4 = reinterpret_cast<const uint4 *>(key);
     for (int i = tid; i < 256; i += nth) hist[i] = 0;
@@ -90,9 +91,10 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int str
         const int bits = min(8, left), shift = left - bits;
         const uint32_t digit = (1u << bits) - 1u;
 #pragma unroll 1
-        for (int j = tid; j < n4; j += nth) {
-            const uint4 k4 = key4[j];
-            const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        for (int j = tid; j < n; j += 4 * nth) {
+            uint32_t k[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) k[x] = j + x * nth < n ? key[j + x * nth] : EMPTY;
 #pragma unroll
             for (int x = 0; x < 4; ++x)
                 if (k[x] != EMPTY && (k[x] & mask) == prefix) atomicAdd(&hist[(k[x] >> shift) & digit], 1);
@@ -111,24 +113,23 @@ __device__ __forceinline__ void pick_blocks(const float *bd, int groups, int str
                 const int y = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += y;
             }
-            int run = incl - sum;
-            if (run < need && need <= incl) {   // exactly one lane
+            int run = incl - sum, x = 0, n_x = c[0];
+            const bool mine = run < need && need <= incl;   // one lane's
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    if (run < need && need <= run + c[x]) {
-                        s_digit = 8 * lane + x;
-                        s_below = run;
-                        s_count = c[x];
-                    }
-                    run += c[x];
-                }
+            for (int y = 0; y < 7; ++y) {   // its first digit that reaches `need`
+                const bool next = run + c[y] < need && x == y;
+                run += next ? c[y] : 0;
+                x += next;
+                n_x = next ? c[y + 1] : n_x;
             }
+            if (mine) found = make_int4(8 * lane + x, run, n_x, 0);
         }
         __syncthreads();
-        prefix |= (uint32_t)s_digit << shift;
+        const int4 f = found;
+        prefix |= (uint32_t)f.x << shift;
         mask |= digit << shift;
-        need -= s_below;
-        cnt = s_count;
+        need -= f.y;
+        cnt = f.z;
         left = shift;
     }
     int lt0 = 0, eq0 = 0;   // below the prefix, equal to it, so far
