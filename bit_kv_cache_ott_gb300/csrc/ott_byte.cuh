@@ -39,6 +39,7 @@ struct ott_byte_cache {
     long long blk_bytes;
     int poisoned, device, sm_count, smem_optin;
     int max_cluster;    // CTAs of a cluster that selects blocks
+    int rows_clusters[4];   // clusters of 2, 4, 8, 16 CTAs of the rows kernel that run at a time
     void *mem;
     size_t mem_bytes;
     uint8_t *blk;
@@ -102,7 +103,8 @@ struct ByteArgs {
     long long W, Wb;           // work items: A, B
     int NWp, wpc, MAXU, RV;    // active warps, warps per CTA, units that a warp's run of A items can touch, rows of a partial
     int NQ, MAXU2;             // runs of B items, units that one can touch
-    bool direct;               // a CTA per unit, which writes its rows
+    bool direct;               // a CTA or a cluster of them per unit, which writes its rows
+    int cluster;               // ... its CTAs
     float sl2;                 // log2(e) / sqrt(d)
 };
 

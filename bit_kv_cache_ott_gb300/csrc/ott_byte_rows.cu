@@ -29,8 +29,11 @@
 // one per warp; the rest (B items) are cut into short runs, about three per
 // warp, which warps claim from a counter when they have nothing else to copy.
 // Who took a run does not show in the result.
-// The shortest calls, units of up to 1,024 tokens and no more of them than SMs,
-// give every unit a CTA, which writes its rows: no second kernel.
+// Short calls, no more units than SMs, give every unit a CTA or a cluster of
+// them, which reads one another's shared memory and writes the unit's rows: no
+// second kernel. One sequence of 1,024 tokens, 8 kv heads (clusters of two): 6.8
+// us, with a merge kernel 8.2; 4 x 2,048: 7.7 and 8.6; five drafts with 40
+// blocks each (a CTA per unit) 26.6 and 29.1; one of 4,096 7.4 and 7.6.
 //
 // What bounds it: HBM. Batch 32 x 4K, 32 heads of d = 128 (1.07 GB of cache)
 // takes 161 us, 6.7 TB/s; with four queries each, 165. Calls of a few ten us
@@ -50,7 +53,11 @@ namespace {
 
 constexpr int ROWS_MAX = 16;   // rows per kv head up to which this file's kernel serves a call
 constexpr int QT = 32, FT = 16;   // tokens of a work item: of a block, fp16
-constexpr int DIRECT_ITEMS = 32;  // items of a unit that a CTA of its own serves
+// Items of a unit per CTA of its own: clusters grow while a CTA has more than
+// SPREAD_ITEMS (32: 4 x 2,048 tokens 7.7 -> 9.5 us) and SMs are left; beyond
+// DIRECT_ITEMS a call is cut into equal runs (8 units of 513 items in clusters
+// of eight, which leave 88 SMs idle: 25.2 us, in runs 19.5; 43 items, above).
+constexpr int DIRECT_ITEMS = 48, SPREAD_ITEMS = 16;
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
@@ -90,6 +97,17 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity) {
         if (ok) return true;
     }
     return false;
+}
+
+// The place of own shared memory in the CTA of that rank of the cluster.
+__device__ __forceinline__ float *of_rank(float *own, int rank) {
+    uint64_t at;
+    asm("mapa.u64 %0, %1, %2;" : "=l"(at) : "l"(own), "r"(rank));
+    return reinterpret_cast<float *>(at);
+}
+// Every thread of the cluster's CTAs that still run comes by; what they wrote before is visible behind it.
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;" ::: "memory");
 }
 
 // NC groups of 8 query rows (the columns of an MMA).
@@ -220,20 +238,22 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     // the run at hand: the next item, how many are left, the places of its partials
     Cursor ic;
     int left;
+    const int rank = a.direct ? (int)blockIdx.x % a.cluster : 0;
     if (a.direct) {   // this CTA's unit, this warp's share of it (there may be none)
+        const int unit = (int)blockIdx.x / a.cluster, part = rank * wpc + warp, parts = a.cluster * wpc;
         int e = 0;
         for (int hi = a.nseq; hi - e > 1;) {
             const int mid = (e + hi) >> 1;
-            if (st.e[mid].ubase <= (int)blockIdx.x) e = mid;
+            if (st.e[mid].ubase <= unit) e = mid;
             else hi = mid;
         }
-        const int h = (int)blockIdx.x - st.e[e].ubase, from = st.e[e].Iu * warp / wpc;
+        const int h = unit - st.e[e].ubase, from = (int)((long long)st.e[e].Iu * part / parts);
         ic.b = false;
         ic.e = e;
         ic.hkv = h / st.e[e].S;
         ic.sl = h % st.e[e].S;
         ic.unit(a, st, from);
-        left = st.e[e].Iu * (warp + 1) / wpc - from;
+        left = (int)((long long)st.e[e].Iu * (part + 1) / parts) - from;
     } else {
         const long long x0 = ch_range_start(a.W, a.NWp, gw);
         left = (int)(ch_range_start(a.W, a.NWp, gw + 1) - x0);
@@ -459,7 +479,11 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 // let the other copies in flight land before giving up the buffers
                 for (int x = 0; x < NST; ++x)
                     if (x != sg) mbar_wait(&bars[x], (phase >> x) & 1u);
-                if (merge) __syncthreads();   // the others' barrier
+                if (merge) __syncthreads();   // the others' barriers
+                if (a.direct && a.cluster > 1) {
+                    cluster_sync();
+                    cluster_sync();
+                }
                 return;
             }
             phase ^= 1u << sg;
@@ -600,7 +624,16 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     const int nw = a.direct ? wpc : min(wpc, a.NWp - (int)blockIdx.x * wpc);
     int v0, rows;
     slice_rows(a, st.e[start.e], start.sl, v0, rows);
-    float *const pb = a.part + (size_t)(blockIdx.x * wpc) * a.MAXU * a.RV * (D + 2);
+    // a CTA's results go to its place among the partials; to the second stage of its first warp, for the cluster
+    float *const pb = a.direct ? reinterpret_cast<float *>(smem + C::STAGE) : a.part + (size_t)(blockIdx.x * wpc) * a.MAXU * a.RV * (D + 2);
+    auto write = [&](int col, float L, const float (&o)[D / 32]) {
+        // a row sees a token at least, so that L = 0 means scores of -inf or NaN alone: NaN
+        const int v = v0 + col;
+        const float inv = 1.0f / L;
+        __half *out = a.out + (((size_t)(a.B0 + start.e) * a.Hq + start.hkv * a.g + v % a.g) * a.n + v / a.g) * D;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) out[32 * c + lane] = __float2half_rn(o[c] * inv);
+    };
     for (int col = warp; col < cnt_rows; col += nw) {
         float M = -CUDART_INF_F, L = 0.0f, o[D / 32];
         for (int w = 0; w < nw; ++w) M = fmaxf(M, reinterpret_cast<const float *>(smem + (size_t)w * C::WARP_SMEM)[col * (D + 2)]);
@@ -614,13 +647,8 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) o[c] = fmaf(sw, p[2 + 32 * c + lane], o[c]);
         }
-        if (a.direct) {
-            // a row sees a token at least, so that L = 0 means scores of -inf or NaN alone: NaN
-            const int v = v0 + col;
-            const float inv = 1.0f / L;
-            __half *out = a.out + (((size_t)(a.B0 + start.e) * a.Hq + start.hkv * a.g + v % a.g) * a.n + v / a.g) * D;
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) out[32 * c + lane] = __float2half_rn(o[c] * inv);
+        if (a.direct && a.cluster == 1) {
+            write(col, L, o);
             continue;
         }
         float *p = pb + (size_t)col * (D + 2);
@@ -628,6 +656,30 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) p[2 + 32 * c + lane] = o[c];
     }
+    if (!a.direct || a.cluster == 1) return;
+    cluster_sync();
+    for (int col = rank + a.cluster * warp; col < cnt_rows; col += a.cluster * wpc) {
+        float *const at = pb + col * (D + 2);
+        float m = -CUDART_INF_F;
+        if (lane < a.cluster) m = *of_rank(at, lane);
+        float M = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        const float mr = M == -CUDART_INF_F ? 0.0f : M;
+        float L = 0.0f, o[D / 32];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) o[c] = 0.0f;
+#pragma unroll 4
+        for (int x = 0; x < a.cluster; ++x) {
+            const float *p = of_rank(at, x);
+            const float sw = ch_ex2(__shfl_sync(0xffffffffu, m, x) - mr);   // 0 where nothing was seen
+            L = fmaf(sw, p[1], L);
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) o[c] = fmaf(sw, p[2 + 32 * c + lane], o[c]);
+        }
+        write(col, L, o);
+    }
+    cluster_sync();   // no CTA ends while its results are read
 }
 
 // Merge a row's partials: a CTA of cw warps per (sequence, query head, token),
@@ -812,12 +864,6 @@ template <int D>
 __host__ __device__ constexpr int heads_bytes() { return D * 16; }   // four heads per channel
 static_assert(KEPT_BYTES <= SEL_THREADS / 32 * heads_bytes<64>(), "keys end before the bounds");
 
-// The place of own shared memory in the CTA of that rank of the cluster.
-__device__ __forceinline__ float *of_rank(float *own, int rank) {
-    uint64_t at;
-    asm("mapa.u64 %0, %1, %2;" : "=l"(at) : "l"(own), "r"(rank));
-    return reinterpret_cast<float *>(at);
-}
 // (q, 0) of a q that is not positive, (0, q) of one that is
 __device__ __forceinline__ uint32_t by_sign(__half q) {
     const uint32_t x = __half_as_ushort(q);
@@ -1033,10 +1079,16 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
     a.wpc = (a.NWp + p.ctas - 1) / p.ctas;
     p.ctas = (a.NWp + a.wpc - 1) / a.wpc;
     a.direct = false;
-    if (units <= c->sm_count && longest <= DIRECT_ITEMS) {
+    a.cluster = 1;
+    int fits = 0;
+    while (fits < 4 && longest > (long long)SPREAD_ITEMS * a.cluster && units <= c->rows_clusters[fits]) {
+        a.cluster *= 2;
+        ++fits;
+    }
+    if (units <= c->sm_count && longest <= (long long)DIRECT_ITEMS * a.cluster) {
         a.direct = true;
-        a.wpc = (int)std::min<long long>(WARPS, longest);
-        p.ctas = (int)units;
+        a.wpc = (int)std::min<long long>(WARPS, (longest + a.cluster - 1) / a.cluster);
+        p.ctas = (int)units * a.cluster;
         a.NWp = p.ctas * a.wpc;
     }
     const long long run = (base + a.NWp - 1) / a.NWp;
@@ -1076,7 +1128,20 @@ bool make_plan(const ott_byte_cache *c, const ByteCall &call, int B0, int Kc, Pl
 template <int D, int NC, int FMT>
 cudaError_t launch_rows(const Plan &p, cudaStream_t s) {
     using C = RowsCfg<D, NC>;
-    return launch_pdl(k_byte_rows<D, NC, FMT>, dim3((unsigned)p.ctas), p.a.wpc * 32, (size_t)C::WARP_SMEM * p.a.wpc, s, p.a, p.st);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.ctas);
+    cfg.blockDim = dim3((unsigned)p.a.wpc * 32);
+    cfg.dynamicSmemBytes = (size_t)C::WARP_SMEM * p.a.wpc;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.a.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.a.direct && p.a.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, k_byte_rows<D, NC, FMT>, p.a, p.st);
 }
 
 template <int D>
@@ -1116,19 +1181,40 @@ cudaError_t launch_plan(const ott_byte_cache *c, const Plan &p, cudaStream_t s) 
     return e;
 }
 
+// clusters: how many of 2, 4, 8 and 16 CTAs run at a time (the least of the instances asked so far)
 template <int D, int NC, int FMT>
-cudaError_t rows_attribute() {
-    return cudaFuncSetAttribute(k_byte_rows<D, NC, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                RowsCfg<D, NC>::WARP_SMEM * RowsCfg<D, NC>::WARPS);
+cudaError_t rows_attribute(int (&clusters)[4]) {
+    using C = RowsCfg<D, NC>;
+    auto *kern = k_byte_rows<D, NC, FMT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::WARP_SMEM * C::WARPS);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    for (int x = 0; x < 4 && e == cudaSuccess; ++x) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2u << x);
+        cfg.blockDim = dim3(C::WARPS * 32);
+        cfg.dynamicSmemBytes = (size_t)C::WARP_SMEM * C::WARPS;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2u << x;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int fit = 0;
+        if (cudaOccupancyMaxActiveClusters(&fit, kern, &cfg) != cudaSuccess) {
+            cudaGetLastError();
+            fit = 0;
+        }
+        clusters[x] = std::min(clusters[x], fit);
+    }
+    return e;
 }
 template <int D>
-cudaError_t set_attributes(int format) {
-    if (format == OTT_BYTE_INT) {
-        const cudaError_t e = rows_attribute<D, 1, OTT_BYTE_INT>();
-        return e != cudaSuccess ? e : rows_attribute<D, 2, OTT_BYTE_INT>();
-    }
-    const cudaError_t e = rows_attribute<D, 1, OTT_BYTE_FLOAT>();
-    return e != cudaSuccess ? e : rows_attribute<D, 2, OTT_BYTE_FLOAT>();
+cudaError_t set_attributes(ott_byte_cache *c) {
+    for (int &x : c->rows_clusters) x = INT_MAX;
+    const bool i8 = c->format == OTT_BYTE_INT;
+    const cudaError_t e = i8 ? rows_attribute<D, 1, OTT_BYTE_INT>(c->rows_clusters) : rows_attribute<D, 1, OTT_BYTE_FLOAT>(c->rows_clusters);
+    if (e != cudaSuccess) return e;
+    return i8 ? rows_attribute<D, 2, OTT_BYTE_INT>(c->rows_clusters) : rows_attribute<D, 2, OTT_BYTE_FLOAT>(c->rows_clusters);
 }
 
 // shared memory of the selection that a launch may ask for
@@ -1137,7 +1223,7 @@ int pick_smem(const ott_byte_cache *c) { return c->smem_optin - 2048; }
 }  // namespace
 
 cudaError_t set_byte_attributes(ott_byte_cache *c) {
-    cudaError_t e = c->d == 128 ? set_attributes<128>(c->format) : set_attributes<64>(c->format);
+    cudaError_t e = c->d == 128 ? set_attributes<128>(c) : set_attributes<64>(c);
     // clusters of 16 CTAs where this GPU has room for them, else of 8
     c->max_cluster = SEL_CLUSTER;
     for (int two = 0; two < 2 && e == cudaSuccess; ++two) {

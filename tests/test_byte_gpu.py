@@ -549,6 +549,41 @@ def test_units_of_a_cta_and_of_several(ott, T):
         c.check_device()
 
 
+@pytest.mark.parametrize("fmt,d,G,g,n,topk", [("int8", 128, 64, 4, 1, 0), ("e4m3", 64, 32, 1, 9, 0), ("int8", 128, 32, 5, 3, 30),
+                                              ("e4m3", 128, 128, 16, 1, 0)])
+@pytest.mark.parametrize("B,Hkv,T", [(12, 5, 1700), (3, 10, 2100), (2, 7, 5000), (1, 3, 9001), (1, 1, 20001)])
+def test_units_of_a_cluster(ott, fmt, d, G, g, n, topk, B, Hkv, T):
+    """Units that clusters of 2, 4, 8 and 16 CTAs serve, beside short ones and empty ones; rows more and fewer than CTAs;
+    the same bits again and from a graph."""
+    Ts = [max(1, T - 301 * b) for b in range(B)]
+    K, V = _kv(71, B, Hkv, T, d)
+    q = draw(73, B, Hkv * g, n, d, outliers=False)
+    k, v = _kv(74, B, Hkv, n, d)
+    ns = [0 if b % 5 == 2 else n - b % n for b in range(B)]
+    with ott.ByteCache(B, Hkv * g, Hkv, d, G, fmt, max_tokens=T) as c:
+        _fill(c, K, V, Ts)
+        dev = [x.to(DEV) for x in (q, k, v)]
+        q1 = dev[0][:, :, 0].contiguous()
+        run = lambda: (c.decode_attn_topk(q1, topk), c.chunk_attn_topk(*dev, topk, lens=ns, out=torch.full_like(dev[0], 7)))
+        one, out = run()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            again = run()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(again[0], one) and torch.equal(again[1], out)
+        for b in range(B):
+            if b and b + 2 < B and b % 5 != 2:
+                continue   # the first, the last, an empty and its neighbours
+            Kb, Vb, m = K[b, :, :Ts[b]], V[b, :, :Ts[b]], ns[b]
+            ch = bu.choose(q[b], Kb, G, topk) if topk else None
+            check(one[b].unsqueeze(1), *bu.attend(q[b, :, :1], Kb, Vb, fmt, G, chosen=ch and ch[:1]))
+            if m:
+                check(out[b, :, :m], *bu.attend(q[b, :, :m], Kb, Vb, fmt, G, k[b, :, :m], v[b, :, :m], ch and ch[:m]))
+            assert (out[b, :, m:] == 7).all()
+        c.check_device()
+
+
 def test_beside_an_ott_cache(ott):
     """A model whose first layer is kept in 8 bits and the second in 2: the same loop over both kinds."""
     B, Hq, Hkv, d, T, n = 2, 8, 2, 128, 300, 20
