@@ -262,9 +262,9 @@ __global__ void __launch_bounds__(READ_WARPS * 32)
     ByteRec rec = {};
     if (t0 < held) {
         const int j = t0 / a.G;
-        const size_t own = (size_t)u * a.NB + j, slot = a.bt ? (size_t)__ldg(a.bt + own) : own;
+        const size_t own = (size_t)u * a.NB + j, slot = a.bt ? (size_t)a.bt[own] : own;
         src = a.blk + slot * (2 * (size_t)a.G * D) + (t0 % a.G) / 16 * (32 * D);
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(a.rec + slot));
+        const float4 f = *reinterpret_cast<const float4 *>(a.rec + slot);
         rec.ks = f.x;
         rec.vs = f.y;
     }
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(READ_WARPS * 32)
         if (src) {
             uint4 p[2 * PP];
 #pragma unroll
-            for (int y = 0; y < 2 * PP; ++y) p[y] = __ldg(reinterpret_cast<const uint4 *>(src + val * 16 * D) + y * 32 + lane);
+            for (int y = 0; y < 2 * PP; ++y) p[y] = reinterpret_cast<const uint4 *>(src + val * 16 * D)[y * 32 + lane];
 #pragma unroll
             for (int y = 0; y < 2 * PP; ++y) {
                 const uint32_t w[4] = {p[y].x, p[y].y, p[y].z, p[y].w};

@@ -22,6 +22,13 @@
 //   values, piece c: byte 4 w + y: channel 32 c + r + 8 w, token 2 i + {0, 1, 8, 9}[y].
 //
 // The open block: tk, tv [U][G][d] fp16, token t at row t mod G.
+//
+// Every kernel starts while the one before it on the stream may still write
+// what it will read (programmatic dependent launches): codes, records, block
+// table, selections, queries that are another call's output. All of that is
+// read by plain loads behind griddepcontrol.wait; a load by way of the
+// read-only path (__ldg) is defined only for data that nobody writes while the
+// kernel runs, and does not have to stay behind the wait.
 #pragma once
 
 #include "ott_chunk.cuh"

@@ -296,9 +296,9 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 slots = -1;
                 if (jp < s.nb) {
                     int j = jp;
-                    if (a.sel) j = __ldg(a.sel + (((size_t)b * a.n + c.sl / a.SG) * a.Hkv + c.hkv) * a.Kc + jp);
+                    if (a.sel) j = a.sel[(((size_t)b * a.n + c.sl / a.SG) * a.Hkv + c.hkv) * a.Kc + jp];
                     const size_t own = (size_t)u * a.NB + j;
-                    if (j >= 0) slots = a.bt ? __ldg(a.bt + own) : (int)own;
+                    if (j >= 0) slots = a.bt ? a.bt[own] : (int)own;
                 }
             }
             const int slot = __shfl_sync(0xffffffffu, slots, c.jp - slots_from);
@@ -370,7 +370,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
             const __half *qp = a.q + (((size_t)b * a.Hq + c.hkv * a.g + v % a.g) * a.n + v / a.g) * D + (D / 4) * i;
 #pragma unroll
             for (int ks = 0; ks < NKS; ++ks) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(qp + 16 * (ks >> 2) + ((4 * (ks & 3)) ^ rot)));
+                const uint2 w = *reinterpret_cast<const uint2 *>(qp + 16 * (ks >> 2) + ((4 * (ks & 3)) ^ rot));
                 Bq[nc][ks][0] = w.x;
                 Bq[nc][ks][1] = w.y;
             }
@@ -900,7 +900,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
         for (int z = threadIdx.x; z < ns * SLAB * V4; z += SEL_THREADS) {
             const int x = z / V4, v = z % V4, j = sb * SLAB + x;
             if (j < nb) {
-                const size_t own = (size_t)u * a.NB + j, slot = a.bt ? (size_t)__ldg(a.bt + own) : own;
+                const size_t own = (size_t)u * a.NB + j, slot = a.bt ? (size_t)a.bt[own] : own;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ch_smem(smem + x * (D * 4) + ((v ^ (x & 7)) << 4))),
                              "l"(a.dig + slot * D + 4 * v)
                              : "memory");
@@ -918,7 +918,7 @@ __global__ void __launch_bounds__(SEL_THREADS, 2)
 #pragma unroll
             for (int p = 0; p < 4; ++p)
 #pragma unroll
-                for (int y = 0; y < D / 32; ++y) qv[p][y] = __ldg(q + (size_t)min(4 * grp + p, a.g - 1) * a.n * D + 32 * y + lane);
+                for (int y = 0; y < D / 32; ++y) qv[p][y] = q[(size_t)min(4 * grp + p, a.g - 1) * a.n * D + 32 * y + lane];
             __syncwarp();
 #pragma unroll
             for (int y = 0; y < D / 32; ++y)

@@ -250,9 +250,9 @@ struct Producer {
             const bool next = k + 1 < n && xn < t.gq;
             const uint8_t *src = nullptr;
             if (next) {
-                const size_t own = (size_t)u * a.NB + xn / per, slot = a.bt ? (size_t)__ldg(a.bt + own) : own;
+                const size_t own = (size_t)u * a.NB + xn / per, slot = a.bt ? (size_t)a.bt[own] : own;
                 src = a.blk + slot * a.blk_bytes + (size_t)(xn % per) * (32 * D);
-                recn = __ldg(reinterpret_cast<const float4 *>(a.rec + slot));
+                recn = *reinterpret_cast<const float4 *>(a.rec + slot);
             }
             if (k >= 0) {
                 wait(B_KEMPTY);
@@ -284,7 +284,7 @@ struct Producer {
 #pragma unroll
                 for (int y = 0; y < 2 * PP; ++y) {
                     const int piece = PP == 2 ? (y & 2) + ((y & 1) ^ (r & 1)) : y;
-                    kr[y] = __ldg(reinterpret_cast<const uint4 *>(src) + piece * 32 + lane);
+                    kr[y] = reinterpret_cast<const uint4 *>(src)[piece * 32 + lane];
                 }
             }
             if (k >= 0) {
@@ -308,7 +308,7 @@ struct Producer {
             }
             if (next) {
 #pragma unroll
-                for (int y = 0; y < 2 * PP; ++y) vr[y] = __ldg(reinterpret_cast<const uint4 *>(src + 16 * D) + y * 32 + lane);
+                for (int y = 0; y < 2 * PP; ++y) vr[y] = reinterpret_cast<const uint4 *>(src + 16 * D)[y * 32 + lane];
             }
             have = next;
             rec = recn;
@@ -338,7 +338,7 @@ struct Producer {
             for (int e = 0; e < 16 / RPI; ++e) {
                 const int row = RPI * e + lane / CPR;
                 kr[e] = make_uint4(0, 0, 0, 0);
-                if (row < left) kr[e] = __ldg(reinterpret_cast<const uint4 *>(ksrc + (size_t)row * D) + lane % CPR);
+                if (row < left) kr[e] = reinterpret_cast<const uint4 *>(ksrc + (size_t)row * D)[lane % CPR];
             }
 #pragma unroll
             for (int e = 0; e < 16 / RPI; ++e) {
@@ -729,7 +729,7 @@ __device__ void role_loop(const TileArgs &ta, const ByteTable &st, uint8_t *sm, 
                 for (int y = 0; y < BATCH; ++y) {
                     const int row = rr + STEP * y, vv = 256 * t.p + row, tk = vv / a.g;
                     v[y] = make_uint4(0, 0, 0, 0);
-                    if (row < t.rows) v[y] = __ldg(reinterpret_cast<const uint4 *>(q0 + ((size_t)(vv - tk * a.g) * a.n + tk) * D));
+                    if (row < t.rows) v[y] = *reinterpret_cast<const uint4 *>(q0 + ((size_t)(vv - tk * a.g) * a.n + tk) * D);
                 }
 #pragma unroll
                 for (int y = 0; y < BATCH; ++y) {
