@@ -698,4 +698,4 @@ class ByteCache:
         return int(self._L.ott_byte_bytes(self._h))
 
     def check_device(self):
-        _check(self._L.ott_byte_check(self._h), "ott_byte_check")
+        _on_device(self._dev, self._L.ott_byte_check, "ott_byte_check", self._h)

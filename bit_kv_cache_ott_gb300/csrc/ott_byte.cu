@@ -335,13 +335,14 @@ int fail_cuda(ott_byte_cache *c, cudaError_t e) {
     return OTT_ERR_CUDA;
 }
 
-// The checks of every call, before anything else is looked at.
-int state_of(const ott_byte_cache *c) {
-    if (c->poisoned) return OTT_ERR_STATE;
+// The cache's device has to be the current one.
+int device_of(const ott_byte_cache *c) {
     int dev = -1;
     if (cudaGetDevice(&dev) != cudaSuccess) return OTT_ERR_CUDA;
     return dev == c->device ? OTT_OK : OTT_ERR_STATE;
 }
+// The checks of every call, before anything else is looked at.
+int state_of(const ott_byte_cache *c) { return c->poisoned ? OTT_ERR_STATE : device_of(c); }
 
 template <int D, int G>
 cudaError_t append_t(const AppendArgs &a, const AppendTable &t, int format, int ctas, cudaStream_t s) {
@@ -515,9 +516,18 @@ int ott_byte_create(int B, int Hq, int Hkv, int d, int G, int format, int max_to
 
 int ott_byte_destroy(ott_byte_cache *c) {
     if (!c) return OTT_OK;
-    cudaError_t e = cudaDeviceSynchronize();
+    // any device may be current: the cache's kernels run on its own
+    int dev = c->device;
+    cudaError_t e = cudaGetDevice(&dev);
+    const bool away = dev != c->device;
+    if (e == cudaSuccess && away) e = cudaSetDevice(c->device);
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
     const cudaError_t e2 = cudaFree(c->mem);
     if (e == cudaSuccess) e = e2;
+    if (away) {
+        const cudaError_t e3 = cudaSetDevice(dev);
+        if (e == cudaSuccess) e = e3;
+    }
     delete c;
     return e == cudaSuccess ? OTT_OK : OTT_ERR_CUDA;
 }
@@ -645,6 +655,7 @@ long long ott_byte_free_blocks(const ott_byte_cache *c) { return c && c->paged ?
 
 int ott_byte_check(ott_byte_cache *c) {
     if (!c) return OTT_ERR_INVALID;
+    if (const int rc = device_of(c)) return rc;
     int flag = 0;
     cudaError_t e = cudaDeviceSynchronize();
     if (e == cudaSuccess) e = cudaMemcpy(&flag, c->ctl + 1, sizeof(int), cudaMemcpyDeviceToHost);

@@ -426,8 +426,9 @@ int ott_rope(const void *q, void *q_out, int Hq, const void *k, void *k_out, int
  * each channel are kept beside it, in fp16, for the Top-K calls' bounds.
  * What the cache holds does not depend on how its tokens were cut into calls.
  *
- * All of these calls need the cache's device to be the current one
- * (OTT_ERR_STATE), and follow the conventions above. Calls on one cache are
+ * All of these calls that use the device need the cache's own to be the
+ * current one (OTT_ERR_STATE), but for ott_byte_destroy, and follow the
+ * conventions above; ott_byte_check synchronizes, too. Calls on one cache are
  * made one after another on one stream (or ordered by events): they share its
  * tables and its scratch, captured graphs of them too. A graph repeats its
  * calls at the lengths that the cache had when they were captured; one that
@@ -445,7 +446,8 @@ enum { OTT_BYTE_INT = 0, OTT_BYTE_FLOAT = 1 };
 int ott_byte_create(int B, int Hq, int Hkv, int d, int G, int format, int max_tokens, long long pool_blocks,
                     ott_byte_cache **out);
 
-/* Free everything. NULL-safe. Waits for the device to finish. */
+/* Free everything. NULL-safe. Waits for the cache's device to finish, whichever one is current, and leaves that one
+ * as it was. */
 int ott_byte_destroy(ott_byte_cache *c);
 
 /*
@@ -526,7 +528,7 @@ int ott_byte_counts(const ott_byte_cache *c, int b, long long *T, int *blocks);
 /* Free blocks of the pool (host-side), -1 without one. */
 long long ott_byte_free_blocks(const ott_byte_cache *c);
 
-/* As ott_check_device. */
+/* As ott_check_device, for the cache's device. */
 int ott_byte_check(ott_byte_cache *c);
 
 /* Bytes of device memory the cache holds. Host-side. */
