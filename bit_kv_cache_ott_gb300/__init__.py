@@ -156,6 +156,23 @@ def _stream(stream) -> int:
     return s.cuda_stream
 
 
+def _new(make, stream, idx: int) -> torch.Tensor:
+    """An output that a call makes itself, make(), for kernels on the given stream: made there if it is not the current
+    one of device idx (whose freed memory may still be read, and whose fills may end late), and kept for the current
+    one's reads."""
+    if stream is None:
+        return make()
+    here = torch.cuda.current_stream(idx)
+    if here.cuda_stream == stream.cuda_stream:
+        return make()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(stream.cuda_stream, device=idx)
+    with torch.cuda.stream(stream):
+        t = make()
+    t.record_stream(here)
+    return t
+
+
 def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, sections, base: float = 10000.0,
          interleaved: bool = False, restart: bool = False, out_q: torch.Tensor | None = None,
          out_k: torch.Tensor | None = None, stream=None):
@@ -180,8 +197,8 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, sect
     if pos.shape != (axes, B, n) or not pos.is_contiguous():
         raise ValueError(f"pos: expected contiguous shape {(axes, B, n)}, got {tuple(pos.shape)}")
     idx = x.get_device()
-    qp, qo, out_q, Hq = _rope_operand(q, out_q, "q", B, n, d)
-    kp, ko, out_k, Hkv = _rope_operand(k, out_k, "k", B, n, d)
+    qp, qo, out_q, Hq = _rope_operand(q, out_q, "q", B, n, d, stream)
+    kp, ko, out_k, Hkv = _rope_operand(k, out_k, "k", B, n, d, stream)
     for t in (pos, q, k, out_q, out_k):
         if t is not None and t.get_device() != idx:
             raise ValueError(f"tensors on {t.device} and cuda:{idx}")
@@ -192,7 +209,7 @@ def rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor, sect
     return out_q, out_k
 
 
-def _rope_operand(x, out, name, B, n, d):
+def _rope_operand(x, out, name, B, n, d, stream):
     """(pointer, output's pointer, output, heads) of one of rope's tensors."""
     if x is None:
         if out is not None:
@@ -201,7 +218,7 @@ def _rope_operand(x, out, name, B, n, d):
     H = x.shape[1]
     p = _dev_ptr(x, (B, H, n, d), name)
     if out is None:
-        out = torch.empty_like(x)
+        out = _new(lambda: torch.empty_like(x), stream, x.get_device())
         return p, out.data_ptr(), out, H
     return p, _dev_ptr(out, (B, H, n, d), f"out_{name}"), out, H
 
@@ -347,10 +364,10 @@ class OTTCache:
 
     def decode_attn(self, q: torch.Tensor, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
         shp = (self.B, self.Hq, self.d)
+        qp = _dev_ptr(q, shp, "q")
         if out is None:
-            out = torch.empty(shp, dtype=torch.float16, device=q.device)
-        _check(load().ott_decode_attn(self._h, _dev_ptr(q, shp, "q"), _dev_ptr(out, shp, "out"),
-                                      _stream(stream)), "ott_decode_attn")
+            out = _new(lambda: torch.empty_like(q), stream, q.get_device())
+        _check(load().ott_decode_attn(self._h, qp, _dev_ptr(out, shp, "out"), _stream(stream)), "ott_decode_attn")
         return out
 
     def decode_attn_topk(self, q: torch.Tensor, K: int, out: torch.Tensor | None = None,
@@ -360,8 +377,9 @@ class OTTCache:
         is a CUDA int32 tensor [B*Hkv][min(K, nf)] that receives the blocks
         (nf: the largest block count of any sequence)."""
         shp = (self.B, self.Hq, self.d)
+        qp = _dev_ptr(q, shp, "q")
         if out is None:
-            out = torch.empty(shp, dtype=torch.float16, device=q.device)
+            out = _new(lambda: torch.empty_like(q), stream, q.get_device())
         sp = None
         if sel is not None:
             nf = max(self.seq_counts(b)[1] for b in range(self.B)) if self.ragged else self.counts()[1]
@@ -370,7 +388,7 @@ class OTTCache:
                     or tuple(sel.shape) != (self.B * self.Hkv, kc)):
                 raise ValueError(f"sel: expected a contiguous CUDA int32 tensor {(self.B * self.Hkv, kc)}")
             sp = sel.data_ptr()
-        _check(load().ott_decode_attn_topk(self._h, _dev_ptr(q, shp, "q"), _dev_ptr(out, shp, "out"), int(K), sp,
+        _check(load().ott_decode_attn_topk(self._h, qp, _dev_ptr(out, shp, "out"), int(K), sp,
                                            _stream(stream)), "ott_decode_attn_topk")
         return out
 
@@ -391,7 +409,7 @@ class OTTCache:
         shp, kshp = (self.B, self.Hq, n, self.d), (self.B, self.Hkv, n, self.d)
         ptr = [_dev_ptr(q, shp, "q"), _dev_ptr(k, kshp, "k"), _dev_ptr(v, kshp, "v")]
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(lambda: torch.empty_like(q), stream, q.get_device())
         ptr.append(_dev_ptr(out, shp, "out"))
         _same_device(self._dev, q, k, v, out)
         _on_device(self._dev, load().ott_chunk_attn, "ott_chunk_attn", self._h, *ptr, n, self._lens(lens),
@@ -414,7 +432,7 @@ class OTTCache:
         shp = (self.B, self.Hq, self.d)
         qp = _dev_ptr(q, shp, "q")
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(lambda: torch.empty_like(q), stream, q.get_device())
         op = _dev_ptr(out, shp, "out")
         _same_device(self._dev, q, out)
         _on_device(self._dev, load().ott_decode_attn_window, "ott_decode_attn_window", self._h, qp, op,
@@ -619,10 +637,11 @@ class ByteCache:
         [B][Hkv][n][d]. Rows of tokens that a sequence does not hold stay as they are (zero in a new tensor)."""
         n = _int32(n, "n")
         shp = (self.B, self.Hkv, n, self.d)
+        zeros = lambda: torch.zeros(shp, dtype=torch.float16, device=f"cuda:{self._dev}")
         if out_k is None:
-            out_k = torch.zeros(shp, dtype=torch.float16, device=f"cuda:{self._dev}")
+            out_k = _new(zeros, stream, self._dev)
         if out_v is None:
-            out_v = torch.zeros(shp, dtype=torch.float16, device=f"cuda:{self._dev}")
+            out_v = _new(zeros, stream, self._dev)
         self._call(self._L.ott_byte_read, "ott_byte_read", self._ptr(out_k, shp, "out_k"), self._ptr(out_v, shp, "out_v"),
                    _int32(start, "start"), n, stream=stream)
         return out_k, out_v
@@ -638,7 +657,7 @@ class ByteCache:
         1), receives the blocks."""
         qp = self._ptr(q, self._qshape, "q")
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(lambda: torch.empty_like(q), stream, self._dev)
         self._call(self._L.ott_byte_decode, "ott_byte_decode", qp, self._ptr(out, self._qshape, "out"), _int32(K, "K"),
                    self._sel(sel, 1, K), stream=stream)
         return out
@@ -659,7 +678,7 @@ class ByteCache:
         shp, kshp = (self.B, self.Hq, n, self.d), (self.B, self.Hkv, n, self.d)
         ptr = [self._ptr(q, shp, "q"), self._ptr(k, kshp, "k"), self._ptr(v, kshp, "v")]
         if out is None:
-            out = torch.empty_like(q)
+            out = _new(lambda: torch.empty_like(q), stream, self._dev)
         lens = self._lens(lens)
         self._call(self._L.ott_byte_attn, "ott_byte_attn", *ptr, self._ptr(out, shp, "out"), n,
                    lens and lens.buffer_info()[0], _int32(K, "K"), self._sel(sel, n, K), stream=stream)
