@@ -591,12 +591,13 @@ class ByteCache:
     def _lens(self, lens):
         if lens is None:
             return None
-        if len(lens) != self.B:
-            raise ValueError("lens must hold one length per sequence")
         try:
-            return array.array("i", lens)
+            lens = array.array("i", [*lens])   # (of the list: bytes alone would be taken for the array's memory)
         except OverflowError:
             raise ValueError("lens: a length does not fit 32 bits") from None
+        if len(lens) != self.B:   # the library reads B of them
+            raise ValueError("lens must hold one length per sequence")
+        return lens
 
     def _append(self, k, v, n, shape, lens, stream):
         lens = self._lens(lens)   # alive during the call
