@@ -538,14 +538,15 @@ class ByteCache:
         self._L = L = load()
         if fmt not in self.FORMATS:
             raise ValueError(f"fmt: expected one of {tuple(self.FORMATS)}, got {fmt!r}")
-        if pool_blocks is not None and int(pool_blocks) < 1:
+        pool = 0 if pool_blocks is None else _int32(pool_blocks, "pool_blocks")
+        if pool_blocks is not None and pool < 1:
             raise ValueError("pool_blocks: at least one block")
         self.B, self.Hq, self.Hkv, self.d, self.G, self.fmt, self.max_tokens = B, Hq, Hkv, d, G, fmt, max_tokens
         self._h = C.c_void_p()
         self._dev = torch.cuda.current_device()
         self._qshape, self._kshape = (B, Hq, d), (B, Hkv, d)
         sizes = [_int32(x, n) for x, n in ((B, "B"), (Hq, "Hq"), (Hkv, "Hkv"), (d, "d"), (G, "G"))]
-        _check(L.ott_byte_create(*sizes, self.FORMATS[fmt], _int32(max_tokens, "max_tokens"), int(pool_blocks or 0),
+        _check(L.ott_byte_create(*sizes, self.FORMATS[fmt], _int32(max_tokens, "max_tokens"), pool,
                                  C.byref(self._h)), "ott_byte_create")
 
     def close(self):

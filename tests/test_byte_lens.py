@@ -40,3 +40,15 @@ def test_of_another_type():
         _cache(2)._lens([1, 1.5])
     with pytest.raises(TypeError):
         _cache(2)._lens("12")
+
+
+@pytest.mark.parametrize("pool", [2 ** 31, 2 ** 32 + 8, 2 ** 64 + 8, -2 ** 64 + 8])
+def test_blocks_of_a_pool(monkeypatch, pool):
+    """A pool is as large as it was asked to be, or refused."""
+    import bit_kv_cache_ott_gb300 as pkg
+    asked = []
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(pkg, "load", lambda: type("L", (), {"ott_byte_create": staticmethod(lambda *a: asked.append(a) or -1)}))
+    with pytest.raises(ValueError):
+        pkg.ByteCache(1, 1, 1, 64, 32, pool_blocks=pool)
+    assert not asked
