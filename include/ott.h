@@ -422,8 +422,12 @@ int ott_rope(const void *q, void *q_out, int Hq, const void *k, void *k_out, int
  *   OTT_BYTE_INT:   code = rint(127 x / a), scale = a / 127;
  *   OTT_BYTE_FLOAT: code = the e4m3 number nearest 448 x / a, scale = a / 448,
  * ties to even, both decided by the exact quotient; a = 0 gives codes and
- * scale 0. A code stands for code * scale. The smallest and largest key of
- * each channel are kept beside it, in fp16, for the Top-K calls' bounds.
+ * scale 0. A code stands for code * scale. All channels of a block share its
+ * scale: beside a channel of large values the others of an OTT_BYTE_INT block
+ * have few steps left (a value is off by up to a / 254), while OTT_BYTE_FLOAT
+ * keeps a value's own leading bits (up to 2^-4 of it). The smallest and largest
+ * key of each channel are kept beside it, in fp16, for the Top-K calls' bounds:
+ * of the keys as given, which the held ones may leave by half a step.
  * What the cache holds does not depend on how its tokens were cut into calls.
  *
  * All of these calls that use the device need the cache's own to be the
@@ -508,10 +512,13 @@ int ott_byte_decode(ott_byte_cache *c, const void *q, void *out, int topk, int32
  * on their own. Keys and values are finite; one that is not spoils rows that
  * do not see it as well. A query that is not finite gets NaN in its own row
  * (with topk the selection of its kv head is then any) and changes no other
- * row's attention. A call gives the same bits every time; the kernel and the
- * order of its sums go by the largest lens of up to 64 sequences and the
- * GPU's SMs. Larger scratch than the cache's own comes from the library's
- * stream-ordered pool (OTT_ERR_OOM before anything is queued).
+ * row's attention. The same call on the same state of the cache gives the same
+ * bits. Up to 64 sequences go in one launch (0 .. 63, 64 .. 127 ..), and the
+ * kernel and the order of its sums go by lens, the tokens that the cache holds
+ * for all of them, topk, and the GPU's SMs: a sequence's last bits may change
+ * when another one of its launch grows. Larger scratch than the cache's own
+ * comes from the library's stream-ordered pool (OTT_ERR_OOM before anything is
+ * queued).
  */
 int ott_byte_attn(ott_byte_cache *c, const void *q, const void *k, const void *v, void *out, int n, const int *lens,
                   int topk, int32_t *sel, void *stream);
