@@ -195,8 +195,8 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
     Cursor cc = ic;
 
     auto cold_of = [&](int u, int &ncold, int &chead) {
-        ncold = a.C > 0 ? __ldg(a.cmeta + 2 * u) : 0;
-        chead = a.C > 0 ? __ldg(a.cmeta + 2 * u + 1) : 0;
+        ncold = a.C > 0 ? a.cmeta[2 * u] : 0;
+        chead = a.C > 0 ? a.cmeta[2 * u + 1] : 0;
     };
     auto issue = [&](const Cursor &c, int sg) {
         const ChunkSeq &s = st.e[c.e];
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
             }
         } else {
             const int jp = c.jp, k = c.k;
-            const int j = jp < s.nsink ? __ldg(a.sel + (size_t)u * a.NB + jp) : s.jlo + jp - s.nsink;
+            const int j = jp < s.nsink ? a.sel[(size_t)u * a.NB + jp] : s.jlo + jp - s.nsink;
             // of a listed block, the first tokens: they come first
             const int rem = j < 0 ? 0 : min(CT, (jp < s.nsink ? min(a.sinks, chunk_block_cnt(a, u, j)) : chunk_block_cnt(a, u, j)) - CT * k);
             if (rem > 0) {
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
                 if (lane == 0) {
                     const int nt = (rem + TILE - 1) / TILE;
                     const size_t own = (size_t)u * a.NB + j;
-                    const uint8_t *src = a.blk + (a.bt ? (size_t)__ldg(a.bt + own) : own) * a.blk_bytes;
+                    const uint8_t *src = a.blk + (a.bt ? (size_t)a.bt[own] : own) * a.blk_bytes;
                     const bool hdr = k == 0 || c.x == x0;
                     expect_tx(&bars[sg], (uint32_t)((hdr ? KSZ : 0) + nt * TB));
                     if (hdr) bulk_copy(dst, src, KSZ, &bars[sg]);
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
             for (int kt = 0; kt < NKT; ++kt)
 #pragma unroll
                 for (int o = 0; o < 2; ++o)
-                    Bq[nc][kt][o] = __ldg(reinterpret_cast<const uint32_t *>(qp + 16 * kt + 2 * i + 8 * o));
+                    Bq[nc][kt][o] = *reinterpret_cast<const uint32_t *>(qp + 16 * kt + 2 * i + 8 * o);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 pos[nc][x] = s.pos0 + min(v0 + 8 * nc + 2 * i + x, vend - 1) / a.g;
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(RowsCfg<D, NC>::WARPS * 32, 1)
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const int x = 16 * tau + r + 8 * h;
-                                const int t = x >= mt_.x ? INT_MAX : (wnd ? __ldg(bi + x) : 0);
+                                const int t = x >= mt_.x ? INT_MAX : (wnd ? bi[x] : 0);
 #pragma unroll
                                 for (int nc = 0; nc < NC; ++nc)
 #pragma unroll
@@ -692,7 +692,7 @@ __global__ void __launch_bounds__(SINK_THREADS)
 #pragma unroll
         for (int y = 0; y < SINK_PER; ++y) {
             const int j = j0 + y * SINK_THREADS + threadIdx.x;
-            first[y] = j < jlo && chunk_block_cnt(a, u, j) > 0 ? __ldg(a.bidx + ((size_t)u * a.NB + j) * a.G) : INT_MAX;
+            first[y] = j < jlo && chunk_block_cnt(a, u, j) > 0 ? a.bidx[((size_t)u * a.NB + j) * a.G] : INT_MAX;
         }
         unsigned bal[SINK_PER];
 #pragma unroll

@@ -64,7 +64,7 @@ struct ChunkArgs {
 
 // Valid tokens of block j of unit u.
 __device__ __forceinline__ int chunk_block_cnt(const ChunkArgs &a, int u, int j) {
-    if (a.bcnt) return __ldg(a.bcnt + (size_t)u * a.NB + j);
+    if (a.bcnt) return a.bcnt[(size_t)u * a.NB + j];
     return j >= a.jfull ? a.G : block_count(a.P, a.G, j);
 }
 
@@ -73,12 +73,12 @@ __device__ __forceinline__ int chunk_block_cnt(const ChunkArgs &a, int u, int j)
 __device__ __forceinline__ int chunk_fp16_pos(const ChunkArgs &a, const ChunkSeq &s, int u, int f, int ncold, int chead) {
     if (f < s.ntail) return s.T - s.ntail + f;
     f -= s.ntail;
-    if (f < s.npool) return __ldg(a.pidx + (size_t)u * a.P + f);
+    if (f < s.npool) return a.pidx[(size_t)u * a.P + f];
     f -= s.npool;
     if (f < ncold) {
         int x = chead + f;
         if (x >= a.C) x -= a.C;
-        return __ldg(a.cidx + (size_t)u * a.C + x);
+        return a.cidx[(size_t)u * a.C + x];
     }
     return s.T + f - ncold;
 }

@@ -243,14 +243,14 @@ __device__ __forceinline__ Group group_at(const ChunkArgs &a, const ChunkSeq &s,
     g.src = nullptr;
     g.j = t.jlo + jp;
     if (listed) {
-        g.j = __ldg(a.sel + (size_t)u * a.NB + jp);
+        g.j = a.sel[(size_t)u * a.NB + jp];
         if (g.j >= t.jlo) g.j = -1;   // in the window's own range
     }
     if (g.j >= 0) {
         const int cnt = chunk_block_cnt(a, u, g.j);
         g.left = (listed ? min(cnt, a.sinks) : cnt) - 16 * g.sub;
         const size_t own = (size_t)u * a.NB + g.j;
-        g.src = a.blk + (a.bt ? (size_t)__ldg(a.bt + own) : own) * a.blk_bytes;
+        g.src = a.blk + (a.bt ? (size_t)a.bt[own] : own) * a.blk_bytes;
     }
     return g;
 }
@@ -343,7 +343,7 @@ struct Producer {
                     gn = gb;
                 } else {   // the run's first group, or one behind a short block's tokens
                     gn = group_at(a, s, t, cpt, u, xn);
-                    if (gn.left > 0 && lane < D / 4) hb = __ldg(reinterpret_cast<const uint4 *>(gn.src) + lane);
+                    if (gn.left > 0 && lane < D / 4) hb = reinterpret_cast<const uint4 *>(gn.src)[lane];
                 }
                 enter = gn.left > 0;
             }
@@ -388,7 +388,7 @@ struct Producer {
                 const bool ask = g.left < 16 || a.window > 0 || wide;
                 int pos = INT_MAX;
                 if (ask && lane < 16 && lane < g.left)
-                    pos = a.window > 0 ? __ldg(a.bidx + ((size_t)u * a.NB + g.j) * a.G + 16 * g.sub + lane) : 0;
+                    pos = a.window > 0 ? a.bidx[((size_t)u * a.NB + g.j) * a.G + 16 * g.sub + lane] : 0;
                 key_done(ask, pos, wide);
             }
             if (enter) {   // the block's scales, through shared memory; then the next block's are fetched
@@ -409,7 +409,7 @@ struct Producer {
                 xb = x + k + 1 - gn.sub + gn.per;
                 if (xb < x + n) {
                     gb = group_at(a, s, t, cpt, u, xb);
-                    if (gb.left > 0 && lane < D / 4) hb = __ldg(reinterpret_cast<const uint4 *>(gb.src) + lane);
+                    if (gb.left > 0 && lane < D / 4) hb = reinterpret_cast<const uint4 *>(gb.src)[lane];
                 }
             }
             const bool load = k + 1 < n && gn.left > 0;
@@ -446,7 +446,7 @@ struct Producer {
                 words(tb + tile_v_off(D), vr);
 #pragma unroll
                 for (int gm = 0; gm < NKT / 2; ++gm) {
-                    const uint4 z = __ldg(reinterpret_cast<const uint4 *>(tb + tile_sz_off(D)) + gm * 4 + i);
+                    const uint4 z = reinterpret_cast<const uint4 *>(tb + tile_sz_off(D))[gm * 4 + i];
                     zr[4 * gm] = z.x; zr[4 * gm + 1] = z.y; zr[4 * gm + 2] = z.z; zr[4 * gm + 3] = z.w;
                 }
             }
@@ -461,7 +461,7 @@ struct Producer {
     // memory, both under one wait. (Loads a group ahead would take registers
     // that the other loop, which has most of the work, would spill.)
     __device__ void plain(int x, int n) {
-        const int ncold = a.C > 0 ? __ldg(a.cmeta + 2 * u) : 0, chead = a.C > 0 ? __ldg(a.cmeta + 2 * u + 1) : 0;
+        const int ncold = a.C > 0 ? a.cmeta[2 * u] : 0, chead = a.C > 0 ? a.cmeta[2 * u + 1] : 0;
         const int nhot = s.ntail + s.npool + ncold;
         uint8_t *const stage = sm + C::OFF_STG + w * (32 * D);   // 16 rows, 16-byte chunks turned by the row
 #pragma unroll 1
@@ -483,7 +483,7 @@ struct Producer {
             for (int e = 0; e < 16 / RPI; ++e) {
                 const unsigned long long p = __shfl_sync(0xffffffffu, at, RPI * e + lane / CPR);
                 kr[e] = make_uint4(0, 0, 0, 0);
-                if (p) kr[e] = __ldg(reinterpret_cast<const uint4 *>(p) + lane % CPR);
+                if (p) kr[e] = reinterpret_cast<const uint4 *>(p)[lane % CPR];
             }
 #pragma unroll
             for (int e = 0; e < 16 / RPI; ++e) {
@@ -526,10 +526,10 @@ struct Producer {
     __device__ static void words(const uint8_t *p, uint32_t (&d)[NW]) {
         const int lane = threadIdx.x & 31;
         if constexpr (NW == 4) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p) + lane);
+            const uint4 x = reinterpret_cast<const uint4 *>(p)[lane];
             d[0] = x.x; d[1] = x.y; d[2] = x.z; d[3] = x.w;
         } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p) + lane);
+            const uint2 x = reinterpret_cast<const uint2 *>(p)[lane];
             d[0] = x.x; d[1] = x.y;
         }
     }
@@ -880,7 +880,7 @@ __device__ void role_loop(const TileArgs &ta, const ChunkTable &st, uint8_t *sm,
                 for (int y = 0; y < BATCH; ++y) {
                     const int row = rr + STEP * y, vv = 256 * t.p + row, tk = vv / a.g;
                     v[y] = make_uint4(0, 0, 0, 0);
-                    if (row < t.rows) v[y] = __ldg(reinterpret_cast<const uint4 *>(q0 + ((size_t)(vv - tk * a.g) * a.n + tk) * D));
+                    if (row < t.rows) v[y] = *reinterpret_cast<const uint4 *>(q0 + ((size_t)(vv - tk * a.g) * a.n + tk) * D);
                 }
 #pragma unroll
                 for (int y = 0; y < BATCH; ++y) {

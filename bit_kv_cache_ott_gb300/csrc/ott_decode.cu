@@ -228,8 +228,8 @@ struct Cfg {
 // tokens are written back, written by the flush under the cold-pool policy.
 template <bool CO, bool MS = false>
 __device__ __forceinline__ int block_cnt(const DecodeArgs &a, int u, int j) {
-    if (MS && a.bcnt) return __ldg(a.bcnt + (size_t)u * a.NB + j);
-    if constexpr (CO) return __ldg(a.bcnt + (size_t)u * a.NB + j);
+    if (MS && a.bcnt) return a.bcnt[(size_t)u * a.NB + j];
+    if constexpr (CO) return a.bcnt[(size_t)u * a.NB + j];
     return j >= a.jfull ? a.G : block_count(a.P, a.G, j);
 }
 
@@ -375,7 +375,7 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
     // rows mode: the listed blocks of the first tokens, then those of the window
     auto block_of = [&](int j) -> int {
         if (j >= ru.s->nsink) return ru.s->jlo + j - ru.s->nsink;
-        return __ldg(a.sel + (size_t)u * a.NB + j);
+        return a.sel[(size_t)u * a.NB + j];
     };
     auto cnt_at = [&](int j) -> int {
         if constexpr (MS) {
@@ -385,7 +385,7 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
             return j < ru.s->nsink ? min(n, a.sinks) : n;   // a listed block: its first tokens come first
         }
         if constexpr (TK) {
-            const int bj = __ldg(a.sel + (size_t)u * a.Ksel + j);
+            const int bj = a.sel[(size_t)u * a.Ksel + j];
             return bj < 0 ? 0 : block_cnt<CO>(a, u, bj);
         }
         return block_cnt<CO>(a, u, j);
@@ -435,10 +435,10 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
             const int t0 = c.k * CHUNK_TILES, nt = min(CHUNK_TILES, vt - t0);
             int bj = c.j;
             if constexpr (MS) bj = block_of(c.j);
-            if constexpr (TK) bj = __ldg(a.sel + (size_t)u * a.Ksel + c.j);
+            if constexpr (TK) bj = a.sel[(size_t)u * a.Ksel + c.j];
             size_t bslot = (size_t)u * a.NB + bj;
             if constexpr (RG || MS) {
-                if (a.bt) bslot = (size_t)__ldg(a.bt + bslot);
+                if (a.bt) bslot = (size_t)a.bt[bslot];
             }
             const uint8_t *bsrc = a.blk + bslot * a.blk_bytes;
             uint8_t *dst = st ? stg1 : stg0;
@@ -534,7 +534,7 @@ __device__ bool quant_segment(const DecodeArgs &a, size_t slot, int u, int uq, i
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int x = 16 * tau + r + 8 * h;
-                    tok[tau][h] = x < cc.cnt - CT * cc.k ? __ldg(bi + x) : 0;
+                    tok[tau][h] = x < cc.cnt - CT * cc.k ? bi[x] : 0;
                 }
         }
         if (!mbar_wait(&bars[st], (phase >> st) & 1u)) {
@@ -867,8 +867,8 @@ __device__ bool fp16_segment(const DecodeArgs &a, const UnitInfo &ui, size_t slo
     int ncold = 0, chead = 0;
     if constexpr (CO || MS) {
         if (a.C > 0) {
-            ncold = __ldg(a.cmeta + 2 * u);
-            chead = __ldg(a.cmeta + 2 * u + 1);
+            ncold = a.cmeta[2 * u];
+            chead = a.cmeta[2 * u + 1];
         }
     }
     const int nhot = ui.ntail + ui.npool, nfp = nhot + ncold + (MS ? ru.s->nnew : 0);
@@ -964,9 +964,9 @@ __device__ bool fp16_segment(const DecodeArgs &a, const UnitInfo &ui, size_t slo
                 if (f < ui.ntail)
                     t = ru.s->T - ui.ntail + f;
                 else if (f < nhot)
-                    t = __ldg(a.pidx + (size_t)u * a.P + (f - ui.ntail));
+                    t = a.pidx[(size_t)u * a.P + (f - ui.ntail)];
                 else if (f < nhot + ncold)
-                    t = __ldg(a.cidx + (size_t)u * a.C + (chead + f - nhot) % a.C);
+                    t = a.cidx[(size_t)u * a.C + (chead + f - nhot) % a.C];
                 if (!chunk_sees(t, ru.pos, ru.lo, a.sinks)) lg = -CUDART_INF_F;
             }
         }

@@ -632,7 +632,7 @@ inline size_t pf_group_smem_bytes(int d, int G) { return (size_t)G * (d + 8) * 2
 // For a chunk, `nu` CTAs more take the old pools: their keys into list 0,
 // their rows aside.
 template <int D>
-__global__ void __launch_bounds__(PF_THREADS) k_pf_group(const __half *__restrict__ srcK, long long src_unit_stride,
+__global__ void __launch_bounds__(PF_THREADS) k_pf_group(const __half *srcK, long long src_unit_stride,
                                                          int src_u0, int u0, int nf, int G, int P,
                                                          uint64_t *__restrict__ gtop, const ChunkFlushes cf) {
     // the group's keys, staged by coalesced asynchronous copies into rows
@@ -750,7 +750,7 @@ inline size_t scan_smem_bytes(int sw, int P) {
     return (size_t)sw * P * (2 + SCAN_AHEAD + 2) * 8 + (size_t)sw * 2 * 4;
 }
 
-__global__ void __launch_bounds__(SCAN_WARPS * 32) k_pf_scan(const uint64_t *__restrict__ gtop,
+__global__ void __launch_bounds__(SCAN_WARPS * 32) k_pf_scan(const uint64_t *gtop,
                                                              uint64_t *__restrict__ phist, int nf_unit, int G, int P,
                                                              int cg, int C, uint64_t *__restrict__ gtot) {
     extern __shared__ uint64_t scan_sm[];
@@ -851,7 +851,7 @@ constexpr int CARRY_MAX_CHUNKS = 32;
 inline size_t carry_smem_bytes(int C, int nw, int P) { return ((size_t)2 * C + nw) * P * 8; }
 
 __global__ void __launch_bounds__(SCAN_WARPS * 32) k_pf_carry(uint64_t *__restrict__ phist,
-                                                              const uint64_t *__restrict__ gtot, int nf, int G,
+                                                              const uint64_t *gtot, int nf, int G,
                                                               int P, int cg, int C) {
     extern __shared__ uint64_t car_sm[];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -909,8 +909,8 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) k_pf_carry(uint64_t *__restri
 // k, v [U][d] -> ring slot `slot` of every unit
 // With qsrc, the step's queries (nq 16-byte vectors) are copied to qdst too
 // (a step fed from host memory: k, v and q are read where they are).
-__global__ void k_append(const uint4 *__restrict__ k, const uint4 *__restrict__ v, __half *rk,
-                         __half *rv, int U, int d, int ring, int slot, const uint4 *__restrict__ qsrc,
+__global__ void k_append(const uint4 * k, const uint4 * v, __half *rk,
+                         __half *rv, int U, int d, int ring, int slot, const uint4 *qsrc,
                          uint4 *__restrict__ qdst, int nq) {
     // a decode queued next may start now; it waits for this grid before reading the ring
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -938,9 +938,9 @@ struct SlotTable {
     int slot[RAGGED_MAX];
 };
 
-__global__ void k_append_ragged(const uint4 *__restrict__ k, const uint4 *__restrict__ v, __half *rk,
+__global__ void k_append_ragged(const uint4 * k, const uint4 * v, __half *rk,
                                 __half *rv, int U, int Hkv, int d, int ring, const __grid_constant__ SlotTable st,
-                                const uint4 *__restrict__ qsrc, uint4 *__restrict__ qdst, int nq) {
+                                const uint4 *qsrc, uint4 *__restrict__ qdst, int nq) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int vpr = d / 8, n = U * vpr;
@@ -978,7 +978,7 @@ __global__ void k_copy_tail(const __half *K, const __half *V, __half *rk, __half
 
 // Tokens [from, to) of each sequence's chunk, k, v [B][Hkv][n][d] -> the ring.
 // One 16-byte vector of k and of v per thread and step; `per` CTAs per unit.
-__global__ void k_append_range(const uint4 *__restrict__ k, const uint4 *__restrict__ v, __half *rk, __half *rv, int n,
+__global__ void k_append_range(const uint4 * k, const uint4 * v, __half *rk, __half *rv, int n,
                                int Hkv, int d, int ring, int b0, int per, const __grid_constant__ ChunkRange r) {
     // a call queued next may start now; it waits for this grid
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
