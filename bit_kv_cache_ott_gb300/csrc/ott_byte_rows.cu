@@ -38,7 +38,7 @@
 // What bounds it: HBM. Batch 32 x 4K, 32 heads of d = 128 (1.07 GB of cache)
 // takes 161 us, 6.7 TB/s; with four queries each, 165. Calls of a few ten us
 // add the start of the copies and the merge: 131K tokens, 8 kv heads (269 MB),
-// 46 us, 5.8 TB/s; 32 sequences of 1K to 7K from a paged pool (272 MB) 50.5. 12
+// 47 us, 5.7 TB/s; 32 sequences of 1K to 7K from a paged pool (272 MB) 51. 12
 // warps with two stages each instead of 8 with three: 161 and 50.5 us became
 // 160 and 53.
 #include <algorithm>

@@ -29,7 +29,8 @@
 // truncate.
 //
 // What bounds it: 512 tokens of four sequences over 32K (8 kv heads, 4 heads
-// each, d = 128) take 850 us, 1.31 PFLOP/s; 2,048 over 131K 3.12 ms, 1.42. A
+// each, d = 128) take 850 to 871 us, 1.27 to 1.31 PFLOP/s; 2,048 over 131K 3.12
+// to 3.37 ms, 1.32 to 1.42 (the power limit: by the GPU and what ran before). A
 // step is some 2,900 cycles, 1,920 of them products (a score product takes as
 // long for 112 keys as for 128: its queries are read at 64 bytes a cycle). The
 // rest is the chain that a tile goes through, since S(j+1) takes the place of
