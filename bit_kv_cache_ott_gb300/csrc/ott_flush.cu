@@ -909,7 +909,7 @@ __global__ void __launch_bounds__(SCAN_WARPS * 32) k_pf_carry(uint64_t *__restri
 // k, v [U][d] -> ring slot `slot` of every unit
 // With qsrc, the step's queries (nq 16-byte vectors) are copied to qdst too
 // (a step fed from host memory: k, v and q are read where they are).
-__global__ void k_append(const uint4 * k, const uint4 * v, __half *rk,
+__global__ void k_append(const uint4 *k, const uint4 *v, __half *rk,
                          __half *rv, int U, int d, int ring, int slot, const uint4 *qsrc,
                          uint4 *__restrict__ qdst, int nq) {
     // a decode queued next may start now; it waits for this grid before reading the ring
@@ -938,7 +938,7 @@ struct SlotTable {
     int slot[RAGGED_MAX];
 };
 
-__global__ void k_append_ragged(const uint4 * k, const uint4 * v, __half *rk,
+__global__ void k_append_ragged(const uint4 *k, const uint4 *v, __half *rk,
                                 __half *rv, int U, int Hkv, int d, int ring, const __grid_constant__ SlotTable st,
                                 const uint4 *qsrc, uint4 *__restrict__ qdst, int nq) {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -978,7 +978,7 @@ __global__ void k_copy_tail(const __half *K, const __half *V, __half *rk, __half
 
 // Tokens [from, to) of each sequence's chunk, k, v [B][Hkv][n][d] -> the ring.
 // One 16-byte vector of k and of v per thread and step; `per` CTAs per unit.
-__global__ void k_append_range(const uint4 * k, const uint4 * v, __half *rk, __half *rv, int n,
+__global__ void k_append_range(const uint4 *k, const uint4 *v, __half *rk, __half *rv, int n,
                                int Hkv, int d, int ring, int b0, int per, const __grid_constant__ ChunkRange r) {
     // a call queued next may start now; it waits for this grid
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

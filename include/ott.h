@@ -425,9 +425,10 @@ int ott_rope(const void *q, void *q_out, int Hq, const void *k, void *k_out, int
  * scale 0. A code stands for code * scale. All channels of a block share its
  * scale: beside a channel of large values the others of an OTT_BYTE_INT block
  * have few steps left (a value is off by up to a / 254), while OTT_BYTE_FLOAT
- * keeps a value's own leading bits (up to 2^-4 of it). The smallest and largest
- * key of each channel are kept beside it, in fp16, for the Top-K calls' bounds:
- * of the keys as given, which the held ones may leave by half a step.
+ * keeps a value's own leading bits (off by up to 2^-4 of it, or by 2^-10 of the
+ * scale if that is more). The smallest and largest key of each channel are kept
+ * beside it, in fp16, for the Top-K calls' bounds: of the keys as given, which
+ * the held ones may leave by half a step.
  * What the cache holds does not depend on how its tokens were cut into calls.
  *
  * All of these calls that use the device need the cache's own to be the

@@ -14,6 +14,8 @@ def test_calls_with_another_device_current(tmp_path):
     from bit_kv_cache_ott_gb300 import build
     build.build()
     obj, exe = os.path.join(build.OUT_DIR, "ott_byte.o"), str(tmp_path / "host")
+    if not os.path.exists(obj):   # the library came without what it was linked of
+        build.build(force=True)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(build.nvcc())))
     inc = [f"-I{d}" for d in (os.path.join(ROOT, "include"), os.path.join(cuda, "include")) if os.path.isdir(d)]
     r = subprocess.run(["g++", "-std=c++17", *inc, os.path.join(ROOT, "tests", "byte_device_host.cpp"), obj, "-o", exe],

@@ -131,3 +131,29 @@ def test_a_side_stream_captured(ott):
     for c in caches:
         c.check_device()
         c.close()
+
+
+@pytest.mark.gpu
+def test_a_side_stream_of_a_capture(ott):
+    """A branch of a graph: the side stream forks from the capturing one and joins it."""
+    calls, caches = _calls(ott)
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+    for name, call, _ in calls:
+        want = call(None)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=main):
+            side.wait_stream(main)
+            out = call(side)
+            main.wait_stream(side)
+            twice = out + out
+        out.zero_()
+        twice.zero_()
+        for _ in range(2):
+            graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(twice, want + want), name
+        del out, twice, graph
+    for c in caches:
+        c.check_device()
+        c.close()
